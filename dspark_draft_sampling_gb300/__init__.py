@@ -1,5 +1,6 @@
 """libdspark: GB300-native DSpark per-cycle draft step (Markov block draft,
-Q8_0 confidence probe, weight-stationary small-M matvec).
+Q8_0 confidence probe, weight-stationary small-M matvec) and its key-value side (paged
+cache, rotary positions, attention of new tokens over the cache).
 
 Every step of the path runs in the CUDA kernels of ``libdspark.so``; this package
 only marshals torch tensors into the C ABI declared in ``include/dspark.h``.
@@ -9,7 +10,9 @@ from .api import (  # noqa: F401
     DsparkError,
     GatedDraftPlan,
     MarkovPlan,
+    PagedCache,
     ProbeCall,
+    RotaryTable,
     conf_probe,
     conf_probe_host,
     conf_probe_split,
@@ -18,7 +21,11 @@ from .api import (  # noqa: F401
     markov_draft,
     markov_draft_host,
     markov_workspace_bytes,
+    paged_attention,
     q8_0_repack,
+    rotary,
+    rotary_append,
+    rotary_frequencies,
     ws_matvec,
     ws_matvec_grouped,
     ws_matvec_host,

@@ -8,6 +8,7 @@ raised.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 import time
@@ -16,12 +17,14 @@ import torch
 
 from . import build as _build
 
-_STATUS_NAMES = {0: "OK", 1: "INVALID", 2: "UNSUPPORTED", 3: "CUDA", 4: "TIMEOUT", 5: "INDEX"}
+_STATUS_NAMES = {0: "OK", 1: "INVALID", 2: "UNSUPPORTED", 3: "CUDA", 4: "TIMEOUT", 5: "INDEX",
+                 6: "CAPACITY"}
 DSPARK_OK, DSPARK_ERR_INVALID, DSPARK_ERR_UNSUPPORTED = 0, 1, 2
-DSPARK_ERR_CUDA, DSPARK_ERR_TIMEOUT, DSPARK_ERR_INDEX = 3, 4, 5
+DSPARK_ERR_CUDA, DSPARK_ERR_TIMEOUT, DSPARK_ERR_INDEX, DSPARK_ERR_CAPACITY = 3, 4, 5, 6
 
 # Every symbol the header declares, with (restype, argtypes).
 _P, _I, _U, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_float, ctypes.c_size_t
+_L = ctypes.c_longlong
 SIGNATURES = {
     "dspark_last_error": (ctypes.c_char_p, []),
     "dspark_version": (ctypes.c_char_p, []),
@@ -69,6 +72,17 @@ SIGNATURES = {
     "dspark_ws_matvec_q8_grouped_workspace_bytes": (_Z, [_P, _I]),
     "dspark_ws_matvec_q8_grouped": (_I, [_P, _I, _P, _Z, _P]),
     "dspark_ws_matvec_q8_grouped_debug": (_I, [_P, _I, _P, _Z, _I, _U, _P]),
+    "dspark_cache_workspace_bytes": (_Z, [_P]),
+    "dspark_cache_extend": (_I, [_P, _P, _P, _I, _P]),
+    "dspark_cache_fork": (_I, [_P, _P, _P, _I, _P]),
+    "dspark_cache_compact": (_I, [_P, _P, _P, _P, _I, _P, _I, _P]),
+    "dspark_cache_free": (_I, [_P, _P, _I, _P]),
+    "dspark_cache_copy_pages": (_I, [_P, _P, _P, _I, _P]),
+    "dspark_cache_status": (_I, [_P, _P]),
+    "dspark_rotary": (_I, [_P, _L, _L, _P, _L, _L, _I, _I, _I, _I, _P, _P, _I, _I, _F, _I, _P]),
+    "dspark_rotary_append": (_I, [_P, _I, _P, _L, _L, _P, _L, _L, _P, _L, _L, _P, _L, _L, _I, _I, _P, _P, _I, _P, _P,
+                                  _I, _I, _F, _P]),
+    "dspark_paged_attention": (_I, [_P, _I, _P, _L, _L, _I, _I, _P, _P, _I, _I, _I, _I, _F, _P, _L, _L, _P, _P]),
 }
 
 _lock = threading.Lock()
@@ -783,3 +797,253 @@ def ws_matvec_grouped_host(problems, scratch, *, inputs_copied=None, stream=None
                                            _stream(stream))
     _check(lib, st)
     return [Y for (_, _, Y) in problems]
+
+
+# ---- the key-value side: paged cache, rotary positions, attention over the cache ----
+
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _raw_stream(stream, device):
+    """The stream's handle; None: the current stream of the tensors' device."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _ints(t, name: str, n=None, *, dtype=torch.int32):
+    """Address of a contiguous CUDA tensor of whole numbers (of n entries)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} entries, expected {n}")
+    return t.data_ptr()
+
+
+def _heads(t, name: str, dtype, head_dim=None):
+    """Address and token and head strides of a CUDA tensor [tokens, heads, head_dim] with a contiguous last axis."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or t.dim() != 3:
+        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, head_dim] of {dtype}")
+    if head_dim is not None and t.shape[2] != head_dim:
+        raise ValueError(f"{name} has head_dim {t.shape[2]}, expected {head_dim}")
+    a, b, c = t.stride()
+    if c != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return t.data_ptr(), a, b
+
+
+class CacheStruct(ctypes.Structure):
+    """Mirror of dspark_cache."""
+    _fields_ = [("pool", _P), ("table", _P), ("length", _P), ("refs", _P), ("workspace", _P), ("workspace_bytes", _Z),
+                ("dtype", _I), ("num_pages", _I), ("layers", _I), ("kv_heads", _I), ("page_size", _I), ("head_dim", _I),
+                ("max_seqs", _I), ("max_pages", _I)]
+
+
+class PagedCache:
+    """A paged key-value cache (see dspark_cache in dspark.h) over the caller's tensors:
+
+    pool fp16 or bf16 [num_pages, layers, 2, kv_heads, page_size, head_dim], table int32 [max_seqs, max_pages] (-1: no
+    page), length int32 [max_seqs], refs int32 [num_pages].  ``PagedCache.empty`` makes them.  The page operations
+    change table, length and refs on the device, in stream order; ``status`` says whether one of them was refused."""
+
+    def __init__(self, pool, table, length, refs, *, workspace=None):
+        self._lib = lib = load_library()
+        if not isinstance(pool, torch.Tensor) or pool.dim() != 6 or pool.shape[2] != 2 or pool.dtype not in (
+                torch.float16, torch.bfloat16):
+            raise ValueError("pool must be fp16 or bf16 [num_pages, layers, 2, kv_heads, page_size, head_dim]")
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError("table must be int32 [max_seqs, max_pages]")
+        pages, layers, _, kv_heads, page_size, head_dim = pool.shape
+        c = CacheStruct(dtype=_DTYPES[pool.dtype], num_pages=pages, layers=layers, kv_heads=kv_heads, page_size=page_size,
+                        head_dim=head_dim, max_seqs=table.shape[0], max_pages=table.shape[1])
+        c.pool = _ptr(pool, "pool")
+        c.table = _ints(table, "table")
+        c.length = _ints(length, "length", table.shape[0])
+        c.refs = _ints(refs, "refs", pages)
+        if workspace is None:
+            n = int(lib.dspark_cache_workspace_bytes(ctypes.byref(c)))
+            if n == 0:
+                raise DsparkError(DSPARK_ERR_UNSUPPORTED, "cache sizes are not supported (page_size 16..256, a power of "
+                                  "two; head_dim 64 or 128)")
+            workspace = torch.zeros(n, dtype=torch.uint8, device=pool.device)
+        c.workspace = _ptr(workspace, "workspace")
+        c.workspace_bytes = workspace.numel() * workspace.element_size()
+        self.pool, self.table, self.length, self.refs, self.workspace = pool, table, length, refs, workspace
+        self.kv_heads, self.page_size, self.head_dim, self.layers = kv_heads, page_size, head_dim, layers
+        self.dtype, self.device = pool.dtype, pool.device
+        self._struct, self._ref = c, ctypes.byref(c)
+
+    @classmethod
+    def empty(cls, num_pages: int, max_seqs: int, max_pages: int, *, layers: int, kv_heads: int, page_size: int,
+              head_dim: int, dtype=torch.bfloat16, device=None):
+        """A cache of empty rows and free pages (the pool's contents are not initialised)."""
+        device = device or "cuda"
+        return cls(torch.empty((num_pages, layers, 2, kv_heads, page_size, head_dim), dtype=dtype, device=device),
+                   torch.full((max_seqs, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(max_seqs, dtype=torch.int32, device=device),
+                   torch.zeros(num_pages, dtype=torch.int32, device=device))
+
+    def extend(self, rows, counts, *, stream=None):
+        """Row rows[i] becomes counts[i] tokens longer; pages are added where needed."""
+        n = rows.numel()
+        _check(self._lib, self._lib.dspark_cache_extend(self._ref, _ints(rows, "rows"), _ints(counts, "counts", n), n,
+                                                        _raw_stream(stream, self.device)))
+
+    def fork(self, src, dst, *, stream=None):
+        """Row dst[i] becomes a copy of what row src[i] was: full pages are shared, a last page that is not full is
+        copied.  Rows can be permuted (beam search)."""
+        n = src.numel()
+        _check(self._lib, self._lib.dspark_cache_fork(self._ref, _ints(src, "src"), _ints(dst, "dst", n), n,
+                                                      _raw_stream(stream, self.device)))
+
+    def compact(self, rows, start, kept=None, n_kept=None, *, stream=None):
+        """Row rows[i] keeps its first start[i] tokens and the n_kept[i] ones at kept[i, :] (int32 [n, at least
+        max n_kept], ascending positions from start[i] on).  Without kept the rows are cut off at start."""
+        n = rows.numel()
+        if kept is None:
+            n_kept = torch.zeros(n, dtype=torch.int32, device=self.device)
+            stride, kept_p = 0, None
+        else:
+            if kept.dim() != 2 or kept.shape[0] != n:
+                raise ValueError("kept must be int32 [rows, tokens]")
+            stride, kept_p = kept.shape[1], _ints(kept, "kept")
+        _check(self._lib, self._lib.dspark_cache_compact(self._ref, _ints(rows, "rows"), _ints(start, "start", n), kept_p,
+                                                         stride, _ints(n_kept, "n_kept", n), n,
+                                                         _raw_stream(stream, self.device)))
+
+    def free(self, rows, *, stream=None):
+        """The rows release their pages and become empty."""
+        _check(self._lib, self._lib.dspark_cache_free(self._ref, _ints(rows, "rows"), rows.numel(),
+                                                      _raw_stream(stream, self.device)))
+
+    def copy_pages(self, src, dst, *, stream=None):
+        """Page dst[i] becomes a copy of page src[i], all layers; table and refs are left alone."""
+        n = src.numel()
+        _check(self._lib, self._lib.dspark_cache_copy_pages(self._ref, _ints(src, "src"), _ints(dst, "dst", n), n,
+                                                            _raw_stream(stream, self.device)))
+
+    def status(self, *, stream=None) -> int:
+        """Synchronize, then report and clear what the calls since the last check recorded on the device: 0 (OK),
+        DSPARK_ERR_INDEX, DSPARK_ERR_CAPACITY or DSPARK_ERR_TIMEOUT."""
+        return int(self._lib.dspark_cache_status(self._ref, _raw_stream(stream, self.device)))
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                       original: int = 0, low: float = 1.0, high: float = 32.0) -> list[int]:
+    """Frequencies base^(-2j / rotary_dim) of the pairs j, as int64 bit patterns of 2^-64 turns a position.
+    ``scaling`` for contexts ``factor`` times as long as the ``original`` one: "linear" divides every frequency by
+    factor; "base" raises the base so that the slowest is divided by factor and the fastest is kept; "by_parts" divides
+    the pairs that make at most ``low`` turns within the original context, keeps those that make at least ``high``, and
+    goes evenly between (a softmax temperature that belongs to it is RotaryTable's amplitude)."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and positive")
+    if base <= 0 or factor < 1:
+        raise ValueError("base must be positive and factor at least 1")
+    if scaling not in (None, "linear", "base", "by_parts"):
+        raise ValueError("scaling must be None, 'linear', 'base' or 'by_parts'")
+    if scaling == "by_parts" and (original <= 0 or high <= low):
+        raise ValueError("by_parts needs the original context's length, and high above low")
+    half = rotary_dim // 2
+    if scaling == "base" and half > 1:
+        base = base * factor ** (half / (half - 1))
+    out = []
+    for j in range(half):
+        f = base ** (-j / half) / (2.0 * math.pi)
+        if scaling == "linear":
+            f /= factor
+        elif scaling == "by_parts":
+            keep = min(1.0, max(0.0, (original * f - low) / (high - low)))
+            f *= keep + (1.0 - keep) / factor
+        whole = int(round(f * 2.0**64)) % 2**64
+        out.append(whole - 2**64 if whole >= 2**63 else whole)
+    return out
+
+
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+class RotaryTable:
+    """What rotary positions need besides the positions: the pairs' frequencies (int64 CUDA tensor [rotary_dim / 2], see
+    rotary_frequencies), where a pair's elements lie ("half" or "interleaved"), and the factor of the turned part."""
+
+    def __init__(self, turns, *, layout: str = "half", amplitude: float = 1.0, device=None):
+        if layout not in ROTARY_LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(ROTARY_LAYOUTS)}")
+        if not isinstance(turns, torch.Tensor):
+            turns = torch.tensor(turns, dtype=torch.int64, device=device or "cuda")
+        self._turns = _ints(turns, "turns", dtype=torch.int64)
+        self.turns, self.layout, self.amplitude = turns, layout, float(amplitude)
+        self.rotary_dim = 2 * turns.numel()
+        self._args = (self._turns, self.rotary_dim, ROTARY_LAYOUTS[layout], self.amplitude)
+
+
+def rotary(x, positions, table: RotaryTable, *, backward: bool = False, out=None, stream=None):
+    """x [tokens, heads, head_dim] (fp16, bf16 or fp32; strided tokens and heads) turned to positions int32 [tokens].
+    backward: the gradient with respect to x from that of the result.  out may be x."""
+    lib = load_library()
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
+        raise ValueError("x must be an fp16, bf16 or fp32 tensor")
+    p, a, b = _heads(x, "x", x.dtype)
+    if out is None:
+        out = x.new_empty(x.shape)
+    elif out.shape != x.shape:
+        raise ValueError("out must have the shape of x")
+    po, ao, bo = _heads(out, "out", x.dtype)
+    tokens, heads, dim = x.shape
+    _check(lib, lib.dspark_rotary(p, a, b, po, ao, bo, _DTYPES[x.dtype], tokens, heads, dim,
+                                  _ints(positions, "positions", tokens), *table._args, 1 if backward else 0,
+                                  _raw_stream(stream, x.device)))
+    return out
+
+
+def rotary_append(q, k, v, cache: PagedCache, layer: int, cu_new, table: RotaryTable, *, rows=None, positions=None,
+                  out=None, stream=None):
+    """The new tokens' keys, turned, and values go to their places in the cache (the last ones of their rows, which
+    ``cache.extend`` has made room for); returns the queries, turned.  q [tokens, q_heads, head_dim], k, v [tokens,
+    kv_heads, head_dim]; cu_new int32 [sequences + 1]: first token of each sequence; rows int32 [sequences]: its row of
+    the cache (None: the same number); positions int32 [tokens]: where the angle's position is not the place in the
+    cache.  out may be q."""
+    lib = cache._lib
+    dtype, dim = cache.dtype, cache.head_dim
+    qp, qa, qb = _heads(q, "q", dtype, dim)
+    kp, ka, kb = _heads(k, "k", dtype, dim)
+    vp, va, vb = _heads(v, "v", dtype, dim)
+    tokens, q_heads = q.shape[0], q.shape[1]
+    if k.shape[0] != tokens or v.shape[0] != tokens or k.shape[1] != cache.kv_heads or v.shape[1] != cache.kv_heads:
+        raise ValueError("k and v must be [tokens of q, the cache's kv_heads, head_dim]")
+    if out is None:
+        out = q.new_empty(q.shape)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    op, oa, ob = _heads(out, "out", dtype, dim)
+    seqs = cu_new.numel() - 1
+    _check(lib, lib.dspark_rotary_append(cache._ref, layer, qp, qa, qb, kp, ka, kb, vp, va, vb, op, oa, ob, tokens, q_heads,
+                                         None if rows is None else _ints(rows, "rows", seqs), _ints(cu_new, "cu_new"), seqs,
+                                         None if positions is None else _ints(positions, "positions", tokens),
+                                         *table._args, _raw_stream(stream, cache.device)))
+    return out
+
+
+def paged_attention(q, cache: PagedCache, layer: int, cu_new, *, rows=None, max_new=None, causal: bool = True,
+                    window: int = 0, scale=None, out=None, lse=None, return_lse: bool = False, stream=None):
+    """Attention of the last tokens of the cache's rows over all that the rows hold (see dspark_paged_attention).
+    q [tokens, q_heads, head_dim]; cu_new and rows as for rotary_append; max_new: the longest chunk, where known;
+    causal=False lets a chunk's tokens see each other; window > 0: only the last window keys; scale: of the scores
+    (None: 1 / sqrt(head_dim)).  Returns out, or (out, lse fp32 [tokens, q_heads]) with return_lse."""
+    lib = cache._lib
+    dim = cache.head_dim
+    qp, qa, qb = _heads(q, "q", cache.dtype, dim)
+    tokens, q_heads = q.shape[0], q.shape[1]
+    if out is None:
+        out = q.new_empty(q.shape)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    op, oa, ob = _heads(out, "out", cache.dtype, dim)
+    if lse is None and return_lse:
+        lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=cache.device)
+    seqs = cu_new.numel() - 1
+    _check(lib, lib.dspark_paged_attention(
+        cache._ref, layer, qp, qa, qb, tokens, q_heads, None if rows is None else _ints(rows, "rows", seqs),
+        _ints(cu_new, "cu_new"), seqs, tokens if max_new is None else max_new, 1 if causal else 0, window,
+        dim ** -0.5 if scale is None else scale, op, oa, ob,
+        None if lse is None else _ints(lse, "lse", tokens * q_heads, dtype=torch.float32),
+        _raw_stream(stream, cache.device)))
+    return (out, lse) if return_lse else out

@@ -18,7 +18,8 @@ SRC_DIR = os.path.join(PKG_DIR, "csrc")
 INCLUDE_DIR = os.path.join(REPO_DIR, "include")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_NAME = "libdspark.so"
-SOURCES = ["common.cu", "markov.cu", "markov_tc.cu", "markov_cluster.cu", "probe.cu", "ws_matvec.cu", "draft_plan.cu", "gated_plan.cu", "ws_q8.cu", "host_api.cu"]
+SOURCES = ["common.cu", "markov.cu", "markov_tc.cu", "markov_cluster.cu", "probe.cu", "ws_matvec.cu", "draft_plan.cu", "gated_plan.cu", "ws_q8.cu", "host_api.cu",
+           "cache.cu", "rotary.cu", "paged_attention.cu"]
 BENCH_LIB_NAME = "libdspark_bench.so"
 BENCH_SOURCES = ["bench_kernels.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -53,7 +54,7 @@ def _stale(out: str, deps) -> bool:
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
-    headers = [os.path.join(SRC_DIR, h) for h in ("common.cuh", "markov.cuh", "tc.cuh")]
+    headers = [os.path.join(SRC_DIR, h) for h in ("common.cuh", "markov.cuh", "tc.cuh", "kv_cache.cuh")]
     headers += [os.path.join(INCLUDE_DIR, h) for h in ("dspark.h", "dspark_bench.h")]
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                      "-I", INCLUDE_DIR, "--expt-relaxed-constexpr"]

@@ -1,0 +1,358 @@
+// Rotary positions: alone (forward and gradient), and on the way into the paged cache.
+//
+// The angle of pair j at position p is frac(p * turns[j] / 2^64) of a turn.  The product is taken
+// modulo 2^64, which drops the whole turns exactly; its top 32 bits, read as a signed fraction of
+// half a turn, give sine and cosine.  The error of the angle is 2^-32 turns whatever the position,
+// where p * frequency in fp32 would lose a bit for every doubling of the context.
+//
+// Bound by memory: every element is read and written once.  A thread takes one 32-byte unit of a
+// head (two 16-byte vectors that hold whole pairs) and walks over heads with it, so that a sine
+// and cosine are computed once for all the heads that the thread turns.
+#include "kv_cache.cuh"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T> struct Vec;  // 16 bytes of a head
+template <> struct Vec<__half> {
+    static constexpr int N = 8;
+    __device__ static void get(const uint4 &u, float (&f)[8]) {
+        const __half2 *h = reinterpret_cast<const __half2 *>(&u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = __half22float2(h[i]);
+            f[2 * i] = v.x, f[2 * i + 1] = v.y;
+        }
+    }
+    __device__ static uint4 put(const float (&f)[8]) {
+        uint4 u;
+        __half2 *h = reinterpret_cast<__half2 *>(&u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        return u;
+    }
+};
+template <> struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    __device__ static void get(const uint4 &u, float (&f)[8]) {
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = __bfloat1622float2(h[i]);
+            f[2 * i] = v.x, f[2 * i + 1] = v.y;
+        }
+    }
+    __device__ static uint4 put(const float (&f)[8]) {
+        uint4 u;
+        __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        return u;
+    }
+};
+template <> struct Vec<float> {
+    static constexpr int N = 4;
+    __device__ static void get(const uint4 &u, float (&f)[4]) {
+        f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y), f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
+    }
+    __device__ static uint4 put(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+};
+
+struct Turns {
+    const long long *turns;
+    int rotary_dim, layout;
+    float amplitude;
+    int backward;
+};
+
+// One unit of a head: its two vectors' first elements, and whether it is turned at all.
+template <typename T>
+struct Unit {
+    static constexpr int V = Vec<T>::N;
+    int a, b;
+    bool turned;
+    float cos[V], sin[V];
+
+    __device__ void init(const Turns &t, int unit) {
+        const int half = t.rotary_dim / 2;
+        turned = unit * 2 * V < t.rotary_dim;
+        const bool split = turned && t.layout == DSPARK_ROTARY_HALF;
+        a = split ? unit * V : unit * 2 * V;
+        b = split ? half + unit * V : a + V;
+    }
+    __device__ void at(const Turns &t, int unit, int position) {
+        if (!turned) return;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const unsigned long long part =
+                static_cast<unsigned long long>(static_cast<long long>(position)) * static_cast<unsigned long long>(__ldg(t.turns + unit * V + i));
+            const float x = static_cast<float>(static_cast<int>(part >> 32)) * 0x1p-31f;  // half turns
+            float s, c;
+            sincospif(x, &s, &c);
+            cos[i] = c * t.amplitude;
+            sin[i] = (t.backward ? -s : s) * t.amplitude;
+        }
+    }
+    __device__ void turn(uint4 &ua, uint4 &ub, int layout) const {
+        if (!turned) return;
+        float x[V], y[V];
+        Vec<T>::get(ua, x);
+        Vec<T>::get(ub, y);
+        if (layout == DSPARK_ROTARY_HALF) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float p = x[i] * cos[i] - y[i] * sin[i];
+                y[i] = y[i] * cos[i] + x[i] * sin[i];
+                x[i] = p;
+            }
+        } else {
+            // pairs lie next to each other: the first vector holds pairs 0 .. V/2 - 1
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                float p = x[2 * i] * cos[i] - x[2 * i + 1] * sin[i];
+                x[2 * i + 1] = x[2 * i + 1] * cos[i] + x[2 * i] * sin[i];
+                x[2 * i] = p;
+                p = y[2 * i] * cos[V / 2 + i] - y[2 * i + 1] * sin[V / 2 + i];
+                y[2 * i + 1] = y[2 * i + 1] * cos[V / 2 + i] + y[2 * i] * sin[V / 2 + i];
+                y[2 * i] = p;
+            }
+        }
+        ua = Vec<T>::put(x);
+        ub = Vec<T>::put(y);
+    }
+};
+
+struct Strided {
+    const void *p;
+    long long token, head;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(Strided x, Strided y, int tokens, int heads, int units,
+                                                          int lanes, const int *positions, Turns t) {
+    // units * lanes threads to a token: `lanes` heads at a time
+    const int per = units * lanes;
+    const int token = static_cast<int>(blockIdx.x) * (kThreads / per) + static_cast<int>(threadIdx.x) / per;
+    if (token >= tokens || static_cast<int>(threadIdx.x) >= kThreads / per * per) return;
+    const int r = threadIdx.x % per, unit = r % units;
+    Unit<T> u;
+    u.init(t, unit);
+    u.at(t, unit, positions[token]);
+    const T *px = static_cast<const T *>(x.p) + token * x.token;
+    T *py = static_cast<T *>(const_cast<void *>(y.p)) + token * y.token;
+    for (int h = r / units + static_cast<int>(blockIdx.y) * lanes; h < heads; h += lanes * static_cast<int>(gridDim.y)) {
+        uint4 a = *reinterpret_cast<const uint4 *>(px + h * x.head + u.a);
+        uint4 b = *reinterpret_cast<const uint4 *>(px + h * x.head + u.b);
+        u.turn(a, b, t.layout);
+        *reinterpret_cast<uint4 *>(py + h * y.head + u.a) = a;
+        *reinterpret_cast<uint4 *>(py + h * y.head + u.b) = b;
+    }
+}
+
+struct Append {
+    Strided q, k, v, out;
+    const int *rows, *cu_new, *positions;
+    int tokens, q_heads, n_seqs, layer;
+};
+
+// Sequence of token t: the last s with cu_new[s] <= t; -1 outside all of them.  One warp.
+__device__ int sequence_of(const int *cu, int n_seqs, int t, int lane) {
+    int at_or_before = 0;
+    for (int s0 = 0; s0 <= n_seqs; s0 += 32) {
+        const int s = s0 + lane;
+        at_or_before += __popc(__ballot_sync(0xffffffffu, s <= n_seqs && cu[s] <= t));
+    }
+    return at_or_before >= 1 && at_or_before <= n_seqs ? at_or_before - 1 : -1;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) append_kernel(CacheView c, Append g, int units, int lanes, Turns t) {
+    __shared__ int s_pos[kThreads / 4];        // angle's position of each token of the block
+    __shared__ long long s_slot[kThreads / 4]; // element of the pool where its first key goes; -1: nowhere; -2: no token
+    const int per = units * lanes, count = kThreads / per;
+    const int token0 = static_cast<int>(blockIdx.x) * count, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long run = static_cast<long long>(c.page_size) * c.head_dim;  // elements of one (page, layer, k or v, head)
+    for (int i = warp; i < count; i += kThreads / 32) {
+        const int token = token0 + i;
+        const int s = token < g.tokens ? sequence_of(g.cu_new, g.n_seqs, token, lane) : -1;
+        if (lane != 0) continue;
+        long long slot = -2;
+        int pos = 0;
+        if (s >= 0) {
+            const int row = g.rows ? g.rows[s] : s;
+            slot = -1;
+            if (static_cast<unsigned>(row) < static_cast<unsigned>(c.max_seqs)) {
+                pos = c.length[row] - g.cu_new[s + 1] + token;
+                const int j = pos >> c.page_shift;
+                if (pos >= 0 && j < c.max_pages) {
+                    const int page = c.table[static_cast<size_t>(row) * c.max_pages + j];
+                    if (static_cast<unsigned>(page) < static_cast<unsigned>(c.num_pages))
+                        slot = (static_cast<long long>(page) * c.layers + g.layer) * 2 * c.kv_heads * run +
+                               static_cast<long long>(pos & (c.page_size - 1)) * c.head_dim;
+                }
+            }
+            if (slot < 0 && blockIdx.y == 0) atomicOr(c.status, kStatusIndex);
+            if (g.positions) pos = g.positions[token];
+        }
+        s_pos[i] = pos;
+        s_slot[i] = slot;
+    }
+    __syncthreads();
+    const int i = threadIdx.x / per;
+    if (i >= count) return;
+    const long long slot = s_slot[i];
+    if (slot == -2) return;
+    const long long token = token0 + i;
+    const int r = threadIdx.x % per, unit = r % units;
+    Unit<T> u;
+    u.init(t, unit);
+    u.at(t, unit, s_pos[i]);
+    const int heads = g.q_heads + 2 * c.kv_heads;
+    T *pool = reinterpret_cast<T *>(c.pool);
+    for (int h = r / units + static_cast<int>(blockIdx.y) * lanes; h < heads; h += lanes * static_cast<int>(gridDim.y)) {
+        const int hk = h - g.q_heads, hv = hk - c.kv_heads;
+        if (hk >= 0 && slot < 0) break;
+        const Strided &from = hk < 0 ? g.q : hv < 0 ? g.k : g.v;
+        const T *px = static_cast<const T *>(from.p) + token * from.token + (hk < 0 ? h : hv < 0 ? hk : hv) * from.head;
+        uint4 a = *reinterpret_cast<const uint4 *>(px + u.a);
+        uint4 b = *reinterpret_cast<const uint4 *>(px + u.b);
+        if (hv < 0) u.turn(a, b, t.layout);
+        // a layer's runs of a page: the kv_heads of k, then those of v
+        T *py = hk < 0 ? static_cast<T *>(const_cast<void *>(g.out.p)) + token * g.out.token + h * g.out.head : pool + slot + hk * run;
+        *reinterpret_cast<uint4 *>(py + u.a) = a;
+        *reinterpret_cast<uint4 *>(py + u.b) = b;
+    }
+}
+
+// Heads that a token's threads take at a time, and the blocks that share a token's heads.  Many tokens: a
+// token's threads walk over all heads, so that its angles are computed once.  Few: the heads are spread until
+// there are about two blocks an SM.
+void shape(int tokens, int heads, int units, int sms, int *lanes, int *blocks_x, int *blocks_y) {
+    int l = 1;
+    while (2 * l * units <= 64 && 2 * l <= heads) l *= 2;
+    while (2 * l * units <= kThreads && 2 * l <= heads &&
+           (static_cast<long long>(tokens) * units * l + kThreads - 1) / kThreads < 2 * sms)
+        l *= 2;
+    const int count = kThreads / (units * l);
+    const int bx = (tokens + count - 1) / count;
+    int by = (2 * sms + bx - 1) / bx;
+    const int most = (heads + l - 1) / l;
+    *lanes = l;
+    *blocks_x = bx;
+    *blocks_y = by < 1 ? 1 : by > most ? most : by;
+}
+
+int element_bytes(int dtype) { return dtype == DSPARK_FP32 ? 4 : 2; }
+
+dspark_status check_turns(const char *who, const int64_t *turns, int rotary_dim, int layout, int head_dim) {
+    if (layout != DSPARK_ROTARY_HALF && layout != DSPARK_ROTARY_INTERLEAVED)
+        return fail(DSPARK_ERR_INVALID, "%s: layout %d", who, layout);
+    if (rotary_dim < 16 || rotary_dim > head_dim || rotary_dim % 16)
+        return fail(DSPARK_ERR_UNSUPPORTED, "%s: rotary_dim %d (a multiple of 16 up to head_dim %d)", who, rotary_dim, head_dim);
+    if (!turns || !aligned(turns, 8)) return fail(DSPARK_ERR_INVALID, "%s: turns must be an 8-byte aligned array", who);
+    return DSPARK_OK;
+}
+
+dspark_status check_strided(const char *who, const char *name, const void *p, long long token, long long head, int bytes) {
+    if (!p) return fail(DSPARK_ERR_INVALID, "%s: null pointer argument (%s)", who, name);
+    if (!aligned(p, 16) || token * bytes % 16 || head * bytes % 16 || token < 0 || head < 0)
+        return fail(DSPARK_ERR_INVALID, "%s: %s must be 16-byte aligned, with strides of whole 16 bytes (%lld, %lld)", who, name,
+                    token, head);
+    return DSPARK_OK;
+}
+
+}  // namespace
+
+}  // namespace dspark
+
+using namespace dspark;
+
+extern "C" dspark_status dspark_rotary(const void *x, long long x_token_stride, long long x_head_stride, void *y,
+                                       long long y_token_stride, long long y_head_stride, int dtype, int tokens,
+                                       int heads, int head_dim, const int32_t *positions, const int64_t *turns,
+                                       int rotary_dim, int layout, float amplitude, int backward,
+                                       dspark_stream_t stream) {
+    clear_error();
+    if (dtype != DSPARK_FP16 && dtype != DSPARK_BF16 && dtype != DSPARK_FP32)
+        return fail(DSPARK_ERR_INVALID, "rotary: dtype %d", dtype);
+    if (tokens < 0 || heads < 0) return fail(DSPARK_ERR_INVALID, "rotary: bad sizes tokens=%d heads=%d", tokens, heads);
+    if (head_dim < 16 || head_dim > 512 || head_dim % 16)
+        return fail(DSPARK_ERR_UNSUPPORTED, "rotary: head_dim %d (a multiple of 16 up to 512)", head_dim);
+    dspark_status st = check_turns("rotary", turns, rotary_dim, layout, head_dim);
+    if (st != DSPARK_OK || tokens == 0 || heads == 0) return st;
+    const int bytes = element_bytes(dtype);
+    if ((st = check_strided("rotary", "x", x, x_token_stride, x_head_stride, bytes)) != DSPARK_OK) return st;
+    if ((st = check_strided("rotary", "y", y, y_token_stride, y_head_stride, bytes)) != DSPARK_OK) return st;
+    if (!positions || !aligned(positions, 4)) return fail(DSPARK_ERR_INVALID, "rotary: positions must be a 4-byte aligned array");
+    int sms = 0;
+    if ((st = static_cast<dspark_status>(current_sm_count(&sms))) != DSPARK_OK) return st;
+    const int units = head_dim * bytes / 32;
+    int lanes, bx, by;
+    shape(tokens, heads, units, sms, &lanes, &bx, &by);
+    const Turns t{reinterpret_cast<const long long *>(turns), rotary_dim, layout, amplitude, backward != 0};
+    const Strided sx{x, x_token_stride, x_head_stride}, sy{y, y_token_stride, y_head_stride};
+    const dim3 grid(bx, by);
+    if (dtype == DSPARK_FP32)
+        rotary_kernel<float><<<grid, kThreads, 0, stream>>>(sx, sy, tokens, heads, units, lanes, positions, t);
+    else if (dtype == DSPARK_BF16)
+        rotary_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(sx, sy, tokens, heads, units, lanes, positions, t);
+    else
+        rotary_kernel<__half><<<grid, kThreads, 0, stream>>>(sx, sy, tokens, heads, units, lanes, positions, t);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "rotary");
+}
+
+extern "C" dspark_status dspark_rotary_append(const dspark_cache *cache, int layer, const void *q,
+                                              long long q_token_stride, long long q_head_stride, const void *k,
+                                              long long k_token_stride, long long k_head_stride, const void *v,
+                                              long long v_token_stride, long long v_head_stride, void *q_out,
+                                              long long out_token_stride, long long out_head_stride, int tokens,
+                                              int q_heads, const int32_t *rows, const int32_t *cu_new, int n_seqs,
+                                              const int32_t *positions, const int64_t *turns, int rotary_dim,
+                                              int layout, float amplitude, dspark_stream_t stream) {
+    const char *who = "rotary_append";
+    CacheView c;
+    dspark_status st = cache_view(cache, who, &c);
+    if (st != DSPARK_OK) return st;
+    if (layer < 0 || layer >= c.layers) return fail(DSPARK_ERR_INVALID, "%s: layer %d of %d", who, layer, c.layers);
+    if (tokens < 0 || q_heads < 0 || n_seqs < 0)
+        return fail(DSPARK_ERR_INVALID, "%s: bad sizes tokens=%d q_heads=%d n_seqs=%d", who, tokens, q_heads, n_seqs);
+    if (n_seqs > kMaxSeqs) return fail(DSPARK_ERR_UNSUPPORTED, "%s: n_seqs %d > %d", who, n_seqs, kMaxSeqs);
+    if ((st = check_turns(who, turns, rotary_dim, layout, c.head_dim)) != DSPARK_OK || tokens == 0 || n_seqs == 0) return st;
+    if (q_heads > 0) {
+        if ((st = check_strided(who, "q", q, q_token_stride, q_head_stride, 2)) != DSPARK_OK) return st;
+        if ((st = check_strided(who, "q_out", q_out, out_token_stride, out_head_stride, 2)) != DSPARK_OK) return st;
+    }
+    if ((st = check_strided(who, "k", k, k_token_stride, k_head_stride, 2)) != DSPARK_OK) return st;
+    if ((st = check_strided(who, "v", v, v_token_stride, v_head_stride, 2)) != DSPARK_OK) return st;
+    if (!cu_new || !aligned(cu_new, 4)) return fail(DSPARK_ERR_INVALID, "%s: cu_new must be a 4-byte aligned array", who);
+    int sms = 0;
+    if ((st = static_cast<dspark_status>(current_sm_count(&sms))) != DSPARK_OK) return st;
+    const int units = c.head_dim * 2 / 32;
+    int lanes, bx, by;
+    shape(tokens, q_heads + 2 * c.kv_heads, units, sms, &lanes, &bx, &by);
+    const Turns t{reinterpret_cast<const long long *>(turns), rotary_dim, layout, amplitude, 0};
+    Append g;
+    g.q = Strided{q, q_token_stride, q_head_stride};
+    g.k = Strided{k, k_token_stride, k_head_stride};
+    g.v = Strided{v, v_token_stride, v_head_stride};
+    g.out = Strided{q_out, out_token_stride, out_head_stride};
+    g.rows = rows;
+    g.cu_new = cu_new;
+    g.positions = positions;
+    g.tokens = tokens;
+    g.q_heads = q_heads;
+    g.n_seqs = n_seqs;
+    g.layer = layer;
+    if (cache->dtype == DSPARK_BF16)
+        append_kernel<__nv_bfloat16><<<dim3(bx, by), kThreads, 0, stream>>>(c, g, units, lanes, t);
+    else
+        append_kernel<__half><<<dim3(bx, by), kThreads, 0, stream>>>(c, g, units, lanes, t);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, who);
+}

@@ -1,11 +1,15 @@
 /*
  * libdspark -- the DSpark per-cycle draft step on one GB300 (sm_103a).
  *
- * Three operations, each a hand-written CUDA kernel:
+ * The draft step's operations, each a hand-written CUDA kernel:
  *   dspark_markov_draft  the sequential Markov block-draft sampler
  *   dspark_conf_probe    the proposer's Q8_0 confidence probe and its gate
  *   dspark_ws_matvec     the weight-stationary small-M fp16 projection matvec
  *   dspark_ws_matvec_q8  the same matvec over Q8_0 weights (after dspark_q8_0_repack)
+ * and the key-value side of a draft or verify step:
+ *   dspark_cache_*         a paged cache's pages: allocate, fork, compact, free, copy
+ *   dspark_rotary(_append) rotary positions, alone (with gradient) or on the way into the cache
+ *   dspark_paged_attention attention of the new tokens over the cache
  *
  * Conventions shared by every entry point
  *   - Tensor pointers are DEVICE pointers (cudaMalloc / PyTorch allocations), owned
@@ -38,7 +42,9 @@ typedef enum dspark_status {
     DSPARK_ERR_UNSUPPORTED = 2, /* valid request outside what the kernels implement */
     DSPARK_ERR_CUDA = 3,        /* a CUDA runtime call failed (message in dspark_last_error) */
     DSPARK_ERR_TIMEOUT = 4,     /* a device-side wait hit its time limit; outputs undefined */
-    DSPARK_ERR_INDEX = 5        /* a prev or d2t entry was out of range; those ids are -1 */
+    DSPARK_ERR_INDEX = 5,       /* a prev or d2t entry was out of range (those ids are -1), or a row,
+                                   token or page index of the paged cache */
+    DSPARK_ERR_CAPACITY = 6     /* the paged cache has too few free pages, or a row too few entries */
 } dspark_status;
 
 /* Message for the last non-OK status on this thread ("" if none).  Thread-local storage
@@ -507,6 +513,161 @@ dspark_status dspark_gated_draft_plan_create(const void *w_q8_0, const float *pr
                                              size_t workspace_bytes, dspark_gated_plan **plan_out);
 dspark_status dspark_gated_draft_plan_launch(dspark_gated_plan *plan, dspark_stream_t stream);
 void dspark_gated_draft_plan_destroy(dspark_gated_plan *plan);
+
+/* =====================================================================================
+ * Paged key-value cache
+ *
+ * What a draft or verify step keeps of the tokens before it.  One cache serves all layers of a
+ * model; the caller owns every array, in device memory:
+ *   pool    fp16 or bf16 [num_pages, layers, 2, kv_heads, page_size, head_dim], 16-byte aligned
+ *           (index 0 of the third axis: keys, 1: values)
+ *   table   int32 [max_seqs, max_pages]: page of each sequence's tokens page_size * i ..; -1
+ *           beyond its pages
+ *   length  int32 [max_seqs]: tokens of each sequence (0: none)
+ *   refs    int32 [num_pages]: sequences that hold the page (0: free)
+ *   workspace  dspark_cache_workspace_bytes() bytes, 256-byte aligned, ZERO-FILLED before its
+ *           first use; holds the status word.  Calls that share one must not overlap.
+ * Supported: page_size 16, 32, 64, 128 or 256; head_dim 64 or 128; 1 <= kv_heads, layers,
+ *   num_pages, max_seqs, max_pages; num_pages < 2^24.
+ *
+ * The page operations work on whole sequences ("rows" of the table), enqueue kernels only, and
+ * either do all of a call or nothing: where a row or token index is out of range
+ * (DSPARK_ERR_INDEX), or more pages are needed than are free or fit a row
+ * (DSPARK_ERR_CAPACITY), the call changes nothing and dspark_cache_status() says so.  A new
+ * page is always the lowest-numbered one that was free before the call, taken in the order of
+ * the call's rows and of the pages within a row, so the tables never depend on timing.  Rows
+ * named in one call have to be distinct (fork: the targets).  n == 0 enqueues nothing;
+ * n <= 1024
+ * and n <= max_seqs.
+ *   extend   row rows[i] becomes counts[i] tokens longer (pages are added where needed; the new
+ *            tokens' contents are whatever the pages hold)
+ *   fork     row dst[i] becomes a copy of row src[i]: it shares the full pages and gets its own
+ *            copy of a last page that is not full; what dst[i] held is released.  All sources
+ *            are read as they were before the call, so rows can be permuted (the reordering of a
+ *            beam search); src[i] == dst[i] leaves a row as it is
+ *   compact  row rows[i] keeps its first start[i] tokens and, behind them, the n_kept[i] tokens
+ *            kept[i * kept_stride ..] (positions >= start[i], ascending), in place; pages past
+ *            the new end are released.  Where tokens would be written to, or the new end lies
+ *            inside, a page that other rows hold too, the row gets its own copy of it.
+ *            n_kept == 0 cuts the row off at start[i]
+ *   free     the rows release their pages and become empty
+ *   copy_pages  page dst[i] becomes a copy of page src[i], all layers; the targets are distinct
+ *            and no page is both source and target; table and refs are left alone.  Any n; a pair
+ *            out of range is skipped and recorded
+ * dspark_cache_status synchronizes `stream`, then reports and clears the status word: DSPARK_OK,
+ * DSPARK_ERR_INDEX, DSPARK_ERR_CAPACITY, or DSPARK_ERR_TIMEOUT after a device-side wait that gave
+ * up (the outputs of that call are undefined and the workspace must be zero-filled again).
+ * ===================================================================================== */
+typedef enum dspark_dtype { DSPARK_FP16 = 0, DSPARK_BF16 = 1, DSPARK_FP32 = 2 } dspark_dtype;
+
+typedef struct dspark_cache {
+    void *pool;
+    int32_t *table;
+    int32_t *length;
+    int32_t *refs;
+    void *workspace;
+    size_t workspace_bytes;
+    int dtype; /* DSPARK_FP16 or DSPARK_BF16 */
+    int num_pages, layers, kv_heads, page_size, head_dim;
+    int max_seqs, max_pages;
+} dspark_cache;
+
+/* Workspace of a cache (pool, table, length, refs and workspace may still be NULL); 0 if the
+ * sizes are not supported. */
+size_t dspark_cache_workspace_bytes(const dspark_cache *cache);
+
+dspark_status dspark_cache_extend(const dspark_cache *cache, const int32_t *rows,
+                                  const int32_t *counts, int n, dspark_stream_t stream);
+dspark_status dspark_cache_fork(const dspark_cache *cache, const int32_t *src, const int32_t *dst,
+                                int n, dspark_stream_t stream);
+dspark_status dspark_cache_compact(const dspark_cache *cache, const int32_t *rows,
+                                   const int32_t *start, const int32_t *kept, int kept_stride,
+                                   const int32_t *n_kept, int n, dspark_stream_t stream);
+dspark_status dspark_cache_free(const dspark_cache *cache, const int32_t *rows, int n,
+                                dspark_stream_t stream);
+dspark_status dspark_cache_copy_pages(const dspark_cache *cache, const int32_t *src,
+                                      const int32_t *dst, int n, dspark_stream_t stream);
+dspark_status dspark_cache_status(const dspark_cache *cache, dspark_stream_t stream);
+
+/* =====================================================================================
+ * Rotary positions
+ *
+ * The first rotary_dim elements of a head are taken in pairs (a, b): elements j and
+ * j + rotary_dim / 2 (DSPARK_ROTARY_HALF), or 2j and 2j + 1 (DSPARK_ROTARY_INTERLEAVED).  At
+ * position p, with t = 2 pi * frac(p * turns[j] / 2^64):
+ *   a' = amplitude * (a cos t - b sin t)        b' = amplitude * (b cos t + a sin t)
+ * The other elements pass through.  turns[j] is pair j's frequency in turns a position, as a
+ * 64-bit fraction of a turn (modulo 2^64): the product's whole turns fall off exactly, so a
+ * position in the millions is as exact as one near zero, and any scaling for long contexts is a
+ * choice of the frequencies.  `backward` is the gradient, y = (dL/dx) for x = dL/dy: the same with
+ * -t.  Arithmetic in fp32, rounded once.
+ *
+ * dspark_rotary: x and y [tokens, heads, head_dim] of one type (fp16, bf16 or fp32), the last
+ *   axis contiguous, the other strides given in elements; positions int32 [tokens] (negative ones
+ *   turn the other way); turns int64 [rotary_dim / 2] (bit patterns).  y may be x.
+ * dspark_rotary_append: for the new tokens of n_seqs sequences (those of sequence s are tokens
+ *   cu_new[s] .. cu_new[s + 1] - 1; its table row is rows[s], or s where rows is NULL; their
+ *   positions are the last ones of the row's length, which dspark_cache_extend has made longer):
+ *   q_out = rotated q, and rotated k and plain v are written to the cache's layer `layer`.
+ *   q, q_out [tokens, q_heads, head_dim], k, v [tokens, kv_heads, head_dim], in the cache's type.
+ *   positions int32 [tokens], or NULL: the angle's position where it is not the token's place in
+ *   the cache (after compaction, or in a tree of drafts).  A token whose place does not exist (length
+ *   shorter than the chunk, no page) is rotated but not written, and DSPARK_ERR_INDEX is recorded.
+ *   Tokens outside cu_new[0] .. cu_new[n_seqs] are not touched.
+ * Supported: rotary_dim a multiple of 16, 16 <= rotary_dim <= head_dim; head_dim a multiple of 16
+ *   (fp32: 16) up to 512; pointers and strides multiples of 16 bytes.  tokens == 0 or heads == 0
+ *   enqueues nothing.
+ * ===================================================================================== */
+#define DSPARK_ROTARY_HALF 0
+#define DSPARK_ROTARY_INTERLEAVED 1
+
+dspark_status dspark_rotary(const void *x, long long x_token_stride, long long x_head_stride, void *y,
+                            long long y_token_stride, long long y_head_stride, int dtype, int tokens,
+                            int heads, int head_dim, const int32_t *positions, const int64_t *turns,
+                            int rotary_dim, int layout, float amplitude, int backward,
+                            dspark_stream_t stream);
+
+dspark_status dspark_rotary_append(const dspark_cache *cache, int layer, const void *q,
+                                   long long q_token_stride, long long q_head_stride, const void *k,
+                                   long long k_token_stride, long long k_head_stride, const void *v,
+                                   long long v_token_stride, long long v_head_stride, void *q_out,
+                                   long long out_token_stride, long long out_head_stride, int tokens,
+                                   int q_heads, const int32_t *rows, const int32_t *cu_new, int n_seqs,
+                                   const int32_t *positions, const int64_t *turns, int rotary_dim,
+                                   int layout, float amplitude, dspark_stream_t stream);
+
+/* =====================================================================================
+ * Attention of new tokens over the paged cache
+ *
+ * The chunk of sequence s (tokens cu_new[s] .. cu_new[s + 1] - 1, n of them; table row rows[s], or
+ * s where rows is NULL) are the last n tokens of the row's length L, so token i of the chunk has
+ * position p = L - n + i.  It sees the keys at positions
+ *   0 <= j < L,   j <= p if causal,   j > p - window if window > 0
+ * and for query head h, with the kv head h / (q_heads / kv_heads):
+ *   s_j = scale * <q, k_j>,   m = max_j s_j,   Z = sum_j exp(s_j - m)
+ *   out = (1 / Z) sum_j exp(s_j - m) v_j       lse = m + log Z
+ * A token that sees no key gets out = 0 and lse = -infinity.  causal = 0 is a draft block whose
+ * positions all see each other; one token per sequence is a decode step.
+ *
+ * Arguments
+ *   q, out   [tokens, q_heads, head_dim] in the cache's type; strides in elements, multiples of 8
+ *            (the last axis contiguous), 16-byte aligned.  out must not overlap q
+ *   lse      float [tokens, q_heads] or NULL
+ *   max_new  the longest chunk, as far as the caller knows (a hint for the tile shape; wrong values
+ *            cost time, not correctness); tokens where it is not known
+ * What lies in the cache behind a row's length, or in pages that no row holds, is never seen,
+ * whatever it is.  Keys and values at positions below the length have to be finite where a token
+ * of the same chunk does not see them.  A table entry outside the pool reads as zeros; it, a row
+ * out of range (taken as empty) and a length longer than the row (cut) record DSPARK_ERR_INDEX.
+ * Supported: q_heads a multiple of kv_heads, at most 128 of them to a kv head; n_seqs <= 4096.
+ * The result is deterministic: it depends on the inputs and the number of SMs only.
+ * ===================================================================================== */
+dspark_status dspark_paged_attention(const dspark_cache *cache, int layer, const void *q,
+                                     long long q_token_stride, long long q_head_stride, int tokens,
+                                     int q_heads, const int32_t *rows, const int32_t *cu_new, int n_seqs,
+                                     int max_new, int causal, int window, float scale, void *out,
+                                     long long out_token_stride, long long out_head_stride, float *lse,
+                                     dspark_stream_t stream);
 
 #ifdef __cplusplus
 }
