@@ -83,6 +83,8 @@ SIGNATURES = {
     "dspark_rotary_append": (_I, [_P, _I, _P, _L, _L, _P, _L, _L, _P, _L, _L, _P, _L, _L, _I, _I, _P, _P, _I, _P, _P,
                                   _I, _I, _F, _P]),
     "dspark_paged_attention": (_I, [_P, _I, _P, _L, _L, _I, _I, _P, _P, _I, _I, _I, _I, _F, _P, _L, _L, _P, _P]),
+    "dspark_paged_attention_debug": (_I, [_P, _I, _P, _L, _L, _I, _I, _P, _P, _I, _I, _I, _I, _F, _P, _L, _L, _P, _U,
+                                          _P]),
 }
 
 _lock = threading.Lock()
@@ -830,6 +832,9 @@ def _heads(t, name: str, dtype, head_dim=None):
     return t.data_ptr(), a, b
 
 
+CACHE_HEADER_BYTES = 2048  # the part of a cache's workspace that has to be zero before its first use
+
+
 class CacheStruct(ctypes.Structure):
     """Mirror of dspark_cache."""
     _fields_ = [("pool", _P), ("table", _P), ("length", _P), ("refs", _P), ("workspace", _P), ("workspace_bytes", _Z),
@@ -863,7 +868,8 @@ class PagedCache:
             if n == 0:
                 raise DsparkError(DSPARK_ERR_UNSUPPORTED, "cache sizes are not supported (page_size 16..256, a power of "
                                   "two; head_dim 64 or 128)")
-            workspace = torch.zeros(n, dtype=torch.uint8, device=pool.device)
+            workspace = torch.empty(n, dtype=torch.uint8, device=pool.device)
+            workspace[:CACHE_HEADER_BYTES].zero_()
         c.workspace = _ptr(workspace, "workspace")
         c.workspace_bytes = workspace.numel() * workspace.element_size()
         self.pool, self.table, self.length, self.refs, self.workspace = pool, table, length, refs, workspace

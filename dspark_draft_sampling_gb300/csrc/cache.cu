@@ -380,7 +380,7 @@ bool sizes_ok(const dspark_cache *c) {
     return c->num_pages >= 1 && c->num_pages < kMaxPages && c->layers >= 1 && c->kv_heads >= 1 && c->max_seqs >= 1 &&
            c->max_pages >= 1 && ps >= 16 && ps <= 256 && (ps & (ps - 1)) == 0 &&
            (c->head_dim == 64 || c->head_dim == 128) && (c->dtype == DSPARK_FP16 || c->dtype == DSPARK_BF16) &&
-           static_cast<long long>(c->max_pages) * ps < (1ll << 31) &&
+           static_cast<long long>(c->max_pages) * ps < (1ll << 30) &&
            2ll * c->layers * c->kv_heads * ps * c->head_dim < (1ll << 31);
 }
 
@@ -397,7 +397,7 @@ dspark_status cache_view(const dspark_cache *c, const char *who, CacheView *v) {
     if (!sizes_ok(c))
         return fail(DSPARK_ERR_UNSUPPORTED,
                     "%s: cache of page_size %d, head_dim %d, dtype %d, %d pages (page_size 16..256, a power of two; "
-                    "head_dim 64 or 128; fp16 or bf16; fewer than 2^24 pages, 2^31 tokens of a row and elements of a page)",
+                    "head_dim 64 or 128; fp16 or bf16; fewer than 2^24 pages, 2^30 tokens of a row and 2^31 elements of a page)",
                     who, c->page_size, c->head_dim, c->dtype, c->num_pages);
     if (!c->pool || !c->table || !c->length || !c->refs || !c->workspace)
         return fail(DSPARK_ERR_INVALID, "%s: null pointer in the cache", who);

@@ -56,7 +56,7 @@ dspark_status encode_tiled(CUtensorMap *map, CUtensorMapDataType dtype, CUtensor
             return fail(DSPARK_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
         encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
-    const cuuint32_t estr[3] = {1, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = encode(map, dtype, rank, const_cast<void *>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -79,6 +79,12 @@ dspark_status make_tmap_2d(CUtensorMap *map, const void *base, bool bf16, uint64
                            uint32_t box_rows, uint32_t box_cols) {
     return encode_tiled_2d(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                            CU_TENSOR_MAP_SWIZZLE_128B, base, rows, cols, box_rows, box_cols);
+}
+
+dspark_status make_tmap_nd(CUtensorMap *map, bool bf16, const void *base, uint32_t rank, const cuuint64_t *dims,
+                           const cuuint64_t *strides, const cuuint32_t *box) {
+    return encode_tiled(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        CU_TENSOR_MAP_SWIZZLE_128B, base, rank, dims, strides, box);
 }
 
 dspark_status make_tmap_kblocks(CUtensorMap *map, const void *base, bool bf16, uint64_t rows, uint64_t cols,

@@ -20,8 +20,8 @@ constexpr int kMaxCtas = 160;      // thread blocks of one attention call (one p
 // attention kernel's arrival counters, then one scratch area that the page operations and the
 // attention kernel's partial results use in turn (calls on one workspace never overlap).
 constexpr size_t kCacheCountersOffset = 256;
-constexpr size_t kCacheScratchOffset = 1024;
-static_assert(kCacheCountersOffset + kMaxCtas * 4 <= kCacheScratchOffset, "counters overlap the scratch area");
+constexpr size_t kCacheScratchOffset = 2048;
+static_assert(kCacheCountersOffset + kMaxCtas * 2 * 4 <= kCacheScratchOffset, "counters overlap the scratch area");
 
 struct CacheView {
     unsigned char *pool;

@@ -1,88 +1,802 @@
-// Attention of a chunk of new tokens over the paged cache.
+// Attention of a chunk of new tokens over the paged cache, on tcgen05 tensor cores.
 //
-// One warp to a (token, query head): the lanes share the head's elements, and the keys that the token
-// sees are taken one after another with the running maximum and sum of the softmax.
+// Rows.  The query heads that share a kv head, of consecutive tokens, are the rows of one 128-row query
+// tile: row r is head r % group of token r / group.  So a decode step of a few heads, a draft block and a long
+// prompt chunk are the same kernel: S = Q K^T is a 128 x 128 tile of rows against 128 keys, and O += P V follows
+// with P = exp2(scale' S - m) in 16 bits, read from tensor memory.  Tensor memory holds two such pipelines
+// ("streams", 128 columns of S and up to 128 of O each), so that one stream's products run while the other's softmax
+// does.  With long chunks (PAIR) the streams are two query tiles over the same keys; with at most 128 rows they are the
+// even and odd key tiles of one query tile, joined at the end.
+//
+// Softmax.  A thread owns a row.  The running maximum only moves (and O is only rescaled) when a tile's maximum
+// exceeds it by more than 8 powers of two: P is then at most 256, and sums stay exact enough in 32 bits, as the final
+// division takes the common factor out.  P is rounded to the inputs' type for the second product, which rounds each weight
+// once (unit roundoff 2^-11 or 2^-8, of the size of the output's own rounding); its sum is taken in 32 bits before
+// that rounding.
+//
+// Work.  All (sequence, kv head, query tile) items, each with its own number of 128-key tiles, form one
+// sequence of tiles that the thread blocks, one to an SM, take in equal contiguous ranges.  Every block finds its range
+// from the lengths on the device, so nothing about them has to be known on the host.  An item cut by a range's end
+// leaves partial sums (32-bit O, maximum, sum) in the workspace; the block that arrives last joins them in
+// block order, so the result does not depend on which one that is.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
 #include "kv_cache.cuh"
+#include "tc.cuh"
 
 namespace dspark {
 
-size_t attention_scratch_bytes(int) { return 0; }
-
 namespace {
 
+constexpr int kTile = 128;                    // query rows of a tile, keys of a tile
+constexpr int kThreads = 320;                 // warps 0-3, 4-7: softmax of stream 0, 1; 8: copies; 9: MMA issue
+constexpr int kTmemCols = 512;
+constexpr size_t kSmemData = 224 * 1024;      // query tiles and the ring of key and value tiles
+constexpr size_t kSmemBytes = 227 * 1024;
+constexpr int kItemCost = 1;                  // an item's fixed cost, in key tiles
+constexpr float kRescale = 8.f;               // powers of two by which a row's maximum may lag
+
 struct Attention {
-    const void *q;
     void *out;
     float *lse;
-    long long q_token, q_head, out_token, out_head;
+    long long out_token, out_head;
     const int *rows, *cu_new;
-    int tokens, q_heads, n_seqs, layer, causal, window;
+    int tokens, group, n_seqs, layer, causal, window, chunk_tiles;  // chunk_tiles: query tiles of the longest chunk (hint)
+    int tile_tokens;    // tokens of a 128-row tile
     float scale;
+    float *partials;
+    unsigned *arrivals;
+    unsigned long long timeout_ns, stall_ns;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(256) attention_kernel(CacheView c, Attention g) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (w >= static_cast<long long>(g.tokens) * g.q_heads) return;
-    const int token = static_cast<int>(w / g.q_heads), head = static_cast<int>(w % g.q_heads);
-    int s = -1;
-    for (int i = 0; i < g.n_seqs; ++i)
-        if (g.cu_new[i] <= token && token < g.cu_new[i + 1]) s = i;
-    if (s < 0) return;
-    const int row = g.rows ? g.rows[s] : s;
-    int length = 0;
-    if (static_cast<unsigned>(row) < static_cast<unsigned>(c.max_seqs)) {
-        length = c.length[row];
-        if (length < 0 || length > static_cast<long long>(c.max_pages) * c.page_size) {
-            if (lane == 0) atomicOr(c.status, kStatusIndex);
-            length = length < 0 ? 0 : c.max_pages * c.page_size;
-        }
-    } else if (lane == 0) {
-        atomicOr(c.status, kStatusIndex);
+template <int D, bool PAIR>
+struct Shape {
+    static constexpr int QT = PAIR ? 2 : 1;
+    static constexpr int kHalves = D / 64;                       // 64-element column blocks of 128 bytes
+    static constexpr uint32_t kTileBytes = kTile * D * 2;
+    static constexpr int kStages = static_cast<int>((kSmemData - QT * kTileBytes) / kTileBytes);
+    static constexpr size_t kSlotFloats = size_t(kTile) * (D + 2);  // partial of one query tile: O, maximum, sum
+};
+
+size_t slot_bytes(int head_dim) { return 4 * size_t(kTile) * (head_dim + 2); }
+
+struct Seq {
+    int row, n, length, q0;  // table row, new tokens, tokens, first query token
+};
+
+__device__ __forceinline__ Seq load_seq(const CacheView &c, const Attention &g, int s) {
+    Seq q;
+    const int a = min(max(g.cu_new[s], 0), g.tokens), b = min(g.cu_new[s + 1], g.tokens);
+    q.q0 = a;
+    q.n = max(b - a, 0);
+    q.row = g.rows ? g.rows[s] : s;
+    q.length = 0;
+    const long long most = static_cast<long long>(c.max_pages) * c.page_size;
+    bool bad = static_cast<unsigned>(q.row) >= static_cast<unsigned>(c.max_seqs);
+    if (bad) {
+        q.row = 0;
+    } else {
+        q.length = c.length[q.row];
+        bad = q.length < 0 || q.length > most;
+        q.length = static_cast<int>(min(max(static_cast<long long>(q.length), 0ll), most));
     }
-    const int pos = length - (g.cu_new[s + 1] - token);
-    const int end = g.causal ? min(length, pos + 1) : length;
-    const int begin = g.window > 0 ? max(0, pos - g.window + 1) : 0;
-    const int kv_head = head / (g.q_heads / c.kv_heads);
-    const T *q = static_cast<const T *>(g.q) + token * g.q_token + head * g.q_head;
-    float x[E], acc[E] = {}, m = -INFINITY, z = 0.f;
-    for (int e = 0; e < E; ++e) x[e] = static_cast<float>(q[lane * E + e]) * g.scale;
-    const size_t run = size_t(c.page_size) * D;
-    for (int j = begin; j < end; ++j) {
-        const int page = c.table[size_t(row) * c.max_pages + (j >> c.page_shift)];
-        const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(c.num_pages);
-        if (!ok && lane == 0) atomicOr(c.status, kStatusIndex);
-        const T *k = reinterpret_cast<const T *>(c.pool) +
-                     ((size_t(ok ? page : 0) * c.layers + g.layer) * 2 * c.kv_heads + kv_head) * run +
-                     size_t(j & (c.page_size - 1)) * D + lane * E;
-        const T *v = k + c.kv_heads * run;
-        float dot = 0.f;
-        for (int e = 0; e < E; ++e) dot += ok ? x[e] * static_cast<float>(k[e]) : 0.f;
-        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        const float up = fmaxf(m, dot), keep = m == -INFINITY ? 0.f : expf(m - up), p = expf(dot - up);
-        z = z * keep + p;
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * keep + (ok ? p * static_cast<float>(v[e]) : 0.f);
-        m = up;
-    }
-    T *out = static_cast<T *>(g.out) + token * g.out_token + head * g.out_head;
-    for (int e = 0; e < E; ++e) out[lane * E + e] = static_cast<T>(end > begin ? acc[e] / z : 0.f);
-    if (g.lse && lane == 0) g.lse[size_t(token) * g.q_heads + head] = end > begin ? m + logf(z) : -INFINITY;
+    if (bad && q.n > 0) atomicOr(c.status, kStatusIndex);
+    return q;
 }
 
-}  // namespace
+// Key tiles [lo, hi) that query tile i (of `step` tokens) of a sequence sees.
+__device__ __forceinline__ void key_tiles(const Attention &g, const Seq &q, int i, int step, int *lo, int *hi) {
+    const int off = q.length - q.n, first = i * step, last = min(first + step, q.n) - 1;
+    const int end = g.causal ? min(q.length, max(off + last + 1, 0)) : q.length;
+    const int begin = g.window > 0 ? max(0, off + first - g.window + 1) : 0;
+    *hi = (end + kTile - 1) / kTile;
+    *lo = min(begin / kTile, *hi);
+    if (begin >= end) *lo = *hi;
+}
 
-}  // namespace dspark
+// One stretch of an item that a block works on.
+struct Segment {
+    int kv_head, tile;        // query tile of the sequence
+    int lo, first, last;      // the item's first key tile; the stretch's, relative to it
+    int tiles;                // of the whole item
+    long long at;             // the item's place in the sequence of all tiles
+};
 
-using namespace dspark;
+// Walks a block's range; all roles walk it in the same way.
+struct Walk {
+    Seq q;
+    int s, kv_head, i, n_tiles, step;
+    long long x, left, pos;  // x: place within the item; pos: absolute place
 
-extern "C" dspark_status dspark_paged_attention(const dspark_cache *cache, int layer, const void *q,
-                                                long long q_token_stride, long long q_head_stride, int tokens,
-                                                int q_heads, const int32_t *rows, const int32_t *cu_new, int n_seqs,
-                                                int max_new, int causal, int window, float scale, void *out,
-                                                long long out_token_stride, long long out_head_stride, float *lse,
-                                                dspark_stream_t stream) {
+    __device__ __forceinline__ bool next(const CacheView &c, const Attention &g, Segment *out) {
+        while (left > 0) {
+            if (i >= n_tiles) {
+                i = 0;
+                if (++kv_head == c.kv_heads) {
+                    kv_head = 0;
+                    do {
+                        q = load_seq(c, g, ++s);
+                    } while (q.n == 0);
+                    n_tiles = (q.n + step - 1) / step;
+                }
+            }
+            int lo, hi;
+            key_tiles(g, q, i, step, &lo, &hi);
+            const int tiles = hi - lo;
+            const long long size = kItemCost + tiles;
+            const long long take = min(left, size - x);
+            out->kv_head = kv_head;
+            out->tile = i;
+            out->lo = lo;
+            out->tiles = tiles;
+            out->first = static_cast<int>(max(x - kItemCost, 0ll));
+            out->last = static_cast<int>(max(x + take - kItemCost, 0ll));
+            out->at = pos - x;
+            const bool starts = x == 0;
+            left -= take;
+            pos += take;
+            x = 0;
+            ++i;
+            if (out->last > out->first || (tiles == 0 && starts)) return true;
+        }
+        return false;
+    }
+};
+
+// Where a block's range begins, found by one warp from the sequences' total costs.
+struct Start {
+    long long begin, end, total, before;  // `before`: cost of the sequences before s
+    int s, blocks, kv_head, i;
+    long long x;
+};
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ long long warp_scan(long long v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    return v;
+}
+
+__device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    uint32_t r;
+    if (BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_plain(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// Descriptor of a value tile as the second product's B operand: N (head elements) is contiguous in 128-byte rows of 64
+// elements, one row a key; 8-key groups are 1024 bytes apart, the 64-element blocks 128 keys apart.
+__device__ __forceinline__ uint64_t smem_desc_values(uint32_t addr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>((kTile * 128u) >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+// Barriers and small state behind the data area.
+template <int STAGES>
+struct Control {
+    uint64_t full[STAGES], empty[STAGES];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_ready[2], o_full[2];
+    uint64_t sync[2];   // softmax threads among themselves: per stream (PAIR), or [0] for both
+    uint64_t drained, never;
+    uint32_t tmem, aborted;
+    unsigned last[2];
+    Start start;
+    float max_sum[2][2][kTile];  // [stream][maximum, sum][row], one query tile's two streams
+};
+
+template <typename C>
+__device__ __forceinline__ bool wait(C *ctl, uint64_t *bar, uint32_t parity, const CacheView &c, unsigned long long timeout_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    volatile uint32_t *aborted = &ctl->aborted;
+    while (!mbar_try_wait(bar, parity)) {
+        if (*aborted) return false;
+        if (global_timer_ns() - t0 > timeout_ns) {
+            *aborted = 1;
+            atomicOr(c.status, kStatusTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+
+// The same for a whole warp: every lane gets the same answer.
+template <typename C>
+__device__ __forceinline__ bool warp_wait(C *ctl, uint64_t *bar, uint32_t parity, const CacheView &c, unsigned long long timeout_ns) {
+    return __all_sync(0xffffffffu, wait(ctl, bar, parity, c, timeout_ns));
+}
+
+template <bool BF16, int D, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, const CacheView c,
+                     const Attention g) {
+    using S = Shape<D, PAIR>;
+    using C = Control<S::kStages>;
+    extern __shared__ __align__(1024) unsigned char smem[];  // swizzled tiles want 1024-byte alignment
+    C *ctl = reinterpret_cast<C *>(smem + kSmemData);
+    static_assert(sizeof(C) <= kSmemBytes - kSmemData, "control block does not fit");
+    const uint32_t q_smem = smem_addr(smem), ring = q_smem + S::QT * S::kTileBytes;
+    unsigned char *ring_ptr = smem + S::QT * S::kTileBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int step = g.tile_tokens * S::QT;  // tokens of an item
+
+    if (warp == 8 && lane == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&ctl->full[i], 1);
+            mbar_init(&ctl->empty[i], 1);
+        }
+        mbar_init(&ctl->q_full, 1);
+        mbar_init(&ctl->q_empty, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&ctl->s_full[s], 1);
+            mbar_init(&ctl->p_ready[s], 4);  // one arrival a warp
+            mbar_init(&ctl->o_full[s], 1);
+            mbar_init(&ctl->sync[s], PAIR ? 128 : 256);
+        }
+        mbar_init(&ctl->drained, 1);
+        mbar_init(&ctl->never, 1);
+        ctl->aborted = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) tmem_alloc(&ctl->tmem, kTmemCols);
+    pdl_launch_dependents();
+    pdl_wait();  // no global-memory access before this point
+
+    // ---- every sequence's cost, then this block's range (the ring serves as scratch) ----
+    {
+        long long *cost = reinterpret_cast<long long *>(ring_ptr);
+        if (g.chunk_tiles <= 1) {
+            for (int s = threadIdx.x; s < g.n_seqs; s += kThreads) {
+                const Seq q = load_seq(c, g, s);
+                long long w = 0;
+                for (int i = 0; i * step < q.n; ++i) {
+                    int lo, hi;
+                    key_tiles(g, q, i, step, &lo, &hi);
+                    w += kItemCost + hi - lo;
+                }
+                cost[s] = w * c.kv_heads;
+            }
+        } else {
+            for (int s = warp; s < g.n_seqs; s += kThreads / 32) {
+                const Seq q = load_seq(c, g, s);
+                long long w = 0;
+                for (int i = lane; i * step < q.n; i += 32) {
+                    int lo, hi;
+                    key_tiles(g, q, i, step, &lo, &hi);
+                    w += kItemCost + hi - lo;
+                }
+                w = warp_sum(w);
+                if (lane == 0) cost[s] = w * c.kv_heads;
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {
+            long long total = 0;
+            for (int s = lane; s < g.n_seqs; s += 32) total += cost[s];
+            total = warp_sum(total);
+            const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+            const int b = blockIdx.x;
+            Start st{};
+            st.total = total;
+            st.blocks = blocks;
+            if (b < blocks) {
+                st.begin = total * b / blocks;
+                st.end = total * (b + 1) / blocks;
+                long long before = 0;
+                for (int s0 = 0; s0 < g.n_seqs; s0 += 32) {
+                    const long long v = s0 + lane < g.n_seqs ? cost[s0 + lane] : 0;
+                    const long long upto = before + warp_scan(v, lane);
+                    const unsigned past = __ballot_sync(0xffffffffu, upto > st.begin);
+                    if (past) {
+                        const int l = __ffs(past) - 1;
+                        st.s = s0 + l;
+                        st.before = __shfl_sync(0xffffffffu, upto - v, l);
+                        break;
+                    }
+                    before = __shfl_sync(0xffffffffu, upto, 31);
+                }
+                const Seq q = load_seq(c, g, st.s);
+                const long long w = cost[st.s] / c.kv_heads;
+                st.kv_head = static_cast<int>((st.begin - st.before) / w);
+                long long rem = st.begin - st.before - st.kv_head * w;
+                for (int i0 = 0;; i0 += 32) {  // the item that holds the range's first tile
+                    long long v = 0;
+                    if ((i0 + lane) * step < q.n) {
+                        int lo, hi;
+                        key_tiles(g, q, i0 + lane, step, &lo, &hi);
+                        v = kItemCost + hi - lo;
+                    }
+                    const long long upto = warp_scan(v, lane);
+                    const unsigned past = __ballot_sync(0xffffffffu, upto > rem);
+                    if (past) {
+                        const int l = __ffs(past) - 1;
+                        st.i = i0 + l;
+                        st.x = rem - __shfl_sync(0xffffffffu, upto - v, l);
+                        break;
+                    }
+                    rem -= __shfl_sync(0xffffffffu, upto, 31);
+                    if (i0 * step >= q.n) break;  // not reached: rem lies within the sequence
+                }
+            }
+            if (lane == 0) ctl->start = st;
+        }
+    }
+    fence_proxy_async_smem();  // the scratch use of the ring comes before the copies into it
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem;
+    const long long total = ctl->start.total;
+    const int blocks = ctl->start.blocks;
+    const bool busy = static_cast<int>(blockIdx.x) < blocks;
+
+    Walk walk;
+    walk.left = 0;
+    if (busy) {
+        const Start &st = ctl->start;
+        walk.s = st.s;
+        walk.q = load_seq(c, g, st.s);
+        walk.kv_head = st.kv_head;
+        walk.i = st.i;
+        walk.step = step;
+        walk.n_tiles = (walk.q.n + step - 1) / step;
+        walk.x = st.x;
+        walk.pos = st.begin;
+        walk.left = st.end - st.begin;
+    }
+    Segment seg;
+
+    if (warp == 8) {
+        // ---- copies: query tiles, then keys and values of each tile through the ring; a lane to a page ----
+        const int box = min(c.page_size, kTile), per_tile = kTile / box;
+        uint32_t n_q = 0, put = 0;  // segments, ring entries so far
+        bool ok = true;
+        while (ok && walk.next(c, g, &seg)) {
+            if (seg.tiles == 0) continue;
+            if (n_q > 0 && !(ok = warp_wait(ctl, &ctl->q_empty, (n_q - 1) & 1, c, g.timeout_ns))) break;
+            ++n_q;
+            const int token = walk.q.q0 + seg.tile * step;
+            if (lane == 0) {
+                const uint32_t rows_bytes = static_cast<uint32_t>(g.tile_tokens * g.group) * 128u;
+                mbar_arrive_expect_tx(&ctl->q_full, rows_bytes * S::kHalves * S::QT);
+                for (int t = 0; t < S::QT; ++t)
+                    for (int h = 0; h < S::kHalves; ++h)
+                        tma_load_3d_plain(q_smem + t * S::kTileBytes + h * (kTile * 128), &tm_q, h * 64, seg.kv_head * g.group,
+                                          token + t * g.tile_tokens, &ctl->q_full);
+            }
+            const int *pages = c.table + static_cast<size_t>(walk.q.row) * c.max_pages;
+            const int run = (g.layer * 2) * c.kv_heads + seg.kv_head;
+            for (int t = seg.first; ok && t < seg.last; ++t) {
+                const int key = (seg.lo + t) * kTile + lane * box;  // first key of this lane's page
+                const bool mine = lane < per_tile && key < walk.q.length;
+                int page = 0;
+                if (mine) {
+                    page = pages[key >> c.page_shift];
+                    if (static_cast<unsigned>(page) >= static_cast<unsigned>(c.num_pages)) {
+                        atomicOr(c.status, kStatusIndex);
+                        page = c.num_pages;  // outside the tensor: reads as zeros
+                    }
+                }
+                const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
+                const int slot = key & (c.page_size - 1);  // pages longer than a tile
+                for (int w = 0; w < 2; ++w, ++put) {
+                    const uint32_t st = put % S::kStages;
+                    if (put >= S::kStages && !(ok = warp_wait(ctl, &ctl->empty[st], ((put / S::kStages) & 1) ^ 1, c, g.timeout_ns))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], boxes * static_cast<uint32_t>(box) * D * 2);
+                    __syncwarp();
+                    if (mine)
+                        for (int h = 0; h < S::kHalves; ++h)
+                            tma_load_4d(ring + st * S::kTileBytes + h * (kTile * 128) + lane * box * 128, &tm_kv, h * 64, slot,
+                                        run + w * c.kv_heads, page, &ctl->full[st]);
+                }
+            }
+        }
+        // copies in flight land before the block ends, also after a wait that gave up
+        for (uint32_t p = put > S::kStages ? put - S::kStages : 0; p < put; ++p)
+            mbar_wait(&ctl->full[p % S::kStages], (p / S::kStages) & 1, g.timeout_ns);
+        if (n_q) mbar_wait(&ctl->q_full, (n_q - 1) & 1, g.timeout_ns);
+    } else if (warp == 9) {
+        // ---- MMA issue ----
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_f16(BF16, kTile, kTile);
+            constexpr uint32_t idesc_o = idesc_f16(BF16, kTile, D) | (1u << 16);  // B is N-contiguous
+            uint32_t n_q = 0, base = 0;          // segments, key tiles before this segment
+            uint32_t n_p[2] = {0, 0};            // second products so far
+            bool ok = true;
+            while (ok && walk.next(c, g, &seg)) {
+                if (seg.tiles == 0) continue;
+                const int nt = seg.last - seg.first;
+                const int steps[2] = {PAIR ? nt : (nt + 1) / 2, PAIR ? nt : nt / 2};
+                if (!(ok = wait(ctl, &ctl->q_full, n_q & 1, c, g.timeout_ns))) break;
+                ++n_q;
+                auto scores = [&](int s, int i) {
+                    const uint32_t p = 2 * (base + (PAIR ? i : 2 * i + s)), st = p % S::kStages;
+                    if (!wait(ctl, &ctl->full[st], (p / S::kStages) & 1, c, g.timeout_ns)) return false;
+                    tc_fence_after();
+                    const uint64_t a = smem_desc_sw128(q_smem + (PAIR ? s * S::kTileBytes : 0));
+                    const uint64_t b = smem_desc_sw128(ring + st * S::kTileBytes);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t o = static_cast<uint64_t>((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
+                        tc_mma_f16(tmem + s * kTile, a + o, b + o, idesc_s, k != 0);
+                    }
+                    tc_commit(&ctl->s_full[s]);
+                    if (!PAIR || s == 1) tc_commit(&ctl->empty[st]);
+                    return true;
+                };
+                auto values = [&](int s, int i) {
+                    const uint32_t p = 2 * (base + (PAIR ? i : 2 * i + s)) + 1, st = p % S::kStages;
+                    if (!wait(ctl, &ctl->p_ready[s], n_p[s] & 1, c, g.timeout_ns)) return false;
+                    ++n_p[s];
+                    if (!wait(ctl, &ctl->full[st], (p / S::kStages) & 1, c, g.timeout_ns)) return false;
+                    tc_fence_after();
+                    const uint64_t b = smem_desc_values(ring + st * S::kTileBytes);
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        tc_mma_f16_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + k * 8, b + ((k * 2048) >> 4), idesc_o,
+                                      i != 0 || k != 0);
+                    if (!PAIR || s == 1) tc_commit(&ctl->empty[st]);
+                    if (i + 1 == steps[s]) tc_commit(&ctl->o_full[s]);
+                    return true;
+                };
+                for (int s = 0; s < 2 && ok; ++s)
+                    if (steps[s] > 0) ok = scores(s, 0);
+                if (steps[0] == 1 && ok) tc_commit(&ctl->q_empty);
+                for (int i = 0; i < steps[0] && ok; ++i) {
+                    for (int s = 0; s < 2 && ok; ++s) {
+                        if (i >= steps[s]) continue;
+                        ok = values(s, i);
+                        if (ok && i + 1 < steps[s]) ok = scores(s, i + 1);
+                    }
+                    if (ok && i + 2 == steps[0]) tc_commit(&ctl->q_empty);  // the last scores of the segment are issued
+                }
+                base += nt;
+            }
+            tc_commit(&ctl->drained);
+            mbar_wait(&ctl->drained, 0, g.timeout_ns);
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax of stream s: a thread owns row r ----
+        const int s = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + s * kTile + lanes, t_o = tmem + 2 * kTile + s * kTile + lanes;
+        const float sc = g.scale * 1.4426950408889634f;
+        const int row_token = r / g.group, row_head = r - row_token * g.group;
+        uint32_t n_s = 0, n_o[2] = {0, 0}, n_sync = 0, base = 0;
+        bool ok = true;
+        if (g.stall_ns && !mbar_wait(&ctl->never, 0, g.stall_ns) && threadIdx.x == 0) atomicOr(c.status, kStatusTimeout);
+        while (ok && walk.next(c, g, &seg)) {
+            const int nt = seg.last - seg.first;
+            const int token = seg.tile * step + (PAIR ? s * g.tile_tokens : 0) + row_token;  // of the chunk
+            const bool real = row_token < g.tile_tokens && token < walk.q.n;
+            const int pos = walk.q.length - walk.q.n + token;
+            // keys that this row sees; rows that are none see all, as what they hold is not written
+            const int see_hi = !real ? 0x7fffffff : g.causal ? min(walk.q.length, pos + 1) : walk.q.length;
+            const int see_lo = real && g.window > 0 ? max(0, pos - g.window + 1) : 0;
+            float m = -INFINITY, l = 0.f;
+            const int steps = PAIR ? nt : (nt + 1 - s) / 2;
+            const bool warp_real = __any_sync(0xffffffffu, real);
+            for (int i = 0; i < steps && ok; ++i) {
+                const int t = PAIR ? i : 2 * i + s;
+                const int key0 = (seg.lo + seg.first + t) * kTile;
+                if (!(ok = warp_wait(ctl, &ctl->s_full[s], n_s & 1, c, g.timeout_ns))) break;
+                ++n_s;
+                tc_fence_after();
+                if (key0 + kTile > walk.q.length) {
+                    // values behind the row's length are whatever the page holds: zeros, so that weights of 0 stay 0
+                    const uint32_t p = 2 * (base + t) + 1, st = p % S::kStages;
+                    if (!(ok = warp_wait(ctl, &ctl->full[st], (p / S::kStages) & 1, c, g.timeout_ns))) break;
+                    const int used = walk.q.length - key0;
+                    unsigned char *v = ring_ptr + st * S::kTileBytes;
+                    for (int h = 0; h < S::kHalves; ++h)
+                        for (int b = used * 8 + r; b < kTile * 8; b += kTile)
+                            reinterpret_cast<uint4 *>(v + h * (kTile * 128))[b] = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                }
+                if (warp_real) {
+                    uint32_t v[kTile];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld_32(t_s + q * 32, v + q * 32);
+                    tmem_wait_ld();
+                    if (__any_sync(0xffffffffu, key0 < see_lo || key0 + kTile > see_hi)) {
+                        const int lo = see_lo - key0;
+                        const unsigned span = static_cast<unsigned>(max(min(see_hi, walk.q.length) - max(see_lo, 0), 0));
+#pragma unroll
+                        for (int q = 0; q < kTile; ++q)
+                            if (static_cast<unsigned>(q - lo) >= span) v[q] = 0xff800000u;
+                    }
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int q = 0; q < kTile; q += 8) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            top[u] = fmaxf(top[u], fmaxf(__uint_as_float(v[q + 2 * u]), __uint_as_float(v[q + 2 * u + 1])));
+                    }
+                    const float tile_max = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    const bool moves = real && (tile_max - m) * sc > kRescale;  // also from -infinity
+                    if (__any_sync(0xffffffffu, moves)) {
+                        const float up = fmaxf(m, tile_max);
+                        const float keep = m == -INFINITY ? 0.f : ex2((m - up) * sc);
+                        if (i > 0) {
+                            // the scores' arrival also says that this stream's earlier second products are done
+#pragma unroll
+                            for (int q = 0; q < D / 32; ++q) {
+                                uint32_t o[32];
+                                tmem_ld_32(t_o + q * 32, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
+                                tmem_st_32(t_o + q * 32, o);
+                            }
+                        }
+                        l *= keep;
+                        m = up;
+                    }
+                    const float shift = m == -INFINITY ? 0.f : m * sc;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int u = 0; u < 32; ++u) {
+                            const float a = ex2(fmaf(__uint_as_float(v[q * 64 + 2 * u]), sc, -shift));
+                            const float b = ex2(fmaf(__uint_as_float(v[q * 64 + 2 * u + 1]), sc, -shift));
+                            sum[(2 * u) & 3] += a;
+                            sum[(2 * u + 1) & 3] += b;
+                            w[u] = pack16<BF16>(a, b);
+                        }
+                        tmem_st_32(t_s + q * 32, w);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->p_ready[s]);
+            }
+            base += nt;
+            if (!ok) break;
+            // the O that this thread reads: its stream's, or (a query tile over two streams) both
+            for (int u = PAIR ? s : 0; u < (PAIR ? s + 1 : 2) && ok; ++u) {
+                if (PAIR ? nt == 0 : nt <= u) continue;
+                ok = warp_wait(ctl, &ctl->o_full[u], n_o[u] & 1, c, g.timeout_ns);
+                ++n_o[u];
+            }
+            if (!ok) break;
+            tc_fence_after();
+            // ---- the segment's result: this thread's columns [c0, c1) of row r ----
+            constexpr int kCols = PAIR ? D : D / 2;
+            const int c0 = PAIR ? 0 : s * kCols;
+            float keep0 = 1.f, keep1 = 0.f;  // factors of the two streams' O
+            bool use0 = steps > 0, use1 = false;
+            if (!PAIR) {
+                ctl->max_sum[s][0][r] = m;
+                ctl->max_sum[s][1][r] = l;
+                mbar_arrive(&ctl->sync[0]);
+                if (!(ok = warp_wait(ctl, &ctl->sync[0], n_sync & 1, c, g.timeout_ns))) break;
+                ++n_sync;
+                const float m0 = ctl->max_sum[0][0][r], m1 = ctl->max_sum[1][0][r];
+                m = fmaxf(m0, m1);
+                keep0 = m0 == -INFINITY ? 0.f : ex2((m0 - m) * sc);
+                keep1 = m1 == -INFINITY ? 0.f : ex2((m1 - m) * sc);
+                l = ctl->max_sum[0][1][r] * keep0 + ctl->max_sum[1][1][r] * keep1;
+                use0 = nt > 0;
+                use1 = nt > 1;
+            }
+            const bool whole = seg.first == 0 && seg.last == seg.tiles;
+            int cf = 0, cl = 0;
+            float *slot = nullptr;
+            if (!whole) {
+                cf = static_cast<int>(((seg.at + kItemCost + 1) * blocks - 1) / total);
+                cl = static_cast<int>(((seg.at + kItemCost + seg.tiles) * blocks - 1) / total);
+                const size_t index = (size_t(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == cf ? 1 : 0)) * S::QT + (PAIR ? s : 0);
+                slot = g.partials + index * S::kSlotFloats;
+            }
+            uint32_t out_head = 0;
+            unsigned short *out = nullptr;
+            if (real) {
+                out_head = seg.kv_head * g.group + row_head;
+                out = static_cast<unsigned short *>(g.out) + static_cast<long long>(walk.q.q0 + token) * g.out_token +
+                      static_cast<long long>(out_head) * g.out_head;
+            }
+            const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays
+            if (warp_real) {
+#pragma unroll
+                for (int q = 0; q < kCols / 32; ++q) {
+                    float o[32];
+                    if (PAIR) {
+                        uint32_t a[32];
+                        tmem_ld_32(t_o + q * 32, a);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int u = 0; u < 32; ++u) o[u] = use0 ? __uint_as_float(a[u]) : 0.f;
+                    } else {
+                        uint32_t a[32], b[32];
+                        const uint32_t col = tmem + 2 * kTile + lanes + c0 + q * 32;
+                        tmem_ld_32(col, a);
+                        tmem_ld_32(col + kTile, b);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int u = 0; u < 32; ++u)
+                            o[u] = (use0 ? __uint_as_float(a[u]) * keep0 : 0.f) + (use1 ? __uint_as_float(b[u]) * keep1 : 0.f);
+                    }
+                    if (whole) {
+                        if (real) {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                *reinterpret_cast<uint4 *>(out + c0 + q * 32 + u * 8) = make_uint4(
+                                    pack16<BF16>(o[8 * u] * inv, o[8 * u + 1] * inv), pack16<BF16>(o[8 * u + 2] * inv, o[8 * u + 3] * inv),
+                                    pack16<BF16>(o[8 * u + 4] * inv, o[8 * u + 5] * inv),
+                                    pack16<BF16>(o[8 * u + 6] * inv, o[8 * u + 7] * inv));
+                        }
+                    } else if (real) {
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            __stcg(reinterpret_cast<float4 *>(slot) + ((c0 + q * 32) / 4 + u) * kTile + r,
+                                   make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]));
+                    }
+                }
+            }
+            if (whole) {
+                if (real && g.lse && (PAIR || s == 0))
+                    g.lse[static_cast<size_t>(walk.q.q0 + token) * (c.kv_heads * g.group) + out_head] =
+                        l == 0.f ? -INFINITY : (m * sc + lg2(l)) * 0.6931471805599453f;
+                if (!PAIR) {  // the other stream's O has been read before it is written again
+                    mbar_arrive(&ctl->sync[0]);
+                    if (!(ok = warp_wait(ctl, &ctl->sync[0], n_sync & 1, c, g.timeout_ns))) break;
+                    ++n_sync;
+                }
+                continue;
+            }
+            // ---- an item cut by ranges' ends: the last of its blocks joins the partial results ----
+            if (real && (PAIR || s == 0)) {
+                __stcg(slot + size_t(kTile) * D + r, m);
+                __stcg(slot + size_t(kTile) * (D + 1) + r, l);
+            }
+            __threadfence();
+            uint64_t *sync = &ctl->sync[PAIR ? s : 0];
+            mbar_arrive(sync);
+            if (!(ok = warp_wait(ctl, sync, n_sync & 1, c, g.timeout_ns))) break;
+            ++n_sync;
+            if (PAIR ? r == 0 : threadIdx.x == 0) {
+                unsigned *count = g.arrivals + cf * 2 + (PAIR ? s : 0);
+                const unsigned before = atomicAdd(count, 1u);
+                const bool is_last = before == static_cast<unsigned>(cl - cf);
+                if (is_last) *count = 0;
+                ctl->last[PAIR ? s : 0] = is_last;
+                __threadfence();
+            }
+            mbar_arrive(sync);
+            if (!(ok = warp_wait(ctl, sync, n_sync & 1, c, g.timeout_ns))) break;
+            ++n_sync;
+            if (!ctl->last[PAIR ? s : 0]) continue;
+            const int first_token = seg.tile * step + (PAIR ? s * g.tile_tokens : 0);
+            const int rows = min(g.tile_tokens, walk.q.n - first_token) * g.group;  // may be <= 0: the second tile of a pair
+            const float *parts = g.partials + (PAIR ? s : 0) * S::kSlotFloats;
+            for (int e = PAIR ? r : static_cast<int>(threadIdx.x); e < rows * (D / 4); e += PAIR ? 128 : 256) {
+                const int c4 = e / rows, row = e - c4 * rows;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                float top = -INFINITY, z = 0.f;
+                constexpr int kBatch = 8;
+                for (int b0 = cf; b0 <= cl; b0 += kBatch) {
+                    float pm[kBatch], pl[kBatch];
+                    float4 po[kBatch];
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) {
+                        const int b = min(b0 + u, cl);
+                        const float *p = parts + (size_t(b) * 2 + (b == cf ? 1 : 0)) * S::QT * S::kSlotFloats;
+                        pm[u] = __ldcg(p + size_t(kTile) * D + row);
+                        pl[u] = __ldcg(p + size_t(kTile) * (D + 1) + row);
+                        po[u] = __ldcg(reinterpret_cast<const float4 *>(p) + c4 * kTile + row);
+                    }
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) {
+                        if (b0 + u > cl) continue;
+                        const float up = fmaxf(top, pm[u]);
+                        const float ka = top == -INFINITY ? 0.f : ex2((top - up) * sc);
+                        const float kb = pm[u] == -INFINITY ? 0.f : ex2((pm[u] - up) * sc);
+                        acc.x = acc.x * ka + po[u].x * kb;
+                        acc.y = acc.y * ka + po[u].y * kb;
+                        acc.z = acc.z * ka + po[u].z * kb;
+                        acc.w = acc.w * ka + po[u].w * kb;
+                        z = z * ka + pl[u] * kb;
+                        top = up;
+                    }
+                }
+                const int tk = row / g.group, hd = seg.kv_head * g.group + row - tk * g.group;
+                const long long qt = walk.q.q0 + first_token + tk;
+                const float f = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
+                unsigned short *o = static_cast<unsigned short *>(g.out) + qt * g.out_token + hd * g.out_head + c4 * 4;
+                *reinterpret_cast<uint2 *>(o) = make_uint2(pack16<BF16>(acc.x * f, acc.y * f), pack16<BF16>(acc.z * f, acc.w * f));
+                if (c4 == 0 && g.lse)
+                    g.lse[qt * (c.kv_heads * g.group) + hd] = z == 0.f ? -INFINITY : (top * sc + lg2(z)) * 0.6931471805599453f;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <bool BF16, int D, bool PAIR>
+dspark_status launch(const CUtensorMap &tm_q, const CUtensorMap &tm_kv, const CacheView &c, const Attention &g, int blocks,
+                     cudaStream_t stream) {
+    auto *kernel = attention_kernel<BF16, D, PAIR>;
+    static int configured = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (configured != dev) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged_attention)");
+        configured = dev;
+    }
+    e = launch_pdl(kernel, dim3(blocks), dim3(kThreads), kSmemBytes, stream, tm_q, tm_kv, c, g);
+    return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "paged_attention");
+}
+
+dspark_status attend(const dspark_cache *cache, int layer, const void *q, long long q_token_stride, long long q_head_stride,
+                     int tokens, int q_heads, const int32_t *rows, const int32_t *cu_new, int n_seqs, int max_new, int causal,
+                     int window, float scale, void *out, long long out_token_stride, long long out_head_stride, float *lse,
+                     unsigned stall_us, cudaStream_t stream) {
     const char *who = "paged_attention";
     CacheView c;
     dspark_status st = cache_view(cache, who, &c);
@@ -92,26 +806,93 @@ extern "C" dspark_status dspark_paged_attention(const dspark_cache *cache, int l
         return fail(DSPARK_ERR_INVALID, "%s: bad sizes tokens=%d q_heads=%d n_seqs=%d max_new=%d window=%d", who, tokens,
                     q_heads, n_seqs, max_new, window);
     if (q_heads % c.kv_heads) return fail(DSPARK_ERR_INVALID, "%s: %d query heads over %d kv heads", who, q_heads, c.kv_heads);
-    if (q_heads / c.kv_heads > 128)
-        return fail(DSPARK_ERR_UNSUPPORTED, "%s: %d query heads to a kv head, at most 128", who, q_heads / c.kv_heads);
+    if (!(scale > 0.f) || scale > 3.0e38f) return fail(DSPARK_ERR_INVALID, "%s: scale %g is not positive and finite", who, scale);
+    const int group = q_heads / c.kv_heads;
+    if (group > kTile) return fail(DSPARK_ERR_UNSUPPORTED, "%s: %d query heads to a kv head, at most %d", who, group, kTile);
     if (n_seqs > kMaxSeqs) return fail(DSPARK_ERR_UNSUPPORTED, "%s: n_seqs %d > %d", who, n_seqs, kMaxSeqs);
     if (tokens == 0 || n_seqs == 0) return DSPARK_OK;
     if (!q || !out || !cu_new) return fail(DSPARK_ERR_INVALID, "%s: null pointer argument", who);
+    if (tokens == 1) q_token_stride = static_cast<long long>(q_heads) * c.head_dim;  // never used: any value will do
+    if (q_heads == 1) q_head_stride = c.head_dim;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(cu_new, 4) || !aligned(lse, 4) || q_token_stride % 8 ||
-        q_head_stride % 8 || out_token_stride % 8 || out_head_stride % 8 || q_token_stride < 0 || q_head_stride < 0 ||
+        q_head_stride % 8 || out_token_stride % 8 || out_head_stride % 8 || q_token_stride <= 0 || q_head_stride <= 0 ||
         out_token_stride < 0 || out_head_stride < 0)
-        return fail(DSPARK_ERR_INVALID, "%s: q and out must be 16-byte aligned, with strides of whole 16 bytes", who);
-    Attention g{q, out, lse, q_token_stride, q_head_stride, out_token_stride, out_head_stride, rows, cu_new, tokens, q_heads,
-                n_seqs, layer, causal != 0, window, scale};
-    const unsigned blocks = static_cast<unsigned>((static_cast<long long>(tokens) * q_heads + 7) / 8);
+        return fail(DSPARK_ERR_INVALID, "%s: q and out must be 16-byte aligned, with positive strides of whole 16 bytes", who);
+    int sms = 0;
+    if ((st = static_cast<dspark_status>(current_sm_count(&sms))) != DSPARK_OK) return st;
+
+    Attention g{};
+    g.out = out;
+    g.lse = lse;
+    g.out_token = out_token_stride;
+    g.out_head = out_head_stride;
+    g.rows = rows;
+    g.cu_new = cu_new;
+    g.tokens = tokens;
+    g.group = group;
+    g.n_seqs = n_seqs;
+    g.layer = layer;
+    g.causal = causal != 0;
+    g.window = window;
+    g.scale = scale;
+    g.tile_tokens = kTile / group;
+    // Two query tiles share each key tile where the chunks fill them; a chunk of one tile splits its keys over the streams.
+    const bool pair = max_new > g.tile_tokens;
+    const int step = g.tile_tokens * (pair ? 2 : 1);
+    g.chunk_tiles = (max_new + step - 1) / step;
+    g.partials = reinterpret_cast<float *>(c.scratch);
+    g.arrivals = c.counters;
+    g.timeout_ns = kDefaultTimeoutNs;
+    g.stall_ns = static_cast<unsigned long long>(stall_us) * 1000ull;
+
     const bool bf16 = cache->dtype == DSPARK_BF16;
-    if (c.head_dim == 128) {
-        if (bf16) attention_kernel<__nv_bfloat16, 128><<<blocks, 256, 0, stream>>>(c, g);
-        else attention_kernel<__half, 128><<<blocks, 256, 0, stream>>>(c, g);
-    } else {
-        if (bf16) attention_kernel<__nv_bfloat16, 64><<<blocks, 256, 0, stream>>>(c, g);
-        else attention_kernel<__half, 64><<<blocks, 256, 0, stream>>>(c, g);
+    CUtensorMap tm_q, tm_kv;
+    {
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(q_heads), static_cast<cuuint64_t>(tokens)};
+        const cuuint64_t strides[2] = {static_cast<cuuint64_t>(q_head_stride) * 2, static_cast<cuuint64_t>(q_token_stride) * 2};
+        const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(g.tile_tokens)};
+        if ((st = make_tmap_nd(&tm_q, bf16, q, 3, dims, strides, box)) != DSPARK_OK) return st;
     }
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, who);
+    {
+        const cuuint64_t runs = 2ull * c.layers * c.kv_heads, run_bytes = 2ull * c.page_size * c.head_dim;
+        const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.page_size), runs,
+                                    static_cast<cuuint64_t>(c.num_pages)};
+        const cuuint64_t strides[3] = {2ull * c.head_dim, run_bytes, runs * run_bytes};
+        const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(c.page_size < kTile ? c.page_size : kTile), 1, 1};
+        if ((st = make_tmap_nd(&tm_kv, bf16, c.pool, 4, dims, strides, box)) != DSPARK_OK) return st;
+    }
+    const int blocks = sms < kMaxCtas ? sms : kMaxCtas;
+    if (c.head_dim == 128) {
+        if (bf16) return pair ? launch<true, 128, true>(tm_q, tm_kv, c, g, blocks, stream) : launch<true, 128, false>(tm_q, tm_kv, c, g, blocks, stream);
+        return pair ? launch<false, 128, true>(tm_q, tm_kv, c, g, blocks, stream) : launch<false, 128, false>(tm_q, tm_kv, c, g, blocks, stream);
+    }
+    if (bf16) return pair ? launch<true, 64, true>(tm_q, tm_kv, c, g, blocks, stream) : launch<true, 64, false>(tm_q, tm_kv, c, g, blocks, stream);
+    return pair ? launch<false, 64, true>(tm_q, tm_kv, c, g, blocks, stream) : launch<false, 64, false>(tm_q, tm_kv, c, g, blocks, stream);
+}
+
+}  // namespace
+
+// Two slots a block, of two query tiles each.
+size_t attention_scratch_bytes(int head_dim) { return size_t(kMaxCtas) * 2 * 2 * slot_bytes(head_dim); }
+
+}  // namespace dspark
+
+extern "C" dspark_status dspark_paged_attention(const dspark_cache *cache, int layer, const void *q,
+                                                long long q_token_stride, long long q_head_stride, int tokens,
+                                                int q_heads, const int32_t *rows, const int32_t *cu_new, int n_seqs,
+                                                int max_new, int causal, int window, float scale, void *out,
+                                                long long out_token_stride, long long out_head_stride, float *lse,
+                                                dspark_stream_t stream) {
+    return dspark::attend(cache, layer, q, q_token_stride, q_head_stride, tokens, q_heads, rows, cu_new, n_seqs, max_new, causal,
+                          window, scale, out, out_token_stride, out_head_stride, lse, 0, stream);
+}
+
+extern "C" dspark_status dspark_paged_attention_debug(const dspark_cache *cache, int layer, const void *q,
+                                                      long long q_token_stride, long long q_head_stride, int tokens,
+                                                      int q_heads, const int32_t *rows, const int32_t *cu_new, int n_seqs,
+                                                      int max_new, int causal, int window, float scale, void *out,
+                                                      long long out_token_stride, long long out_head_stride, float *lse,
+                                                      unsigned stall_us, dspark_stream_t stream) {
+    return dspark::attend(cache, layer, q, q_token_stride, q_head_stride, tokens, q_heads, rows, cu_new, n_seqs, max_new, causal,
+                          window, scale, out, out_token_stride, out_head_stride, lse, stall_us, stream);
 }

@@ -33,6 +33,12 @@ dspark_status make_tmap_kblocks(CUtensorMap *map, const void *base, bool bf16, u
 dspark_status make_tmap_rows_f32(CUtensorMap *map, const float *base, uint64_t planes, uint64_t rows, uint64_t cols,
                                  uint32_t box_planes, uint32_t box_cols);
 
+// Tensor map of `rank` (at most 4) dimensions over 16-bit elements, innermost first, with the byte
+// strides of the outer ones; boxes of 64 x ... elements with the 128-byte swizzle.  Out-of-bounds
+// elements read as zero.
+dspark_status make_tmap_nd(CUtensorMap *map, bool bf16, const void *base, uint32_t rank, const cuuint64_t *dims,
+                           const cuuint64_t *strides, const cuuint32_t *box);
+
 // ---- device ----------------------------------------------------------------------
 // Make this thread's generic-proxy shared-memory writes visible to the async proxy
 // (tensor-core operand reads, TMA).

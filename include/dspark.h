@@ -525,8 +525,9 @@ void dspark_gated_draft_plan_destroy(dspark_gated_plan *plan);
  *           beyond its pages
  *   length  int32 [max_seqs]: tokens of each sequence (0: none)
  *   refs    int32 [num_pages]: sequences that hold the page (0: free)
- *   workspace  dspark_cache_workspace_bytes() bytes, 256-byte aligned, ZERO-FILLED before its
- *           first use; holds the status word.  Calls that share one must not overlap.
+ *   workspace  dspark_cache_workspace_bytes() bytes, 256-byte aligned, the first 2048 of them
+ *           ZERO-FILLED before its first use; holds the status word.  Calls that share one must
+ *           not overlap.
  * Supported: page_size 16, 32, 64, 128 or 256; head_dim 64 or 128; 1 <= kv_heads, layers,
  *   num_pages, max_seqs, max_pages; num_pages < 2^24.
  *
@@ -653,6 +654,7 @@ dspark_status dspark_rotary_append(const dspark_cache *cache, int layer, const v
  *   q, out   [tokens, q_heads, head_dim] in the cache's type; strides in elements, multiples of 8
  *            (the last axis contiguous), 16-byte aligned.  out must not overlap q
  *   lse      float [tokens, q_heads] or NULL
+ *   scale    positive
  *   max_new  the longest chunk, as far as the caller knows (a hint for the tile shape; wrong values
  *            cost time, not correctness); tokens where it is not known
  * What lies in the cache behind a row's length, or in pages that no row holds, is never seen,
@@ -668,6 +670,18 @@ dspark_status dspark_paged_attention(const dspark_cache *cache, int layer, const
                                      int max_new, int causal, int window, float scale, void *out,
                                      long long out_token_stride, long long out_head_stride, float *lse,
                                      dspark_stream_t stream);
+
+/* Fault-injection hook for testing the device-side wait limit: the same launch as
+ * dspark_paged_attention, except that the softmax threads first wait `stall_us` microseconds on a
+ * barrier that nothing signals; the wait gives up, DSPARK_ERR_TIMEOUT is recorded and the kernel
+ * finishes normally.  Not for production use. */
+dspark_status dspark_paged_attention_debug(const dspark_cache *cache, int layer, const void *q,
+                                           long long q_token_stride, long long q_head_stride, int tokens,
+                                           int q_heads, const int32_t *rows, const int32_t *cu_new,
+                                           int n_seqs, int max_new, int causal, int window, float scale,
+                                           void *out, long long out_token_stride,
+                                           long long out_head_stride, float *lse, unsigned stall_us,
+                                           dspark_stream_t stream);
 
 #ifdef __cplusplus
 }

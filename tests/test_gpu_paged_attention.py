@@ -212,3 +212,22 @@ def test_refusals():
     # nothing to do is no error
     assert api.paged_attention(q[:0], cache, 0, cu).shape == (0, 4, 64)
     assert cache.status() == 0
+
+
+@pytest.mark.parametrize("n", [3, 200])
+def test_a_wait_that_gave_up_is_reported(n):
+    # every softmax thread first waits 20 ms on a barrier that nothing signals; the results are whole all the same
+    gen = torch.Generator().manual_seed(12)
+    cache, _, _ = make_cache(gen, [700], dtype=BF16, dim=128, kv_heads=1, page=16)
+    q = torch.randn((n, 4, 128), generator=gen).to(BF16).cuda()
+    cu = torch.tensor([0, n], dtype=torch.int32).cuda()
+    want = api.paged_attention(q, cache, 0, cu)
+    assert cache.status() == 0
+    got = torch.empty_like(want)
+    lib = api.load_library()
+    status = lib.dspark_paged_attention_debug(cache._ref, 0, q.data_ptr(), 512, 128, n, 4, None, cu.data_ptr(), 1, n, 1, 0,
+                                              128 ** -0.5, got.data_ptr(), 512, 128, None, 20000,
+                                              torch.cuda.current_stream().cuda_stream)
+    assert status == 0 and cache.status() == api.DSPARK_ERR_TIMEOUT
+    assert torch.equal(got, want)
+    assert torch.equal(api.paged_attention(q, cache, 0, cu), want) and cache.status() == 0

@@ -27,8 +27,8 @@ BAD_CACHES = [(dict(pool=None), INVALID), (dict(table=None), INVALID), (dict(len
 
 
 def attend(lib, c, layer=0, q=FAKE, qs=(512, 128), tokens=3, heads=4, cu=FAKE, seqs=1, max_new=3, window=0, out=FAKE,
-           os=(512, 128), lse=None):
-    return lib.dspark_paged_attention(c, layer, q, *qs, tokens, heads, None, cu, seqs, max_new, 1, window, 1.0, out, *os, lse, None)
+           os=(512, 128), lse=None, scale=1.0):
+    return lib.dspark_paged_attention(c, layer, q, *qs, tokens, heads, None, cu, seqs, max_new, 1, window, scale, out, *os, lse, None)
 
 
 def append(lib, c, layer=0, q=FAKE, k=FAKE, v=FAKE, out=FAKE, stride=512, tokens=3, heads=4, cu=FAKE, seqs=1, turns=FAKE, dim=128,
@@ -82,7 +82,8 @@ def test_attention_refuses(dspark_lib):
     lib, c = dspark_lib, cache()
     for kw in (dict(layer=2), dict(layer=-1), dict(q=None), dict(out=None), dict(cu=None), dict(q=ODD), dict(out=ODD), dict(lse=0x10002),
                dict(tokens=-1), dict(heads=0), dict(heads=3), dict(seqs=-1), dict(max_new=-1), dict(window=-1), dict(qs=(516, 128)),
-               dict(os=(512, 129)), dict(qs=(-512, 128))):
+               dict(os=(512, 129)), dict(qs=(-512, 128)), dict(qs=(0, 128)), dict(scale=0.0),
+               dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan)):
         assert attend(lib, c, **kw) == INVALID, kw
     assert attend(lib, c, heads=258) == UNSUPPORTED
     assert attend(lib, c, seqs=4097) == UNSUPPORTED
