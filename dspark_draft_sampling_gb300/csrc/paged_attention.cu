@@ -30,7 +30,10 @@ namespace dspark {
 namespace {
 
 constexpr int kTile = 128;                    // query rows of a tile, keys of a tile
-constexpr int kThreads = 320;                 // warps 0-3, 4-7: softmax of stream 0, 1; 8: copies; 9: MMA issue
+constexpr int kThreads = 384;                 // warps 0-3, 4-7: softmax of stream 0, 1; 8: copies; 9: MMA issue; 10, 11: none
+// Registers of a softmax and of another thread: the launch gives all kThreads 168, and 256 * 208 + 128 * 80 is less.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80, kLaunchRegs = 168;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "more registers than the block was launched with");
 constexpr int kTmemCols = 512;
 constexpr size_t kSmemData = 224 * 1024;      // query tiles and the ring of key and value tiles
 constexpr size_t kSmemBytes = 227 * 1024;
@@ -95,19 +98,20 @@ __device__ __forceinline__ void key_tiles(const Attention &g, const Seq &q, int 
     if (begin >= end) *lo = *hi;
 }
 
-// One stretch of an item that a block works on.
+// One stretch of an item that a block works on, as the copying warp hands it to the others.
 struct Segment {
     int kv_head, tile;        // query tile of the sequence
     int lo, first, last;      // the item's first key tile; the stretch's, relative to it
-    int tiles;                // of the whole item
-    long long at;             // the item's place in the sequence of all tiles
+    int tiles;                // of the whole item; -1: no more segments
+    int q0, n, length;        // the sequence's first query token, its new tokens, its tokens
+    int cf, cl;               // first and last block that work on the item
 };
 
-// Walks a block's range; all roles walk it in the same way.
+// Walks a block's range.
 struct Walk {
     Seq q;
     int s, kv_head, i, n_tiles, step;
-    long long x, left, pos;  // x: place within the item; pos: absolute place
+    long long x, left, pos, at;  // x: place within the item; pos: absolute place; at: the last segment's item's
 
     __device__ __forceinline__ bool next(const CacheView &c, const Attention &g, Segment *out) {
         while (left > 0) {
@@ -132,7 +136,10 @@ struct Walk {
             out->tiles = tiles;
             out->first = static_cast<int>(max(x - kItemCost, 0ll));
             out->last = static_cast<int>(max(x + take - kItemCost, 0ll));
-            out->at = pos - x;
+            out->q0 = q.q0;
+            out->n = q.n;
+            out->length = q.length;
+            at = pos - x;
             const bool starts = x == 0;
             left -= take;
             pos += take;
@@ -200,6 +207,48 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     return r;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ unsigned long long pair_u32(uint32_t a, uint32_t b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ unsigned long long pair_f32(float a, float b) { return pair_u32(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ void split_f32(unsigned long long v, float *a, float *b) {
+    uint32_t x, y;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(v));
+    *a = __uint_as_float(x);
+    *b = __uint_as_float(y);
+}
+__device__ __forceinline__ unsigned long long fma_f32x2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add_f32x2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 32 lanes x 16 columns from registers; awaited with tmem_wait_st().
+__device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// Scores of keys key0 .. key0 + 31 that a row does not see become -infinity; skipped where every row sees all.
+__device__ __forceinline__ void mask_keys(uint32_t *v, int key0, int see_lo, int see_hi) {
+    if (!__any_sync(0xffffffffu, key0 < see_lo || key0 + 32 > see_hi)) return;
+    const int lo = see_lo - key0, hi = see_hi - key0;
+#pragma unroll
+    for (int q = 0; q < 32; ++q)
+        if (q < lo || q >= hi) v[q] = 0xff800000u;
+}
+
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
@@ -226,6 +275,8 @@ __device__ __forceinline__ uint64_t smem_desc_values(uint32_t addr) {
     return d;
 }
 
+constexpr int kSegments = 4;  // segments handed over ahead
+
 // Barriers and small state behind the data area.
 template <int STAGES>
 struct Control {
@@ -233,7 +284,9 @@ struct Control {
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_ready[2], o_full[2];
     uint64_t sync[2];   // softmax threads among themselves: per stream (PAIR), or [0] for both
+    uint64_t seg_full[kSegments], seg_empty[kSegments];
     uint64_t drained, never;
+    Segment segs[kSegments];
     uint32_t tmem, aborted;
     unsigned last[2];
     Start start;
@@ -262,6 +315,18 @@ __device__ __forceinline__ bool warp_wait(C *ctl, uint64_t *bar, uint32_t parity
     return __all_sync(0xffffffffu, wait(ctl, bar, parity, c, timeout_ns));
 }
 
+// The next segment, read by one warp.
+template <typename C>
+__device__ __forceinline__ bool next_segment(C *ctl, uint32_t &n_seg, Segment *seg, const CacheView &c, unsigned long long timeout_ns) {
+    const uint32_t slot = n_seg % kSegments;
+    if (!warp_wait(ctl, &ctl->seg_full[slot], (n_seg / kSegments) & 1, c, timeout_ns)) return false;
+    ++n_seg;
+    *seg = ctl->segs[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl->seg_empty[slot]);
+    return seg->tiles >= 0;
+}
+
 template <bool BF16, int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, const CacheView c,
@@ -288,6 +353,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ctl->p_ready[s], 4);  // one arrival a warp
             mbar_init(&ctl->o_full[s], 1);
             mbar_init(&ctl->sync[s], PAIR ? 128 : 256);
+        }
+        for (int i = 0; i < kSegments; ++i) {
+            mbar_init(&ctl->seg_full[i], 1);
+            mbar_init(&ctl->seg_empty[i], 9);  // the softmax warps and the MMA warp
         }
         mbar_init(&ctl->drained, 1);
         mbar_init(&ctl->never, 1);
@@ -382,36 +451,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem;
-    const long long total = ctl->start.total;
-    const int blocks = ctl->start.blocks;
-    const bool busy = static_cast<int>(blockIdx.x) < blocks;
-
-    Walk walk;
-    walk.left = 0;
-    if (busy) {
-        const Start &st = ctl->start;
-        walk.s = st.s;
-        walk.q = load_seq(c, g, st.s);
-        walk.kv_head = st.kv_head;
-        walk.i = st.i;
-        walk.step = step;
-        walk.n_tiles = (walk.q.n + step - 1) / step;
-        walk.x = st.x;
-        walk.pos = st.begin;
-        walk.left = st.end - st.begin;
-    }
-    Segment seg;
-
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8) {
         // ---- copies: query tiles, then keys and values of each tile through the ring; a lane to a page ----
         const int box = min(c.page_size, kTile), per_tile = kTile / box;
-        uint32_t n_q = 0, put = 0;  // segments, ring entries so far
+        uint32_t n_q = 0, n_seg = 0, put = 0;  // segments with keys, segments, ring entries so far
+        const Start st = ctl->start;
+        Walk walk;
+        walk.left = 0;
+        if (static_cast<int>(blockIdx.x) < st.blocks) {
+            walk.s = st.s;
+            walk.q = load_seq(c, g, st.s);
+            walk.kv_head = st.kv_head;
+            walk.i = st.i;
+            walk.step = step;
+            walk.n_tiles = (walk.q.n + step - 1) / step;
+            walk.x = st.x;
+            walk.pos = st.begin;
+            walk.left = st.end - st.begin;
+        }
         bool ok = true;
-        while (ok && walk.next(c, g, &seg)) {
-            if (seg.tiles == 0) continue;
+        for (bool more = true; ok && more;) {
+            Segment seg;
+            more = walk.next(c, g, &seg);
+            if (!more) seg.tiles = -1;
+            const uint32_t entry = n_seg % kSegments;
+            if (n_seg >= kSegments && !(ok = warp_wait(ctl, &ctl->seg_empty[entry], ((n_seg / kSegments) & 1) ^ 1, c, g.timeout_ns))) break;
+            ++n_seg;
+            if (lane == 0) {
+                if (more && (seg.first != 0 || seg.last != seg.tiles)) {
+                    seg.cf = static_cast<int>(((walk.at + kItemCost + 1) * st.blocks - 1) / st.total);
+                    seg.cl = static_cast<int>(((walk.at + kItemCost + seg.tiles) * st.blocks - 1) / st.total);
+                }
+                ctl->segs[entry] = seg;
+                mbar_arrive(&ctl->seg_full[entry]);
+            }
+            __syncwarp();
+            if (!more || seg.tiles == 0) continue;
             if (n_q > 0 && !(ok = warp_wait(ctl, &ctl->q_empty, (n_q - 1) & 1, c, g.timeout_ns))) break;
             ++n_q;
-            const int token = walk.q.q0 + seg.tile * step;
+            const int token = seg.q0 + seg.tile * step;
             if (lane == 0) {
                 const uint32_t rows_bytes = static_cast<uint32_t>(g.tile_tokens * g.group) * 128u;
                 mbar_arrive_expect_tx(&ctl->q_full, rows_bytes * S::kHalves * S::QT);
@@ -424,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int run = (g.layer * 2) * c.kv_heads + seg.kv_head;
             for (int t = seg.first; ok && t < seg.last; ++t) {
                 const int key = (seg.lo + t) * kTile + lane * box;  // first key of this lane's page
-                const bool mine = lane < per_tile && key < walk.q.length;
+                const bool mine = lane < per_tile && key < seg.length;
                 int page = 0;
                 if (mine) {
                     page = pages[key >> c.page_shift];
@@ -456,12 +536,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             constexpr uint32_t idesc_s = idesc_f16(BF16, kTile, kTile);
             constexpr uint32_t idesc_o = idesc_f16(BF16, kTile, D) | (1u << 16);  // B is N-contiguous
-            uint32_t n_q = 0, base = 0;          // segments, key tiles before this segment
+            uint32_t n_q = 0, base = 0;          // segments with keys, key tiles before this segment
             uint32_t n_p[2] = {0, 0};            // second products so far
+            uint32_t n_seg = 0;
             bool ok = true;
-            while (ok && walk.next(c, g, &seg)) {
-                if (seg.tiles == 0) continue;
-                const int nt = seg.last - seg.first;
+            while (ok) {
+                // as next_segment(), by one thread
+                const uint32_t entry = n_seg % kSegments;
+                if (!(ok = wait(ctl, &ctl->seg_full[entry], (n_seg / kSegments) & 1, c, g.timeout_ns))) break;
+                ++n_seg;
+                const Segment &seg = ctl->segs[entry];
+                const int nt = seg.last - seg.first, tiles = seg.tiles;
+                mbar_arrive(&ctl->seg_empty[entry]);
+                if (tiles < 0) break;
+                if (tiles == 0) continue;
                 const int steps[2] = {PAIR ? nt : (nt + 1) / 2, PAIR ? nt : nt / 2};
                 if (!(ok = wait(ctl, &ctl->q_full, n_q & 1, c, g.timeout_ns))) break;
                 ++n_q;
@@ -495,12 +583,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (i + 1 == steps[s]) tc_commit(&ctl->o_full[s]);
                     return true;
                 };
-                for (int s = 0; s < 2 && ok; ++s)
-                    if (steps[s] > 0) ok = scores(s, 0);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    if (ok && steps[s] > 0) ok = scores(s, 0);
                 if (steps[0] == 1 && ok) tc_commit(&ctl->q_empty);
                 for (int i = 0; i < steps[0] && ok; ++i) {
-                    for (int s = 0; s < 2 && ok; ++s) {
-                        if (i >= steps[s]) continue;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (!ok || i >= steps[s]) continue;
                         ok = values(s, i);
                         if (ok && i + 1 < steps[s]) ok = scores(s, i + 1);
                     }
@@ -512,23 +602,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(&ctl->drained, 0, g.timeout_ns);
         }
         __syncwarp();
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ---- softmax of stream s: a thread owns row r ----
         const int s = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + s * kTile + lanes, t_o = tmem + 2 * kTile + s * kTile + lanes;
         const float sc = g.scale * 1.4426950408889634f;
         const int row_token = r / g.group, row_head = r - row_token * g.group;
-        uint32_t n_s = 0, n_o[2] = {0, 0}, n_sync = 0, base = 0;
+        uint32_t n_s = 0, n_seg = 0, n_o0 = 0, n_o1 = 0, n_sync = 0, base = 0;
         bool ok = true;
         if (g.stall_ns && !mbar_wait(&ctl->never, 0, g.stall_ns) && threadIdx.x == 0) atomicOr(c.status, kStatusTimeout);
-        while (ok && walk.next(c, g, &seg)) {
+        Segment seg;
+        while (ok && next_segment(ctl, n_seg, &seg, c, g.timeout_ns)) {
             const int nt = seg.last - seg.first;
             const int token = seg.tile * step + (PAIR ? s * g.tile_tokens : 0) + row_token;  // of the chunk
-            const bool real = row_token < g.tile_tokens && token < walk.q.n;
-            const int pos = walk.q.length - walk.q.n + token;
+            const bool real = row_token < g.tile_tokens && token < seg.n;
+            const int pos = seg.length - seg.n + token;
             // keys that this row sees; rows that are none see all, as what they hold is not written
-            const int see_hi = !real ? 0x7fffffff : g.causal ? min(walk.q.length, pos + 1) : walk.q.length;
+            const int see_hi = !real ? 0x7fffffff : g.causal ? min(seg.length, pos + 1) : seg.length;
             const int see_lo = real && g.window > 0 ? max(0, pos - g.window + 1) : 0;
             float m = -INFINITY, l = 0.f;
             const int steps = PAIR ? nt : (nt + 1 - s) / 2;
@@ -539,11 +632,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = warp_wait(ctl, &ctl->s_full[s], n_s & 1, c, g.timeout_ns))) break;
                 ++n_s;
                 tc_fence_after();
-                if (key0 + kTile > walk.q.length) {
+                if (key0 + kTile > seg.length) {
                     // values behind the row's length are whatever the page holds: zeros, so that weights of 0 stay 0
                     const uint32_t p = 2 * (base + t) + 1, st = p % S::kStages;
                     if (!(ok = warp_wait(ctl, &ctl->full[st], (p / S::kStages) & 1, c, g.timeout_ns))) break;
-                    const int used = walk.q.length - key0;
+                    const int used = seg.length - key0;
                     unsigned char *v = ring_ptr + st * S::kTileBytes;
                     for (int h = 0; h < S::kHalves; ++h)
                         for (int b = used * 8 + r; b < kTile * 8; b += kTile)
@@ -552,22 +645,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (warp_real) {
                     uint32_t v[kTile];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld_32(t_s + q * 32, v + q * 32);
-                    tmem_wait_ld();
-                    if (__any_sync(0xffffffffu, key0 < see_lo || key0 + kTile > see_hi)) {
-                        const int lo = see_lo - key0;
-                        const unsigned span = static_cast<unsigned>(max(min(see_hi, walk.q.length) - max(see_lo, 0), 0));
-#pragma unroll
-                        for (int q = 0; q < kTile; ++q)
-                            if (static_cast<unsigned>(q - lo) >= span) v[q] = 0xff800000u;
-                    }
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    const bool edge = __any_sync(0xffffffffu, key0 < see_lo || key0 + kTile > see_hi);
+                    tmem_ld_32(t_s, v);
 #pragma unroll
-                    for (int q = 0; q < kTile; q += 8) {
+                    for (int q = 0; q < 4; ++q) {
+                        tmem_wait_ld();
+                        if (q < 3) tmem_ld_32(t_s + (q + 1) * 32, v + (q + 1) * 32);
+                        if (edge) mask_keys(v + q * 32, key0 + q * 32, see_lo, see_hi);
 #pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            top[u] = fmaxf(top[u], fmaxf(__uint_as_float(v[q + 2 * u]), __uint_as_float(v[q + 2 * u + 1])));
+                        for (int u = 0; u < 32; u += 8) {
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+                                top[w] = fmaxf(top[w], fmaxf(__uint_as_float(v[q * 32 + u + 2 * w]), __uint_as_float(v[q * 32 + u + 2 * w + 1])));
+                        }
                     }
                     const float tile_max = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     const bool moves = real && (tile_max - m) * sc > kRescale;  // also from -infinity
@@ -577,33 +668,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (i > 0) {
                             // the scores' arrival also says that this stream's earlier second products are done
 #pragma unroll
-                            for (int q = 0; q < D / 32; ++q) {
-                                uint32_t o[32];
-                                tmem_ld_32(t_o + q * 32, o);
-                                tmem_wait_ld();
+                            for (int q = 0; q < D / 16; ++q) {
+                                uint32_t o[16];
+                                tmem_ld_16(t_o + q * 16, o);
 #pragma unroll
-                                for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
-                                tmem_st_32(t_o + q * 32, o);
+                                for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
+                                tmem_st_16(t_o + q * 16, o);
                             }
                         }
                         l *= keep;
                         m = up;
                     }
-                    const float shift = m == -INFINITY ? 0.f : m * sc;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float shift = m == -INFINITY ? 0.f : -m * sc;
+                    const unsigned long long sc2 = pair_f32(sc, sc), shift2 = pair_f32(shift, shift);
+                    unsigned long long sum2[2] = {0ull, 0ull};
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t w[32];
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w[16];
 #pragma unroll
-                        for (int u = 0; u < 32; ++u) {
-                            const float a = ex2(fmaf(__uint_as_float(v[q * 64 + 2 * u]), sc, -shift));
-                            const float b = ex2(fmaf(__uint_as_float(v[q * 64 + 2 * u + 1]), sc, -shift));
-                            sum[(2 * u) & 3] += a;
-                            sum[(2 * u + 1) & 3] += b;
+                        for (int u = 0; u < 16; ++u) {
+                            float a, b;
+                            split_f32(fma_f32x2(pair_u32(v[q * 32 + 2 * u], v[q * 32 + 2 * u + 1]), sc2, shift2), &a, &b);
+                            a = ex2(a);
+                            b = ex2(b);
+                            sum2[u & 1] = add_f32x2(sum2[u & 1], pair_f32(a, b));
                             w[u] = pack16<BF16>(a, b);
                         }
-                        tmem_st_32(t_s + q * 32, w);
+                        tmem_st_16(t_s + q * 16, w);
                     }
+                    float sum[4];
+                    split_f32(sum2[0], &sum[0], &sum[1]);
+                    split_f32(sum2[1], &sum[2], &sum[3]);
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tmem_wait_st();
                 }
@@ -614,10 +709,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             base += nt;
             if (!ok) break;
             // the O that this thread reads: its stream's, or (a query tile over two streams) both
-            for (int u = PAIR ? s : 0; u < (PAIR ? s + 1 : 2) && ok; ++u) {
-                if (PAIR ? nt == 0 : nt <= u) continue;
-                ok = warp_wait(ctl, &ctl->o_full[u], n_o[u] & 1, c, g.timeout_ns);
-                ++n_o[u];
+            if (PAIR) {
+                if (nt > 0) ok = warp_wait(ctl, &ctl->o_full[s], n_o0++ & 1, c, g.timeout_ns);
+            } else {
+                if (nt > 0) ok = warp_wait(ctl, &ctl->o_full[0], n_o0++ & 1, c, g.timeout_ns);
+                if (ok && nt > 1) ok = warp_wait(ctl, &ctl->o_full[1], n_o1++ & 1, c, g.timeout_ns);
             }
             if (!ok) break;
             tc_fence_after();
@@ -644,8 +740,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int cf = 0, cl = 0;
             float *slot = nullptr;
             if (!whole) {
-                cf = static_cast<int>(((seg.at + kItemCost + 1) * blocks - 1) / total);
-                cl = static_cast<int>(((seg.at + kItemCost + seg.tiles) * blocks - 1) / total);
+                cf = seg.cf;
+                cl = seg.cl;
                 const size_t index = (size_t(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == cf ? 1 : 0)) * S::QT + (PAIR ? s : 0);
                 slot = g.partials + index * S::kSlotFloats;
             }
@@ -653,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned short *out = nullptr;
             if (real) {
                 out_head = seg.kv_head * g.group + row_head;
-                out = static_cast<unsigned short *>(g.out) + static_cast<long long>(walk.q.q0 + token) * g.out_token +
+                out = static_cast<unsigned short *>(g.out) + static_cast<long long>(seg.q0 + token) * g.out_token +
                       static_cast<long long>(out_head) * g.out_head;
             }
             const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays
@@ -696,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (whole) {
                 if (real && g.lse && (PAIR || s == 0))
-                    g.lse[static_cast<size_t>(walk.q.q0 + token) * (c.kv_heads * g.group) + out_head] =
+                    g.lse[static_cast<size_t>(seg.q0 + token) * (c.kv_heads * g.group) + out_head] =
                         l == 0.f ? -INFINITY : (m * sc + lg2(l)) * 0.6931471805599453f;
                 if (!PAIR) {  // the other stream's O has been read before it is written again
                     mbar_arrive(&ctl->sync[0]);
@@ -728,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++n_sync;
             if (!ctl->last[PAIR ? s : 0]) continue;
             const int first_token = seg.tile * step + (PAIR ? s * g.tile_tokens : 0);
-            const int rows = min(g.tile_tokens, walk.q.n - first_token) * g.group;  // may be <= 0: the second tile of a pair
+            const int rows = min(g.tile_tokens, seg.n - first_token) * g.group;  // may be <= 0: the second tile of a pair
             const float *parts = g.partials + (PAIR ? s : 0) * S::kSlotFloats;
             for (int e = PAIR ? r : static_cast<int>(threadIdx.x); e < rows * (D / 4); e += PAIR ? 128 : 256) {
                 const int c4 = e / rows, row = e - c4 * rows;
@@ -761,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const int tk = row / g.group, hd = seg.kv_head * g.group + row - tk * g.group;
-                const long long qt = walk.q.q0 + first_token + tk;
+                const long long qt = seg.q0 + first_token + tk;
                 const float f = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
                 unsigned short *o = static_cast<unsigned short *>(g.out) + qt * g.out_token + hd * g.out_head + c4 * 4;
                 *reinterpret_cast<uint2 *>(o) = make_uint2(pack16<BF16>(acc.x * f, acc.y * f), pack16<BF16>(acc.z * f, acc.w * f));
@@ -787,6 +883,11 @@ dspark_status launch(const CUtensorMap &tm_q, const CUtensorMap &tm_kv, const Ca
     if (configured != dev) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged_attention)");
+        // the register shares are taken from what the block is launched with: never ask for more
+        cudaFuncAttributes attr;
+        e = cudaFuncGetAttributes(&attr, kernel);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes(paged_attention)");
+        if (attr.numRegs < kLaunchRegs) return fail(DSPARK_ERR_CUDA, "paged_attention: built with %d registers a thread", attr.numRegs);
         configured = dev;
     }
     e = launch_pdl(kernel, dim3(blocks), dim3(kThreads), kSmemBytes, stream, tm_q, tm_kv, c, g);
