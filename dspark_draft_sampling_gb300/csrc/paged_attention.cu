@@ -185,6 +185,12 @@ __device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t *v) {
         : "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -282,7 +288,7 @@ template <int STAGES>
 struct Control {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_ready[2], o_full[2];
+    uint64_t s_full[2], p_half[2], p_ready[2], o_full[2];
     uint64_t sync[2];   // softmax threads among themselves: per stream (PAIR), or [0] for both
     uint64_t seg_full[kSegments], seg_empty[kSegments];
     uint64_t drained, never;
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(sizeof(C) <= kSmemBytes - kSmemData, "control block does not fit");
     const uint32_t q_smem = smem_addr(smem), ring = q_smem + S::QT * S::kTileBytes;
     unsigned char *ring_ptr = smem + S::QT * S::kTileBytes;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int step = g.tile_tokens * S::QT;  // tokens of an item
 
     if (warp == 8 && lane == 0) {
@@ -350,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&ctl->q_empty, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&ctl->s_full[s], 1);
-            mbar_init(&ctl->p_ready[s], 4);  // one arrival a warp
+            mbar_init(&ctl->p_half[s], 4);  // one arrival a warp
+            mbar_init(&ctl->p_ready[s], 4);
             mbar_init(&ctl->o_full[s], 1);
             mbar_init(&ctl->sync[s], PAIR ? 128 : 256);
         }
@@ -532,76 +539,96 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(&ctl->full[p % S::kStages], (p / S::kStages) & 1, g.timeout_ns);
         if (n_q) mbar_wait(&ctl->q_full, (n_q - 1) & 1, g.timeout_ns);
     } else if (warp == 9) {
-        // ---- MMA issue ----
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = idesc_f16(BF16, kTile, kTile);
-            constexpr uint32_t idesc_o = idesc_f16(BF16, kTile, D) | (1u << 16);  // B is N-contiguous
-            uint32_t n_q = 0, base = 0;          // segments with keys, key tiles before this segment
-            uint32_t n_p[2] = {0, 0};            // second products so far
-            uint32_t n_seg = 0;
-            bool ok = true;
-            while (ok) {
-                // as next_segment(), by one thread
-                const uint32_t entry = n_seg % kSegments;
-                if (!(ok = wait(ctl, &ctl->seg_full[entry], (n_seg / kSegments) & 1, c, g.timeout_ns))) break;
-                ++n_seg;
-                const Segment &seg = ctl->segs[entry];
-                const int nt = seg.last - seg.first, tiles = seg.tiles;
-                mbar_arrive(&ctl->seg_empty[entry]);
-                if (tiles < 0) break;
-                if (tiles == 0) continue;
-                const int steps[2] = {PAIR ? nt : (nt + 1) / 2, PAIR ? nt : nt / 2};
-                if (!(ok = wait(ctl, &ctl->q_full, n_q & 1, c, g.timeout_ns))) break;
-                ++n_q;
-                auto scores = [&](int s, int i) {
-                    const uint32_t p = 2 * (base + (PAIR ? i : 2 * i + s)), st = p % S::kStages;
-                    if (!wait(ctl, &ctl->full[st], (p / S::kStages) & 1, c, g.timeout_ns)) return false;
-                    tc_fence_after();
-                    const uint64_t a = smem_desc_sw128(q_smem + (PAIR ? s * S::kTileBytes : 0));
-                    const uint64_t b = smem_desc_sw128(ring + st * S::kTileBytes);
+        // ---- MMA issue: the warp runs as one, an elected lane issues ----
+        constexpr uint32_t idesc_s = idesc_f16(BF16, kTile, kTile);
+        constexpr uint32_t idesc_o = idesc_f16(BF16, kTile, D) | (1u << 16);  // B is N-contiguous
+        uint32_t n_q = 0, n_seg = 0, base = 0;  // segments with keys, segments, key tiles before this segment
+        uint32_t p_phase = 0;                   // one bit a stream: the phase of its next P
+        bool ok = true;
+        Segment seg;
+        while (ok && next_segment(ctl, n_seg, &seg, c, g.timeout_ns)) {
+            if (seg.tiles == 0) continue;
+            const int nt = seg.last - seg.first;
+            const int steps0 = PAIR ? nt : (nt + 1) / 2, steps1 = PAIR ? nt : nt / 2;
+            if (!(ok = warp_wait(ctl, &ctl->q_full, n_q & 1, c, g.timeout_ns))) break;
+            ++n_q;
+            // Ring entries and their phases: key tile j of the segment is entry 2 * j, its values the next one.
+            struct Entry {
+                uint32_t st, phase;
+            };
+            auto entry = [&](uint32_t p) {
+                const uint32_t turn = p / S::kStages;
+                return Entry{__shfl_sync(0xffffffffu, p - turn * S::kStages, 0), turn & 1};
+            };
+            auto issue_scores = [&](const int s, const Entry &e, bool last) {
+                const uint64_t a = smem_desc_sw128(q_smem + (PAIR ? s * S::kTileBytes : 0));
+                const uint64_t b = smem_desc_sw128(ring + e.st * S::kTileBytes);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t o = static_cast<uint64_t>((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
-                        tc_mma_f16(tmem + s * kTile, a + o, b + o, idesc_s, k != 0);
-                    }
-                    tc_commit(&ctl->s_full[s]);
-                    if (!PAIR || s == 1) tc_commit(&ctl->empty[st]);
-                    return true;
-                };
-                auto values = [&](int s, int i) {
-                    const uint32_t p = 2 * (base + (PAIR ? i : 2 * i + s)) + 1, st = p % S::kStages;
-                    if (!wait(ctl, &ctl->p_ready[s], n_p[s] & 1, c, g.timeout_ns)) return false;
-                    ++n_p[s];
-                    if (!wait(ctl, &ctl->full[st], (p / S::kStages) & 1, c, g.timeout_ns)) return false;
-                    tc_fence_after();
-                    const uint64_t b = smem_desc_values(ring + st * S::kTileBytes);
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        tc_mma_f16_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + k * 8, b + ((k * 2048) >> 4), idesc_o,
-                                      i != 0 || k != 0);
-                    if (!PAIR || s == 1) tc_commit(&ctl->empty[st]);
-                    if (i + 1 == steps[s]) tc_commit(&ctl->o_full[s]);
-                    return true;
-                };
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    if (ok && steps[s] > 0) ok = scores(s, 0);
-                if (steps[0] == 1 && ok) tc_commit(&ctl->q_empty);
-                for (int i = 0; i < steps[0] && ok; ++i) {
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (!ok || i >= steps[s]) continue;
-                        ok = values(s, i);
-                        if (ok && i + 1 < steps[s]) ok = scores(s, i + 1);
-                    }
-                    if (ok && i + 2 == steps[0]) tc_commit(&ctl->q_empty);  // the last scores of the segment are issued
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t o = static_cast<uint64_t>((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
+                    tc_mma_f16(tmem + s * kTile, a + o, b + o, idesc_s, k != 0);
                 }
-                base += nt;
+                tc_commit(&ctl->s_full[s]);
+                if (!PAIR || s == 1) tc_commit(&ctl->empty[e.st]);
+                if (last) tc_commit(&ctl->q_empty);  // the segment's last scores free its query tiles
+            };
+            auto issue_values = [&](const int s, const Entry &e, const int k0, bool add) {
+                const uint64_t b = smem_desc_values(ring + e.st * S::kTileBytes);
+#pragma unroll
+                for (int k = k0; k < k0 + kTile / 32; ++k)
+                    tc_mma_f16_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + k * 8, b + ((k * 2048) >> 4), idesc_o, add || k != 0);
+            };
+            auto ready = [&](uint64_t *bar, uint32_t phase) { return warp_wait(ctl, bar, phase, c, g.timeout_ns); };
+            // Step i of stream s: its second product, then the scores of its next key tile.
+            auto advance = [&](const int s, int i, int steps, bool frees_q) {
+                const uint32_t p = 2 * (base + (PAIR ? i : 2 * i + s));
+                const bool more = i + 1 < steps;
+                const Entry v = entry(p + 1), k = entry(p + (PAIR ? 2 : 4));
+                if (!ready(&ctl->full[v.st], v.phase)) return false;
+                // With two query tiles the next keys have long arrived; otherwise they may be on their way, and the values' slot
+                // is wanted back first.
+                if (PAIR && more && !ready(&ctl->full[k.st], k.phase)) return false;
+                if (!ready(&ctl->p_half[s], (p_phase >> s) & 1)) return false;
+                tc_fence_after();
+                if (elect_one()) issue_values(s, v, 0, i != 0);
+                __syncwarp();
+                if (!ready(&ctl->p_ready[s], (p_phase >> s) & 1)) return false;
+                p_phase ^= 1u << s;
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_values(s, v, kTile / 32, true);
+                    if (!PAIR || s == 1) tc_commit(&ctl->empty[v.st]);
+                    if (!more) tc_commit(&ctl->o_full[s]);
+                    if (PAIR && more) issue_scores(s, k, frees_q);
+                }
+                __syncwarp();
+                if (!PAIR && more) {
+                    if (!ready(&ctl->full[k.st], k.phase)) return false;
+                    tc_fence_after();
+                    if (elect_one()) issue_scores(s, k, frees_q);
+                    __syncwarp();
+                }
+                return true;
+            };
+            auto first_scores = [&](const int s, bool frees_q) {
+                const Entry k = entry(2 * (base + (PAIR ? 0 : s)));
+                if (!ready(&ctl->full[k.st], k.phase)) return false;
+                tc_fence_after();
+                if (elect_one()) issue_scores(s, k, frees_q);
+                __syncwarp();
+                return true;
+            };
+            ok = first_scores(0, steps0 == 1 && steps1 == 0);
+            if (ok && steps1 > 0) ok = first_scores(1, steps0 == 1);
+            for (int i = 0; i < steps0 && ok; ++i) {
+                ok = advance(0, i, steps0, i + 2 == steps0 && i + 1 >= steps1);
+                if (ok && i < steps1) ok = advance(1, i, steps1, i + 2 == steps0);
             }
-            tc_commit(&ctl->drained);
-            mbar_wait(&ctl->drained, 0, g.timeout_ns);
+            base += nt;
         }
+        if (elect_one()) tc_commit(&ctl->drained);
         __syncwarp();
+        mbar_wait(&ctl->drained, 0, g.timeout_ns);
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -682,19 +709,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float shift = m == -INFINITY ? 0.f : -m * sc;
                     const unsigned long long sc2 = pair_f32(sc, sc), shift2 = pair_f32(shift, shift);
                     unsigned long long sum2[2] = {0ull, 0ull};
+                    // groups of 8 weights: one group's exponentials between the next one's arguments and the last one's sums,
+                    // so that none of them waits for another's latency
+                    unsigned long long x[kTile / 2];
+                    uint32_t w[kTile / 2];
+                    auto arguments = [&](int g8) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t w[16];
+                        for (int u = 4 * g8; u < 4 * g8 + 4; ++u) x[u] = fma_f32x2(pair_u32(v[2 * u], v[2 * u + 1]), sc2, shift2);
+                    };
+                    arguments(0);
+                    arguments(1);
 #pragma unroll
-                        for (int u = 0; u < 16; ++u) {
-                            float a, b;
-                            split_f32(fma_f32x2(pair_u32(v[q * 32 + 2 * u], v[q * 32 + 2 * u + 1]), sc2, shift2), &a, &b);
-                            a = ex2(a);
-                            b = ex2(b);
-                            sum2[u & 1] = add_f32x2(sum2[u & 1], pair_f32(a, b));
-                            w[u] = pack16<BF16>(a, b);
+                    for (int g8 = 0; g8 <= kTile / 8; ++g8) {
+                        if (g8 + 2 < kTile / 8) arguments(g8 + 2);
+                        if (g8 < kTile / 8) {
+#pragma unroll
+                            for (int u = 4 * g8; u < 4 * g8 + 4; ++u) {
+                                float a, b;
+                                split_f32(x[u], &a, &b);
+                                x[u] = pair_f32(ex2(a), ex2(b));
+                            }
                         }
-                        tmem_st_16(t_s + q * 16, w);
+                        if (g8 > 0) {
+#pragma unroll
+                            for (int u = 4 * g8 - 4; u < 4 * g8; ++u) {
+                                float a, b;
+                                split_f32(x[u], &a, &b);
+                                sum2[u & 1] = add_f32x2(sum2[u & 1], x[u]);
+                                w[u] = pack16<BF16>(a, b);
+                            }
+                            if (g8 % 4 == 0) tmem_st_16(t_s + (g8 / 4 - 1) * 16, w + (g8 / 4 - 1) * 16);
+                            if (g8 == kTile / 16) {  // the first half of P is ready for its products
+                                tmem_wait_st();
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&ctl->p_half[s]);
+                            }
+                        }
                     }
                     float sum[4];
                     split_f32(sum2[0], &sum[0], &sum[1]);
@@ -704,7 +755,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->p_ready[s]);
+                if (lane == 0) {
+                    if (!warp_real) mbar_arrive(&ctl->p_half[s]);
+                    mbar_arrive(&ctl->p_ready[s]);
+                }
             }
             base += nt;
             if (!ok) break;
