@@ -299,26 +299,22 @@ struct Control {
     float max_sum[2][2][kTile];  // [stream][maximum, sum][row], one query tile's two streams
 };
 
-template <typename C>
-__device__ __forceinline__ bool wait(C *ctl, uint64_t *bar, uint32_t parity, const CacheView &c, unsigned long long timeout_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_timer_ns();
-    volatile uint32_t *aborted = &ctl->aborted;
-    while (!mbar_try_wait(bar, parity)) {
-        if (*aborted) return false;
-        if (global_timer_ns() - t0 > timeout_ns) {
-            *aborted = 1;
-            atomicOr(c.status, kStatusTimeout);
-            return false;
-        }
-    }
-    return true;
-}
-
-// The same for a whole warp: every lane gets the same answer.
+// A whole warp waits.  The lanes decide together at every turn, so that the warp stays converged: with
+// each lane in a loop of its own the code behind the wait ran in pieces.
 template <typename C>
 __device__ __forceinline__ bool warp_wait(C *ctl, uint64_t *bar, uint32_t parity, const CacheView &c, unsigned long long timeout_ns) {
-    return __all_sync(0xffffffffu, wait(ctl, bar, parity, c, timeout_ns));
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const unsigned long long t0 = global_timer_ns();
+    volatile uint32_t *aborted = &ctl->aborted;
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+        const bool late = global_timer_ns() - t0 > timeout_ns;
+        if (late) {
+            *aborted = 1;
+            atomicOr(c.status, kStatusTimeout);
+        }
+        if (__any_sync(0xffffffffu, late || *aborted)) return false;
+    }
+    return true;
 }
 
 // The next segment, read by one warp.
@@ -546,85 +542,97 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t p_phase = 0;                   // one bit a stream: the phase of its next P
         bool ok = true;
         Segment seg;
-        while (ok && next_segment(ctl, n_seg, &seg, c, g.timeout_ns)) {
-            if (seg.tiles == 0) continue;
-            const int nt = seg.last - seg.first;
-            const int steps0 = PAIR ? nt : (nt + 1) / 2, steps1 = PAIR ? nt : nt / 2;
-            if (!(ok = warp_wait(ctl, &ctl->q_full, n_q & 1, c, g.timeout_ns))) break;
-            ++n_q;
-            // Ring entries and their phases: key tile j of the segment is entry 2 * j, its values the next one.
-            struct Entry {
-                uint32_t st, phase;
-            };
-            auto entry = [&](uint32_t p) {
-                const uint32_t turn = p / S::kStages;
-                return Entry{__shfl_sync(0xffffffffu, p - turn * S::kStages, 0), turn & 1};
-            };
-            auto issue_scores = [&](const int s, const Entry &e, bool last) {
-                const uint64_t a = smem_desc_sw128(q_smem + (PAIR ? s * S::kTileBytes : 0));
-                const uint64_t b = smem_desc_sw128(ring + e.st * S::kTileBytes);
+        // Ring entries and their phases: key tile j of all is entry 2 * j, its values the next one.
+        struct Entry {
+            uint32_t st, phase;
+        };
+        auto entry = [&](uint32_t p) {
+            const uint32_t turn = p / S::kStages;
+            return Entry{__shfl_sync(0xffffffffu, p - turn * S::kStages, 0), turn & 1};
+        };
+        auto ready = [&](uint64_t *bar, uint32_t phase) { return warp_wait(ctl, bar, phase, c, g.timeout_ns); };
+        auto issue_scores = [&](const int s, const Entry &e, bool frees_q) {
+            const uint64_t a = smem_desc_sw128(q_smem + (PAIR ? s * S::kTileBytes : 0));
+            const uint64_t b = smem_desc_sw128(ring + e.st * S::kTileBytes);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t o = static_cast<uint64_t>((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
-                    tc_mma_f16(tmem + s * kTile, a + o, b + o, idesc_s, k != 0);
-                }
-                tc_commit(&ctl->s_full[s]);
-                if (!PAIR || s == 1) tc_commit(&ctl->empty[e.st]);
-                if (last) tc_commit(&ctl->q_empty);  // the segment's last scores free its query tiles
-            };
-            auto issue_values = [&](const int s, const Entry &e, const int k0, bool add) {
-                const uint64_t b = smem_desc_values(ring + e.st * S::kTileBytes);
+            for (int k = 0; k < D / 16; ++k) {
+                const uint64_t o = static_cast<uint64_t>((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
+                tc_mma_f16(tmem + s * kTile, a + o, b + o, idesc_s, k != 0);
+            }
+            tc_commit(&ctl->s_full[s]);
+            if (!PAIR || s == 1) tc_commit(&ctl->empty[e.st]);
+            if (frees_q) tc_commit(&ctl->q_empty);  // the segment's last scores free its query tiles
+        };
+        auto issue_values = [&](const int s, const Entry &e, const int half, bool add) {
+            const uint64_t b = smem_desc_values(ring + e.st * S::kTileBytes);
 #pragma unroll
-                for (int k = k0; k < k0 + kTile / 32; ++k)
-                    tc_mma_f16_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + k * 8, b + ((k * 2048) >> 4), idesc_o, add || k != 0);
-            };
-            auto ready = [&](uint64_t *bar, uint32_t phase) { return warp_wait(ctl, bar, phase, c, g.timeout_ns); };
-            // Step i of stream s: its second product, then the scores of its next key tile.
-            auto advance = [&](const int s, int i, int steps, bool frees_q) {
-                const uint32_t p = 2 * (base + (PAIR ? i : 2 * i + s));
-                const bool more = i + 1 < steps;
-                const Entry v = entry(p + 1), k = entry(p + (PAIR ? 2 : 4));
-                if (!ready(&ctl->full[v.st], v.phase)) return false;
-                // With two query tiles the next keys have long arrived; otherwise they may be on their way, and the values' slot
-                // is wanted back first.
-                if (PAIR && more && !ready(&ctl->full[k.st], k.phase)) return false;
-                if (!ready(&ctl->p_half[s], (p_phase >> s) & 1)) return false;
-                tc_fence_after();
-                if (elect_one()) issue_values(s, v, 0, i != 0);
-                __syncwarp();
-                if (!ready(&ctl->p_ready[s], (p_phase >> s) & 1)) return false;
-                p_phase ^= 1u << s;
-                tc_fence_after();
-                if (elect_one()) {
-                    issue_values(s, v, kTile / 32, true);
-                    if (!PAIR || s == 1) tc_commit(&ctl->empty[v.st]);
-                    if (!more) tc_commit(&ctl->o_full[s]);
-                    if (PAIR && more) issue_scores(s, k, frees_q);
-                }
-                __syncwarp();
-                if (!PAIR && more) {
-                    if (!ready(&ctl->full[k.st], k.phase)) return false;
-                    tc_fence_after();
-                    if (elect_one()) issue_scores(s, k, frees_q);
-                    __syncwarp();
-                }
-                return true;
-            };
-            auto first_scores = [&](const int s, bool frees_q) {
-                const Entry k = entry(2 * (base + (PAIR ? 0 : s)));
+            for (int k = half * (kTile / 32); k < (half + 1) * (kTile / 32); ++k)
+                tc_mma_f16_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + k * 8, b + ((k * 2048) >> 4), idesc_o, add || k != 0);
+        };
+        // One step of stream s: its second product, then the scores of its next key tile.
+        auto advance = [&](const int s, const Entry &v, const Entry &k, bool first, bool more, bool frees_q) {
+            if (!ready(&ctl->p_half[s], (p_phase >> s) & 1)) return false;
+            tc_fence_after();
+            if (elect_one()) issue_values(s, v, 0, !first);
+            __syncwarp();
+            if (!ready(&ctl->p_ready[s], (p_phase >> s) & 1)) return false;
+            p_phase ^= 1u << s;
+            tc_fence_after();
+            if (elect_one()) {
+                issue_values(s, v, 1, true);
+                if (!PAIR || s == 1) tc_commit(&ctl->empty[v.st]);
+                if (!more) tc_commit(&ctl->o_full[s]);
+                if (PAIR && more) issue_scores(s, k, frees_q);
+            }
+            __syncwarp();
+            if (!PAIR && more) {
+                // these keys may be on their way still, and the values' slot was wanted back first
                 if (!ready(&ctl->full[k.st], k.phase)) return false;
                 tc_fence_after();
                 if (elect_one()) issue_scores(s, k, frees_q);
                 __syncwarp();
-                return true;
-            };
-            ok = first_scores(0, steps0 == 1 && steps1 == 0);
-            if (ok && steps1 > 0) ok = first_scores(1, steps0 == 1);
-            for (int i = 0; i < steps0 && ok; ++i) {
-                ok = advance(0, i, steps0, i + 2 == steps0 && i + 1 >= steps1);
-                if (ok && i < steps1) ok = advance(1, i, steps1, i + 2 == steps0);
             }
+            return true;
+        };
+        while (ok && next_segment(ctl, n_seg, &seg, c, g.timeout_ns)) {
+            if (seg.tiles == 0) continue;
+            const int nt = seg.last - seg.first;
+            const int steps0 = PAIR ? nt : (nt + 1) / 2, steps1 = PAIR ? nt : nt / 2;
+            const uint32_t p0 = 2 * base;
             base += nt;
+            if (!(ok = ready(&ctl->q_full, n_q & 1))) break;
+            ++n_q;
+            {
+                const Entry k0 = entry(p0), k1 = PAIR ? k0 : entry(p0 + 2);
+                if (!(ok = ready(&ctl->full[k0.st], k0.phase))) break;
+                tc_fence_after();
+                if (elect_one()) issue_scores(0, k0, steps0 == 1 && steps1 == 0);
+                __syncwarp();
+                if (steps1 > 0) {
+                    if (!PAIR && !(ok = ready(&ctl->full[k1.st], k1.phase))) break;
+                    tc_fence_after();
+                    if (elect_one()) issue_scores(1, k1, steps0 == 1);
+                    __syncwarp();
+                }
+            }
+            for (int i = 0; i < steps0; ++i) {
+                if (PAIR) {
+                    // both streams read the same tiles; the next keys have long arrived when they are looked at
+                    const bool more = i + 1 < nt;
+                    const Entry v = entry(p0 + 2 * i + 1), k = entry(p0 + 2 * i + 2);
+                    if (!(ok = ready(&ctl->full[v.st], v.phase) && (!more || ready(&ctl->full[k.st], k.phase)))) break;
+                    if (!(ok = advance(0, v, k, i == 0, more, false))) break;
+                    if (!(ok = advance(1, v, k, i == 0, more, i + 2 == nt))) break;
+                } else {
+                    const Entry v0 = entry(p0 + 4 * i + 1), k0 = entry(p0 + 4 * i + 4);
+                    if (!(ok = ready(&ctl->full[v0.st], v0.phase))) break;
+                    if (!(ok = advance(0, v0, k0, i == 0, i + 1 < steps0, i + 2 == steps0 && i + 1 >= steps1))) break;
+                    if (i >= steps1) continue;
+                    const Entry v1 = entry(p0 + 4 * i + 3), k1 = entry(p0 + 4 * i + 6);
+                    if (!(ok = ready(&ctl->full[v1.st], v1.phase))) break;
+                    if (!(ok = advance(1, v1, k1, i == 0, i + 1 < steps1, i + 2 == steps0))) break;
+                }
+            }
         }
         if (elect_one()) tc_commit(&ctl->drained);
         __syncwarp();
@@ -674,18 +682,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t v[kTile];
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     const bool edge = __any_sync(0xffffffffu, key0 < see_lo || key0 + kTile > see_hi);
-                    tmem_ld_32(t_s, v);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        tmem_wait_ld();
-                        if (q < 3) tmem_ld_32(t_s + (q + 1) * 32, v + (q + 1) * 32);
-                        if (edge) mask_keys(v + q * 32, key0 + q * 32, see_lo, see_hi);
+                    for (int q = 0; q < 4; ++q) tmem_ld_32(t_s + q * 32, v + q * 32);
+                    tmem_wait_ld();
+                    if (edge) {
 #pragma unroll
-                        for (int u = 0; u < 32; u += 8) {
+                        for (int q = 0; q < 4; ++q) mask_keys(v + q * 32, key0 + q * 32, see_lo, see_hi);
+                    }
 #pragma unroll
-                            for (int w = 0; w < 4; ++w)
-                                top[w] = fmaxf(top[w], fmaxf(__uint_as_float(v[q * 32 + u + 2 * w]), __uint_as_float(v[q * 32 + u + 2 * w + 1])));
-                        }
+                    for (int q = 0; q < kTile; q += 8) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            top[w] = fmaxf(top[w], fmaxf(__uint_as_float(v[q + 2 * w]), __uint_as_float(v[q + 2 * w + 1])));
                     }
                     const float tile_max = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     const bool moves = real && (tile_max - m) * sc > kRescale;  // also from -infinity
@@ -739,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 w[u] = pack16<BF16>(a, b);
                             }
                             if (g8 % 4 == 0) tmem_st_16(t_s + (g8 / 4 - 1) * 16, w + (g8 / 4 - 1) * 16);
-                            if (g8 == kTile / 16) {  // the first half of P is ready for its products
+                            if (g8 == kTile / 16 + 2) {  // by now the first half of P has been written: its products may start
                                 tmem_wait_st();
                                 tc_fence_before();
                                 __syncwarp();
