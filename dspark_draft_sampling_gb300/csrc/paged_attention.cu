@@ -104,14 +104,14 @@ struct Segment {
     int lo, first, last;      // the item's first key tile; the stretch's, relative to it
     int tiles;                // of the whole item; -1: no more segments
     int q0, n, length;        // the sequence's first query token, its new tokens, its tokens
-    int cf, cl;               // first and last block that work on the item
+    long long at;             // the item's place in the sequence of all tiles
 };
 
 // Walks a block's range.
 struct Walk {
     Seq q;
     int s, kv_head, i, n_tiles, step;
-    long long x, left, pos, at;  // x: place within the item; pos: absolute place; at: the last segment's item's
+    long long x, left, pos;  // x: place within the item; pos: absolute place
 
     __device__ __forceinline__ bool next(const CacheView &c, const Attention &g, Segment *out) {
         while (left > 0) {
@@ -139,7 +139,7 @@ struct Walk {
             out->q0 = q.q0;
             out->n = q.n;
             out->length = q.length;
-            at = pos - x;
+            out->at = pos - x;
             const bool starts = x == 0;
             left -= take;
             pos += take;
@@ -151,11 +151,27 @@ struct Walk {
     }
 };
 
-// Where a block's range begins, found by one warp from the sequences' total costs.
+// a / b for a >= 0, b > 0: in 32 bits wherever it fits, as the 64-bit division is a long routine that every block's start would
+// wait for; otherwise an estimate in floating point, corrected until the remainder is right.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    const float inverse = 1.f / static_cast<float>(b);
+    long long q = 0, r = a;
+#pragma unroll 1
+    while (r < 0 || r >= b) {
+        const long long step = max(1ll, static_cast<long long>(static_cast<float>(r < 0 ? -r : r) * inverse));
+        q += r < 0 ? -step : step;
+        r = a - q * b;
+    }
+    return q;
+}
+
+// Where a block's range begins, found by one warp from the sequences' costs.  Every block takes `per` tiles (the last one what is
+// left, blocks behind it none).
 struct Start {
-    long long begin, end, total, before;  // `before`: cost of the sequences before s
-    int s, blocks, kv_head, i;
-    long long x;
+    long long per, begin, end, x;
+    Seq q;
+    int s, kv_head, i;
 };
 
 __device__ __forceinline__ long long warp_sum(long long v) {
@@ -281,6 +297,51 @@ __device__ __forceinline__ uint64_t smem_desc_values(uint32_t addr) {
     return d;
 }
 
+// Block b's part of an item that begins with block cf: in its second slot where the block is the first, else in its first.
+template <int D, int QT>
+__device__ __forceinline__ const float *part_of(const float *parts, int b, int cf) {
+    return parts + (size_t(b) * 2 + (b == cf ? 1 : 0)) * QT * (size_t(kTile) * (D + 2));
+}
+
+// Joins columns c4, c4 + step, ... (of four values each) of one row: COLS columns of PARTS parts are in flight at a time.
+template <bool BF16, int D, int QT, int COLS, int PARTS>
+__device__ __forceinline__ void join_columns(const float *parts, int cf, int cl, int row, int c4, int step, float top, float inv, float sc,
+                                             unsigned short *to) {
+    for (; c4 < D / 4; c4 += COLS * step) {
+        float4 acc[COLS];
+#pragma unroll
+        for (int q = 0; q < COLS; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b0 = cf; b0 <= cl; b0 += PARTS) {
+            float w[PARTS];
+            float4 o[PARTS][COLS];
+#pragma unroll
+            for (int u = 0; u < PARTS; ++u) {  // behind the last part: the last one again, with weight 0
+                const float *p = part_of<D, QT>(parts, min(b0 + u, cl), cf);
+                w[u] = b0 + u <= cl ? __ldcg(p + size_t(kTile) * D + row) : -INFINITY;
+#pragma unroll
+                for (int q = 0; q < COLS; ++q)
+                    o[u][q] = __ldcg(reinterpret_cast<const float4 *>(p) + min(c4 + q * step, D / 4 - 1) * kTile + row);
+            }
+#pragma unroll
+            for (int u = 0; u < PARTS; ++u) {
+                const float k = w[u] == -INFINITY ? 0.f : ex2((w[u] - top) * sc);  // a part that saw nothing holds zeros
+#pragma unroll
+                for (int q = 0; q < COLS; ++q) {
+                    acc[q].x += o[u][q].x * k;
+                    acc[q].y += o[u][q].y * k;
+                    acc[q].z += o[u][q].z * k;
+                    acc[q].w += o[u][q].w * k;
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < COLS; ++q)
+            if (c4 + q * step < D / 4)
+                *reinterpret_cast<uint2 *>(to + (c4 + q * step) * 4) =
+                    make_uint2(pack16<BF16>(acc[q].x * inv, acc[q].y * inv), pack16<BF16>(acc[q].z * inv, acc[q].w * inv));
+    }
+}
+
 constexpr int kSegments = 4;  // segments handed over ahead
 
 // Barriers and small state behind the data area.
@@ -340,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(sizeof(C) <= kSmemBytes - kSmemData, "control block does not fit");
     const uint32_t q_smem = smem_addr(smem), ring = q_smem + S::QT * S::kTileBytes;
     unsigned char *ring_ptr = smem + S::QT * S::kTileBytes;
-    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int warp = (__shfl_sync(0xffffffffu, threadIdx.x >> 5, 0) + 8) % 12, lane = threadIdx.x & 31;
     const int step = g.tile_tokens * S::QT;  // tokens of an item
 
     if (warp == 8 && lane == 0) {
@@ -382,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     key_tiles(g, q, i, step, &lo, &hi);
                     w += kItemCost + hi - lo;
                 }
-                cost[s] = w * c.kv_heads;
+                cost[s] = w;
             }
         } else {
             for (int s = warp; s < g.n_seqs; s += kThreads / 32) {
@@ -394,39 +455,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                     w += kItemCost + hi - lo;
                 }
                 w = warp_sum(w);
-                if (lane == 0) cost[s] = w * c.kv_heads;
+                if (lane == 0) cost[s] = w;
             }
         }
         __syncthreads();
         if (warp == 0) {
             long long total = 0;
             for (int s = lane; s < g.n_seqs; s += 32) total += cost[s];
-            total = warp_sum(total);
-            const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-            const int b = blockIdx.x;
+            total = warp_sum(total) * c.kv_heads;
             Start st{};
-            st.total = total;
-            st.blocks = blocks;
-            if (b < blocks) {
-                st.begin = total * b / blocks;
-                st.end = total * (b + 1) / blocks;
+            st.per = divide(total + gridDim.x - 1, gridDim.x);
+            st.begin = min(st.per * blockIdx.x, total);
+            st.end = min(st.begin + st.per, total);
+            if (st.begin < st.end) {
                 long long before = 0;
                 for (int s0 = 0; s0 < g.n_seqs; s0 += 32) {
-                    const long long v = s0 + lane < g.n_seqs ? cost[s0 + lane] : 0;
+                    const long long v = s0 + lane < g.n_seqs ? cost[s0 + lane] * c.kv_heads : 0;
                     const long long upto = before + warp_scan(v, lane);
                     const unsigned past = __ballot_sync(0xffffffffu, upto > st.begin);
                     if (past) {
                         const int l = __ffs(past) - 1;
                         st.s = s0 + l;
-                        st.before = __shfl_sync(0xffffffffu, upto - v, l);
+                        before = __shfl_sync(0xffffffffu, upto - v, l);
                         break;
                     }
                     before = __shfl_sync(0xffffffffu, upto, 31);
                 }
                 const Seq q = load_seq(c, g, st.s);
-                const long long w = cost[st.s] / c.kv_heads;
-                st.kv_head = static_cast<int>((st.begin - st.before) / w);
-                long long rem = st.begin - st.before - st.kv_head * w;
+                st.q = q;
+                const long long w = cost[st.s];
+                st.kv_head = static_cast<int>(divide(st.begin - before, w));
+                long long rem = st.begin - before - st.kv_head * w;
                 for (int i0 = 0;; i0 += 32) {  // the item that holds the range's first tile
                     long long v = 0;
                     if ((i0 + lane) * step < q.n) {
@@ -463,9 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Start st = ctl->start;
         Walk walk;
         walk.left = 0;
-        if (static_cast<int>(blockIdx.x) < st.blocks) {
+        if (st.begin < st.end) {
             walk.s = st.s;
-            walk.q = load_seq(c, g, st.s);
+            walk.q = st.q;
             walk.kv_head = st.kv_head;
             walk.i = st.i;
             walk.step = step;
@@ -483,10 +542,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n_seg >= kSegments && !(ok = warp_wait(ctl, &ctl->seg_empty[entry], ((n_seg / kSegments) & 1) ^ 1, c, g.timeout_ns))) break;
             ++n_seg;
             if (lane == 0) {
-                if (more && (seg.first != 0 || seg.last != seg.tiles)) {
-                    seg.cf = static_cast<int>(((walk.at + kItemCost + 1) * st.blocks - 1) / st.total);
-                    seg.cl = static_cast<int>(((walk.at + kItemCost + seg.tiles) * st.blocks - 1) / st.total);
-                }
                 ctl->segs[entry] = seg;
                 mbar_arrive(&ctl->seg_full[entry]);
             }
@@ -648,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row_token = r / g.group, row_head = r - row_token * g.group;
         uint32_t n_s = 0, n_seg = 0, n_o0 = 0, n_o1 = 0, n_sync = 0, base = 0;
         bool ok = true;
-        if (g.stall_ns && !mbar_wait(&ctl->never, 0, g.stall_ns) && threadIdx.x == 0) atomicOr(c.status, kStatusTimeout);
+        if (g.stall_ns && !mbar_wait(&ctl->never, 0, g.stall_ns) && warp == 0 && lane == 0) atomicOr(c.status, kStatusTimeout);
         Segment seg;
         while (ok && next_segment(ctl, n_seg, &seg, c, g.timeout_ns)) {
             const int nt = seg.last - seg.first;
@@ -802,8 +857,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             int cf = 0, cl = 0;
             float *slot = nullptr;
             if (!whole) {
-                cf = seg.cf;
-                cl = seg.cl;
+                const long long per = ctl->start.per;
+                cf = cl = blockIdx.x;
+                if (seg.first != 0) cf = static_cast<int>(divide(seg.at + kItemCost, per));
+                if (seg.last != seg.tiles) cl = static_cast<int>(divide(seg.at + kItemCost + seg.tiles - 1, per));
                 const size_t index = (size_t(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == cf ? 1 : 0)) * S::QT + (PAIR ? s : 0);
                 slot = g.partials + index * S::kSlotFloats;
             }
@@ -873,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(sync);
             if (!(ok = warp_wait(ctl, sync, n_sync & 1, c, g.timeout_ns))) break;
             ++n_sync;
-            if (PAIR ? r == 0 : threadIdx.x == 0) {
+            if (r == 0 && (PAIR || s == 0)) {
                 unsigned *count = g.arrivals + cf * 2 + (PAIR ? s : 0);
                 const unsigned before = atomicAdd(count, 1u);
                 const bool is_last = before == static_cast<unsigned>(cl - cf);
@@ -888,44 +945,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int first_token = seg.tile * step + (PAIR ? s * g.tile_tokens : 0);
             const int rows = min(g.tile_tokens, seg.n - first_token) * g.group;  // may be <= 0: the second tile of a pair
             const float *parts = g.partials + (PAIR ? s : 0) * S::kSlotFloats;
-            for (int e = PAIR ? r : static_cast<int>(threadIdx.x); e < rows * (D / 4); e += PAIR ? 128 : 256) {
-                const int c4 = e / rows, row = e - c4 * rows;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                float top = -INFINITY, z = 0.f;
-                constexpr int kBatch = 8;
-                for (int b0 = cf; b0 <= cl; b0 += kBatch) {
-                    float pm[kBatch], pl[kBatch];
-                    float4 po[kBatch];
+            // A thread keeps to one row and takes its columns, four at a time, in strides.
+            constexpr int kJoiners = PAIR ? 128 : 256;
+            const int shift = rows > 1 ? 32 - __clz(rows - 1) : 0, joiner = PAIR ? r : s * kTile + r;
+            const int my_row = joiner & ((1 << shift) - 1), c4_step = kJoiners >> shift;
+            const int row = min(my_row, rows - 1);  // the threads beyond the rows only load
+            if (rows <= 0) continue;
+            float top = -INFINITY, z = 0.f;
+            for (int b0 = cf; b0 <= cl; b0 += 8) {
+                float pm[8], pl[8];
 #pragma unroll
-                    for (int u = 0; u < kBatch; ++u) {
-                        const int b = min(b0 + u, cl);
-                        const float *p = parts + (size_t(b) * 2 + (b == cf ? 1 : 0)) * S::QT * S::kSlotFloats;
-                        pm[u] = __ldcg(p + size_t(kTile) * D + row);
-                        pl[u] = __ldcg(p + size_t(kTile) * (D + 1) + row);
-                        po[u] = __ldcg(reinterpret_cast<const float4 *>(p) + c4 * kTile + row);
-                    }
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u) {
-                        if (b0 + u > cl) continue;
-                        const float up = fmaxf(top, pm[u]);
-                        const float ka = top == -INFINITY ? 0.f : ex2((top - up) * sc);
-                        const float kb = pm[u] == -INFINITY ? 0.f : ex2((pm[u] - up) * sc);
-                        acc.x = acc.x * ka + po[u].x * kb;
-                        acc.y = acc.y * ka + po[u].y * kb;
-                        acc.z = acc.z * ka + po[u].z * kb;
-                        acc.w = acc.w * ka + po[u].w * kb;
-                        z = z * ka + pl[u] * kb;
-                        top = up;
+                for (int u = 0; u < 8; ++u) {
+                    pm[u] = -INFINITY, pl[u] = 0.f;
+                    if (b0 + u <= cl) {
+                        pm[u] = __ldcg(part_of<D, S::QT>(parts, b0 + u, cf) + size_t(kTile) * D + row);
+                        pl[u] = __ldcg(part_of<D, S::QT>(parts, b0 + u, cf) + size_t(kTile) * (D + 1) + row);
                     }
                 }
-                const int tk = row / g.group, hd = seg.kv_head * g.group + row - tk * g.group;
-                const long long qt = seg.q0 + first_token + tk;
-                const float f = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
-                unsigned short *o = static_cast<unsigned short *>(g.out) + qt * g.out_token + hd * g.out_head + c4 * 4;
-                *reinterpret_cast<uint2 *>(o) = make_uint2(pack16<BF16>(acc.x * f, acc.y * f), pack16<BF16>(acc.z * f, acc.w * f));
-                if (c4 == 0 && g.lse)
-                    g.lse[qt * (c.kv_heads * g.group) + hd] = z == 0.f ? -INFINITY : (top * sc + lg2(z)) * 0.6931471805599453f;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float up = fmaxf(top, pm[u]);
+                    z = z * (top == -INFINITY ? 0.f : ex2((top - up) * sc)) + pl[u] * (pm[u] == -INFINITY ? 0.f : ex2((pm[u] - up) * sc));
+                    top = up;
+                }
             }
+            const int tk = row / g.group, hd = seg.kv_head * g.group + row - tk * g.group;
+            const long long qt = seg.q0 + first_token + tk;
+            const float f = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
+            unsigned short *to = static_cast<unsigned short *>(g.out) + qt * g.out_token + hd * g.out_head;
+            if (g.lse && (joiner >> shift) == 0 && my_row == row)
+                g.lse[qt * (c.kv_heads * g.group) + hd] = z == 0.f ? -INFINITY : (top * sc + lg2(z)) * 0.6931471805599453f;
+            const int c4 = my_row == row ? joiner >> shift : D / 4;
+            if (c4_step * 4 <= D / 4)
+                join_columns<BF16, D, S::QT, 4, 2>(parts, cf, cl, row, c4, c4_step, top, f, sc, to);
+            else
+                join_columns<BF16, D, S::QT, 1, 8>(parts, cf, cl, row, c4, c4_step, top, f, sc, to);
         }
     }
     tc_fence_before();
