@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 import time
 
@@ -24,7 +25,7 @@ DSPARK_ERR_CUDA, DSPARK_ERR_TIMEOUT, DSPARK_ERR_INDEX, DSPARK_ERR_CAPACITY = 3, 
 
 # Every symbol the header declares, with (restype, argtypes).
 _P, _I, _U, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_float, ctypes.c_size_t
-_L = ctypes.c_longlong
+_S = ctypes.c_char_p  # a struct, packed into bytes
 SIGNATURES = {
     "dspark_last_error": (ctypes.c_char_p, []),
     "dspark_version": (ctypes.c_char_p, []),
@@ -79,12 +80,10 @@ SIGNATURES = {
     "dspark_cache_free": (_I, [_P, _P, _I, _P]),
     "dspark_cache_copy_pages": (_I, [_P, _P, _P, _I, _P]),
     "dspark_cache_status": (_I, [_P, _P]),
-    "dspark_rotary": (_I, [_P, _L, _L, _P, _L, _L, _I, _I, _I, _I, _P, _P, _I, _I, _F, _I, _P]),
-    "dspark_rotary_append": (_I, [_P, _I, _P, _L, _L, _P, _L, _L, _P, _L, _L, _P, _L, _L, _I, _I, _P, _P, _I, _P, _P,
-                                  _I, _I, _F, _P]),
-    "dspark_paged_attention": (_I, [_P, _I, _P, _L, _L, _I, _I, _P, _P, _I, _I, _I, _I, _F, _P, _L, _L, _P, _P]),
-    "dspark_paged_attention_debug": (_I, [_P, _I, _P, _L, _L, _I, _I, _P, _P, _I, _I, _I, _I, _F, _P, _L, _L, _P, _U,
-                                          _P]),
+    "dspark_rotary": (_I, [_S, _P]),
+    "dspark_rotary_append": (_I, [_P, _S, _P]),
+    "dspark_paged_attention": (_I, [_P, _S, _P]),
+    "dspark_paged_attention_debug": (_I, [_P, _S, _U, _P]),
 }
 
 _lock = threading.Lock()
@@ -820,16 +819,22 @@ def _ints(t, name: str, n=None, *, dtype=torch.int32):
     return t.data_ptr()
 
 
-def _heads(t, name: str, dtype, head_dim=None):
-    """Address and token and head strides of a CUDA tensor [tokens, heads, head_dim] with a contiguous last axis."""
+# The argument structs of dspark.h as their bytes: packing them costs a fraction of converting as many ctypes arguments.
+_ROTARY_ARGS = struct.Struct("@4P4q7if")
+_APPEND_ARGS = struct.Struct("@8P8q6if4x")
+_ATTENTION_ARGS = struct.Struct("@5P4q7if")
+
+
+def _heads(t, name: str, dtype, shape=None):
+    """Token and head strides of a CUDA tensor [tokens, heads, head_dim] with a contiguous last axis."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or t.dim() != 3:
         raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, head_dim] of {dtype}")
-    if head_dim is not None and t.shape[2] != head_dim:
-        raise ValueError(f"{name} has head_dim {t.shape[2]}, expected {head_dim}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     a, b, c = t.stride()
     if c != 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    return t.data_ptr(), a, b
+    return a, b
 
 
 CACHE_HEADER_BYTES = 2048  # the part of a cache's workspace that has to be zero before its first use
@@ -987,16 +992,19 @@ def rotary(x, positions, table: RotaryTable, *, backward: bool = False, out=None
     lib = load_library()
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
         raise ValueError("x must be an fp16, bf16 or fp32 tensor")
-    p, a, b = _heads(x, "x", x.dtype)
+    a, b = _heads(x, "x", x.dtype)
+    shape = x.shape
     if out is None:
-        out = x.new_empty(x.shape)
-    elif out.shape != x.shape:
-        raise ValueError("out must have the shape of x")
-    po, ao, bo = _heads(out, "out", x.dtype)
-    tokens, heads, dim = x.shape
-    _check(lib, lib.dspark_rotary(p, a, b, po, ao, bo, _DTYPES[x.dtype], tokens, heads, dim,
-                                  _ints(positions, "positions", tokens), *table._args, 1 if backward else 0,
-                                  _raw_stream(stream, x.device)))
+        out = torch.empty_like(x)
+    ao, bo = _heads(out, "out", x.dtype, shape)
+    tokens, heads, dim = shape
+    turns, rotary_dim, layout, amplitude = table._args
+    status = lib.dspark_rotary(
+        _ROTARY_ARGS.pack(x.data_ptr(), out.data_ptr(), _ints(positions, "positions", tokens), turns, a, b, ao, bo,
+                          _DTYPES[x.dtype], tokens, heads, dim, rotary_dim, layout, 1 if backward else 0, amplitude),
+        _raw_stream(stream, x.device))
+    if status:
+        _check(lib, status)
     return out
 
 
@@ -1008,23 +1016,29 @@ def rotary_append(q, k, v, cache: PagedCache, layer: int, cu_new, table: RotaryT
     the cache (None: the same number); positions int32 [tokens]: where the angle's position is not the place in the
     cache.  out may be q."""
     lib = cache._lib
-    dtype, dim = cache.dtype, cache.head_dim
-    qp, qa, qb = _heads(q, "q", dtype, dim)
-    kp, ka, kb = _heads(k, "k", dtype, dim)
-    vp, va, vb = _heads(v, "v", dtype, dim)
-    tokens, q_heads = q.shape[0], q.shape[1]
-    if k.shape[0] != tokens or v.shape[0] != tokens or k.shape[1] != cache.kv_heads or v.shape[1] != cache.kv_heads:
-        raise ValueError("k and v must be [tokens of q, the cache's kv_heads, head_dim]")
+    dtype = cache.dtype
+    qa, qb = _heads(q, "q", dtype)
+    shape = q.shape
+    tokens, q_heads, dim = shape
+    if dim != cache.head_dim:
+        raise ValueError(f"q has head_dim {dim}, the cache {cache.head_dim}")
+    kv_shape = (tokens, cache.kv_heads, dim)
+    ka, kb = _heads(k, "k", dtype, kv_shape)
+    va, vb = _heads(v, "v", dtype, kv_shape)
     if out is None:
-        out = q.new_empty(q.shape)
-    elif out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    op, oa, ob = _heads(out, "out", dtype, dim)
+        out = torch.empty_like(q)
+    oa, ob = _heads(out, "out", dtype, shape)
     seqs = cu_new.numel() - 1
-    _check(lib, lib.dspark_rotary_append(cache._ref, layer, qp, qa, qb, kp, ka, kb, vp, va, vb, op, oa, ob, tokens, q_heads,
-                                         None if rows is None else _ints(rows, "rows", seqs), _ints(cu_new, "cu_new"), seqs,
-                                         None if positions is None else _ints(positions, "positions", tokens),
-                                         *table._args, _raw_stream(stream, cache.device)))
+    turns, rotary_dim, layout, amplitude = table._args
+    status = lib.dspark_rotary_append(
+        cache._ref,
+        _APPEND_ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                          0 if rows is None else _ints(rows, "rows", seqs), _ints(cu_new, "cu_new"),
+                          0 if positions is None else _ints(positions, "positions", tokens), turns, qa, qb, ka, kb, va, vb,
+                          oa, ob, layer, tokens, q_heads, seqs, rotary_dim, layout, amplitude),
+        _raw_stream(stream, cache.device))
+    if status:
+        _check(lib, status)
     return out
 
 
@@ -1035,21 +1049,26 @@ def paged_attention(q, cache: PagedCache, layer: int, cu_new, *, rows=None, max_
     causal=False lets a chunk's tokens see each other; window > 0: only the last window keys; scale: of the scores
     (None: 1 / sqrt(head_dim)).  Returns out, or (out, lse fp32 [tokens, q_heads]) with return_lse."""
     lib = cache._lib
-    dim = cache.head_dim
-    qp, qa, qb = _heads(q, "q", cache.dtype, dim)
-    tokens, q_heads = q.shape[0], q.shape[1]
+    dtype = cache.dtype
+    qa, qb = _heads(q, "q", dtype)
+    shape = q.shape
+    tokens, q_heads, dim = shape
+    if dim != cache.head_dim:
+        raise ValueError(f"q has head_dim {dim}, the cache {cache.head_dim}")
     if out is None:
-        out = q.new_empty(q.shape)
-    elif out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    op, oa, ob = _heads(out, "out", cache.dtype, dim)
+        out = torch.empty_like(q)
+    oa, ob = _heads(out, "out", dtype, shape)
     if lse is None and return_lse:
         lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=cache.device)
     seqs = cu_new.numel() - 1
-    _check(lib, lib.dspark_paged_attention(
-        cache._ref, layer, qp, qa, qb, tokens, q_heads, None if rows is None else _ints(rows, "rows", seqs),
-        _ints(cu_new, "cu_new"), seqs, tokens if max_new is None else max_new, 1 if causal else 0, window,
-        dim ** -0.5 if scale is None else scale, op, oa, ob,
-        None if lse is None else _ints(lse, "lse", tokens * q_heads, dtype=torch.float32),
-        _raw_stream(stream, cache.device)))
+    status = lib.dspark_paged_attention(
+        cache._ref,
+        _ATTENTION_ARGS.pack(q.data_ptr(), out.data_ptr(),
+                             0 if lse is None else _ints(lse, "lse", tokens * q_heads, dtype=torch.float32),
+                             0 if rows is None else _ints(rows, "rows", seqs), _ints(cu_new, "cu_new"), qa, qb, oa, ob, layer,
+                             tokens, q_heads, seqs, tokens if max_new is None else max_new, 1 if causal else 0, window,
+                             dim ** -0.5 if scale is None else scale),
+        _raw_stream(stream, cache.device))
+    if status:
+        _check(lib, status)
     return (out, lse) if return_lse else out

@@ -1,12 +1,14 @@
 // Page operations of the paged cache: allocate (extend), fork, compact, free, copy.
 //
-// A call's bookkeeping is decided by one thread block, so that it is all or nothing and the
-// lowest-numbered free pages are taken in a fixed order: it checks the arguments, counts the
-// pages each row needs, adds the counts up (a scan over the rows), finds that many free pages
-// (a scan over refs) and only then changes table, length and refs.  Counts are changed by integer
-// atomics, whose order does not change the sums.  Tokens are moved by a second kernel that reads
-// what the first one decided.
+// A call's bookkeeping is all or nothing, and the lowest-numbered free pages are taken in a fixed order: the
+// arguments are checked, the pages each row needs are counted and added up (a scan over the rows), the free pages are
+// counted (a scan over refs), and only then table, length and refs change.  One cluster of eight thread blocks does
+// it: each block looks at an eighth of refs and keeps what it found in registers, so refs is read once; the blocks exchange
+// their counts, and a free page's number among all free ones says which row takes it (a search in the rows' running
+// sums).  Counts are changed by integer atomics, whose order does not change the sums.  Tokens are moved by a second kernel
+// that reads what the first one decided.
 #include "kv_cache.cuh"
+#include "tc.cuh"
 
 namespace dspark {
 
@@ -17,13 +19,21 @@ constexpr int kShared = 1 << 30;  // flag in a snapshot entry: the page was shar
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Scratch area of the page operations: fresh pages, then the snapshot of the rows' old tables.
-__device__ __forceinline__ int *scratch_fresh(const CacheView &c) { return reinterpret_cast<int *>(c.scratch); }
-__host__ __device__ inline size_t fresh_entries(int max_seqs, int max_pages) {
-    return size_t(max_seqs < kMaxRows ? max_seqs : kMaxRows) * max_pages;
+constexpr int kBooksBlocks = 8;  // of one cluster
+
+// Scratch area of the page operations: the rows' own new pages' count (compact), then the snapshot of the rows' old tables.
+__device__ __forceinline__ int *scratch_need(const CacheView &c) { return reinterpret_cast<int *>(c.scratch); }
+__device__ __forceinline__ int *scratch_snapshot(const CacheView &c) { return scratch_need(c) + kMaxRows; }
+size_t snapshot_entries(int max_seqs, int max_pages) { return size_t(max_seqs < kMaxRows ? max_seqs : kMaxRows) * max_pages; }
+
+__device__ __forceinline__ int cluster_block() {
+    unsigned r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return static_cast<int>(r);
 }
-__device__ __forceinline__ int *scratch_snapshot(const CacheView &c) {
-    return scratch_fresh(c) + fresh_entries(c.max_seqs, c.max_pages);
+// Every thread of the cluster; orders their memory accesses.
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ bool page_ok(const CacheView &c, int page) {
@@ -65,49 +75,124 @@ __device__ int block_scan(int v, int *total, int *warp_sums) {
     return x - v + (warp ? warp_sums[warp - 1] : 0);
 }
 
-// The `want` lowest-numbered free pages, ascending, to out[0..want); false if there are fewer.
-__device__ bool find_free(const CacheView &c, int want, int *out, int *warp_sums) {
-    constexpr int kPer = 16;
-    int found = 0;
-    for (int base = 0; base < c.num_pages && found < want; base += kBooksThreads * kPer) {
-        const int p0 = base + static_cast<int>(threadIdx.x) * kPer;
-        unsigned free = 0;
-        if (p0 + kPer <= c.num_pages) {
-            const int4 *r = reinterpret_cast<const int4 *>(c.refs + p0);
-#pragma unroll
-            for (int q = 0; q < kPer / 4; ++q) {
-                const int4 v = r[q];
-                free |= (unsigned(v.x == 0) | unsigned(v.y == 0) << 1 | unsigned(v.z == 0) << 2 | unsigned(v.w == 0) << 3)
-                        << (4 * q);
-            }
-        } else {
-            for (int q = 0; q < kPer && p0 + q < c.num_pages; ++q) free |= unsigned(c.refs[p0 + q] == 0) << q;
-        }
-        int total = 0;
-        int at = found + block_scan(__popc(free), &total, warp_sums);
-        while (free && at < want) {
-            out[at++] = p0 + __ffs(free) - 1;
-            free &= free - 1;
-        }
-        found += total;
-    }
-    __syncthreads();
-    return found >= want;
+// The free pages among refs, kept by the threads that found them: thread t of block b holds the 16 pages from
+// (b * rounds + i) * 16384 + 16 t on for each round i of its block, the first kHeld rounds in registers, those of larger pools
+// in the scratch area (refs may have changed by the time they are wanted).
+constexpr int kPer = 16, kHeld = 4;
+
+__device__ __forceinline__ unsigned short *scratch_bits(const CacheView &c) {
+    return reinterpret_cast<unsigned short *>(scratch_snapshot(c) + size_t(c.max_seqs < kMaxRows ? c.max_seqs : kMaxRows) * c.max_pages);
+}
+__host__ __device__ inline int free_rounds(int num_pages) {
+    constexpr int kRound = kBooksBlocks * kBooksThreads * kPer;
+    return (num_pages + kRound - 1) / kRound;
 }
 
-// Whether the call goes ahead; records why not.
+struct FreePages {
+    unsigned held[kHeld];  // bits of free pages
+    int rounds, before, count;  // rounds of a block; free pages in earlier threads of the cluster (set by number()), in all
+};
+
+__device__ __forceinline__ unsigned free_bits(const CacheView &c, long long first) {
+    unsigned bits = 0;
+    if (first + kPer <= c.num_pages) {
+        const int4 *r = reinterpret_cast<const int4 *>(c.refs + first);
+#pragma unroll
+        for (int q = 0; q < kPer / 4; ++q) {
+            const int4 v = r[q];
+            bits |= (unsigned(v.x == 0) | unsigned(v.y == 0) << 1 | unsigned(v.z == 0) << 2 | unsigned(v.w == 0) << 3) << (4 * q);
+        }
+    } else {
+        for (int q = 0; q < kPer && first + q < c.num_pages; ++q) bits |= unsigned(c.refs[first + q] == 0) << q;
+    }
+    return bits;
+}
+
+__device__ __forceinline__ long long free_first(const FreePages &f, int round) {
+    return (static_cast<long long>(cluster_block()) * f.rounds + round) * (kBooksThreads * kPer) + threadIdx.x * kPer;
+}
+
+// Counts the free pages of the cluster's blocks; block counts are exchanged through `counts` in every block's shared memory.
+// Ends with a cluster barrier: refs may be changed after it.
+__device__ void find_free(const CacheView &c, FreePages *f, int *counts, int *warp_sums) {
+    f->rounds = free_rounds(c.num_pages);
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        f->held[i] = i < f->rounds ? free_bits(c, free_first(*f, i)) : 0;
+        mine += __popc(f->held[i]);
+    }
+    for (int i = kHeld; i < f->rounds; ++i) {
+        const unsigned bits = free_bits(c, free_first(*f, i));
+        scratch_bits(c)[free_first(*f, i) / kPer] = static_cast<unsigned short>(bits);
+        mine += __popc(bits);
+    }
+    int total = 0;
+    block_scan(mine, &total, warp_sums);
+    if (threadIdx.x < kBooksBlocks) {
+        uint32_t at = smem_addr(counts + cluster_block()), there;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(threadIdx.x));
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there), "r"(total) : "memory");
+    }
+    cluster_barrier();
+    f->before = f->count = 0;
+    for (int b = 0; b < kBooksBlocks; ++b) {
+        if (b < cluster_block()) f->before += counts[b];
+        f->count += counts[b];
+    }
+}
+
+// Calls give(number, page) for the free pages below `want`, numbered from the lowest.
+template <typename Give>
+__device__ void give_free(const CacheView &c, const FreePages &f, int want, int *warp_sums, Give give) {
+    int at = f.before;
+    for (int i = 0; i < f.rounds && at < want; ++i) {  // the same number of turns for the whole block
+        unsigned bits = 0;
+#pragma unroll
+        for (int q = 0; q < kHeld; ++q)
+            if (i == q) bits = f.held[q];
+        if (i >= kHeld) bits = scratch_bits(c)[free_first(f, i) / kPer];
+        int total = 0, n = at + block_scan(__popc(bits), &total, warp_sums);
+        const int first = static_cast<int>(free_first(f, i));
+        while (bits && n < want) {
+            give(n++, first + __ffs(bits) - 1);
+            bits &= bits - 1;
+        }
+        at += total;
+    }
+}
+
+// The row whose running sum of needs holds number k: the last r of n with at[r] <= k.
+__device__ __forceinline__ int row_of(const int *at, int n, int k) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (at[mid] <= k) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Whether the call goes ahead; the first block records why not.  Every block comes to the same answer.
 __device__ bool decide(const CacheView &c, bool bad_index, bool full) {
     const int bits = (bad_index ? kStatusIndex : 0) | (full ? kStatusCapacity : 0);
     const bool go = !__syncthreads_or(bits);
-    if (bits) atomicOr(c.status, static_cast<unsigned>(bits));
-    if (threadIdx.x == 0) c.status[1] = go ? 1u : 0u;
+    if (cluster_block() == 0) {
+        if (bits) atomicOr(c.status, static_cast<unsigned>(bits));
+        if (threadIdx.x == 0) c.status[1] = go ? 1u : 0u;
+    }
     return go;
 }
 
-__global__ void __launch_bounds__(kBooksThreads) extend_kernel(CacheView c, const int *rows, const int *counts, int n) {
-    __shared__ int warp_sums[32];
-    __shared__ int s_row[kMaxRows], s_first[kMaxRows], s_need[kMaxRows], s_at[kMaxRows];
+__global__ void __cluster_dims__(kBooksBlocks, 1, 1) __launch_bounds__(kBooksThreads, 1)
+    extend_kernel(CacheView c, const int *rows, const int *counts, int n) {
+    __shared__ int warp_sums[32], block_counts[kBooksBlocks];
+    __shared__ int s_row[kMaxRows], s_first[kMaxRows], s_at[kMaxRows];
+    pdl_launch_dependents();
+    cluster_barrier();  // every block has started: its shared memory can be written to
+    pdl_wait();
     const int i = threadIdx.x;
+    FreePages free;
     bool bad = false, full = false;
     int row = 0, old = 0, grown = 0, need = 0;
     if (i < n) {
@@ -126,22 +211,22 @@ __global__ void __launch_bounds__(kBooksThreads) extend_kernel(CacheView c, cons
     }
     int total = 0;
     const int at = block_scan(need, &total, warp_sums);
-    if (i < n) s_row[i] = row, s_first[i] = pages_of(c, old), s_need[i] = need, s_at[i] = at;
-    int *fresh = scratch_fresh(c);
-    const bool enough = total <= c.num_pages && find_free(c, total, fresh, warp_sums);
-    if (!decide(c, bad, full || !enough)) return;
-    if (i < n) c.length[row] = grown;
-    for (int r = i >> 5; r < n; r += kBooksThreads / 32) {
-        int *t = c.table + size_t(s_row[r]) * c.max_pages + s_first[r];
-        for (int j = i & 31; j < s_need[r]; j += 32) {
-            const int page = fresh[s_at[r] + j];
-            t[j] = page;
-            c.refs[page] = 1;
-        }
-    }
+    // rows are at most max_pages each and n at most 1024, but the sum may pass 32 bits: then some prefix does not fit the pool either
+    const bool huge = __syncthreads_or(at < 0 || at > c.num_pages || total < 0);
+    if (i < n) s_row[i] = row, s_first[i] = pages_of(c, old), s_at[i] = at;
+    find_free(c, &free, block_counts, warp_sums);
+    if (!decide(c, bad, full || huge || total > free.count)) return;
+    if (i < n && cluster_block() == 0) c.length[row] = grown;
+    give_free(c, free, total, warp_sums, [&](int k, int page) {
+        const int r = row_of(s_at, n, k);
+        c.table[size_t(s_row[r]) * c.max_pages + s_first[r] + k - s_at[r]] = page;
+        c.refs[page] = 1;
+    });
 }
 
 __global__ void __launch_bounds__(256) free_kernel(CacheView c, const int *rows, int n) {
+    pdl_launch_dependents();
+    pdl_wait();
     bool bad = false;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const int row = rows[i];
@@ -164,11 +249,16 @@ __global__ void __launch_bounds__(256) free_kernel(CacheView c, const int *rows,
     }
 }
 
-__global__ void __launch_bounds__(kBooksThreads) fork_books_kernel(CacheView c, const int *src, const int *dst, int n) {
-    __shared__ int warp_sums[32];
+__global__ void __cluster_dims__(kBooksBlocks, 1, 1) __launch_bounds__(kBooksThreads, 1)
+    fork_books_kernel(CacheView c, const int *src, const int *dst, int n) {
+    __shared__ int warp_sums[32], block_counts[kBooksBlocks];
     __shared__ int s_src[kMaxRows], s_dst[kMaxRows], s_at[kMaxRows];
     __shared__ int s_len[kMaxRows], s_old[kMaxRows];  // tokens of the source, and of the target before
+    pdl_launch_dependents();
+    cluster_barrier();
+    pdl_wait();
     const int i = threadIdx.x;
+    FreePages free;
     bool bad = false;
     int s = 0, d = 0, len = 0, old = 0;
     if (i < n) {
@@ -185,11 +275,11 @@ __global__ void __launch_bounds__(kBooksThreads) fork_books_kernel(CacheView c, 
     int total = 0;
     const int at = block_scan(need, &total, warp_sums);
     if (i < n) s_src[i] = s, s_dst[i] = d, s_len[i] = len, s_old[i] = old, s_at[i] = at;
-    int *fresh = scratch_fresh(c), *snap = scratch_snapshot(c);
-    const bool enough = total <= c.num_pages && find_free(c, total, fresh, warp_sums);
-    if (!decide(c, bad, !enough)) return;
-    const int lane = i & 31;
-    for (int r = i >> 5; r < n; r += kBooksThreads / 32) {
+    find_free(c, &free, block_counts, warp_sums);  // the lengths have been read by every block
+    if (!decide(c, bad, total > free.count)) return;
+    int *snap = scratch_snapshot(c);
+    const int lane = i & 31, first = cluster_block() * (kBooksThreads / 32) + (i >> 5), step = kBooksBlocks * (kBooksThreads / 32);
+    for (int r = first; r < n; r += step) {
         if (s_src[r] == s_dst[r]) continue;
         const int *ts = c.table + size_t(s_src[r]) * c.max_pages, *td = c.table + size_t(s_dst[r]) * c.max_pages;
         for (int j = lane; j < pages_of(c, s_len[r]); j += 32) snap[size_t(r) * c.max_pages + j] = ts[j];
@@ -198,24 +288,34 @@ __global__ void __launch_bounds__(kBooksThreads) fork_books_kernel(CacheView c, 
             if (page_ok(c, page)) atomicSub(c.refs + page, 1);
         }
     }
-    __syncthreads();
-    for (int r = i >> 5; r < n; r += kBooksThreads / 32) {
+    cluster_barrier();  // every source has been read
+    for (int r = first; r < n; r += step) {
         if (s_src[r] == s_dst[r]) continue;
         int *td = c.table + size_t(s_dst[r]) * c.max_pages;
-        const int pages = pages_of(c, s_len[r]), full = s_len[r] >> c.page_shift;
-        for (int j = lane; j < pages; j += 32) {
-            const int page = j < full ? snap[size_t(r) * c.max_pages + j] : fresh[s_at[r]];
+        const int pages = pages_of(c, s_len[r]), whole = s_len[r] >> c.page_shift;
+        for (int j = lane; j < whole; j += 32) {
+            const int page = snap[size_t(r) * c.max_pages + j];
             td[j] = page;
             if (page_ok(c, page)) atomicAdd(c.refs + page, 1);
         }
         for (int j = pages + lane; j < pages_of(c, s_old[r]); j += 32) td[j] = -1;
         if (lane == 0) c.length[s_dst[r]] = s_len[r];
     }
+    // a row that takes a page has number at[r]; rows that take none share the next one's, and come before it
+    give_free(c, free, total, warp_sums, [&](int k, int page) {
+        const int r = row_of(s_at, n, k);
+        c.table[size_t(s_dst[r]) * c.max_pages + (s_len[r] >> c.page_shift)] = page;
+        c.refs[page] = 1;
+    });
 }
 
 // The filled slots of each forked row's last page: blockIdx.x = fork, blockIdx.y = slice of the page's
 // layers * 2 * kv_heads runs of head_dim * page_size elements.
-__global__ void __launch_bounds__(256) fork_copy_kernel(CacheView c, const int *src, const int *dst) {
+constexpr int kForkThreads = 256, kForkVecs = 8;
+
+__global__ void __launch_bounds__(kForkThreads) fork_copy_kernel(CacheView c, const int *src, const int *dst) {
+    pdl_launch_dependents();
+    pdl_wait();
     if (c.status[1] == 0) return;
     const int i = blockIdx.x;
     const int d = dst[i];
@@ -232,16 +332,36 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(CacheView c, const int *
     const int run_v = c.page_size * c.head_dim / 8, used_v = slots * c.head_dim / 8;
     const uint4 *a = reinterpret_cast<const uint4 *>(c.pool) + size_t(from) * runs * run_v;
     uint4 *b = reinterpret_cast<uint4 *>(c.pool) + size_t(to) * runs * run_v;
-    for (int run = blockIdx.y; run < runs; run += gridDim.y)
-        for (int v = threadIdx.x; v < used_v; v += blockDim.x) b[size_t(run) * run_v + v] = a[size_t(run) * run_v + v];
+    // this block's runs as one sequence of vectors; eight of them in flight per thread
+    const int run0 = static_cast<int>(static_cast<long long>(runs) * blockIdx.y / gridDim.y);
+    const int run1 = static_cast<int>(static_cast<long long>(runs) * (blockIdx.y + 1) / gridDim.y);
+    const int count = (run1 - run0) * used_v;
+    for (int v0 = threadIdx.x; v0 < count; v0 += kForkThreads * kForkVecs) {
+        uint4 x[kForkVecs];
+        int at[kForkVecs];
+#pragma unroll
+        for (int q = 0; q < kForkVecs; ++q) {
+            const int v = v0 + q * kForkThreads, run = v / used_v;
+            at[q] = (run0 + run) * run_v + v - run * used_v;
+            if (v < count) x[q] = ldg_nc_v4(a + at[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < kForkVecs; ++q)
+            if (v0 + q * kForkThreads < count) __stcs(b + at[q], x[q]);
+    }
 }
 
-__global__ void __launch_bounds__(kBooksThreads) compact_books_kernel(CacheView c, const int *rows, const int *start,
-                                                                      const int *kept, int kept_stride,
-                                                                      const int *n_kept, int n) {
-    __shared__ int warp_sums[32];
-    __shared__ int s_row[kMaxRows], s_start[kMaxRows], s_len[kMaxRows], s_new[kMaxRows], s_need[kMaxRows];
+__global__ void __cluster_dims__(kBooksBlocks, 1, 1) __launch_bounds__(kBooksThreads, 1)
+    compact_books_kernel(CacheView c, const int *rows, const int *start, const int *kept, int kept_stride, const int *n_kept, int n) {
+    __shared__ int warp_sums[32], block_counts[kBooksBlocks];
+    __shared__ int s_row[kMaxRows], s_start[kMaxRows], s_len[kMaxRows], s_new[kMaxRows], s_at[kMaxRows];
+    __shared__ int s_bad;
     const int i = threadIdx.x, lane = i & 31;
+    if (i == 0) s_bad = 0;
+    pdl_launch_dependents();
+    cluster_barrier();
+    pdl_wait();
+    FreePages free;
     bool bad = false;
     if (i < n) {
         const int row = rows[i], st = start[i], k = n_kept[i];
@@ -254,103 +374,173 @@ __global__ void __launch_bounds__(kBooksThreads) compact_books_kernel(CacheView 
         s_new[i] = bad ? 0 : st + k;
     }
     __syncthreads();
-    int *fresh = scratch_fresh(c), *snap = scratch_snapshot(c);
-    for (int r = i >> 5; r < n; r += kBooksThreads / 32) {
+    int *snap = scratch_snapshot(c), *needs = scratch_need(c);
+    const int first = cluster_block() * (kBooksThreads / 32) + (i >> 5), step = kBooksBlocks * (kBooksThreads / 32);
+    for (int r = first; r < n; r += step) {
         const int st = s_start[r], k = s_new[r] - st, len = s_len[r];
         const int *w = kept + size_t(r) * kept_stride;
+#pragma unroll 4
         for (int j = lane; j < k; j += 32) {
             const int at = w[j];
             bad |= at < (j ? w[j - 1] + 1 : st) || at >= len;
         }
         const int *t = c.table + size_t(s_row[r]) * c.max_pages;
-        const int first = st >> c.page_shift, last = pages_of(c, s_new[r]);
+        const int lo = st >> c.page_shift, hi = pages_of(c, s_new[r]);
         int need = 0;
+#pragma unroll 4
         for (int j = lane; j < pages_of(c, len); j += 32) {
             const int page = t[j];
-            const bool own = j >= first && j < last && page_ok(c, page) && c.refs[page] > 1;
+            const bool own = j >= lo && j < hi && page_ok(c, page) && c.refs[page] > 1;
             bad |= !page_ok(c, page);
             snap[size_t(r) * c.max_pages + j] = own ? page | kShared : page;
             need += own;
         }
         need = __reduce_add_sync(0xffffffffu, need);
-        if (lane == 0) s_need[r] = need;
+        if (lane == 0) needs[r] = need;
     }
-    __syncthreads();
+    // what one block found wrong, every block has to know
+    if (bad) {
+#pragma unroll
+        for (int b = 0; b < kBooksBlocks; ++b) {
+            uint32_t there;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem_addr(&s_bad)), "r"(b));
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there), "r"(1) : "memory");
+        }
+    }
+    find_free(c, &free, block_counts, warp_sums);  // its barrier also orders the needs and the flag
     int total = 0;
-    const int at = block_scan(i < n ? s_need[i] : 0, &total, warp_sums);
-    __syncthreads();
-    if (i < n) s_need[i] = at;
-    const bool enough = total <= c.num_pages && find_free(c, total, fresh, warp_sums);
-    if (!decide(c, bad, !enough)) return;
-    for (int r = i >> 5; r < n; r += kBooksThreads / 32) {
+    const int at = block_scan(i < n ? __ldcg(needs + i) : 0, &total, warp_sums);
+    if (i < n) s_at[i] = at;
+    if (!decide(c, s_bad != 0, total > free.count)) return;
+    for (int r = first; r < n; r += step) {
         int *t = c.table + size_t(s_row[r]) * c.max_pages;
         const int last = pages_of(c, s_new[r]), pages = pages_of(c, s_len[r]);
-        int next = s_need[r];
-        for (int j0 = 0; j0 < pages; j0 += 32) {
-            const int j = j0 + lane;
-            const int entry = j < pages ? snap[size_t(r) * c.max_pages + j] : 0;
-            const bool own = (entry & kShared) != 0, drop = j >= last && j < pages;
-            const unsigned mine = __ballot_sync(0xffffffffu, own);
-            if (own) {
-                const int page = fresh[next + __popc(mine & ((1u << lane) - 1))];
-                t[j] = page;
-                c.refs[page] = 1;
+        for (int j = lane; j < pages; j += 32) {
+            const int entry = snap[size_t(r) * c.max_pages + j];
+            if (entry & kShared) {
                 atomicSub(c.refs + (entry & ~kShared), 1);
-            } else if (drop) {
+            } else if (j >= last) {
                 t[j] = -1;
                 atomicSub(c.refs + entry, 1);
             }
-            next += __popc(mine);
         }
         if (lane == 0) c.length[s_row[r]] = s_new[r];
     }
+    // the k-th new page of all is the row's (k - at)-th shared one's replacement
+    give_free(c, free, total, warp_sums, [&](int k, int page) {
+        const int r = row_of(s_at, n, k);
+        const int *old = snap + size_t(r) * c.max_pages;
+        int j = s_start[r] >> c.page_shift;
+        for (int left = k - s_at[r];; ++j)
+            if ((old[j] & kShared) && left-- == 0) break;
+        c.table[size_t(s_row[r]) * c.max_pages + j] = page;
+        c.refs[page] = 1;
+    });
 }
 
-// Moves the kept tokens of one row (blockIdx.y) in one (layer, k or v, head) run (blockIdx.x) to the front.
+// Moves the kept tokens of one row (blockIdx.y) in one (layer, k or v, head) run (blockIdx.x) to the front; one warp.
 //
-// In place and in parallel: token j's new slot is never behind its old one, and both ascend, so a write to
-// slot j only lands on the old slot of a token that was read before.  A tile of tokens is therefore read whole
-// into registers, and written after a barrier; the next tile's reads need no wait for these writes.
-constexpr int kMoveThreads = 256, kMoveVecs = 8;
+// In place and in parallel: token j's new slot is never behind its old one, and both ascend, so a write to slot j only
+// lands on the old slot of a token of the same or an earlier tile.  A tile of 32 tokens is read whole into shared memory, by
+// bulk copies of as many neighbouring tokens as lie together, before it is written; the next tiles' reads are under way
+// meanwhile and need no wait for these writes.
+constexpr int kMoveTokens = 32, kMoveStages = 4;
 
-__global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(CacheView c, const int *rows, const int *start,
-                                                                    const int *kept, int kept_stride, const int *n_kept) {
+__device__ __forceinline__ void bulk_load(uint32_t to, const void *from, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from), "r"(bytes),
+                 "r"(smem_addr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_store(void *to, uint32_t from, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(from), "r"(bytes) : "memory");
+}
+
+// Length, in lanes, of the stretch that begins at this lane if it is a head; `heads` and `active` are ballots.
+__device__ __forceinline__ int stretch(unsigned heads, unsigned active, int lane) {
+    const unsigned ends = (heads | ~active) & ~((2u << lane) - 1);
+    return (ends ? __ffs(ends) - 1 : 32) - lane;
+}
+
+__global__ void __launch_bounds__(32) compact_move_kernel(CacheView c, const int *rows, const int *start, const int *kept, int kept_stride,
+                                                          const int *n_kept) {
+    extern __shared__ __align__(128) unsigned char stages[];
+    __shared__ uint64_t full[kMoveStages];
+    __shared__ unsigned char *s_to[kMoveStages][kMoveTokens];
+    const int lane = threadIdx.x;
+    if (lane == 0) {
+        for (int q = 0; q < kMoveStages; ++q) mbar_init(&full[q], 1);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    __syncwarp();
+    pdl_launch_dependents();
+    pdl_wait();
     if (c.status[1] == 0) return;
     const int i = blockIdx.y, run = blockIdx.x;
-    const int st = start[i], end = st + n_kept[i];
+    const int st = start[i], end = st + n_kept[i], mask = c.page_size - 1;
     const int *t = c.table + size_t(rows[i]) * c.max_pages;
     const int *snap = scratch_snapshot(c) + size_t(i) * c.max_pages;
     const int *w = kept + size_t(i) * kept_stride;
-    const int vecs = c.head_dim / 8;                       // 16-byte vectors of a token: 8 or 16
-    const int per = kMoveThreads / vecs * kMoveVecs;       // tokens of a tile
-    const int vec = threadIdx.x % vecs, sub = threadIdx.x / vecs, step = kMoveThreads / vecs;
-    const size_t run_v = size_t(c.page_size) * vecs, page_v = run_v * c.layers * 2 * c.kv_heads;
-    uint4 *pool = reinterpret_cast<uint4 *>(c.pool) + run * run_v + vec;
-    const int mask = c.page_size - 1;
-    for (int j0 = st & ~mask; j0 < end; j0 += per) {
-        uint4 x[kMoveVecs];
-        size_t to[kMoveVecs];
-#pragma unroll
-        for (int q = 0; q < kMoveVecs; ++q) {
-            const int j = j0 + q * step + sub;
-            to[q] = ~size_t(0);
-            if (j < end) {
-                const int s = j < st ? j : w[j - st];
-                const int from = snap[s >> c.page_shift] & ~kShared, page = t[j >> c.page_shift];
-                if (from != page || s != j) {
-                    to[q] = page * page_v + size_t(j & mask) * vecs;
-                    x[q] = pool[from * page_v + size_t(s & mask) * vecs];
-                }
-            }
+    const uint32_t token_b = c.head_dim * 2;
+    const size_t run_b = size_t(c.page_size) * token_b, page_b = run_b * c.layers * 2 * c.kv_heads;
+    unsigned char *pool = c.pool + run * run_b;
+    const uint32_t base = smem_addr(stages), stage_b = kMoveTokens * token_b;
+    const int first = st & ~mask, tiles = (end - first + kMoveTokens - 1) / kMoveTokens;
+    auto position = [&](int tile) {  // where the lane's token of a tile is now
+        const int j = first + tile * kMoveTokens + lane;
+        return j >= end || j < st ? j : w[j - st];
+    };
+    int ahead = position(0);
+    auto load = [&](int tile) {
+        const int j = first + tile * kMoveTokens + lane, s = ahead, q = tile % kMoveStages;
+        ahead = position(tile + 1);
+        const unsigned char *from = nullptr;
+        unsigned char *to = nullptr;
+        if (j < end) {
+            from = pool + (snap[s >> c.page_shift] & ~kShared) * page_b + size_t(s & mask) * token_b;
+            to = pool + t[j >> c.page_shift] * page_b + size_t(j & mask) * token_b;
+            if (from == to) to = nullptr;  // stays where it is
         }
-        __syncthreads();
-#pragma unroll
-        for (int q = 0; q < kMoveVecs; ++q)
-            if (to[q] != ~size_t(0)) pool[to[q]] = x[q];
+        s_to[q][lane] = to;
+        const unsigned active = __ballot_sync(0xffffffffu, to != nullptr);
+        const unsigned long long last = __shfl_up_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), 1);
+        const bool head = to && (lane == 0 || !((active >> (lane - 1)) & 1) || last + token_b != reinterpret_cast<unsigned long long>(from));
+        const unsigned heads = __ballot_sync(0xffffffffu, head);
+        if (lane == 0) mbar_arrive_expect_tx(&full[q], __popc(active) * token_b);
+        __syncwarp();
+        if (head) bulk_load(base + q * stage_b + lane * token_b, from, stretch(heads, active, lane) * token_b, &full[q]);
+    };
+    for (int tile = 0; tile < kMoveStages - 1 && tile < tiles; ++tile) load(tile);
+    int loaded = tiles < kMoveStages - 1 ? tiles : kMoveStages - 1;
+    for (int tile = 0; tile < tiles; ++tile) {
+        const int q = tile % kMoveStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[q], (tile / kMoveStages) & 1, kDefaultTimeoutNs))) {
+            if (lane == 0) atomicOr(c.status, kStatusTimeout);
+            break;
+        }
+        unsigned char *to = s_to[q][lane];
+        const unsigned active = __ballot_sync(0xffffffffu, to != nullptr);
+        const unsigned long long last = __shfl_up_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), 1);
+        const bool head = to && (lane == 0 || last + token_b != reinterpret_cast<unsigned long long>(to));
+        const unsigned heads = __ballot_sync(0xffffffffu, head);
+        if (head) bulk_store(to, base + q * stage_b + lane * token_b, stretch(heads, active, lane) * token_b);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        if (tile + kMoveStages - 1 < tiles) {
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the slot's last tile has been written from it
+            __syncwarp();
+            load(tile + kMoveStages - 1);
+            ++loaded;
+        }
     }
+    // copies in flight end before the block does, also after a wait that gave up
+    for (int tile = loaded > kMoveStages ? loaded - kMoveStages : 0; tile < loaded; ++tile)
+        mbar_wait(&full[tile % kMoveStages], (tile / kMoveStages) & 1, kDefaultTimeoutNs);
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 __global__ void __launch_bounds__(256) copy_pages_kernel(CacheView c, const int *src, const int *dst, size_t page_v) {
+    pdl_launch_dependents();
+    pdl_wait();
     const int i = blockIdx.x, a = src[i], b = dst[i];
     if (!page_ok(c, a) || !page_ok(c, b)) {
         if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(c.status, kStatusIndex);
@@ -358,14 +548,19 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(CacheView c, const int 
     }
     const uint4 *from = reinterpret_cast<const uint4 *>(c.pool) + a * page_v;
     uint4 *to = reinterpret_cast<uint4 *>(c.pool) + b * page_v;
-    for (size_t v = size_t(blockIdx.y) * blockDim.x + threadIdx.x; v < page_v; v += size_t(gridDim.y) * blockDim.x)
-        to[v] = from[v];
+    const size_t step = size_t(gridDim.y) * blockDim.x;
+    for (size_t v0 = size_t(blockIdx.y) * blockDim.x + threadIdx.x; v0 < page_v; v0 += 4 * step) {
+        uint4 x[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (v0 + q * step < page_v) x[q] = ldg_nc_v4(from + v0 + q * step);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (v0 + q * step < page_v) to[v0 + q * step] = x[q];
+    }
 }
 
-dspark_status launched(const char *what) {
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, what);
-}
+dspark_status launched(cudaError_t e, const char *what) { return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, what); }
 
 dspark_status check_rows(const char *who, const CacheView &c, const void *a, const void *b, int n) {
     if (n < 0) return fail(DSPARK_ERR_INVALID, "%s: n=%d is negative", who, n);
@@ -386,7 +581,11 @@ bool sizes_ok(const dspark_cache *c) {
 
 }  // namespace
 
-size_t cache_ops_scratch_bytes(int max_seqs, int max_pages) { return up256(2 * 4 * fresh_entries(max_seqs, max_pages)); }
+size_t cache_ops_scratch_bytes(int max_seqs, int max_pages, int num_pages) {
+    const int rounds = free_rounds(num_pages);
+    const size_t bits = rounds > kHeld ? size_t(rounds) * kBooksBlocks * kBooksThreads * 2 : 0;
+    return up256(4 * (kMaxRows + snapshot_entries(max_seqs, max_pages)) + bits);
+}
 
 dspark_status cache_view(const dspark_cache *c, const char *who, CacheView *v) {
     clear_error();
@@ -432,7 +631,7 @@ using namespace dspark;
 
 extern "C" size_t dspark_cache_workspace_bytes(const dspark_cache *c) {
     if (!c || !sizes_ok(c)) return 0;
-    const size_t ops = cache_ops_scratch_bytes(c->max_seqs, c->max_pages), att = attention_scratch_bytes(c->head_dim);
+    const size_t ops = cache_ops_scratch_bytes(c->max_seqs, c->max_pages, c->num_pages), att = attention_scratch_bytes(c->head_dim);
     return kCacheScratchOffset + (ops > att ? ops : att);
 }
 
@@ -441,16 +640,14 @@ extern "C" dspark_status dspark_cache_extend(const dspark_cache *cache, const in
     CacheView c;
     dspark_status st = cache_view(cache, "cache_extend", &c);
     if (st != DSPARK_OK || (st = check_rows("cache_extend", c, rows, counts, n)) != DSPARK_OK || n == 0) return st;
-    extend_kernel<<<1, kBooksThreads, 0, stream>>>(c, rows, counts, n);
-    return launched("cache_extend");
+    return launched(launch_pdl(extend_kernel, dim3(kBooksBlocks), dim3(kBooksThreads), 0, stream, c, rows, counts, n), "cache_extend");
 }
 
 extern "C" dspark_status dspark_cache_free(const dspark_cache *cache, const int32_t *rows, int n, dspark_stream_t stream) {
     CacheView c;
     dspark_status st = cache_view(cache, "cache_free", &c);
     if (st != DSPARK_OK || (st = check_rows("cache_free", c, rows, rows, n)) != DSPARK_OK || n == 0) return st;
-    free_kernel<<<n, 256, 0, stream>>>(c, rows, n);
-    return launched("cache_free");
+    return launched(launch_pdl(free_kernel, dim3(n), dim3(256), 0, stream, c, rows, n), "cache_free");
 }
 
 extern "C" dspark_status dspark_cache_fork(const dspark_cache *cache, const int32_t *src, const int32_t *dst, int n,
@@ -458,10 +655,12 @@ extern "C" dspark_status dspark_cache_fork(const dspark_cache *cache, const int3
     CacheView c;
     dspark_status st = cache_view(cache, "cache_fork", &c);
     if (st != DSPARK_OK || (st = check_rows("cache_fork", c, src, dst, n)) != DSPARK_OK || n == 0) return st;
-    fork_books_kernel<<<1, kBooksThreads, 0, stream>>>(c, src, dst, n);
-    const int runs = c.layers * 2 * c.kv_heads;
-    fork_copy_kernel<<<dim3(n, runs < 64 ? runs : 64), 256, 0, stream>>>(c, src, dst);
-    return launched("cache_fork");
+    st = launched(launch_pdl(fork_books_kernel, dim3(kBooksBlocks), dim3(kBooksThreads), 0, stream, c, src, dst, n), "cache_fork");
+    if (st != DSPARK_OK) return st;
+    // at most 2048 vectors a block, so that each thread's eight are in flight at once
+    const long long vecs = 2ll * c.layers * c.kv_heads * c.page_size * c.head_dim / 8;
+    const unsigned slices = static_cast<unsigned>(vecs / (kForkThreads * kForkVecs) < 1 ? 1 : vecs / (kForkThreads * kForkVecs) > 4096 ? 4096 : vecs / (kForkThreads * kForkVecs));
+    return launched(launch_pdl(fork_copy_kernel, dim3(n, slices), dim3(kForkThreads), 0, stream, c, src, dst), "cache_fork");
 }
 
 extern "C" dspark_status dspark_cache_compact(const dspark_cache *cache, const int32_t *rows, const int32_t *start,
@@ -473,10 +672,12 @@ extern "C" dspark_status dspark_cache_compact(const dspark_cache *cache, const i
     if (kept_stride < 0) return fail(DSPARK_ERR_INVALID, "cache_compact: kept_stride=%d is negative", kept_stride);
     if (n == 0) return DSPARK_OK;
     if (!n_kept || (!kept && kept_stride > 0)) return fail(DSPARK_ERR_INVALID, "cache_compact: null pointer argument");
-    compact_books_kernel<<<1, kBooksThreads, 0, stream>>>(c, rows, start, kept, kept_stride, n_kept, n);
-    compact_move_kernel<<<dim3(c.layers * 2 * c.kv_heads, n), kMoveThreads, 0, stream>>>(c, rows, start, kept, kept_stride,
-                                                                                         n_kept);
-    return launched("cache_compact");
+    st = launched(launch_pdl(compact_books_kernel, dim3(kBooksBlocks), dim3(kBooksThreads), 0, stream, c, rows, start, kept, kept_stride, n_kept, n),
+                  "cache_compact");
+    if (st != DSPARK_OK) return st;
+    return launched(launch_pdl(compact_move_kernel, dim3(c.layers * 2 * c.kv_heads, n), dim3(32), size_t(kMoveStages) * kMoveTokens * c.head_dim * 2,
+                               stream, c, rows, start, kept, kept_stride, n_kept),
+                    "cache_compact");
 }
 
 extern "C" dspark_status dspark_cache_copy_pages(const dspark_cache *cache, const int32_t *src, const int32_t *dst, int n,
@@ -489,8 +690,8 @@ extern "C" dspark_status dspark_cache_copy_pages(const dspark_cache *cache, cons
     if (!src || !dst) return fail(DSPARK_ERR_INVALID, "cache_copy_pages: null pointer argument");
     const size_t page_v = size_t(c.layers) * 2 * c.kv_heads * c.page_size * c.head_dim / 8;
     const size_t blocks = (page_v + 1023) / 1024;
-    copy_pages_kernel<<<dim3(n, static_cast<unsigned>(blocks < 64 ? blocks : 64)), 256, 0, stream>>>(c, src, dst, page_v);
-    return launched("cache_copy_pages");
+    return launched(launch_pdl(copy_pages_kernel, dim3(n, static_cast<unsigned>(blocks < 64 ? blocks : 64)), dim3(256), 0, stream, c, src, dst, page_v),
+                    "cache_copy_pages");
 }
 
 extern "C" dspark_status dspark_cache_status(const dspark_cache *cache, dspark_stream_t stream) {

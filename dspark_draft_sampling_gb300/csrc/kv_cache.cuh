@@ -36,7 +36,7 @@ struct CacheView {
 dspark_status cache_view(const dspark_cache *c, const char *who, CacheView *v);
 
 // Bytes of the two uses of the scratch area (cache.cu, paged_attention.cu).
-size_t cache_ops_scratch_bytes(int max_seqs, int max_pages);
+size_t cache_ops_scratch_bytes(int max_seqs, int max_pages, int num_pages);
 size_t attention_scratch_bytes(int head_dim);
 
 }  // namespace dspark

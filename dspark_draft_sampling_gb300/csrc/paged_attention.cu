@@ -1010,14 +1010,14 @@ dspark_status launch(const CUtensorMap &tm_q, const CUtensorMap &tm_kv, const Ca
     return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "paged_attention");
 }
 
-dspark_status attend(const dspark_cache *cache, int layer, const void *q, long long q_token_stride, long long q_head_stride,
-                     int tokens, int q_heads, const int32_t *rows, const int32_t *cu_new, int n_seqs, int max_new, int causal,
-                     int window, float scale, void *out, long long out_token_stride, long long out_head_stride, float *lse,
-                     unsigned stall_us, cudaStream_t stream) {
+dspark_status attend(const dspark_cache *cache, const dspark_attention_args *args, unsigned stall_us, cudaStream_t stream) {
     const char *who = "paged_attention";
     CacheView c;
     dspark_status st = cache_view(cache, who, &c);
     if (st != DSPARK_OK) return st;
+    if (!args) return fail(DSPARK_ERR_INVALID, "%s: null arguments", who);
+    auto [q, out, lse, rows, cu_new, q_token_stride, q_head_stride, out_token_stride, out_head_stride, layer, tokens, q_heads, n_seqs,
+          max_new, causal, window, scale] = *args;
     if (layer < 0 || layer >= c.layers) return fail(DSPARK_ERR_INVALID, "%s: layer %d of %d", who, layer, c.layers);
     if (tokens < 0 || q_heads < 1 || n_seqs < 0 || max_new < 0 || window < 0)
         return fail(DSPARK_ERR_INVALID, "%s: bad sizes tokens=%d q_heads=%d n_seqs=%d max_new=%d window=%d", who, tokens,
@@ -1094,22 +1094,11 @@ size_t attention_scratch_bytes(int head_dim) { return size_t(kMaxCtas) * 2 * 2 *
 
 }  // namespace dspark
 
-extern "C" dspark_status dspark_paged_attention(const dspark_cache *cache, int layer, const void *q,
-                                                long long q_token_stride, long long q_head_stride, int tokens,
-                                                int q_heads, const int32_t *rows, const int32_t *cu_new, int n_seqs,
-                                                int max_new, int causal, int window, float scale, void *out,
-                                                long long out_token_stride, long long out_head_stride, float *lse,
-                                                dspark_stream_t stream) {
-    return dspark::attend(cache, layer, q, q_token_stride, q_head_stride, tokens, q_heads, rows, cu_new, n_seqs, max_new, causal,
-                          window, scale, out, out_token_stride, out_head_stride, lse, 0, stream);
+extern "C" dspark_status dspark_paged_attention(const dspark_cache *cache, const dspark_attention_args *args, dspark_stream_t stream) {
+    return dspark::attend(cache, args, 0, stream);
 }
 
-extern "C" dspark_status dspark_paged_attention_debug(const dspark_cache *cache, int layer, const void *q,
-                                                      long long q_token_stride, long long q_head_stride, int tokens,
-                                                      int q_heads, const int32_t *rows, const int32_t *cu_new, int n_seqs,
-                                                      int max_new, int causal, int window, float scale, void *out,
-                                                      long long out_token_stride, long long out_head_stride, float *lse,
-                                                      unsigned stall_us, dspark_stream_t stream) {
-    return dspark::attend(cache, layer, q, q_token_stride, q_head_stride, tokens, q_heads, rows, cu_new, n_seqs, max_new, causal,
-                          window, scale, out, out_token_stride, out_head_stride, lse, stall_us, stream);
+extern "C" dspark_status dspark_paged_attention_debug(const dspark_cache *cache, const dspark_attention_args *args, unsigned stall_us,
+                                                      dspark_stream_t stream) {
+    return dspark::attend(cache, args, stall_us, stream);
 }

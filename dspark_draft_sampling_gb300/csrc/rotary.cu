@@ -15,6 +15,7 @@ namespace dspark {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kHeads = 4;  // heads of a thread in flight
 
 template <typename T> struct Vec;  // 16 bytes of a head
 template <> struct Vec<__half> {
@@ -135,6 +136,8 @@ struct Strided {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(Strided x, Strided y, int tokens, int heads, int units,
                                                           int lanes, const int *positions, Turns t) {
+    pdl_launch_dependents();
+    pdl_wait();
     // units * lanes threads to a token: `lanes` heads at a time
     const int per = units * lanes;
     const int token = static_cast<int>(blockIdx.x) * (kThreads / per) + static_cast<int>(threadIdx.x) / per;
@@ -145,12 +148,26 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(Strided x, Strided y, 
     u.at(t, unit, positions[token]);
     const T *px = static_cast<const T *>(x.p) + token * x.token;
     T *py = static_cast<T *>(const_cast<void *>(y.p)) + token * y.token;
-    for (int h = r / units + static_cast<int>(blockIdx.y) * lanes; h < heads; h += lanes * static_cast<int>(gridDim.y)) {
-        uint4 a = *reinterpret_cast<const uint4 *>(px + h * x.head + u.a);
-        uint4 b = *reinterpret_cast<const uint4 *>(px + h * x.head + u.b);
-        u.turn(a, b, t.layout);
-        *reinterpret_cast<uint4 *>(py + h * y.head + u.a) = a;
-        *reinterpret_cast<uint4 *>(py + h * y.head + u.b) = b;
+    const int step = lanes * static_cast<int>(gridDim.y);
+    for (int h0 = r / units + static_cast<int>(blockIdx.y) * lanes; h0 < heads; h0 += kHeads * step) {
+        uint4 a[kHeads], b[kHeads];
+#pragma unroll
+        for (int q = 0; q < kHeads; ++q) {
+            const int h = h0 + q * step;
+            if (h < heads) {
+                a[q] = *reinterpret_cast<const uint4 *>(px + h * x.head + u.a);
+                b[q] = *reinterpret_cast<const uint4 *>(px + h * x.head + u.b);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kHeads; ++q) {
+            const int h = h0 + q * step;
+            if (h < heads) {
+                u.turn(a[q], b[q], t.layout);
+                *reinterpret_cast<uint4 *>(py + h * y.head + u.a) = a[q];
+                *reinterpret_cast<uint4 *>(py + h * y.head + u.b) = b[q];
+            }
+        }
     }
 }
 
@@ -174,6 +191,8 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) append_kernel(CacheView c, Append g, int units, int lanes, Turns t) {
     __shared__ int s_pos[kThreads / 4];        // angle's position of each token of the block
     __shared__ long long s_slot[kThreads / 4]; // element of the pool where its first key goes; -1: nowhere; -2: no token
+    pdl_launch_dependents();
+    pdl_wait();
     const int per = units * lanes, count = kThreads / per;
     const int token0 = static_cast<int>(blockIdx.x) * count, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long run = static_cast<long long>(c.page_size) * c.head_dim;  // elements of one (page, layer, k or v, head)
@@ -214,18 +233,30 @@ __global__ void __launch_bounds__(kThreads) append_kernel(CacheView c, Append g,
     u.at(t, unit, s_pos[i]);
     const int heads = g.q_heads + 2 * c.kv_heads;
     T *pool = reinterpret_cast<T *>(c.pool);
-    for (int h = r / units + static_cast<int>(blockIdx.y) * lanes; h < heads; h += lanes * static_cast<int>(gridDim.y)) {
-        const int hk = h - g.q_heads, hv = hk - c.kv_heads;
-        if (hk >= 0 && slot < 0) break;
-        const Strided &from = hk < 0 ? g.q : hv < 0 ? g.k : g.v;
-        const T *px = static_cast<const T *>(from.p) + token * from.token + (hk < 0 ? h : hv < 0 ? hk : hv) * from.head;
-        uint4 a = *reinterpret_cast<const uint4 *>(px + u.a);
-        uint4 b = *reinterpret_cast<const uint4 *>(px + u.b);
-        if (hv < 0) u.turn(a, b, t.layout);
-        // a layer's runs of a page: the kv_heads of k, then those of v
-        T *py = hk < 0 ? static_cast<T *>(const_cast<void *>(g.out.p)) + token * g.out.token + h * g.out.head : pool + slot + hk * run;
-        *reinterpret_cast<uint4 *>(py + u.a) = a;
-        *reinterpret_cast<uint4 *>(py + u.b) = b;
+    const int step = lanes * static_cast<int>(gridDim.y);
+    for (int h0 = r / units + static_cast<int>(blockIdx.y) * lanes; h0 < heads; h0 += kHeads * step) {
+        uint4 a[kHeads], b[kHeads];
+#pragma unroll
+        for (int q = 0; q < kHeads; ++q) {
+            const int h = h0 + q * step, hk = h - g.q_heads, hv = hk - c.kv_heads;
+            if (h < heads) {
+                const Strided &from = hk < 0 ? g.q : hv < 0 ? g.k : g.v;
+                const T *px = static_cast<const T *>(from.p) + token * from.token + (hk < 0 ? h : hv < 0 ? hk : hv) * from.head;
+                a[q] = *reinterpret_cast<const uint4 *>(px + u.a);
+                b[q] = *reinterpret_cast<const uint4 *>(px + u.b);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kHeads; ++q) {
+            const int h = h0 + q * step, hk = h - g.q_heads, hv = hk - c.kv_heads;
+            if (h < heads && (hk < 0 || slot >= 0)) {
+                if (hv < 0) u.turn(a[q], b[q], t.layout);
+                // a layer's runs of a page: the kv_heads of k, then those of v
+                T *py = hk < 0 ? static_cast<T *>(const_cast<void *>(g.out.p)) + token * g.out.token + h * g.out.head : pool + slot + hk * run;
+                *reinterpret_cast<uint4 *>(py + u.a) = a[q];
+                *reinterpret_cast<uint4 *>(py + u.b) = b[q];
+            }
+        }
     }
 }
 
@@ -272,12 +303,11 @@ dspark_status check_strided(const char *who, const char *name, const void *p, lo
 
 using namespace dspark;
 
-extern "C" dspark_status dspark_rotary(const void *x, long long x_token_stride, long long x_head_stride, void *y,
-                                       long long y_token_stride, long long y_head_stride, int dtype, int tokens,
-                                       int heads, int head_dim, const int32_t *positions, const int64_t *turns,
-                                       int rotary_dim, int layout, float amplitude, int backward,
-                                       dspark_stream_t stream) {
+extern "C" dspark_status dspark_rotary(const dspark_rotary_args *args, dspark_stream_t stream) {
     clear_error();
+    if (!args) return fail(DSPARK_ERR_INVALID, "rotary: null arguments");
+    const auto [x, y, positions, turns, x_token_stride, x_head_stride, y_token_stride, y_head_stride, dtype, tokens, heads, head_dim,
+                rotary_dim, layout, backward, amplitude] = *args;
     if (dtype != DSPARK_FP16 && dtype != DSPARK_BF16 && dtype != DSPARK_FP32)
         return fail(DSPARK_ERR_INVALID, "rotary: dtype %d", dtype);
     if (tokens < 0 || heads < 0) return fail(DSPARK_ERR_INVALID, "rotary: bad sizes tokens=%d heads=%d", tokens, heads);
@@ -297,28 +327,20 @@ extern "C" dspark_status dspark_rotary(const void *x, long long x_token_stride, 
     const Turns t{reinterpret_cast<const long long *>(turns), rotary_dim, layout, amplitude, backward != 0};
     const Strided sx{x, x_token_stride, x_head_stride}, sy{y, y_token_stride, y_head_stride};
     const dim3 grid(bx, by);
-    if (dtype == DSPARK_FP32)
-        rotary_kernel<float><<<grid, kThreads, 0, stream>>>(sx, sy, tokens, heads, units, lanes, positions, t);
-    else if (dtype == DSPARK_BF16)
-        rotary_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(sx, sy, tokens, heads, units, lanes, positions, t);
-    else
-        rotary_kernel<__half><<<grid, kThreads, 0, stream>>>(sx, sy, tokens, heads, units, lanes, positions, t);
-    const cudaError_t e = cudaGetLastError();
+    auto *kernel = dtype == DSPARK_FP32 ? rotary_kernel<float> : dtype == DSPARK_BF16 ? rotary_kernel<__nv_bfloat16> : rotary_kernel<__half>;
+    const cudaError_t e = launch_pdl(kernel, grid, dim3(kThreads), 0, stream, sx, sy, tokens, heads, units, lanes, positions, t);
     return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "rotary");
 }
 
-extern "C" dspark_status dspark_rotary_append(const dspark_cache *cache, int layer, const void *q,
-                                              long long q_token_stride, long long q_head_stride, const void *k,
-                                              long long k_token_stride, long long k_head_stride, const void *v,
-                                              long long v_token_stride, long long v_head_stride, void *q_out,
-                                              long long out_token_stride, long long out_head_stride, int tokens,
-                                              int q_heads, const int32_t *rows, const int32_t *cu_new, int n_seqs,
-                                              const int32_t *positions, const int64_t *turns, int rotary_dim,
-                                              int layout, float amplitude, dspark_stream_t stream) {
+extern "C" dspark_status dspark_rotary_append(const dspark_cache *cache, const dspark_append_args *args, dspark_stream_t stream) {
     const char *who = "rotary_append";
     CacheView c;
     dspark_status st = cache_view(cache, who, &c);
     if (st != DSPARK_OK) return st;
+    if (!args) return fail(DSPARK_ERR_INVALID, "%s: null arguments", who);
+    const auto [q, k, v, q_out, rows, cu_new, positions, turns, q_token_stride, q_head_stride, k_token_stride, k_head_stride,
+                v_token_stride, v_head_stride, out_token_stride, out_head_stride, layer, tokens, q_heads, n_seqs, rotary_dim, layout,
+                amplitude] = *args;
     if (layer < 0 || layer >= c.layers) return fail(DSPARK_ERR_INVALID, "%s: layer %d of %d", who, layer, c.layers);
     if (tokens < 0 || q_heads < 0 || n_seqs < 0)
         return fail(DSPARK_ERR_INVALID, "%s: bad sizes tokens=%d q_heads=%d n_seqs=%d", who, tokens, q_heads, n_seqs);
@@ -349,10 +371,7 @@ extern "C" dspark_status dspark_rotary_append(const dspark_cache *cache, int lay
     g.q_heads = q_heads;
     g.n_seqs = n_seqs;
     g.layer = layer;
-    if (cache->dtype == DSPARK_BF16)
-        append_kernel<__nv_bfloat16><<<dim3(bx, by), kThreads, 0, stream>>>(c, g, units, lanes, t);
-    else
-        append_kernel<__half><<<dim3(bx, by), kThreads, 0, stream>>>(c, g, units, lanes, t);
-    const cudaError_t e = cudaGetLastError();
+    auto *kernel = cache->dtype == DSPARK_BF16 ? append_kernel<__nv_bfloat16> : append_kernel<__half>;
+    const cudaError_t e = launch_pdl(kernel, dim3(bx, by), dim3(kThreads), 0, stream, c, g, units, lanes, t);
     return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, who);
 }

@@ -622,20 +622,31 @@ dspark_status dspark_cache_status(const dspark_cache *cache, dspark_stream_t str
 #define DSPARK_ROTARY_HALF 0
 #define DSPARK_ROTARY_INTERLEAVED 1
 
-dspark_status dspark_rotary(const void *x, long long x_token_stride, long long x_head_stride, void *y,
-                            long long y_token_stride, long long y_head_stride, int dtype, int tokens,
-                            int heads, int head_dim, const int32_t *positions, const int64_t *turns,
-                            int rotary_dim, int layout, float amplitude, int backward,
-                            dspark_stream_t stream);
+typedef struct dspark_rotary_args {
+    const void *x;
+    void *y;
+    const int32_t *positions;
+    const int64_t *turns;
+    long long x_token_stride, x_head_stride, y_token_stride, y_head_stride;
+    int dtype, tokens, heads, head_dim, rotary_dim, layout, backward;
+    float amplitude;
+} dspark_rotary_args;
 
-dspark_status dspark_rotary_append(const dspark_cache *cache, int layer, const void *q,
-                                   long long q_token_stride, long long q_head_stride, const void *k,
-                                   long long k_token_stride, long long k_head_stride, const void *v,
-                                   long long v_token_stride, long long v_head_stride, void *q_out,
-                                   long long out_token_stride, long long out_head_stride, int tokens,
-                                   int q_heads, const int32_t *rows, const int32_t *cu_new, int n_seqs,
-                                   const int32_t *positions, const int64_t *turns, int rotary_dim,
-                                   int layout, float amplitude, dspark_stream_t stream);
+dspark_status dspark_rotary(const dspark_rotary_args *args, dspark_stream_t stream);
+
+typedef struct dspark_append_args {
+    const void *q, *k, *v;
+    void *q_out;
+    const int32_t *rows, *cu_new, *positions; /* rows and positions may be NULL */
+    const int64_t *turns;
+    long long q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride,
+        out_token_stride, out_head_stride;
+    int layer, tokens, q_heads, n_seqs, rotary_dim, layout;
+    float amplitude;
+} dspark_append_args;
+
+dspark_status dspark_rotary_append(const dspark_cache *cache, const dspark_append_args *args,
+                                   dspark_stream_t stream);
 
 /* =====================================================================================
  * Attention of new tokens over the paged cache
@@ -664,24 +675,25 @@ dspark_status dspark_rotary_append(const dspark_cache *cache, int layer, const v
  * Supported: q_heads a multiple of kv_heads, at most 128 of them to a kv head; n_seqs <= 4096.
  * The result is deterministic: it depends on the inputs and the number of SMs only.
  * ===================================================================================== */
-dspark_status dspark_paged_attention(const dspark_cache *cache, int layer, const void *q,
-                                     long long q_token_stride, long long q_head_stride, int tokens,
-                                     int q_heads, const int32_t *rows, const int32_t *cu_new, int n_seqs,
-                                     int max_new, int causal, int window, float scale, void *out,
-                                     long long out_token_stride, long long out_head_stride, float *lse,
+typedef struct dspark_attention_args {
+    const void *q;
+    void *out;
+    float *lse;
+    const int32_t *rows, *cu_new; /* rows may be NULL */
+    long long q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+    int layer, tokens, q_heads, n_seqs, max_new, causal, window;
+    float scale;
+} dspark_attention_args;
+
+dspark_status dspark_paged_attention(const dspark_cache *cache, const dspark_attention_args *args,
                                      dspark_stream_t stream);
 
 /* Fault-injection hook for testing the device-side wait limit: the same launch as
  * dspark_paged_attention, except that the softmax threads first wait `stall_us` microseconds on a
  * barrier that nothing signals; the wait gives up, DSPARK_ERR_TIMEOUT is recorded and the kernel
  * finishes normally.  Not for production use. */
-dspark_status dspark_paged_attention_debug(const dspark_cache *cache, int layer, const void *q,
-                                           long long q_token_stride, long long q_head_stride, int tokens,
-                                           int q_heads, const int32_t *rows, const int32_t *cu_new,
-                                           int n_seqs, int max_new, int causal, int window, float scale,
-                                           void *out, long long out_token_stride,
-                                           long long out_head_stride, float *lse, unsigned stall_us,
-                                           dspark_stream_t stream);
+dspark_status dspark_paged_attention_debug(const dspark_cache *cache, const dspark_attention_args *args,
+                                           unsigned stall_us, dspark_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -225,9 +225,9 @@ def test_a_wait_that_gave_up_is_reported(n):
     assert cache.status() == 0
     got = torch.empty_like(want)
     lib = api.load_library()
-    status = lib.dspark_paged_attention_debug(cache._ref, 0, q.data_ptr(), 512, 128, n, 4, None, cu.data_ptr(), 1, n, 1, 0,
-                                              128 ** -0.5, got.data_ptr(), 512, 128, None, 20000,
-                                              torch.cuda.current_stream().cuda_stream)
+    args = api._ATTENTION_ARGS.pack(q.data_ptr(), got.data_ptr(), 0, 0, cu.data_ptr(), 512, 128, 512, 128, 0, n, 4, 1, n, 1, 0,
+                                    128 ** -0.5)
+    status = lib.dspark_paged_attention_debug(cache._ref, args, 20000, torch.cuda.current_stream().cuda_stream)
     assert status == 0 and cache.status() == api.DSPARK_ERR_TIMEOUT
     assert torch.equal(got, want)
     assert torch.equal(api.paged_attention(q, cache, 0, cu), want) and cache.status() == 0

@@ -1,6 +1,7 @@
 """The cache operators' C entries without a GPU: arguments are refused before the device is touched."""
 import ctypes
 import math
+import os
 
 import pytest
 
@@ -27,18 +28,30 @@ BAD_CACHES = [(dict(pool=None), INVALID), (dict(table=None), INVALID), (dict(len
 
 
 def attend(lib, c, layer=0, q=FAKE, qs=(512, 128), tokens=3, heads=4, cu=FAKE, seqs=1, max_new=3, window=0, out=FAKE,
-           os=(512, 128), lse=None, scale=1.0):
-    return lib.dspark_paged_attention(c, layer, q, *qs, tokens, heads, None, cu, seqs, max_new, 1, window, scale, out, *os, lse, None)
+           os=(512, 128), lse=0, scale=1.0):
+    return lib.dspark_paged_attention(c, api._ATTENTION_ARGS.pack(q, out, lse, 0, cu, *qs, *os, layer, tokens, heads, seqs, max_new, 1,
+                                                                  window, scale), None)
 
 
 def append(lib, c, layer=0, q=FAKE, k=FAKE, v=FAKE, out=FAKE, stride=512, tokens=3, heads=4, cu=FAKE, seqs=1, turns=FAKE, dim=128,
            layout=0):
-    return lib.dspark_rotary_append(c, layer, q, stride, 128, k, stride, 128, v, stride, 128, out, stride, 128, tokens, heads, None,
-                                    cu, seqs, None, turns, dim, layout, 1.0, None)
+    return lib.dspark_rotary_append(c, api._APPEND_ARGS.pack(q, k, v, out, 0, cu, 0, turns, *(stride, 128) * 4, layer, tokens, heads, seqs,
+                                                             dim, layout, 1.0), None)
 
 
 def turn(lib, x=FAKE, y=FAKE, stride=512, dtype=1, tokens=3, heads=4, head_dim=128, pos=FAKE, turns=FAKE, dim=128, layout=0):
-    return lib.dspark_rotary(x, stride, 128, y, stride, 128, dtype, tokens, heads, head_dim, pos, turns, dim, layout, 1.0, 0, None)
+    return lib.dspark_rotary(api._ROTARY_ARGS.pack(x, y, pos, turns, stride, 128, stride, 128, dtype, tokens, heads, head_dim, dim, layout,
+                                                   0, 1.0), None)
+
+
+def test_argument_structs_have_the_sizes_of_the_header(dspark_lib, tmp_path):
+    import subprocess
+    names = {"dspark_rotary_args": api._ROTARY_ARGS.size, "dspark_append_args": api._APPEND_ARGS.size,
+             "dspark_attention_args": api._ATTENTION_ARGS.size, "dspark_cache": ctypes.sizeof(api.CacheStruct)}
+    src = tmp_path / "sizes.c"
+    src.write_text('#include "dspark.h"\n' + "".join(f"_Static_assert(sizeof({n}) == {s}, \"{n}\");\n" for n, s in names.items()))
+    subprocess.run(["gcc", "-fsyntax-only", "-I", os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include"),
+                    str(src)], check=True)
 
 
 @pytest.mark.parametrize("change,status", BAD_CACHES)
@@ -80,7 +93,7 @@ def test_workspace_bytes(dspark_lib):
 
 def test_attention_refuses(dspark_lib):
     lib, c = dspark_lib, cache()
-    for kw in (dict(layer=2), dict(layer=-1), dict(q=None), dict(out=None), dict(cu=None), dict(q=ODD), dict(out=ODD), dict(lse=0x10002),
+    for kw in (dict(layer=2), dict(layer=-1), dict(q=0), dict(out=0), dict(cu=0), dict(q=ODD), dict(out=ODD), dict(lse=0x10002),
                dict(tokens=-1), dict(heads=0), dict(heads=3), dict(seqs=-1), dict(max_new=-1), dict(window=-1), dict(qs=(516, 128)),
                dict(os=(512, 129)), dict(qs=(-512, 128)), dict(qs=(0, 128)), dict(scale=0.0),
                dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan)):
@@ -88,19 +101,21 @@ def test_attention_refuses(dspark_lib):
     assert attend(lib, c, heads=258) == UNSUPPORTED
     assert attend(lib, c, seqs=4097) == UNSUPPORTED
     assert attend(lib, c, tokens=0) == 0 and attend(lib, c, seqs=0) == 0
+    assert lib.dspark_paged_attention(c, None, None) == INVALID and lib.dspark_rotary_append(c, None, None) == INVALID
+    assert lib.dspark_rotary(None, None) == INVALID
 
 
 def test_rotary_refuses(dspark_lib):
     lib, c = dspark_lib, cache()
-    for kw in (dict(turns=None), dict(turns=ODD), dict(layout=2), dict(stride=516), dict(tokens=-1)):
+    for kw in (dict(turns=0), dict(turns=ODD), dict(layout=2), dict(stride=516), dict(tokens=-1)):
         assert append(lib, c, **kw) == INVALID, kw
         assert turn(lib, **kw) == INVALID, kw
     for kw in (dict(dim=120), dict(dim=8), dict(dim=144), dict(dim=0)):
         assert append(lib, c, **kw) == UNSUPPORTED and turn(lib, **kw) == UNSUPPORTED, kw
-    for kw in (dict(layer=2), dict(k=None), dict(v=ODD), dict(q=None), dict(out=None), dict(cu=None), dict(seqs=-1)):
+    for kw in (dict(layer=2), dict(k=0), dict(v=ODD), dict(q=0), dict(out=0), dict(cu=0), dict(seqs=-1)):
         assert append(lib, c, **kw) == INVALID, kw
     assert append(lib, c, seqs=4097) == UNSUPPORTED
-    for kw in (dict(x=None), dict(y=ODD), dict(pos=None), dict(dtype=3), dict(heads=-1)):
+    for kw in (dict(x=0), dict(y=ODD), dict(pos=0), dict(dtype=3), dict(heads=-1)):
         assert turn(lib, **kw) == INVALID, kw
     assert turn(lib, head_dim=136) == UNSUPPORTED and turn(lib, head_dim=528) == UNSUPPORTED
     assert turn(lib, tokens=0) == 0 and turn(lib, heads=0) == 0 and append(lib, c, tokens=0) == 0
