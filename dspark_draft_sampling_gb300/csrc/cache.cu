@@ -75,13 +75,14 @@ __device__ int block_scan(int v, int *total, int *warp_sums) {
     return x - v + (warp ? warp_sums[warp - 1] : 0);
 }
 
-// The free pages among refs, kept by the threads that found them: thread t of block b holds the 16 pages from
-// (b * rounds + i) * 16384 + 16 t on for each round i of its block, the first kHeld rounds in registers, those of larger pools
-// in the scratch area (refs may have changed by the time they are wanted).
-constexpr int kPer = 16, kHeld = 4;
+// The free pages among refs, kept by the threads that found them: thread t of block b holds the 4 pages from
+// (b * rounds + i) * 4096 + 4 t on for each round i of its block, the first 16 rounds in a register, those of larger pools
+// in the scratch area (refs may have changed by the time they are wanted).  With few pages to a thread a block's stores to
+// the tables fall on few lines (16 pages to a thread took four times as long for 16,000 new pages).
+constexpr int kPer = 4, kHeld = 16;
 
-__device__ __forceinline__ unsigned short *scratch_bits(const CacheView &c) {
-    return reinterpret_cast<unsigned short *>(scratch_snapshot(c) + size_t(c.max_seqs < kMaxRows ? c.max_seqs : kMaxRows) * c.max_pages);
+__device__ __forceinline__ unsigned char *scratch_bits(const CacheView &c) {
+    return reinterpret_cast<unsigned char *>(scratch_snapshot(c) + size_t(c.max_seqs < kMaxRows ? c.max_seqs : kMaxRows) * c.max_pages);
 }
 __host__ __device__ inline int free_rounds(int num_pages) {
     constexpr int kRound = kBooksBlocks * kBooksThreads * kPer;
@@ -89,22 +90,17 @@ __host__ __device__ inline int free_rounds(int num_pages) {
 }
 
 struct FreePages {
-    unsigned held[kHeld];  // bits of free pages
-    int rounds, before, count;  // rounds of a block; free pages in earlier threads of the cluster (set by number()), in all
+    unsigned long long held;  // bits of free pages, four a round
+    int rounds, before, count;  // rounds of a block; free pages of earlier blocks, of all (set by find_free)
 };
 
 __device__ __forceinline__ unsigned free_bits(const CacheView &c, long long first) {
-    unsigned bits = 0;
     if (first + kPer <= c.num_pages) {
-        const int4 *r = reinterpret_cast<const int4 *>(c.refs + first);
-#pragma unroll
-        for (int q = 0; q < kPer / 4; ++q) {
-            const int4 v = r[q];
-            bits |= (unsigned(v.x == 0) | unsigned(v.y == 0) << 1 | unsigned(v.z == 0) << 2 | unsigned(v.w == 0) << 3) << (4 * q);
-        }
-    } else {
-        for (int q = 0; q < kPer && first + q < c.num_pages; ++q) bits |= unsigned(c.refs[first + q] == 0) << q;
+        const int4 v = *reinterpret_cast<const int4 *>(c.refs + first);
+        return unsigned(v.x == 0) | unsigned(v.y == 0) << 1 | unsigned(v.z == 0) << 2 | unsigned(v.w == 0) << 3;
     }
+    unsigned bits = 0;
+    for (int q = 0; q < kPer && first + q < c.num_pages; ++q) bits |= unsigned(c.refs[first + q] == 0) << q;
     return bits;
 }
 
@@ -116,15 +112,15 @@ __device__ __forceinline__ long long free_first(const FreePages &f, int round) {
 // Ends with a cluster barrier: refs may be changed after it.
 __device__ void find_free(const CacheView &c, FreePages *f, int *counts, int *warp_sums) {
     f->rounds = free_rounds(c.num_pages);
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        f->held[i] = i < f->rounds ? free_bits(c, free_first(*f, i)) : 0;
-        mine += __popc(f->held[i]);
-    }
+    f->held = 0;
+    const int held = min(f->rounds, kHeld);
+#pragma unroll 4
+    for (int i = 0; i < held; ++i) f->held |= static_cast<unsigned long long>(free_bits(c, free_first(*f, i))) << (kPer * i);
+    int mine = __popcll(f->held);
+#pragma unroll 4
     for (int i = kHeld; i < f->rounds; ++i) {
         const unsigned bits = free_bits(c, free_first(*f, i));
-        scratch_bits(c)[free_first(*f, i) / kPer] = static_cast<unsigned short>(bits);
+        scratch_bits(c)[free_first(*f, i) / kPer] = static_cast<unsigned char>(bits);
         mine += __popc(bits);
     }
     int total = 0;
@@ -147,11 +143,7 @@ template <typename Give>
 __device__ void give_free(const CacheView &c, const FreePages &f, int want, int *warp_sums, Give give) {
     int at = f.before;
     for (int i = 0; i < f.rounds && at < want; ++i) {  // the same number of turns for the whole block
-        unsigned bits = 0;
-#pragma unroll
-        for (int q = 0; q < kHeld; ++q)
-            if (i == q) bits = f.held[q];
-        if (i >= kHeld) bits = scratch_bits(c)[free_first(f, i) / kPer];
+        unsigned bits = i < kHeld ? static_cast<unsigned>(f.held >> (kPer * i)) & ((1u << kPer) - 1) : scratch_bits(c)[free_first(f, i) / kPer];
         int total = 0, n = at + block_scan(__popc(bits), &total, warp_sums);
         const int first = static_cast<int>(free_first(f, i));
         while (bits && n < want) {
@@ -282,8 +274,11 @@ __global__ void __cluster_dims__(kBooksBlocks, 1, 1) __launch_bounds__(kBooksThr
     for (int r = first; r < n; r += step) {
         if (s_src[r] == s_dst[r]) continue;
         const int *ts = c.table + size_t(s_src[r]) * c.max_pages, *td = c.table + size_t(s_dst[r]) * c.max_pages;
-        for (int j = lane; j < pages_of(c, s_len[r]); j += 32) snap[size_t(r) * c.max_pages + j] = ts[j];
-        for (int j = lane; j < pages_of(c, s_old[r]); j += 32) {
+        const int pages = pages_of(c, s_len[r]), old_pages = pages_of(c, s_old[r]);
+#pragma unroll 4
+        for (int j = lane; j < pages; j += 32) snap[size_t(r) * c.max_pages + j] = ts[j];
+#pragma unroll 4
+        for (int j = lane; j < old_pages; j += 32) {
             const int page = td[j];
             if (page_ok(c, page)) atomicSub(c.refs + page, 1);
         }
@@ -293,6 +288,7 @@ __global__ void __cluster_dims__(kBooksBlocks, 1, 1) __launch_bounds__(kBooksThr
         if (s_src[r] == s_dst[r]) continue;
         int *td = c.table + size_t(s_dst[r]) * c.max_pages;
         const int pages = pages_of(c, s_len[r]), whole = s_len[r] >> c.page_shift;
+#pragma unroll 4
         for (int j = lane; j < whole; j += 32) {
             const int page = snap[size_t(r) * c.max_pages + j];
             td[j] = page;
@@ -375,20 +371,25 @@ __global__ void __cluster_dims__(kBooksBlocks, 1, 1) __launch_bounds__(kBooksThr
     }
     __syncthreads();
     int *snap = scratch_snapshot(c), *needs = scratch_need(c);
-    const int first = cluster_block() * (kBooksThreads / 32) + (i >> 5), step = kBooksBlocks * (kBooksThreads / 32);
-    for (int r = first; r < n; r += step) {
-        const int st = s_start[r], k = s_new[r] - st, len = s_len[r];
+    // `per` warps of the cluster to a row, each with a stretch of its list and of its pages
+    constexpr int kWarps = kBooksBlocks * (kBooksThreads / 32);
+    const int warp = cluster_block() * (kBooksThreads / 32) + (i >> 5), per = max(1, kWarps / n), step = kWarps / per;
+    const int part = warp % per;
+    for (int r = warp / per; r < n && warp < step * per; r += step) {
+        const int st = s_start[r], k = s_new[r] - st, len = s_len[r], pages = pages_of(c, len);
         const int *w = kept + size_t(r) * kept_stride;
+        const int k1 = static_cast<int>(static_cast<long long>(k) * (part + 1) / per);
 #pragma unroll 4
-        for (int j = lane; j < k; j += 32) {
+        for (int j = static_cast<int>(static_cast<long long>(k) * part / per) + lane; j < k1; j += 32) {
             const int at = w[j];
             bad |= at < (j ? w[j - 1] + 1 : st) || at >= len;
         }
         const int *t = c.table + size_t(s_row[r]) * c.max_pages;
         const int lo = st >> c.page_shift, hi = pages_of(c, s_new[r]);
+        const int p1 = static_cast<int>(static_cast<long long>(pages) * (part + 1) / per);
         int need = 0;
 #pragma unroll 4
-        for (int j = lane; j < pages_of(c, len); j += 32) {
+        for (int j = static_cast<int>(static_cast<long long>(pages) * part / per) + lane; j < p1; j += 32) {
             const int page = t[j];
             const bool own = j >= lo && j < hi && page_ok(c, page) && c.refs[page] > 1;
             bad |= !page_ok(c, page);
@@ -396,7 +397,7 @@ __global__ void __cluster_dims__(kBooksBlocks, 1, 1) __launch_bounds__(kBooksThr
             need += own;
         }
         need = __reduce_add_sync(0xffffffffu, need);
-        if (lane == 0) needs[r] = need;
+        if (lane == 0) needs[r * per + part] = need;
     }
     // what one block found wrong, every block has to know
     if (bad) {
@@ -409,13 +410,18 @@ __global__ void __cluster_dims__(kBooksBlocks, 1, 1) __launch_bounds__(kBooksThr
     }
     find_free(c, &free, block_counts, warp_sums);  // its barrier also orders the needs and the flag
     int total = 0;
-    const int at = block_scan(i < n ? __ldcg(needs + i) : 0, &total, warp_sums);
+    int need = 0;
+    if (i < n)
+        for (int q = 0; q < per; ++q) need += __ldcg(needs + i * per + q);
+    const int at = block_scan(need, &total, warp_sums);
     if (i < n) s_at[i] = at;
     if (!decide(c, s_bad != 0, total > free.count)) return;
-    for (int r = first; r < n; r += step) {
+    for (int r = warp / per; r < n && warp < step * per; r += step) {
         int *t = c.table + size_t(s_row[r]) * c.max_pages;
         const int last = pages_of(c, s_new[r]), pages = pages_of(c, s_len[r]);
-        for (int j = lane; j < pages; j += 32) {
+        const int p1 = static_cast<int>(static_cast<long long>(pages) * (part + 1) / per);
+#pragma unroll 4
+        for (int j = static_cast<int>(static_cast<long long>(pages) * part / per) + lane; j < p1; j += 32) {
             const int entry = snap[size_t(r) * c.max_pages + j];
             if (entry & kShared) {
                 atomicSub(c.refs + (entry & ~kShared), 1);
@@ -424,7 +430,7 @@ __global__ void __cluster_dims__(kBooksBlocks, 1, 1) __launch_bounds__(kBooksThr
                 atomicSub(c.refs + entry, 1);
             }
         }
-        if (lane == 0) c.length[s_row[r]] = s_new[r];
+        if (lane == 0 && part == 0) c.length[s_row[r]] = s_new[r];
     }
     // the k-th new page of all is the row's (k - at)-th shared one's replacement
     give_free(c, free, total, warp_sums, [&](int k, int page) {
@@ -583,7 +589,7 @@ bool sizes_ok(const dspark_cache *c) {
 
 size_t cache_ops_scratch_bytes(int max_seqs, int max_pages, int num_pages) {
     const int rounds = free_rounds(num_pages);
-    const size_t bits = rounds > kHeld ? size_t(rounds) * kBooksBlocks * kBooksThreads * 2 : 0;
+    const size_t bits = rounds > kHeld ? size_t(rounds) * kBooksBlocks * kBooksThreads : 0;
     return up256(4 * (kMaxRows + snapshot_entries(max_seqs, max_pages)) + bits);
 }
 
@@ -657,9 +663,13 @@ extern "C" dspark_status dspark_cache_fork(const dspark_cache *cache, const int3
     if (st != DSPARK_OK || (st = check_rows("cache_fork", c, src, dst, n)) != DSPARK_OK || n == 0) return st;
     st = launched(launch_pdl(fork_books_kernel, dim3(kBooksBlocks), dim3(kBooksThreads), 0, stream, c, src, dst, n), "cache_fork");
     if (st != DSPARK_OK) return st;
-    // at most 2048 vectors a block, so that each thread's eight are in flight at once
-    const long long vecs = 2ll * c.layers * c.kv_heads * c.page_size * c.head_dim / 8;
-    const unsigned slices = static_cast<unsigned>(vecs / (kForkThreads * kForkVecs) < 1 ? 1 : vecs / (kForkThreads * kForkVecs) > 4096 ? 4096 : vecs / (kForkThreads * kForkVecs));
+    // Slices of a page: as many as give each thread its eight vectors of a full one, but not more blocks than four rounds
+    // of the SMs, as each begins with a chain of lookups.
+    int sms = 0;
+    if ((st = static_cast<dspark_status>(current_sm_count(&sms))) != DSPARK_OK) return st;
+    const long long full = 2ll * c.layers * c.kv_heads * c.page_size * c.head_dim / 8 / (kForkThreads * kForkVecs);
+    const long long most = 4ll * 6 * sms / n;
+    const unsigned slices = static_cast<unsigned>(full < 1 || most < 1 ? 1 : full < most ? full : most);
     return launched(launch_pdl(fork_copy_kernel, dim3(n, slices), dim3(kForkThreads), 0, stream, c, src, dst), "cache_fork");
 }
 
