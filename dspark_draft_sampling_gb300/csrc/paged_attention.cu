@@ -37,7 +37,7 @@ static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "
 constexpr int kTmemCols = 512;
 constexpr size_t kSmemData = 224 * 1024;      // query tiles and the ring of key and value tiles
 constexpr size_t kSmemBytes = 227 * 1024;
-constexpr int kItemCost = 1;                  // an item's fixed cost, in key tiles
+constexpr int kItemCost = 2;                  // an item's fixed cost, in key tiles
 constexpr float kRescale = 8.f;               // powers of two by which a row's maximum may lag
 
 struct Attention {
@@ -96,6 +96,13 @@ __device__ __forceinline__ void key_tiles(const Attention &g, const Seq &q, int 
     *hi = (end + kTile - 1) / kTile;
     *lo = min(begin / kTile, *hi);
     if (begin >= end) *lo = *hi;
+}
+
+// What an item counts among all tiles.
+__device__ __forceinline__ int item_cost(const Attention &g, const Seq &q, int i, int step) {
+    int lo, hi;
+    key_tiles(g, q, i, step, &lo, &hi);
+    return kItemCost + hi - lo;
 }
 
 // One stretch of an item that a block works on, as the copying warp hands it to the others.
@@ -165,14 +172,6 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
     }
     return q;
 }
-
-// Where a block's range begins, found by one warp from the sequences' costs.  Every block takes `per` tiles (the last one what is
-// left, blocks behind it none).
-struct Start {
-    long long per, begin, end, x;
-    Seq q;
-    int s, kv_head, i;
-};
 
 __device__ __forceinline__ long long warp_sum(long long v) {
 #pragma unroll
@@ -356,7 +355,7 @@ struct Control {
     Segment segs[kSegments];
     uint32_t tmem, aborted;
     unsigned last[2];
-    Start start;
+    long long per;      // key tiles of a block (the last one takes what is left, blocks behind it none)
     float max_sum[2][2][kTile];  // [stream][maximum, sum][row], one query tile's two streams
 };
 
@@ -405,6 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int step = g.tile_tokens * S::QT;  // tokens of an item
 
     if (warp == 8 && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_kv)) : "memory");
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&ctl->full[i], 1);
             mbar_init(&ctl->empty[i], 1);
@@ -430,108 +431,89 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) tmem_alloc(&ctl->tmem, kTmemCols);
     pdl_launch_dependents();
     pdl_wait();  // no global-memory access before this point
-
-    // ---- every sequence's cost, then this block's range (the ring serves as scratch) ----
-    {
-        long long *cost = reinterpret_cast<long long *>(ring_ptr);
-        if (g.chunk_tiles <= 1) {
-            for (int s = threadIdx.x; s < g.n_seqs; s += kThreads) {
-                const Seq q = load_seq(c, g, s);
-                long long w = 0;
-                for (int i = 0; i * step < q.n; ++i) {
-                    int lo, hi;
-                    key_tiles(g, q, i, step, &lo, &hi);
-                    w += kItemCost + hi - lo;
-                }
-                cost[s] = w;
-            }
-        } else {
-            for (int s = warp; s < g.n_seqs; s += kThreads / 32) {
-                const Seq q = load_seq(c, g, s);
-                long long w = 0;
-                for (int i = lane; i * step < q.n; i += 32) {
-                    int lo, hi;
-                    key_tiles(g, q, i, step, &lo, &hi);
-                    w += kItemCost + hi - lo;
-                }
-                w = warp_sum(w);
-                if (lane == 0) cost[s] = w;
-            }
+    // Every sequence's cost.  Up to 32 sequences of few query tiles are left to the copying warp, a lane each.
+    long long *cost = reinterpret_cast<long long *>(ring_ptr);  // the ring serves as scratch until the first copy
+    const bool few = g.n_seqs <= 32 && g.chunk_tiles <= 4;
+    if (!few) {
+        const int of_seq = g.chunk_tiles <= 4 ? 1 : 32;  // threads to a sequence
+        for (int s = threadIdx.x / of_seq; s < g.n_seqs; s += kThreads / of_seq) {
+            const Seq q = load_seq(c, g, s);
+            long long w = 0;
+            for (int i = threadIdx.x % of_seq; i * step < q.n; i += of_seq) w += item_cost(g, q, i, step);
+            if (of_seq == 32) w = warp_sum(w);
+            if (threadIdx.x % of_seq == 0) cost[s] = w;
         }
-        __syncthreads();
-        if (warp == 0) {
-            long long total = 0;
-            for (int s = lane; s < g.n_seqs; s += 32) total += cost[s];
-            total = warp_sum(total) * c.kv_heads;
-            Start st{};
-            st.per = divide(total + gridDim.x - 1, gridDim.x);
-            st.begin = min(st.per * blockIdx.x, total);
-            st.end = min(st.begin + st.per, total);
-            if (st.begin < st.end) {
-                long long before = 0;
-                for (int s0 = 0; s0 < g.n_seqs; s0 += 32) {
-                    const long long v = s0 + lane < g.n_seqs ? cost[s0 + lane] * c.kv_heads : 0;
-                    const long long upto = before + warp_scan(v, lane);
-                    const unsigned past = __ballot_sync(0xffffffffu, upto > st.begin);
-                    if (past) {
-                        const int l = __ffs(past) - 1;
-                        st.s = s0 + l;
-                        before = __shfl_sync(0xffffffffu, upto - v, l);
-                        break;
-                    }
-                    before = __shfl_sync(0xffffffffu, upto, 31);
-                }
-                const Seq q = load_seq(c, g, st.s);
-                st.q = q;
-                const long long w = cost[st.s];
-                st.kv_head = static_cast<int>(divide(st.begin - before, w));
-                long long rem = st.begin - before - st.kv_head * w;
-                for (int i0 = 0;; i0 += 32) {  // the item that holds the range's first tile
-                    long long v = 0;
-                    if ((i0 + lane) * step < q.n) {
-                        int lo, hi;
-                        key_tiles(g, q, i0 + lane, step, &lo, &hi);
-                        v = kItemCost + hi - lo;
-                    }
-                    const long long upto = warp_scan(v, lane);
-                    const unsigned past = __ballot_sync(0xffffffffu, upto > rem);
-                    if (past) {
-                        const int l = __ffs(past) - 1;
-                        st.i = i0 + l;
-                        st.x = rem - __shfl_sync(0xffffffffu, upto - v, l);
-                        break;
-                    }
-                    rem -= __shfl_sync(0xffffffffu, upto, 31);
-                    if (i0 * step >= q.n) break;  // not reached: rem lies within the sequence
-                }
-            }
-            if (lane == 0) ctl->start = st;
-        }
+        fence_proxy_async_smem();  // the scratch use comes before the copies into the ring
     }
-    fence_proxy_async_smem();  // the scratch use of the ring comes before the copies into it
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem;
+
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8) {
         // ---- copies: query tiles, then keys and values of each tile through the ring; a lane to a page ----
         const int box = min(c.page_size, kTile), per_tile = kTile / box;
         uint32_t n_q = 0, n_seg = 0, put = 0;  // segments with keys, segments, ring entries so far
-        const Start st = ctl->start;
         Walk walk;
         walk.left = 0;
-        if (st.begin < st.end) {
-            walk.s = st.s;
-            walk.q = st.q;
-            walk.kv_head = st.kv_head;
-            walk.i = st.i;
-            walk.step = step;
-            walk.n_tiles = (walk.q.n + step - 1) / step;
-            walk.x = st.x;
-            walk.pos = st.begin;
-            walk.left = st.end - st.begin;
+        walk.step = step;
+        {
+            // ---- this block's range of all items' tiles, and the item that it begins with ----
+            Seq mine{};
+            long long w = 0;
+            if (few && lane < g.n_seqs) {
+                mine = load_seq(c, g, lane);
+                for (int i = 0; i * step < mine.n; ++i) w += item_cost(g, mine, i, step);
+            }
+            long long total = few ? w : 0;
+            if (!few)
+                for (int s = lane; s < g.n_seqs; s += 32) total += cost[s];
+            total = warp_sum(total) * c.kv_heads;
+            const long long per = divide(total + gridDim.x - 1, gridDim.x);
+            if (lane == 0) ctl->per = per;
+            walk.pos = min(per * blockIdx.x, total);
+            walk.left = min(walk.pos + per, total) - walk.pos;
+            if (walk.left > 0) {
+                long long before = 0;
+                for (int s0 = 0;; s0 += 32) {
+                    if (!few) w = s0 + lane < g.n_seqs ? cost[s0 + lane] : 0;
+                    const long long upto = before + warp_scan(w, lane) * c.kv_heads;
+                    const unsigned past = __ballot_sync(0xffffffffu, upto > walk.pos);
+                    if (past || s0 + 32 >= g.n_seqs) {  // the range lies within the sequences: found in the last stretch at the latest
+                        const int l = past ? __ffs(past) - 1 : 0;
+                        walk.s = s0 + l;
+                        w = __shfl_sync(0xffffffffu, w, l);
+                        before = __shfl_sync(0xffffffffu, upto, l) - w * c.kv_heads;
+                        if (few) {
+                            walk.q.row = __shfl_sync(0xffffffffu, mine.row, l);
+                            walk.q.n = __shfl_sync(0xffffffffu, mine.n, l);
+                            walk.q.length = __shfl_sync(0xffffffffu, mine.length, l);
+                            walk.q.q0 = __shfl_sync(0xffffffffu, mine.q0, l);
+                        } else {
+                            walk.q = load_seq(c, g, walk.s);
+                        }
+                        break;
+                    }
+                    before = __shfl_sync(0xffffffffu, upto, 31);
+                }
+                walk.n_tiles = (walk.q.n + step - 1) / step;
+                walk.kv_head = static_cast<int>(divide(walk.pos - before, w));
+                long long rem = walk.pos - before - walk.kv_head * w;
+                for (int i0 = 0; i0 < walk.n_tiles; i0 += 32) {
+                    const long long v = i0 + lane < walk.n_tiles ? item_cost(g, walk.q, i0 + lane, step) : 0;
+                    const long long upto = warp_scan(v, lane);
+                    const unsigned past = __ballot_sync(0xffffffffu, upto > rem);
+                    if (past) {
+                        const int l = __ffs(past) - 1;
+                        walk.i = i0 + l;
+                        walk.x = rem - __shfl_sync(0xffffffffu, upto - v, l);
+                        break;
+                    }
+                    rem -= __shfl_sync(0xffffffffu, upto, 31);
+                }
+            }
         }
         bool ok = true;
         for (bool more = true; ok && more;) {
@@ -857,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int cf = 0, cl = 0;
             float *slot = nullptr;
             if (!whole) {
-                const long long per = ctl->start.per;
+                const long long per = ctl->per;
                 cf = cl = blockIdx.x;
                 if (seg.first != 0) cf = static_cast<int>(divide(seg.at + kItemCost, per));
                 if (seg.last != seg.tiles) cl = static_cast<int>(divide(seg.at + kItemCost + seg.tiles - 1, per));
@@ -976,10 +958,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (g.lse && (joiner >> shift) == 0 && my_row == row)
                 g.lse[qt * (c.kv_heads * g.group) + hd] = z == 0.f ? -INFINITY : (top * sc + lg2(z)) * 0.6931471805599453f;
             const int c4 = my_row == row ? joiner >> shift : D / 4;
-            if (c4_step * 4 <= D / 4)
+            // Eight to sixteen vectors in flight a thread: two parts are the rule where query tiles fill their rows; with few rows there may be
+            // many parts.
+            if (PAIR)
+                join_columns<BF16, D, S::QT, 8, 2>(parts, cf, cl, row, c4, c4_step, top, f, sc, to);
+            else if (c4_step * 2 <= D / 4)
                 join_columns<BF16, D, S::QT, 4, 2>(parts, cf, cl, row, c4, c4_step, top, f, sc, to);
             else
-                join_columns<BF16, D, S::QT, 1, 8>(parts, cf, cl, row, c4, c4_step, top, f, sc, to);
+                join_columns<BF16, D, S::QT, 1, 16>(parts, cf, cl, row, c4, c4_step, top, f, sc, to);
         }
     }
     tc_fence_before();
