@@ -50,7 +50,8 @@ struct Attention {
     float scale;
     float *partials;
     unsigned *arrivals;
-    unsigned long long timeout_ns, stall_ns;
+    unsigned long long timeout_ns, stall_ns;  // of waits at the block's end, of the debug entry's
+    uint32_t tries;                            // of the pipeline's waits
 };
 
 template <int D, bool PAIR>
@@ -75,14 +76,14 @@ __device__ __forceinline__ Seq load_seq(const CacheView &c, const Attention &g, 
     q.n = max(b - a, 0);
     q.row = g.rows ? g.rows[s] : s;
     q.length = 0;
-    const long long most = static_cast<long long>(c.max_pages) * c.page_size;
+    const int most = c.max_pages << c.page_shift;  // below 2^30
     bool bad = static_cast<unsigned>(q.row) >= static_cast<unsigned>(c.max_seqs);
     if (bad) {
         q.row = 0;
     } else {
-        q.length = c.length[q.row];
-        bad = q.length < 0 || q.length > most;
-        q.length = static_cast<int>(min(max(static_cast<long long>(q.length), 0ll), most));
+        const int length = c.length[q.row];
+        q.length = min(max(length, 0), most);
+        bad = q.length != length;
     }
     if (bad && q.n > 0) atomicOr(c.status, kStatusIndex);
     return q;
@@ -111,14 +112,15 @@ struct Segment {
     int lo, first, last;      // the item's first key tile; the stretch's, relative to it
     int tiles;                // of the whole item; -1: no more segments
     int q0, n, length;        // the sequence's first query token, its new tokens, its tokens
-    long long at;             // the item's place in the sequence of all tiles
+    int cf, cl;               // first and last block that work on the item (where that is more than one)
 };
 
 // Walks a block's range.
 struct Walk {
     Seq q;
     int s, kv_head, i, n_tiles, step;
-    long long x, left, pos;  // x: place within the item; pos: absolute place
+    unsigned per;              // key tiles of a block (the last one takes what is left, blocks behind it none)
+    unsigned x, left, pos, at; // x: place within the item; pos: absolute place; at: the last segment's item's
 
     __device__ __forceinline__ bool next(const CacheView &c, const Attention &g, Segment *out) {
         while (left > 0) {
@@ -135,18 +137,17 @@ struct Walk {
             int lo, hi;
             key_tiles(g, q, i, step, &lo, &hi);
             const int tiles = hi - lo;
-            const long long size = kItemCost + tiles;
-            const long long take = min(left, size - x);
+            const unsigned take = min(left, kItemCost + tiles - x);
             out->kv_head = kv_head;
             out->tile = i;
             out->lo = lo;
             out->tiles = tiles;
-            out->first = static_cast<int>(max(x - kItemCost, 0ll));
-            out->last = static_cast<int>(max(x + take - kItemCost, 0ll));
+            out->first = max(static_cast<int>(x) - kItemCost, 0);
+            out->last = max(static_cast<int>(x + take) - kItemCost, 0);
             out->q0 = q.q0;
             out->n = q.n;
             out->length = q.length;
-            out->at = pos - x;
+            at = pos - x;
             const bool starts = x == 0;
             left -= take;
             pos += take;
@@ -158,31 +159,10 @@ struct Walk {
     }
 };
 
-// a / b for a >= 0, b > 0: in 32 bits wherever it fits, as the 64-bit division is a long routine that every block's start would
-// wait for; otherwise an estimate in floating point, corrected until the remainder is right.
-__device__ __forceinline__ long long divide(long long a, long long b) {
-    if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
-    const float inverse = 1.f / static_cast<float>(b);
-    long long q = 0, r = a;
-#pragma unroll 1
-    while (r < 0 || r >= b) {
-        const long long step = max(1ll, static_cast<long long>(static_cast<float>(r < 0 ? -r : r) * inverse));
-        q += r < 0 ? -step : step;
-        r = a - q * b;
-    }
-    return q;
-}
-
-__device__ __forceinline__ long long warp_sum(long long v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-__device__ __forceinline__ long long warp_scan(long long v, int lane) {
+__device__ __forceinline__ unsigned warp_scan(unsigned v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, v, o);
+        const unsigned y = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += y;
     }
     return v;
@@ -261,13 +241,22 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t *v) {
         : "memory");
 }
 
-// Scores of keys key0 .. key0 + 31 that a row does not see become -infinity; skipped where every row sees all.
-__device__ __forceinline__ void mask_keys(uint32_t *v, int key0, int see_lo, int see_hi) {
-    if (!__any_sync(0xffffffffu, key0 < see_lo || key0 + 32 > see_hi)) return;
-    const int lo = see_lo - key0, hi = see_hi - key0;
+// Lane l of four holds w[0..3] of its row; afterwards w[k] is the l-th of lane k's.
+__device__ __forceinline__ void transpose_4(uint32_t (&w)[4][4], int lane) {
 #pragma unroll
-    for (int q = 0; q < 32; ++q)
-        if (q < lo || q >= hi) v[q] = 0xff800000u;
+    for (int by = 1; by <= 2; by *= 2) {
+        const bool upper = (lane & by) != 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j & by) continue;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? w[j][x] : w[j + by][x], by);
+                if (upper) w[j][x] = got;
+                else w[j + by][x] = got;
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
@@ -355,33 +344,43 @@ struct Control {
     Segment segs[kSegments];
     uint32_t tmem, aborted;
     unsigned last[2];
-    long long per;      // key tiles of a block (the last one takes what is left, blocks behind it none)
     float max_sum[2][2][kTile];  // [stream][maximum, sum][row], one query tile's two streams
 };
 
-// A whole warp waits.  The lanes decide together at every turn, so that the warp stays converged: with
-// each lane in a loop of its own the code behind the wait ran in pieces.
+// As mbar_try_wait, suspended for up to `ns` nanoseconds.
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t *bar, uint32_t parity, uint32_t ns) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(ns)
+        : "memory");
+    return ok != 0;
+}
+
+// A whole warp waits, `tries` times 1000 ns at most.  The lanes decide together at every turn, so that the warp stays converged:
+// with each lane in a loop of its own the code behind the wait ran in pieces.  Turns are counted, as reading the clock takes longer than
+// most waits and as this code stands in many places.
 template <typename C>
-__device__ __forceinline__ bool warp_wait(C *ctl, uint64_t *bar, uint32_t parity, const CacheView &c, unsigned long long timeout_ns) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    const unsigned long long t0 = global_timer_ns();
-    volatile uint32_t *aborted = &ctl->aborted;
-    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
-        const bool late = global_timer_ns() - t0 > timeout_ns;
-        if (late) {
-            *aborted = 1;
+__device__ __forceinline__ bool warp_wait(C *ctl, uint64_t *bar, uint32_t parity, const CacheView &c, uint32_t tries) {
+#pragma unroll 1
+    for (; !__all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, 1000)); --tries) {
+        if (tries == 0) {
+            *static_cast<volatile uint32_t *>(&ctl->aborted) = 1;
             atomicOr(c.status, kStatusTimeout);
         }
-        if (__any_sync(0xffffffffu, late || *aborted)) return false;
+        if (__any_sync(0xffffffffu, *static_cast<volatile uint32_t *>(&ctl->aborted))) return false;
     }
     return true;
 }
 
 // The next segment, read by one warp.
 template <typename C>
-__device__ __forceinline__ bool next_segment(C *ctl, uint32_t &n_seg, Segment *seg, const CacheView &c, unsigned long long timeout_ns) {
+__device__ __forceinline__ bool next_segment(C *ctl, uint32_t &n_seg, Segment *seg, const CacheView &c, uint32_t tries) {
     const uint32_t slot = n_seg % kSegments;
-    if (!warp_wait(ctl, &ctl->seg_full[slot], (n_seg / kSegments) & 1, c, timeout_ns)) return false;
+    if (!warp_wait(ctl, &ctl->seg_full[slot], (n_seg / kSegments) & 1, c, tries)) return false;
     ++n_seg;
     *seg = ctl->segs[slot];
     __syncwarp();
@@ -432,15 +431,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     pdl_wait();  // no global-memory access before this point
     // Every sequence's cost.  Up to 32 sequences of few query tiles are left to the copying warp, a lane each.
-    long long *cost = reinterpret_cast<long long *>(ring_ptr);  // the ring serves as scratch until the first copy
+    unsigned *cost = reinterpret_cast<unsigned *>(ring_ptr);  // the ring serves as scratch until the first copy
     const bool few = g.n_seqs <= 32 && g.chunk_tiles <= 4;
     if (!few) {
         const int of_seq = g.chunk_tiles <= 4 ? 1 : 32;  // threads to a sequence
         for (int s = threadIdx.x / of_seq; s < g.n_seqs; s += kThreads / of_seq) {
             const Seq q = load_seq(c, g, s);
-            long long w = 0;
+            unsigned w = 0;
             for (int i = threadIdx.x % of_seq; i * step < q.n; i += of_seq) w += item_cost(g, q, i, step);
-            if (of_seq == 32) w = warp_sum(w);
+            if (of_seq == 32) w = __reduce_add_sync(0xffffffffu, w);
             if (threadIdx.x % of_seq == 0) cost[s] = w;
         }
         fence_proxy_async_smem();  // the scratch use comes before the copies into the ring
@@ -461,49 +460,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         walk.step = step;
         {
             // ---- this block's range of all items' tiles, and the item that it begins with ----
+            // in 32 bits: the host has made sure that the tiles' number fits
             Seq mine{};
-            long long w = 0;
+            unsigned w = 0;
             if (few && lane < g.n_seqs) {
                 mine = load_seq(c, g, lane);
                 for (int i = 0; i * step < mine.n; ++i) w += item_cost(g, mine, i, step);
             }
-            long long total = few ? w : 0;
+            unsigned total = few ? w : 0;
             if (!few)
                 for (int s = lane; s < g.n_seqs; s += 32) total += cost[s];
-            total = warp_sum(total) * c.kv_heads;
-            const long long per = divide(total + gridDim.x - 1, gridDim.x);
-            if (lane == 0) ctl->per = per;
+            total = __reduce_add_sync(0xffffffffu, total) * c.kv_heads;
+            const unsigned per = (total + gridDim.x - 1) / gridDim.x;
+            walk.per = per;
             walk.pos = min(per * blockIdx.x, total);
-            walk.left = min(walk.pos + per, total) - walk.pos;
+            walk.left = min(per, total - walk.pos);
             if (walk.left > 0) {
-                long long before = 0;
+                unsigned before = 0;
                 for (int s0 = 0;; s0 += 32) {
                     if (!few) w = s0 + lane < g.n_seqs ? cost[s0 + lane] : 0;
-                    const long long upto = before + warp_scan(w, lane) * c.kv_heads;
+                    const unsigned upto = before + warp_scan(w, lane) * c.kv_heads;
                     const unsigned past = __ballot_sync(0xffffffffu, upto > walk.pos);
                     if (past || s0 + 32 >= g.n_seqs) {  // the range lies within the sequences: found in the last stretch at the latest
                         const int l = past ? __ffs(past) - 1 : 0;
                         walk.s = s0 + l;
                         w = __shfl_sync(0xffffffffu, w, l);
                         before = __shfl_sync(0xffffffffu, upto, l) - w * c.kv_heads;
-                        if (few) {
-                            walk.q.row = __shfl_sync(0xffffffffu, mine.row, l);
-                            walk.q.n = __shfl_sync(0xffffffffu, mine.n, l);
-                            walk.q.length = __shfl_sync(0xffffffffu, mine.length, l);
-                            walk.q.q0 = __shfl_sync(0xffffffffu, mine.q0, l);
-                        } else {
-                            walk.q = load_seq(c, g, walk.s);
-                        }
+                        if (!few) mine = load_seq(c, g, s0 + lane < g.n_seqs ? s0 + lane : walk.s);
+                        walk.q.row = __shfl_sync(0xffffffffu, mine.row, l);
+                        walk.q.n = __shfl_sync(0xffffffffu, mine.n, l);
+                        walk.q.length = __shfl_sync(0xffffffffu, mine.length, l);
+                        walk.q.q0 = __shfl_sync(0xffffffffu, mine.q0, l);
                         break;
                     }
                     before = __shfl_sync(0xffffffffu, upto, 31);
                 }
                 walk.n_tiles = (walk.q.n + step - 1) / step;
-                walk.kv_head = static_cast<int>(divide(walk.pos - before, w));
-                long long rem = walk.pos - before - walk.kv_head * w;
+                walk.kv_head = (walk.pos - before) / w;
+                unsigned rem = walk.pos - before - walk.kv_head * w;
                 for (int i0 = 0; i0 < walk.n_tiles; i0 += 32) {
-                    const long long v = i0 + lane < walk.n_tiles ? item_cost(g, walk.q, i0 + lane, step) : 0;
-                    const long long upto = warp_scan(v, lane);
+                    const unsigned v = i0 + lane < walk.n_tiles ? item_cost(g, walk.q, i0 + lane, step) : 0;
+                    const unsigned upto = warp_scan(v, lane);
                     const unsigned past = __ballot_sync(0xffffffffu, upto > rem);
                     if (past) {
                         const int l = __ffs(past) - 1;
@@ -520,8 +517,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             Segment seg;
             more = walk.next(c, g, &seg);
             if (!more) seg.tiles = -1;
+            seg.cf = seg.cl = blockIdx.x;
+            if (more && (seg.first != 0 || seg.last != seg.tiles)) {
+                if (seg.first != 0) seg.cf = (walk.at + kItemCost) / walk.per;
+                if (seg.last != seg.tiles) seg.cl = (walk.at + kItemCost + seg.tiles - 1) / walk.per;
+            }
             const uint32_t entry = n_seg % kSegments;
-            if (n_seg >= kSegments && !(ok = warp_wait(ctl, &ctl->seg_empty[entry], ((n_seg / kSegments) & 1) ^ 1, c, g.timeout_ns))) break;
+            if (n_seg >= kSegments && !(ok = warp_wait(ctl, &ctl->seg_empty[entry], ((n_seg / kSegments) & 1) ^ 1, c, g.tries))) break;
             ++n_seg;
             if (lane == 0) {
                 ctl->segs[entry] = seg;
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (!more || seg.tiles == 0) continue;
-            if (n_q > 0 && !(ok = warp_wait(ctl, &ctl->q_empty, (n_q - 1) & 1, c, g.timeout_ns))) break;
+            if (n_q > 0 && !(ok = warp_wait(ctl, &ctl->q_empty, (n_q - 1) & 1, c, g.tries))) break;
             ++n_q;
             const int token = seg.q0 + seg.tile * step;
             if (lane == 0) {
@@ -557,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int slot = key & (c.page_size - 1);  // pages longer than a tile
                 for (int w = 0; w < 2; ++w, ++put) {
                     const uint32_t st = put % S::kStages;
-                    if (put >= S::kStages && !(ok = warp_wait(ctl, &ctl->empty[st], ((put / S::kStages) & 1) ^ 1, c, g.timeout_ns))) break;
+                    if (put >= S::kStages && !(ok = warp_wait(ctl, &ctl->empty[st], ((put / S::kStages) & 1) ^ 1, c, g.tries))) break;
                     if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], boxes * static_cast<uint32_t>(box) * D * 2);
                     __syncwarp();
                     if (mine)
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t turn = p / S::kStages;
             return Entry{__shfl_sync(0xffffffffu, p - turn * S::kStages, 0), turn & 1};
         };
-        auto ready = [&](uint64_t *bar, uint32_t phase) { return warp_wait(ctl, bar, phase, c, g.timeout_ns); };
+        auto ready = [&](uint64_t *bar, uint32_t phase) { return warp_wait(ctl, bar, phase, c, g.tries); };
         auto issue_scores = [&](const int s, const Entry &e, bool frees_q) {
             const uint64_t a = smem_desc_sw128(q_smem + (PAIR ? s * S::kTileBytes : 0));
             const uint64_t b = smem_desc_sw128(ring + e.st * S::kTileBytes);
@@ -631,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return true;
         };
-        while (ok && next_segment(ctl, n_seg, &seg, c, g.timeout_ns)) {
+        while (ok && next_segment(ctl, n_seg, &seg, c, g.tries)) {
             if (seg.tiles == 0) continue;
             const int nt = seg.last - seg.first;
             const int steps0 = PAIR ? nt : (nt + 1) / 2, steps1 = PAIR ? nt : nt / 2;
@@ -687,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         if (g.stall_ns && !mbar_wait(&ctl->never, 0, g.stall_ns) && warp == 0 && lane == 0) atomicOr(c.status, kStatusTimeout);
         Segment seg;
-        while (ok && next_segment(ctl, n_seg, &seg, c, g.timeout_ns)) {
+        while (ok && next_segment(ctl, n_seg, &seg, c, g.tries)) {
             const int nt = seg.last - seg.first;
             const int token = seg.tile * step + (PAIR ? s * g.tile_tokens : 0) + row_token;  // of the chunk
             const bool real = row_token < g.tile_tokens && token < seg.n;
@@ -701,13 +703,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < steps && ok; ++i) {
                 const int t = PAIR ? i : 2 * i + s;
                 const int key0 = (seg.lo + seg.first + t) * kTile;
-                if (!(ok = warp_wait(ctl, &ctl->s_full[s], n_s & 1, c, g.timeout_ns))) break;
+                if (!(ok = warp_wait(ctl, &ctl->s_full[s], n_s & 1, c, g.tries))) break;
                 ++n_s;
                 tc_fence_after();
                 if (key0 + kTile > seg.length) {
                     // values behind the row's length are whatever the page holds: zeros, so that weights of 0 stay 0
                     const uint32_t p = 2 * (base + t) + 1, st = p % S::kStages;
-                    if (!(ok = warp_wait(ctl, &ctl->full[st], (p / S::kStages) & 1, c, g.timeout_ns))) break;
+                    if (!(ok = warp_wait(ctl, &ctl->full[st], (p / S::kStages) & 1, c, g.tries))) break;
                     const int used = seg.length - key0;
                     unsigned char *v = ring_ptr + st * S::kTileBytes;
                     for (int h = 0; h < S::kHalves; ++h)
@@ -719,13 +721,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t v[kTile];
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     const bool edge = __any_sync(0xffffffffu, key0 < see_lo || key0 + kTile > see_hi);
+                    if (edge) {
+                        // masked in place, a quarter at a time: few tiles have an edge, and their code stands here once
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q) {
+                            const int lo = see_lo - key0 - q * 32, hi = see_hi - key0 - q * 32;
+                            if (!__any_sync(0xffffffffu, lo > 0 || hi < 32)) continue;
+                            uint32_t w[32];
+                            tmem_ld_32(t_s + q * 32, w);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int u = 0; u < 32; ++u)
+                                if (u < lo || u >= hi) w[u] = 0xff800000u;
+                            tmem_st_32(t_s + q * 32, w);
+                        }
+                        tmem_wait_st();
+                    }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) tmem_ld_32(t_s + q * 32, v + q * 32);
                     tmem_wait_ld();
-                    if (edge) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) mask_keys(v + q * 32, key0 + q * 32, see_lo, see_hi);
-                    }
 #pragma unroll
                     for (int q = 0; q < kTile; q += 8) {
 #pragma unroll
@@ -739,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float keep = m == -INFINITY ? 0.f : ex2((m - up) * sc);
                         if (i > 0) {
                             // the scores' arrival also says that this stream's earlier second products are done
-#pragma unroll
+#pragma unroll 1
                             for (int q = 0; q < D / 16; ++q) {
                                 uint32_t o[16];
                                 tmem_ld_16(t_o + q * 16, o);
@@ -809,10 +823,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             // the O that this thread reads: its stream's, or (a query tile over two streams) both
             if (PAIR) {
-                if (nt > 0) ok = warp_wait(ctl, &ctl->o_full[s], n_o0++ & 1, c, g.timeout_ns);
+                if (nt > 0) ok = warp_wait(ctl, &ctl->o_full[s], n_o0++ & 1, c, g.tries);
             } else {
-                if (nt > 0) ok = warp_wait(ctl, &ctl->o_full[0], n_o0++ & 1, c, g.timeout_ns);
-                if (ok && nt > 1) ok = warp_wait(ctl, &ctl->o_full[1], n_o1++ & 1, c, g.timeout_ns);
+                if (nt > 0) ok = warp_wait(ctl, &ctl->o_full[0], n_o0++ & 1, c, g.tries);
+                if (ok && nt > 1) ok = warp_wait(ctl, &ctl->o_full[1], n_o1++ & 1, c, g.tries);
             }
             if (!ok) break;
             tc_fence_after();
@@ -825,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ctl->max_sum[s][0][r] = m;
                 ctl->max_sum[s][1][r] = l;
                 mbar_arrive(&ctl->sync[0]);
-                if (!(ok = warp_wait(ctl, &ctl->sync[0], n_sync & 1, c, g.timeout_ns))) break;
+                if (!(ok = warp_wait(ctl, &ctl->sync[0], n_sync & 1, c, g.tries))) break;
                 ++n_sync;
                 const float m0 = ctl->max_sum[0][0][r], m1 = ctl->max_sum[1][0][r];
                 m = fmaxf(m0, m1);
@@ -839,10 +853,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int cf = 0, cl = 0;
             float *slot = nullptr;
             if (!whole) {
-                const long long per = ctl->per;
-                cf = cl = blockIdx.x;
-                if (seg.first != 0) cf = static_cast<int>(divide(seg.at + kItemCost, per));
-                if (seg.last != seg.tiles) cl = static_cast<int>(divide(seg.at + kItemCost + seg.tiles - 1, per));
+                cf = seg.cf;
+                cl = seg.cl;
                 const size_t index = (size_t(blockIdx.x) * 2 + (static_cast<int>(blockIdx.x) == cf ? 1 : 0)) * S::QT + (PAIR ? s : 0);
                 slot = g.partials + index * S::kSlotFloats;
             }
@@ -854,8 +866,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                       static_cast<long long>(out_head) * g.out_head;
             }
             const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays
-            if (warp_real) {
+            // Four lanes exchange their rows' quarters of 32 columns, so that a store instruction writes 64 bytes of each of eight rows
+            // instead of 16 of each of 32.
+            unsigned long long row_to[4];
 #pragma unroll
+            for (int k = 0; k < 4; ++k) row_to[k] = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), (lane & ~3) + k);
+            if (warp_real) {
+#pragma unroll 1
                 for (int q = 0; q < kCols / 32; ++q) {
                     float o[32];
                     if (PAIR) {
@@ -875,14 +892,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             o[u] = (use0 ? __uint_as_float(a[u]) * keep0 : 0.f) + (use1 ? __uint_as_float(b[u]) * keep1 : 0.f);
                     }
                     if (whole) {
-                        if (real) {
+                        uint32_t w[4][4];
 #pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                *reinterpret_cast<uint4 *>(out + c0 + q * 32 + u * 8) = make_uint4(
-                                    pack16<BF16>(o[8 * u] * inv, o[8 * u + 1] * inv), pack16<BF16>(o[8 * u + 2] * inv, o[8 * u + 3] * inv),
-                                    pack16<BF16>(o[8 * u + 4] * inv, o[8 * u + 5] * inv),
-                                    pack16<BF16>(o[8 * u + 6] * inv, o[8 * u + 7] * inv));
-                        }
+                        for (int u = 0; u < 16; ++u) w[u / 4][u % 4] = pack16<BF16>(o[2 * u] * inv, o[2 * u + 1] * inv);
+                        transpose_4(w, lane);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (row_to[k] != 0)
+                                *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned short *>(row_to[k]) + c0 + q * 32 + (lane & 3) * 8) =
+                                    make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
                     } else if (real) {
 #pragma unroll
                         for (int u = 0; u < 8; ++u)
@@ -897,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         l == 0.f ? -INFINITY : (m * sc + lg2(l)) * 0.6931471805599453f;
                 if (!PAIR) {  // the other stream's O has been read before it is written again
                     mbar_arrive(&ctl->sync[0]);
-                    if (!(ok = warp_wait(ctl, &ctl->sync[0], n_sync & 1, c, g.timeout_ns))) break;
+                    if (!(ok = warp_wait(ctl, &ctl->sync[0], n_sync & 1, c, g.tries))) break;
                     ++n_sync;
                 }
                 continue;
@@ -910,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __threadfence();
             uint64_t *sync = &ctl->sync[PAIR ? s : 0];
             mbar_arrive(sync);
-            if (!(ok = warp_wait(ctl, sync, n_sync & 1, c, g.timeout_ns))) break;
+            if (!(ok = warp_wait(ctl, sync, n_sync & 1, c, g.tries))) break;
             ++n_sync;
             if (r == 0 && (PAIR || s == 0)) {
                 unsigned *count = g.arrivals + cf * 2 + (PAIR ? s : 0);
@@ -921,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __threadfence();
             }
             mbar_arrive(sync);
-            if (!(ok = warp_wait(ctl, sync, n_sync & 1, c, g.timeout_ns))) break;
+            if (!(ok = warp_wait(ctl, sync, n_sync & 1, c, g.tries))) break;
             ++n_sync;
             if (!ctl->last[PAIR ? s : 0]) continue;
             const int first_token = seg.tile * step + (PAIR ? s * g.tile_tokens : 0);
@@ -1023,6 +1041,11 @@ dspark_status attend(const dspark_cache *cache, const dspark_attention_args *arg
         return fail(DSPARK_ERR_INVALID, "%s: q and out must be 16-byte aligned, with positive strides of whole 16 bytes", who);
     int sms = 0;
     if ((st = static_cast<dspark_status>(current_sm_count(&sms))) != DSPARK_OK) return st;
+    // The kernel counts key tiles in 32 bits: at most one item for each token and sequence of a kv head, of all the tiles of a row.
+    const double items = (static_cast<double>(tokens) / (kTile / group) + n_seqs) * c.kv_heads;
+    if (items * (static_cast<double>(c.max_pages) * c.page_size / kTile + 1 + kItemCost) > 4.0e9)
+        return fail(DSPARK_ERR_UNSUPPORTED, "%s: %d tokens of %d sequences over rows of %d pages pass 2^32 key tiles", who, tokens, n_seqs,
+                    c.max_pages);
 
     Attention g{};
     g.out = out;
@@ -1046,6 +1069,7 @@ dspark_status attend(const dspark_cache *cache, const dspark_attention_args *arg
     g.partials = reinterpret_cast<float *>(c.scratch);
     g.arrivals = c.counters;
     g.timeout_ns = kDefaultTimeoutNs;
+    g.tries = static_cast<uint32_t>(kDefaultTimeoutNs / 1000);
     g.stall_ns = static_cast<unsigned long long>(stall_us) * 1000ull;
 
     const bool bf16 = cache->dtype == DSPARK_BF16;
