@@ -996,7 +996,9 @@ def rotary(x, positions, table: RotaryTable, *, backward: bool = False, out=None
     shape = x.shape
     if out is None:
         out = torch.empty_like(x)
-    ao, bo = _heads(out, "out", x.dtype, shape)
+        ao, bo, _ = out.stride()
+    else:
+        ao, bo = _heads(out, "out", x.dtype, shape)
     tokens, heads, dim = shape
     turns, rotary_dim, layout, amplitude = table._args
     status = lib.dspark_rotary(
@@ -1027,7 +1029,9 @@ def rotary_append(q, k, v, cache: PagedCache, layer: int, cu_new, table: RotaryT
     va, vb = _heads(v, "v", dtype, kv_shape)
     if out is None:
         out = torch.empty_like(q)
-    oa, ob = _heads(out, "out", dtype, shape)
+        oa, ob, _ = out.stride()
+    else:
+        oa, ob = _heads(out, "out", dtype, shape)
     seqs = cu_new.numel() - 1
     turns, rotary_dim, layout, amplitude = table._args
     status = lib.dspark_rotary_append(
@@ -1057,7 +1061,9 @@ def paged_attention(q, cache: PagedCache, layer: int, cu_new, *, rows=None, max_
         raise ValueError(f"q has head_dim {dim}, the cache {cache.head_dim}")
     if out is None:
         out = torch.empty_like(q)
-    oa, ob = _heads(out, "out", dtype, shape)
+        oa, ob, _ = out.stride()
+    else:
+        oa, ob = _heads(out, "out", dtype, shape)
     if lse is None and return_lse:
         lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=cache.device)
     seqs = cu_new.numel() - 1
