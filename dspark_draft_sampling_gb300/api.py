@@ -810,6 +810,14 @@ def _raw_stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
+def _empty_like(t, stream):
+    """An output of t's shape and type, in the memory of the stream that writes it."""
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
 def _ints(t, name: str, n=None, *, dtype=torch.int32):
     """Address of a contiguous CUDA tensor of whole numbers (of n entries)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or not t.is_contiguous():
@@ -909,16 +917,13 @@ class PagedCache:
         """Row rows[i] keeps its first start[i] tokens and the n_kept[i] ones at kept[i, :] (int32 [n, at least
         max n_kept], ascending positions from start[i] on).  Without kept the rows are cut off at start."""
         n = rows.numel()
-        if kept is None:
-            n_kept = torch.zeros(n, dtype=torch.int32, device=self.device)
-            stride, kept_p = 0, None
-        else:
+        stride, kept_p, n_kept_p = 0, None, None
+        if kept is not None:
             if kept.dim() != 2 or kept.shape[0] != n:
                 raise ValueError("kept must be int32 [rows, tokens]")
-            stride, kept_p = kept.shape[1], _ints(kept, "kept")
+            stride, kept_p, n_kept_p = kept.shape[1], _ints(kept, "kept"), _ints(n_kept, "n_kept", n)
         _check(self._lib, self._lib.dspark_cache_compact(self._ref, _ints(rows, "rows"), _ints(start, "start", n), kept_p,
-                                                         stride, _ints(n_kept, "n_kept", n), n,
-                                                         _raw_stream(stream, self.device)))
+                                                         stride, n_kept_p, n, _raw_stream(stream, self.device)))
 
     def free(self, rows, *, stream=None):
         """The rows release their pages and become empty."""
@@ -995,7 +1000,7 @@ def rotary(x, positions, table: RotaryTable, *, backward: bool = False, out=None
     a, b = _heads(x, "x", x.dtype)
     shape = x.shape
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty_like(x, stream)
         ao, bo, _ = out.stride()
     else:
         ao, bo = _heads(out, "out", x.dtype, shape)
@@ -1028,7 +1033,7 @@ def rotary_append(q, k, v, cache: PagedCache, layer: int, cu_new, table: RotaryT
     ka, kb = _heads(k, "k", dtype, kv_shape)
     va, vb = _heads(v, "v", dtype, kv_shape)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
         oa, ob, _ = out.stride()
     else:
         oa, ob = _heads(out, "out", dtype, shape)
@@ -1060,12 +1065,16 @@ def paged_attention(q, cache: PagedCache, layer: int, cu_new, *, rows=None, max_
     if dim != cache.head_dim:
         raise ValueError(f"q has head_dim {dim}, the cache {cache.head_dim}")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
         oa, ob, _ = out.stride()
     else:
         oa, ob = _heads(out, "out", dtype, shape)
     if lse is None and return_lse:
-        lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=cache.device)
+        if stream is None:
+            lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=cache.device)
+        else:
+            with torch.cuda.stream(stream):
+                lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=cache.device)
     seqs = cu_new.numel() - 1
     status = lib.dspark_paged_attention(
         cache._ref,

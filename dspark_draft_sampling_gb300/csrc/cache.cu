@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kBooksThreads, 1)
     FreePages free;
     bool bad = false;
     if (i < n) {
-        const int row = rows[i], st = start[i], k = n_kept[i];
+        const int row = rows[i], st = start[i], k = n_kept ? n_kept[i] : 0;
         bad = !row_ok(c, row) || st < 0 || k < 0 || k > kept_stride;
         const int len = bad ? 0 : c.length[row];
         bad |= !length_ok(c, len) || st > len || k > len - st;
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(32) compact_move_kernel(CacheView c, const int
     pdl_wait();
     if (c.status[1] == 0) return;
     const int i = blockIdx.y, run = blockIdx.x;
-    const int st = start[i], end = st + n_kept[i], mask = c.page_size - 1;
+    const int st = start[i], end = st + (n_kept ? n_kept[i] : 0), mask = c.page_size - 1;
     const int *t = c.table + size_t(rows[i]) * c.max_pages;
     const int *snap = scratch_snapshot(c) + size_t(i) * c.max_pages;
     const int *w = kept + size_t(i) * kept_stride;
@@ -703,7 +703,7 @@ extern "C" dspark_status dspark_cache_compact(const dspark_cache *cache, const i
     if (st != DSPARK_OK || (st = check_rows("cache_compact", c, rows, start, n)) != DSPARK_OK) return st;
     if (kept_stride < 0) return fail(DSPARK_ERR_INVALID, "cache_compact: kept_stride=%d is negative", kept_stride);
     if (n == 0) return DSPARK_OK;
-    if (!n_kept || (!kept && kept_stride > 0)) return fail(DSPARK_ERR_INVALID, "cache_compact: null pointer argument");
+    if (kept_stride > 0 && (!kept || !n_kept)) return fail(DSPARK_ERR_INVALID, "cache_compact: null pointer argument");
     st = launched(launch_books(compact_books_kernel, c, static_cast<long long>(n) * (kept_stride + c.max_pages), stream, c, rows, start, kept, kept_stride, n_kept, n),
                   "cache_compact");
     if (st != DSPARK_OK) return st;

@@ -89,21 +89,25 @@ __device__ __forceinline__ Seq load_seq(const CacheView &c, const Attention &g, 
     return q;
 }
 
-// Key tiles [lo, hi) that query tile i (of `step` tokens) of a sequence sees.
-__device__ __forceinline__ void key_tiles(const Attention &g, const Seq &q, int i, int step, int *lo, int *hi) {
+// Keys [begin, end) that some token of query tile i (of `step` tokens) of a sequence sees, and the key tiles [lo, hi) they lie in.
+struct Keys {
+    int begin, end, lo, hi;
+};
+
+__device__ __forceinline__ Keys keys_of(const Attention &g, const Seq &q, int i, int step) {
     const int off = q.length - q.n, first = i * step, last = min(first + step, q.n) - 1;
-    const int end = g.causal ? min(q.length, max(off + last + 1, 0)) : q.length;
-    const int begin = g.window > 0 ? max(0, off + first - g.window + 1) : 0;
-    *hi = (end + kTile - 1) / kTile;
-    *lo = min(begin / kTile, *hi);
-    if (begin >= end) *lo = *hi;
+    Keys k;
+    k.end = g.causal ? min(q.length, max(off + last + 1, 0)) : q.length;
+    k.begin = g.window > 0 ? max(0, off + first - g.window + 1) : 0;
+    k.hi = (k.end + kTile - 1) / kTile;
+    k.lo = k.begin < k.end ? k.begin / kTile : k.hi;
+    return k;
 }
 
 // What an item counts among all tiles.
 __device__ __forceinline__ int item_cost(const Attention &g, const Seq &q, int i, int step) {
-    int lo, hi;
-    key_tiles(g, q, i, step, &lo, &hi);
-    return kItemCost + hi - lo;
+    const Keys k = keys_of(g, q, i, step);
+    return kItemCost + k.hi - k.lo;
 }
 
 // One stretch of an item that a block works on, as the copying warp hands it to the others.
@@ -111,6 +115,7 @@ struct Segment {
     int kv_head, tile;        // query tile of the sequence
     int lo, first, last;      // the item's first key tile; the stretch's, relative to it
     int tiles;                // of the whole item; -1: no more segments
+    int begin, end;           // keys that some row of the item sees
     int q0, n, length;        // the sequence's first query token, its new tokens, its tokens
     int cf, cl;               // first and last block that work on the item (where that is more than one)
 };
@@ -134,13 +139,14 @@ struct Walk {
                     n_tiles = (q.n + step - 1) / step;
                 }
             }
-            int lo, hi;
-            key_tiles(g, q, i, step, &lo, &hi);
-            const int tiles = hi - lo;
+            const Keys k = keys_of(g, q, i, step);
+            const int tiles = k.hi - k.lo;
             const unsigned take = min(left, kItemCost + tiles - x);
             out->kv_head = kv_head;
             out->tile = i;
-            out->lo = lo;
+            out->lo = k.lo;
+            out->begin = k.begin;
+            out->end = k.end;
             out->tiles = tiles;
             out->first = max(static_cast<int>(x) - kItemCost, 0);
             out->last = max(static_cast<int>(x + take) - kItemCost, 0);
@@ -546,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int run = (g.layer * 2) * c.kv_heads + seg.kv_head;
             for (int t = seg.first; ok && t < seg.last; ++t) {
                 const int key = (seg.lo + t) * kTile + lane * box;  // first key of this lane's page
-                const bool mine = lane < per_tile && key < seg.length;
+                const bool mine = lane < per_tile && key < seg.end && key + box > seg.begin;  // pages that no row sees are not looked at
                 int page = 0;
                 if (mine) {
                     page = pages[key >> c.page_shift];
@@ -706,15 +712,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = warp_wait(ctl, &ctl->s_full[s], n_s & 1, c, g.tries))) break;
                 ++n_s;
                 tc_fence_after();
-                if (key0 + kTile > seg.length) {
-                    // values behind the row's length are whatever the page holds: zeros, so that weights of 0 stay 0
+                if (key0 < seg.begin || key0 + kTile > seg.end) {
+                    // Values that no row of the item sees are whatever the pages hold, or were not copied: zeros, so that weights of 0
+                    // stay 0.
                     const uint32_t p = 2 * (base + t) + 1, st = p % S::kStages;
                     if (!(ok = warp_wait(ctl, &ctl->full[st], (p / S::kStages) & 1, c, g.tries))) break;
-                    const int used = seg.length - key0;
+                    const int first = max(seg.begin - key0, 0) * 8, last = min(seg.end - key0, kTile) * 8;
                     unsigned char *v = ring_ptr + st * S::kTileBytes;
-                    for (int h = 0; h < S::kHalves; ++h)
-                        for (int b = used * 8 + r; b < kTile * 8; b += kTile)
-                            reinterpret_cast<uint4 *>(v + h * (kTile * 128))[b] = make_uint4(0u, 0u, 0u, 0u);
+                    for (int h = 0; h < S::kHalves; ++h) {
+                        uint4 *at = reinterpret_cast<uint4 *>(v + h * (kTile * 128));
+                        for (int b = r; b < first; b += kTile) at[b] = make_uint4(0u, 0u, 0u, 0u);
+                        for (int b = last + r; b < kTile * 8; b += kTile) at[b] = make_uint4(0u, 0u, 0u, 0u);
+                    }
                     fence_proxy_async_smem();
                 }
                 if (warp_real) {

@@ -550,7 +550,8 @@ void dspark_gated_draft_plan_destroy(dspark_gated_plan *plan);
  *            kept[i * kept_stride ..] (positions >= start[i], ascending), in place; pages past
  *            the new end are released.  Where tokens would be written to, or the new end lies
  *            inside, a page that other rows hold too, the row gets its own copy of it.
- *            n_kept == 0 cuts the row off at start[i]
+ *            n_kept[i] == 0 cuts the row off at start[i]; n_kept and kept may be NULL with
+ *            kept_stride 0: all rows are cut off
  *   free     the rows release their pages and become empty
  *   copy_pages  page dst[i] becomes a copy of page src[i], all layers; the targets are distinct
  *            and no page is both source and target; table and refs are left alone.  Any n; a pair
@@ -668,10 +669,12 @@ dspark_status dspark_rotary_append(const dspark_cache *cache, const dspark_appen
  *   scale    positive
  *   max_new  the longest chunk, as far as the caller knows (a hint for the tile shape; wrong values
  *            cost time, not correctness); tokens where it is not known
- * What lies in the cache behind a row's length, or in pages that no row holds, is never seen,
- * whatever it is.  Keys and values at positions below the length have to be finite where a token
- * of the same chunk does not see them.  A table entry outside the pool reads as zeros; it, a row
- * out of range (taken as empty) and a length longer than the row (cut) record DSPARK_ERR_INDEX.
+ * What lies in the cache where no token of the chunk sees it is never used, whatever it is:
+ * behind a row's length, before the window of all, in pages that no row holds (whose table entries
+ * are not looked at either).  Keys that only some tokens of a chunk see may hold anything for the
+ * others; their values have to be finite, as a weight of 0 multiplies them.  A table entry outside
+ * the pool reads as zeros; it, a row out of range (taken as empty) and a length longer than the row
+ * (cut) record DSPARK_ERR_INDEX.
  * Supported: q_heads a multiple of kv_heads, at most 128 of them to a kv head; n_seqs <= 4096.
  * The result is deterministic: it depends on the inputs and the number of SMs only.
  * ===================================================================================== */

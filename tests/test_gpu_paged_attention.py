@@ -231,3 +231,46 @@ def test_a_wait_that_gave_up_is_reported(n):
     assert status == 0 and cache.status() == api.DSPARK_ERR_TIMEOUT
     assert torch.equal(got, want)
     assert torch.equal(api.paged_attention(q, cache, 0, cu), want) and cache.status() == 0
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_pages_before_the_window_may_be_gone(causal):
+    # what no token of the chunk sees is NaN, and the table entries of whole pages before the window point nowhere
+    gen = torch.Generator().manual_seed(13)
+    n, window, lens = 5, 100, [400, 131, 90]
+    cache, pool, table = make_cache(gen, lens, dtype=F16, dim=64, kv_heads=1, page=16)
+    q = torch.randn((n * 3, 2, 64), generator=gen).to(F16).cuda()
+    cu = torch.tensor([0, n, 2 * n, 3 * n], dtype=torch.int32).cuda()
+    first = [max(0, length - n - window + 1) for length in lens]
+    clean = pool.clone()
+    for r, f in enumerate(first):
+        for p in range(f):
+            pool[table[r, p // 16], :, :, :, p % 16] = math.nan
+    cache.pool.copy_(pool)
+    gone = cache.table.clone()
+    for r, f in enumerate(first):
+        gone[r, : f // 16] = torch.tensor([-1, 10**6, -(2**31)] * 10, dtype=torch.int32)[: f // 16].cuda()
+    cache.table.copy_(gone)
+    got = api.paged_attention(q, cache, 0, cu, causal=causal, window=window)
+    assert cache.status() == 0
+    for s, length in enumerate(lens):
+        k, v = ref.row_tokens(clean, table, 0, s, length)
+        want, _, w_abs, p_abs, dots = ref.attention(q[s * n:(s + 1) * n].cpu().double(), k, v, n, causal=causal, window=window, scale=0.125)
+        tol = 2.0**-11 * want.abs() + (2.0**-11 + 2 * 64 * 2.0**-24 * dots + 2.0**-20) * w_abs + 2.0**-24 * (1 + p_abs)
+        assert ((got[s * n:(s + 1) * n].cpu().double() - want).abs() <= 2 * tol).all()
+
+
+def test_outputs_belong_to_the_stream_that_writes_them():
+    gen = torch.Generator().manual_seed(14)
+    cache, _, _ = make_cache(gen, [3000], dtype=BF16, dim=128, kv_heads=2, page=16)
+    q = torch.randn((4, 8, 128), generator=gen).to(BF16).cuda()
+    cu = torch.tensor([0, 4], dtype=torch.int32).cuda()
+    want = api.paged_attention(q, cache, 0, cu)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(20):  # outputs dropped at once: their memory may only be taken up again on the same stream
+        got, _ = api.paged_attention(q, cache, 0, cu, return_lse=True, stream=side)
+        trash = torch.full_like(q, float("nan"))
+        del trash
+    side.synchronize()
+    assert torch.equal(got, want)

@@ -76,6 +76,7 @@ def test_page_operations_refuse(dspark_lib):
     assert lib.dspark_cache_compact(c, FAKE, FAKE, FAKE, -1, FAKE, 1, None) == INVALID
     assert lib.dspark_cache_compact(c, FAKE, FAKE, None, 3, FAKE, 1, None) == INVALID
     assert lib.dspark_cache_compact(c, FAKE, FAKE, FAKE, 3, None, 1, None) == INVALID
+    assert lib.dspark_cache_compact(c, FAKE, None, None, 0, None, 1, None) == INVALID
     assert lib.dspark_cache_copy_pages(c, FAKE, None, 1, None) == INVALID
     assert lib.dspark_cache_copy_pages(c, FAKE, FAKE, -1, None) == INVALID
     for name in ("extend", "fork", "copy_pages"):
