@@ -19,6 +19,13 @@
 // from the lengths on the device, so nothing about them has to be known on the host.  An item cut by a range's end
 // leaves partial sums (32-bit O, maximum, sum) in the workspace; the block that arrives last joins them in
 // block order, so the result does not depend on which one that is.
+//
+// Measured (GB300). 8192 tokens after 8192, 32 / 8 heads of 128: 1.02 ms, 1.62 PFLOP/s under the power cap, where the library's
+// matrix product sustains 1.75; one cold launch 0.94 ms with the tensor pipe active for 74 % of it. 1-8 tokens over 16,000-66,000
+// keys: 182 us for 1.2 GB, 98 % of a copy's rate. 16 x 7 tokens over 300-6000 keys: 45 us for 183 MB, of which 32 are that
+// stream, the rest start and joins. Chunks of 90-1500 tokens in a window of 1000, 28 / 4 heads of 64: 69 us, where the chain
+// of one stream (scores, softmax, second product) takes 2500 cycles a pair of key tiles and the products 1024. One token
+// over 777 keys: 11 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -37,8 +44,11 @@ static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "
 constexpr int kTmemCols = 512;
 constexpr size_t kSmemData = 224 * 1024;      // query tiles and the ring of key and value tiles
 constexpr size_t kSmemBytes = 227 * 1024;
-constexpr int kItemCost = 2;                  // an item's fixed cost, in key tiles
-constexpr float kRescale = 8.f;               // powers of two by which a row's maximum may lag
+// An item's fixed cost, in key tiles. With 1, 2, 3, 4, 6: 16 blocks of 7 tokens over 300-6000 keys 44.7, 44.8, 46.0, 46.0, 49.4 us;
+// chunks in a window of 1000 70.7, 68.8, 69.0, 68.2, 69.4; 4 chunks of 64 tokens over 3000 keys 36.8, 34.9, 32.7, 33.0, 33.5.
+constexpr int kItemCost = 2;
+// Powers of two by which a row's maximum may lag. With 0, 4, 8: prompt of 8192 tokens after 8192 1176, 1023, 1019 us.
+constexpr float kRescale = 8.f;
 
 struct Attention {
     void *out;
@@ -456,233 +466,233 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = ctl->tmem;
 
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8) {
-        // ---- copies: query tiles, then keys and values of each tile through the ring; a lane to a page ----
-        const int box = min(c.page_size, kTile), per_tile = kTile / box;
-        uint32_t n_q = 0, n_seg = 0, put = 0;  // segments with keys, segments, ring entries so far
-        Walk walk;
-        walk.left = 0;
-        walk.step = step;
-        {
-            // ---- this block's range of all items' tiles, and the item that it begins with ----
-            // in 32 bits: the host has made sure that the tiles' number fits
-            Seq mine{};
-            unsigned w = 0;
-            if (few && lane < g.n_seqs) {
-                mine = load_seq(c, g, lane);
-                for (int i = 0; i * step < mine.n; ++i) w += item_cost(g, mine, i, step);
-            }
-            unsigned total = few ? w : 0;
-            if (!few)
-                for (int s = lane; s < g.n_seqs; s += 32) total += cost[s];
-            total = __reduce_add_sync(0xffffffffu, total) * c.kv_heads;
-            const unsigned per = (total + gridDim.x - 1) / gridDim.x;
-            walk.per = per;
-            walk.pos = min(per * blockIdx.x, total);
-            walk.left = min(per, total - walk.pos);
-            if (walk.left > 0) {
-                unsigned before = 0;
-                for (int s0 = 0;; s0 += 32) {
-                    if (!few) w = s0 + lane < g.n_seqs ? cost[s0 + lane] : 0;
-                    const unsigned upto = before + warp_scan(w, lane) * c.kv_heads;
-                    const unsigned past = __ballot_sync(0xffffffffu, upto > walk.pos);
-                    if (past || s0 + 32 >= g.n_seqs) {  // the range lies within the sequences: found in the last stretch at the latest
-                        const int l = past ? __ffs(past) - 1 : 0;
-                        walk.s = s0 + l;
-                        w = __shfl_sync(0xffffffffu, w, l);
-                        before = __shfl_sync(0xffffffffu, upto, l) - w * c.kv_heads;
-                        if (!few) mine = load_seq(c, g, s0 + lane < g.n_seqs ? s0 + lane : walk.s);
-                        walk.q.row = __shfl_sync(0xffffffffu, mine.row, l);
-                        walk.q.n = __shfl_sync(0xffffffffu, mine.n, l);
-                        walk.q.length = __shfl_sync(0xffffffffu, mine.length, l);
-                        walk.q.q0 = __shfl_sync(0xffffffffu, mine.q0, l);
-                        break;
-                    }
-                    before = __shfl_sync(0xffffffffu, upto, 31);
-                }
-                walk.n_tiles = (walk.q.n + step - 1) / step;
-                walk.kv_head = (walk.pos - before) / w;
-                unsigned rem = walk.pos - before - walk.kv_head * w;
-                for (int i0 = 0; i0 < walk.n_tiles; i0 += 32) {
-                    const unsigned v = i0 + lane < walk.n_tiles ? item_cost(g, walk.q, i0 + lane, step) : 0;
-                    const unsigned upto = warp_scan(v, lane);
-                    const unsigned past = __ballot_sync(0xffffffffu, upto > rem);
-                    if (past) {
-                        const int l = __ffs(past) - 1;
-                        walk.i = i0 + l;
-                        walk.x = rem - __shfl_sync(0xffffffffu, upto - v, l);
-                        break;
-                    }
-                    rem -= __shfl_sync(0xffffffffu, upto, 31);
-                }
-            }
-        }
-        bool ok = true;
-        for (bool more = true; ok && more;) {
-            Segment seg;
-            more = walk.next(c, g, &seg);
-            if (!more) seg.tiles = -1;
-            seg.cf = seg.cl = blockIdx.x;
-            if (more && (seg.first != 0 || seg.last != seg.tiles)) {
-                if (seg.first != 0) seg.cf = (walk.at + kItemCost) / walk.per;
-                if (seg.last != seg.tiles) seg.cl = (walk.at + kItemCost + seg.tiles - 1) / walk.per;
-            }
-            const uint32_t entry = n_seg % kSegments;
-            if (n_seg >= kSegments && !(ok = warp_wait(ctl, &ctl->seg_empty[entry], ((n_seg / kSegments) & 1) ^ 1, c, g.tries))) break;
-            ++n_seg;
-            if (lane == 0) {
-                ctl->segs[entry] = seg;
-                mbar_arrive(&ctl->seg_full[entry]);
-            }
-            __syncwarp();
-            if (!more || seg.tiles == 0) continue;
-            if (n_q > 0 && !(ok = warp_wait(ctl, &ctl->q_empty, (n_q - 1) & 1, c, g.tries))) break;
-            ++n_q;
-            const int token = seg.q0 + seg.tile * step;
-            if (lane == 0) {
-                const uint32_t rows_bytes = static_cast<uint32_t>(g.tile_tokens * g.group) * 128u;
-                mbar_arrive_expect_tx(&ctl->q_full, rows_bytes * S::kHalves * S::QT);
-                for (int t = 0; t < S::QT; ++t)
-                    for (int h = 0; h < S::kHalves; ++h)
-                        tma_load_3d_plain(q_smem + t * S::kTileBytes + h * (kTile * 128), &tm_q, h * 64, seg.kv_head * g.group,
-                                          token + t * g.tile_tokens, &ctl->q_full);
-            }
-            const int *pages = c.table + static_cast<size_t>(walk.q.row) * c.max_pages;
-            const int run = (g.layer * 2) * c.kv_heads + seg.kv_head;
-            for (int t = seg.first; ok && t < seg.last; ++t) {
-                const int key = (seg.lo + t) * kTile + lane * box;  // first key of this lane's page
-                const bool mine = lane < per_tile && key < seg.end && key + box > seg.begin;  // pages that no row sees are not looked at
-                int page = 0;
-                if (mine) {
-                    page = pages[key >> c.page_shift];
-                    if (static_cast<unsigned>(page) >= static_cast<unsigned>(c.num_pages)) {
-                        atomicOr(c.status, kStatusIndex);
-                        page = c.num_pages;  // outside the tensor: reads as zeros
-                    }
-                }
-                const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
-                const int slot = key & (c.page_size - 1);  // pages longer than a tile
-                for (int w = 0; w < 2; ++w, ++put) {
-                    const uint32_t st = put % S::kStages;
-                    if (put >= S::kStages && !(ok = warp_wait(ctl, &ctl->empty[st], ((put / S::kStages) & 1) ^ 1, c, g.tries))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], boxes * static_cast<uint32_t>(box) * D * 2);
-                    __syncwarp();
-                    if (mine)
-                        for (int h = 0; h < S::kHalves; ++h)
-                            tma_load_4d(ring + st * S::kTileBytes + h * (kTile * 128) + lane * box * 128, &tm_kv, h * 64, slot,
-                                        run + w * c.kv_heads, page, &ctl->full[st]);
-                }
-            }
-        }
-        // copies in flight land before the block ends, also after a wait that gave up
-        for (uint32_t p = put > S::kStages ? put - S::kStages : 0; p < put; ++p)
-            mbar_wait(&ctl->full[p % S::kStages], (p / S::kStages) & 1, g.timeout_ns);
-        if (n_q) mbar_wait(&ctl->q_full, (n_q - 1) & 1, g.timeout_ns);
-    } else if (warp == 9) {
-        // ---- MMA issue: the warp runs as one, an elected lane issues ----
-        constexpr uint32_t idesc_s = idesc_f16(BF16, kTile, kTile);
-        constexpr uint32_t idesc_o = idesc_f16(BF16, kTile, D) | (1u << 16);  // B is N-contiguous
-        uint32_t n_q = 0, n_seg = 0, base = 0;  // segments with keys, segments, key tiles before this segment
-        uint32_t p_phase = 0;                   // one bit a stream: the phase of its next P
-        bool ok = true;
-        Segment seg;
-        // Ring entries and their phases: key tile j of all is entry 2 * j, its values the next one.
-        struct Entry {
-            uint32_t st, phase;
-        };
-        auto entry = [&](uint32_t p) {
-            const uint32_t turn = p / S::kStages;
-            return Entry{__shfl_sync(0xffffffffu, p - turn * S::kStages, 0), turn & 1};
-        };
-        auto ready = [&](uint64_t *bar, uint32_t phase) { return warp_wait(ctl, bar, phase, c, g.tries); };
-        auto issue_scores = [&](const int s, const Entry &e, bool frees_q) {
-            const uint64_t a = smem_desc_sw128(q_smem + (PAIR ? s * S::kTileBytes : 0));
-            const uint64_t b = smem_desc_sw128(ring + e.st * S::kTileBytes);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint64_t o = static_cast<uint64_t>((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
-                tc_mma_f16(tmem + s * kTile, a + o, b + o, idesc_s, k != 0);
-            }
-            tc_commit(&ctl->s_full[s]);
-            if (!PAIR || s == 1) tc_commit(&ctl->empty[e.st]);
-            if (frees_q) tc_commit(&ctl->q_empty);  // the segment's last scores free its query tiles
-        };
-        auto issue_values = [&](const int s, const Entry &e, const int half, bool add) {
-            const uint64_t b = smem_desc_values(ring + e.st * S::kTileBytes);
-#pragma unroll
-            for (int k = half * (kTile / 32); k < (half + 1) * (kTile / 32); ++k)
-                tc_mma_f16_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + k * 8, b + ((k * 2048) >> 4), idesc_o, add || k != 0);
-        };
-        // One step of stream s: its second product, then the scores of its next key tile.
-        auto advance = [&](const int s, const Entry &v, const Entry &k, bool first, bool more, bool frees_q) {
-            if (!ready(&ctl->p_half[s], (p_phase >> s) & 1)) return false;
-            tc_fence_after();
-            if (elect_one()) issue_values(s, v, 0, !first);
-            __syncwarp();
-            if (!ready(&ctl->p_ready[s], (p_phase >> s) & 1)) return false;
-            p_phase ^= 1u << s;
-            tc_fence_after();
-            if (elect_one()) {
-                issue_values(s, v, 1, true);
-                if (!PAIR || s == 1) tc_commit(&ctl->empty[v.st]);
-                if (!more) tc_commit(&ctl->o_full[s]);
-                if (PAIR && more) issue_scores(s, k, frees_q);
-            }
-            __syncwarp();
-            if (!PAIR && more) {
-                // these keys may be on their way still, and the values' slot was wanted back first
-                if (!ready(&ctl->full[k.st], k.phase)) return false;
-                tc_fence_after();
-                if (elect_one()) issue_scores(s, k, frees_q);
-                __syncwarp();
-            }
-            return true;
-        };
-        while (ok && next_segment(ctl, n_seg, &seg, c, g.tries)) {
-            if (seg.tiles == 0) continue;
-            const int nt = seg.last - seg.first;
-            const int steps0 = PAIR ? nt : (nt + 1) / 2, steps1 = PAIR ? nt : nt / 2;
-            const uint32_t p0 = 2 * base;
-            base += nt;
-            if (!(ok = ready(&ctl->q_full, n_q & 1))) break;
-            ++n_q;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 8) {
+            // ---- copies: query tiles, then keys and values of each tile through the ring; a lane to a page ----
+            const int box = min(c.page_size, kTile), per_tile = kTile / box;
+            uint32_t n_q = 0, n_seg = 0, put = 0;  // segments with keys, segments, ring entries so far
+            Walk walk;
+            walk.left = 0;
+            walk.step = step;
             {
-                const Entry k0 = entry(p0), k1 = PAIR ? k0 : entry(p0 + 2);
-                if (!(ok = ready(&ctl->full[k0.st], k0.phase))) break;
-                tc_fence_after();
-                if (elect_one()) issue_scores(0, k0, steps0 == 1 && steps1 == 0);
+                // ---- this block's range of all items' tiles, and the item that it begins with ----
+                // in 32 bits: the host has made sure that the tiles' number fits
+                Seq mine{};
+                unsigned w = 0;
+                if (few && lane < g.n_seqs) {
+                    mine = load_seq(c, g, lane);
+                    for (int i = 0; i * step < mine.n; ++i) w += item_cost(g, mine, i, step);
+                }
+                unsigned total = few ? w : 0;
+                if (!few)
+                    for (int s = lane; s < g.n_seqs; s += 32) total += cost[s];
+                total = __reduce_add_sync(0xffffffffu, total) * c.kv_heads;
+                const unsigned per = (total + gridDim.x - 1) / gridDim.x;
+                walk.per = per;
+                walk.pos = min(per * blockIdx.x, total);
+                walk.left = min(per, total - walk.pos);
+                if (walk.left > 0) {
+                    unsigned before = 0;
+                    for (int s0 = 0;; s0 += 32) {
+                        if (!few) w = s0 + lane < g.n_seqs ? cost[s0 + lane] : 0;
+                        const unsigned upto = before + warp_scan(w, lane) * c.kv_heads;
+                        const unsigned past = __ballot_sync(0xffffffffu, upto > walk.pos);
+                        if (past || s0 + 32 >= g.n_seqs) {  // the range lies within the sequences: found in the last stretch at the latest
+                            const int l = past ? __ffs(past) - 1 : 0;
+                            walk.s = s0 + l;
+                            w = __shfl_sync(0xffffffffu, w, l);
+                            before = __shfl_sync(0xffffffffu, upto, l) - w * c.kv_heads;
+                            if (!few) mine = load_seq(c, g, s0 + lane < g.n_seqs ? s0 + lane : walk.s);
+                            walk.q.row = __shfl_sync(0xffffffffu, mine.row, l);
+                            walk.q.n = __shfl_sync(0xffffffffu, mine.n, l);
+                            walk.q.length = __shfl_sync(0xffffffffu, mine.length, l);
+                            walk.q.q0 = __shfl_sync(0xffffffffu, mine.q0, l);
+                            break;
+                        }
+                        before = __shfl_sync(0xffffffffu, upto, 31);
+                    }
+                    walk.n_tiles = (walk.q.n + step - 1) / step;
+                    walk.kv_head = (walk.pos - before) / w;
+                    unsigned rem = walk.pos - before - walk.kv_head * w;
+                    for (int i0 = 0; i0 < walk.n_tiles; i0 += 32) {
+                        const unsigned v = i0 + lane < walk.n_tiles ? item_cost(g, walk.q, i0 + lane, step) : 0;
+                        const unsigned upto = warp_scan(v, lane);
+                        const unsigned past = __ballot_sync(0xffffffffu, upto > rem);
+                        if (past) {
+                            const int l = __ffs(past) - 1;
+                            walk.i = i0 + l;
+                            walk.x = rem - __shfl_sync(0xffffffffu, upto - v, l);
+                            break;
+                        }
+                        rem -= __shfl_sync(0xffffffffu, upto, 31);
+                    }
+                }
+            }
+            bool ok = true;
+            for (bool more = true; ok && more;) {
+                Segment seg;
+                more = walk.next(c, g, &seg);
+                if (!more) seg.tiles = -1;
+                seg.cf = seg.cl = blockIdx.x;
+                if (more && (seg.first != 0 || seg.last != seg.tiles)) {
+                    if (seg.first != 0) seg.cf = (walk.at + kItemCost) / walk.per;
+                    if (seg.last != seg.tiles) seg.cl = (walk.at + kItemCost + seg.tiles - 1) / walk.per;
+                }
+                const uint32_t entry = n_seg % kSegments;
+                if (n_seg >= kSegments && !(ok = warp_wait(ctl, &ctl->seg_empty[entry], ((n_seg / kSegments) & 1) ^ 1, c, g.tries))) break;
+                ++n_seg;
+                if (lane == 0) {
+                    ctl->segs[entry] = seg;
+                    mbar_arrive(&ctl->seg_full[entry]);
+                }
                 __syncwarp();
-                if (steps1 > 0) {
-                    if (!PAIR && !(ok = ready(&ctl->full[k1.st], k1.phase))) break;
+                if (!more || seg.tiles == 0) continue;
+                if (n_q > 0 && !(ok = warp_wait(ctl, &ctl->q_empty, (n_q - 1) & 1, c, g.tries))) break;
+                ++n_q;
+                const int token = seg.q0 + seg.tile * step;
+                if (lane == 0) {
+                    const uint32_t rows_bytes = static_cast<uint32_t>(g.tile_tokens * g.group) * 128u;
+                    mbar_arrive_expect_tx(&ctl->q_full, rows_bytes * S::kHalves * S::QT);
+                    for (int t = 0; t < S::QT; ++t)
+                        for (int h = 0; h < S::kHalves; ++h)
+                            tma_load_3d_plain(q_smem + t * S::kTileBytes + h * (kTile * 128), &tm_q, h * 64, seg.kv_head * g.group,
+                                              token + t * g.tile_tokens, &ctl->q_full);
+                }
+                const int *pages = c.table + static_cast<size_t>(walk.q.row) * c.max_pages;
+                const int run = (g.layer * 2) * c.kv_heads + seg.kv_head;
+                for (int t = seg.first; ok && t < seg.last; ++t) {
+                    const int key = (seg.lo + t) * kTile + lane * box;  // first key of this lane's page
+                    const bool mine = lane < per_tile && key < seg.end && key + box > seg.begin;  // pages that no row sees are not looked at
+                    int page = 0;
+                    if (mine) {
+                        page = pages[key >> c.page_shift];
+                        if (static_cast<unsigned>(page) >= static_cast<unsigned>(c.num_pages)) {
+                            atomicOr(c.status, kStatusIndex);
+                            page = c.num_pages;  // outside the tensor: reads as zeros
+                        }
+                    }
+                    const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
+                    const int slot = key & (c.page_size - 1);  // pages longer than a tile
+                    for (int w = 0; w < 2; ++w, ++put) {
+                        const uint32_t st = put % S::kStages;
+                        if (put >= S::kStages && !(ok = warp_wait(ctl, &ctl->empty[st], ((put / S::kStages) & 1) ^ 1, c, g.tries))) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], boxes * static_cast<uint32_t>(box) * D * 2);
+                        __syncwarp();
+                        if (mine)
+                            for (int h = 0; h < S::kHalves; ++h)
+                                tma_load_4d(ring + st * S::kTileBytes + h * (kTile * 128) + lane * box * 128, &tm_kv, h * 64, slot,
+                                            run + w * c.kv_heads, page, &ctl->full[st]);
+                    }
+                }
+            }
+            // copies in flight land before the block ends, also after a wait that gave up
+            for (uint32_t p = put > S::kStages ? put - S::kStages : 0; p < put; ++p)
+                mbar_wait(&ctl->full[p % S::kStages], (p / S::kStages) & 1, g.timeout_ns);
+            if (n_q) mbar_wait(&ctl->q_full, (n_q - 1) & 1, g.timeout_ns);
+        } else if (warp == 9) {
+            // ---- MMA issue: the warp runs as one, an elected lane issues ----
+            constexpr uint32_t idesc_s = idesc_f16(BF16, kTile, kTile);
+            constexpr uint32_t idesc_o = idesc_f16(BF16, kTile, D) | (1u << 16);  // B is N-contiguous
+            uint32_t n_q = 0, n_seg = 0, base = 0;  // segments with keys, segments, key tiles before this segment
+            uint32_t p_phase = 0;                   // one bit a stream: the phase of its next P
+            bool ok = true;
+            Segment seg;
+            // Ring entries and their phases: key tile j of all is entry 2 * j, its values the next one.
+            struct Entry {
+                uint32_t st, phase;
+            };
+            auto entry = [&](uint32_t p) {
+                const uint32_t turn = p / S::kStages;
+                return Entry{__shfl_sync(0xffffffffu, p - turn * S::kStages, 0), turn & 1};
+            };
+            auto ready = [&](uint64_t *bar, uint32_t phase) { return warp_wait(ctl, bar, phase, c, g.tries); };
+            auto issue_scores = [&](const int s, const Entry &e, bool frees_q) {
+                const uint64_t a = smem_desc_sw128(q_smem + (PAIR ? s * S::kTileBytes : 0));
+                const uint64_t b = smem_desc_sw128(ring + e.st * S::kTileBytes);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t o = static_cast<uint64_t>((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
+                    tc_mma_f16(tmem + s * kTile, a + o, b + o, idesc_s, k != 0);
+                }
+                tc_commit(&ctl->s_full[s]);
+                if (!PAIR || s == 1) tc_commit(&ctl->empty[e.st]);
+                if (frees_q) tc_commit(&ctl->q_empty);  // the segment's last scores free its query tiles
+            };
+            auto issue_values = [&](const int s, const Entry &e, const int half, bool add) {
+                const uint64_t b = smem_desc_values(ring + e.st * S::kTileBytes);
+#pragma unroll
+                for (int k = half * (kTile / 32); k < (half + 1) * (kTile / 32); ++k)
+                    tc_mma_f16_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + k * 8, b + ((k * 2048) >> 4), idesc_o, add || k != 0);
+            };
+            // One step of stream s: its second product, then the scores of its next key tile.
+            auto advance = [&](const int s, const Entry &v, const Entry &k, bool first, bool more, bool frees_q) {
+                if (!ready(&ctl->p_half[s], (p_phase >> s) & 1)) return false;
+                tc_fence_after();
+                if (elect_one()) issue_values(s, v, 0, !first);
+                __syncwarp();
+                if (!ready(&ctl->p_ready[s], (p_phase >> s) & 1)) return false;
+                p_phase ^= 1u << s;
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_values(s, v, 1, true);
+                    if (!PAIR || s == 1) tc_commit(&ctl->empty[v.st]);
+                    if (!more) tc_commit(&ctl->o_full[s]);
+                    if (PAIR && more) issue_scores(s, k, frees_q);
+                }
+                __syncwarp();
+                if (!PAIR && more) {
+                    // these keys may be on their way still, and the values' slot was wanted back first
+                    if (!ready(&ctl->full[k.st], k.phase)) return false;
                     tc_fence_after();
-                    if (elect_one()) issue_scores(1, k1, steps0 == 1);
+                    if (elect_one()) issue_scores(s, k, frees_q);
                     __syncwarp();
                 }
-            }
-            for (int i = 0; i < steps0; ++i) {
-                if (PAIR) {
-                    // both streams read the same tiles; the next keys have long arrived when they are looked at
-                    const bool more = i + 1 < nt;
-                    const Entry v = entry(p0 + 2 * i + 1), k = entry(p0 + 2 * i + 2);
-                    if (!(ok = ready(&ctl->full[v.st], v.phase) && (!more || ready(&ctl->full[k.st], k.phase)))) break;
-                    if (!(ok = advance(0, v, k, i == 0, more, false))) break;
-                    if (!(ok = advance(1, v, k, i == 0, more, i + 2 == nt))) break;
-                } else {
-                    const Entry v0 = entry(p0 + 4 * i + 1), k0 = entry(p0 + 4 * i + 4);
-                    if (!(ok = ready(&ctl->full[v0.st], v0.phase))) break;
-                    if (!(ok = advance(0, v0, k0, i == 0, i + 1 < steps0, i + 2 == steps0 && i + 1 >= steps1))) break;
-                    if (i >= steps1) continue;
-                    const Entry v1 = entry(p0 + 4 * i + 3), k1 = entry(p0 + 4 * i + 6);
-                    if (!(ok = ready(&ctl->full[v1.st], v1.phase))) break;
-                    if (!(ok = advance(1, v1, k1, i == 0, i + 1 < steps1, i + 2 == steps0))) break;
+                return true;
+            };
+            while (ok && next_segment(ctl, n_seg, &seg, c, g.tries)) {
+                if (seg.tiles == 0) continue;
+                const int nt = seg.last - seg.first;
+                const int steps0 = PAIR ? nt : (nt + 1) / 2, steps1 = PAIR ? nt : nt / 2;
+                const uint32_t p0 = 2 * base;
+                base += nt;
+                if (!(ok = ready(&ctl->q_full, n_q & 1))) break;
+                ++n_q;
+                {
+                    const Entry k0 = entry(p0), k1 = PAIR ? k0 : entry(p0 + 2);
+                    if (!(ok = ready(&ctl->full[k0.st], k0.phase))) break;
+                    tc_fence_after();
+                    if (elect_one()) issue_scores(0, k0, steps0 == 1 && steps1 == 0);
+                    __syncwarp();
+                    if (steps1 > 0) {
+                        if (!PAIR && !(ok = ready(&ctl->full[k1.st], k1.phase))) break;
+                        tc_fence_after();
+                        if (elect_one()) issue_scores(1, k1, steps0 == 1);
+                        __syncwarp();
+                    }
+                }
+                for (int i = 0; i < steps0; ++i) {
+                    if (PAIR) {
+                        // both streams read the same tiles; the next keys have long arrived when they are looked at
+                        const bool more = i + 1 < nt;
+                        const Entry v = entry(p0 + 2 * i + 1), k = entry(p0 + 2 * i + 2);
+                        if (!(ok = ready(&ctl->full[v.st], v.phase) && (!more || ready(&ctl->full[k.st], k.phase)))) break;
+                        if (!(ok = advance(0, v, k, i == 0, more, false))) break;
+                        if (!(ok = advance(1, v, k, i == 0, more, i + 2 == nt))) break;
+                    } else {
+                        const Entry v0 = entry(p0 + 4 * i + 1), k0 = entry(p0 + 4 * i + 4);
+                        if (!(ok = ready(&ctl->full[v0.st], v0.phase))) break;
+                        if (!(ok = advance(0, v0, k0, i == 0, i + 1 < steps0, i + 2 == steps0 && i + 1 >= steps1))) break;
+                        if (i >= steps1) continue;
+                        const Entry v1 = entry(p0 + 4 * i + 3), k1 = entry(p0 + 4 * i + 6);
+                        if (!(ok = ready(&ctl->full[v1.st], v1.phase))) break;
+                        if (!(ok = advance(1, v1, k1, i == 0, i + 1 < steps1, i + 2 == steps0))) break;
+                    }
                 }
             }
+            if (elect_one()) tc_commit(&ctl->drained);
+            __syncwarp();
+            mbar_wait(&ctl->drained, 0, g.timeout_ns);
         }
-        if (elect_one()) tc_commit(&ctl->drained);
-        __syncwarp();
-        mbar_wait(&ctl->drained, 0, g.timeout_ns);
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ---- softmax of stream s: a thread owns row r ----
@@ -1071,7 +1081,10 @@ dspark_status attend(const dspark_cache *cache, const dspark_attention_args *arg
     g.window = window;
     g.scale = scale;
     g.tile_tokens = kTile / group;
-    // Two query tiles share each key tile where the chunks fill them; a chunk of one tile splits its keys over the streams.
+    // Two query tiles share each key tile where chunks have two; a chunk of one tile splits its keys over the streams. Query tiles
+    // in pairs against one at a time: 16 chunks of 33 tokens (a tile holds 32) over 3000 keys 52 against 77 us, of 96
+    // tokens 92 against 110, 8192 tokens after 8192 1019 against 1147; of chunks that one tile holds, 1-8 tokens over 16,000-66,000
+    // keys 200 against 182. Four chunks of 64 tokens are the exception (35 against 29): few items, so more blocks join each.
     const bool pair = max_new > g.tile_tokens;
     const int step = g.tile_tokens * (pair ? 2 : 1);
     g.chunk_tiles = (max_new + step - 1) / step;

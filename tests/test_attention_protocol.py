@@ -43,6 +43,7 @@ class Model:
     def __init__(self, mode, segments, rng):
         self.pair, self.stages = MODES[mode]
         self.segments, self.rng = segments, rng
+        self.edges = [{t for t in range(nt) if t in (0, nt - 1) or rng.random() < 0.3} for nt in segments]
         b = self.b = {}
         for i in range(self.stages):
             b["full", i], b["empty", i] = Bar(1), Bar(1)
@@ -170,7 +171,7 @@ class Model:
             for i, t in enumerate(mine):
                 yield ("s_full", s), tile
                 tile += 1
-                if t + 1 == nt:  # the last tile's values behind the end are cleared
+                if t in self.edges[g]:  # values that no row sees are cleared
                     p = 2 * (base + t) + 1
                     yield ("full", p % self.stages), p // self.stages
                     assert self.ring[p % self.stages] == ["v", g, t]
