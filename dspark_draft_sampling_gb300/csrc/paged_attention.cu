@@ -18,7 +18,7 @@
 // sequence of tiles that the thread blocks, one to an SM, take in equal contiguous ranges.  Every block finds its range
 // from the lengths on the device, so nothing about them has to be known on the host.  An item cut by a range's end
 // leaves partial sums (32-bit O, maximum, sum) in the workspace; the block that arrives last joins them in
-// block order, so the result does not depend on which one that is.
+// block order, many of them in two steps, so the result does not depend on which one that is.
 //
 // Measured (GB300). 8192 tokens after 8192, 32 / 8 heads of 128: 1.02 ms, 1.62 PFLOP/s under the power cap, where the library's
 // matrix product sustains 1.75; one cold launch 0.94 ms with the tensor pipe active for 74 % of it. 1-8 tokens over 16,000-66,000
@@ -28,6 +28,8 @@
 // over 777 keys: 11 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "kv_cache.cuh"
 #include "tc.cuh"
@@ -49,6 +51,10 @@ constexpr size_t kSmemBytes = 227 * 1024;
 constexpr int kItemCost = 2;
 // Powers of two by which a row's maximum may lag. With 0, 4, 8: prompt of 8192 tokens after 8192 1176, 1023, 1019 us.
 constexpr float kRescale = 8.f;
+// Rows (rounded up to a power of two) x parts of an item from which its parts are joined in two steps. One step | two: 49 tokens over
+// 8720 keys in 35 parts 52 | 32 us, 64 tokens over 8000 keys in 19 parts 47 | 39; 32 tokens over 1000 keys in 10 parts 21.4 | 22.6.
+constexpr int kTwoSteps = 2048;
+static_assert(kMaxCtas < 256, "arrivals are counted in bytes");
 
 struct Attention {
     void *out;
@@ -70,10 +76,10 @@ struct Shape {
     static constexpr int kHalves = D / 64;                       // 64-element column blocks of 128 bytes
     static constexpr uint32_t kTileBytes = kTile * D * 2;
     static constexpr int kStages = static_cast<int>((kSmemData - QT * kTileBytes) / kTileBytes);
-    static constexpr size_t kSlotFloats = size_t(kTile) * (D + 2);  // partial of one query tile: O, maximum, sum
+    static constexpr size_t kSlotFloats = size_t(kTile) * (D + 4);  // partial of one query tile: O, maximum, sum; maximum, sum of a joined O
 };
 
-size_t slot_bytes(int head_dim) { return 4 * size_t(kTile) * (head_dim + 2); }
+size_t slot_bytes(int head_dim) { return 4 * size_t(kTile) * (head_dim + 4); }
 
 struct Seq {
     int row, n, length, q0;  // table row, new tokens, tokens, first query token
@@ -301,27 +307,33 @@ __device__ __forceinline__ uint64_t smem_desc_values(uint32_t addr) {
     return d;
 }
 
-// Block b's part of an item that begins with block cf: in its second slot where the block is the first, else in its first.
-template <int D, int QT>
-__device__ __forceinline__ const float *part_of(const float *parts, int b, int cf) {
-    return parts + (size_t(b) * 2 + (b == cf ? 1 : 0)) * QT * (size_t(kTile) * (D + 2));
-}
+// What is joined at once: count parts of one item. A block that an item begins with keeps its part in its second slot, the
+// others in their first, so the parts are a stride apart but for the first one, which may lie `lead` further on. Their maxima stand in
+// column max_col of a part, their sums in the next.
+struct Join {
+    float *base;
+    unsigned stride, lead;  // in floats
+    int count, max_col;
+    __device__ __forceinline__ float *part(int k) const { return base + (k * stride + (k == 0 ? lead : 0u)); }
+};
 
-// Joins columns c4, c4 + step, ... (of four values each) of one row: COLS columns of PARTS parts are in flight at a time.
-template <bool BF16, int D, int QT, int COLS, int PARTS>
-__device__ __forceinline__ void join_columns(const float *parts, int cf, int cl, int row, int c4, int step, float top, float inv, float sc,
+// Joins columns c4, c4 + step, ... (of four values each) of one row: COLS columns of PARTS parts are in flight at a time. The
+// result goes to the output, or, in 32 bits and not divided, in place of the first part.
+template <bool BF16, int D, int COLS, int PARTS>
+__device__ __forceinline__ void join_columns(const Join &j, int row, int c4, int step, float top, float inv, float sc, bool final,
                                              unsigned short *to) {
+    float4 *joined = reinterpret_cast<float4 *>(j.part(0)) + row;
     for (; c4 < D / 4; c4 += COLS * step) {
         float4 acc[COLS];
 #pragma unroll
         for (int q = 0; q < COLS; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int b0 = cf; b0 <= cl; b0 += PARTS) {
+        for (int k0 = 0; k0 < j.count; k0 += PARTS) {
             float w[PARTS];
             float4 o[PARTS][COLS];
 #pragma unroll
             for (int u = 0; u < PARTS; ++u) {  // behind the last part: the last one again, with weight 0
-                const float *p = part_of<D, QT>(parts, min(b0 + u, cl), cf);
-                w[u] = b0 + u <= cl ? __ldcg(p + size_t(kTile) * D + row) : -INFINITY;
+                const float *p = j.part(min(k0 + u, j.count - 1));
+                w[u] = k0 + u < j.count ? __ldcg(p + size_t(kTile) * j.max_col + row) : -INFINITY;
 #pragma unroll
                 for (int q = 0; q < COLS; ++q)
                     o[u][q] = __ldcg(reinterpret_cast<const float4 *>(p) + min(c4 + q * step, D / 4 - 1) * kTile + row);
@@ -340,9 +352,13 @@ __device__ __forceinline__ void join_columns(const float *parts, int cf, int cl,
         }
 #pragma unroll
         for (int q = 0; q < COLS; ++q)
-            if (c4 + q * step < D / 4)
-                *reinterpret_cast<uint2 *>(to + (c4 + q * step) * 4) =
-                    make_uint2(pack16<BF16>(acc[q].x * inv, acc[q].y * inv), pack16<BF16>(acc[q].z * inv, acc[q].w * inv));
+            if (c4 + q * step < D / 4) {
+                if (final)
+                    *reinterpret_cast<uint2 *>(to + (c4 + q * step) * 4) =
+                        make_uint2(pack16<BF16>(acc[q].x * inv, acc[q].y * inv), pack16<BF16>(acc[q].z * inv, acc[q].w * inv));
+                else
+                    __stcg(joined + (c4 + q * step) * kTile, acc[q]);
+            }
     }
 }
 
@@ -487,7 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!few)
                     for (int s = lane; s < g.n_seqs; s += 32) total += cost[s];
                 total = __reduce_add_sync(0xffffffffu, total) * c.kv_heads;
-                const unsigned per = (total + gridDim.x - 1) / gridDim.x;
+                // not less than an item's fixed cost: 32 tokens over 1000 keys take 17 us, 21 in ranges of one tile; 7 over 2000 keys 12.0,
+                // 14.2. Ranges of 4 and more pay for some (300 tokens 11.5 against 15.7), but one token over 776 keys takes 14.3 against 10.6.
+                const unsigned per = max((total + gridDim.x - 1) / gridDim.x, static_cast<unsigned>(kItemCost));
                 walk.per = per;
                 walk.pos = min(per * blockIdx.x, total);
                 walk.left = min(per, total - walk.pos);
@@ -940,69 +958,104 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             // ---- an item cut by ranges' ends: the last of its blocks joins the partial results ----
+            // Where that is more data than one SM should read, in two steps: groups of neighbouring blocks' parts first.
             if (real && (PAIR || s == 0)) {
                 __stcg(slot + size_t(kTile) * D + r, m);
                 __stcg(slot + size_t(kTile) * (D + 1) + r, l);
             }
-            __threadfence();
-            uint64_t *sync = &ctl->sync[PAIR ? s : 0];
-            mbar_arrive(sync);
-            if (!(ok = warp_wait(ctl, sync, n_sync & 1, c, g.tries))) break;
-            ++n_sync;
-            if (r == 0 && (PAIR || s == 0)) {
-                unsigned *count = g.arrivals + cf * 2 + (PAIR ? s : 0);
-                const unsigned before = atomicAdd(count, 1u);
-                const bool is_last = before == static_cast<unsigned>(cl - cf);
-                if (is_last) *count = 0;
-                ctl->last[PAIR ? s : 0] = is_last;
-                __threadfence();
-            }
-            mbar_arrive(sync);
-            if (!(ok = warp_wait(ctl, sync, n_sync & 1, c, g.tries))) break;
-            ++n_sync;
-            if (!ctl->last[PAIR ? s : 0]) continue;
             const int first_token = seg.tile * step + (PAIR ? s * g.tile_tokens : 0);
             const int rows = min(g.tile_tokens, seg.n - first_token) * g.group;  // may be <= 0: the second tile of a pair
-            const float *parts = g.partials + (PAIR ? s : 0) * S::kSlotFloats;
-            // A thread keeps to one row and takes its columns, four at a time, in strides.
-            constexpr int kJoiners = PAIR ? 128 : 256;
-            const int shift = rows > 1 ? 32 - __clz(rows - 1) : 0, joiner = PAIR ? r : s * kTile + r;
-            const int my_row = joiner & ((1 << shift) - 1), c4_step = kJoiners >> shift;
-            const int row = min(my_row, rows - 1);  // the threads beyond the rows only load
-            if (rows <= 0) continue;
-            float top = -INFINITY, z = 0.f;
-            for (int b0 = cf; b0 <= cl; b0 += 8) {
-                float pm[8], pl[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    pm[u] = -INFINITY, pl[u] = 0.f;
-                    if (b0 + u <= cl) {
-                        pm[u] = __ldcg(part_of<D, S::QT>(parts, b0 + u, cf) + size_t(kTile) * D + row);
-                        pl[u] = __ldcg(part_of<D, S::QT>(parts, b0 + u, cf) + size_t(kTile) * (D + 1) + row);
+            const int shift = rows > 1 ? 32 - __clz(rows - 1) : 0;
+            auto join = [&](auto steps) {  // whether its waits ended well
+                constexpr bool TWO = decltype(steps)::value == 2;
+                constexpr unsigned kSlot = static_cast<unsigned>(S::QT * S::kSlotFloats), kBlock = 2 * kSlot;
+                int first = cf, span = 2;  // first block of the parts
+                Join j;
+                j.stride = kBlock;
+                j.count = cl - cf + 1;
+                j.max_col = D;
+                bool final = !TWO;
+                if (TWO) {
+                    while (span * span < j.count) ++span;
+                    first += (static_cast<int>(blockIdx.x) - cf) / span * span;
+                    j.count = min(span, cl + 1 - first);
+                }
+                for (;; final = true) {
+                    __threadfence();
+                    uint64_t *sync = &ctl->sync[PAIR ? s : 0];
+                    mbar_arrive(sync);
+                    if (!warp_wait(ctl, sync, n_sync & 1, c, g.tries)) return false;
+                    ++n_sync;
+                    if (r == 0 && (PAIR || s == 0)) {
+                        // a byte for each stream's arrivals at a first and at the last join
+                        unsigned *count = g.arrivals + first * 2 + (first == cf ? 1 : 0);
+                        const unsigned at = (PAIR ? s * 16 : 0) + (j.stride != kBlock ? 8 : 0);
+                        const bool is_last = ((atomicAdd(count, 1u << at) >> at) & 255u) + 1u == static_cast<unsigned>(j.count);
+                        ctl->last[PAIR ? s : 0] = is_last;
+                        __threadfence();
+                        if (is_last) atomicSub(count, static_cast<unsigned>(j.count) << at);
                     }
-                }
+                    mbar_arrive(sync);
+                    if (!warp_wait(ctl, sync, n_sync & 1, c, g.tries)) return false;
+                    ++n_sync;
+                    if (!ctl->last[PAIR ? s : 0] || rows <= 0) return true;
+                    j.base = g.partials + (PAIR ? s : 0) * S::kSlotFloats + static_cast<unsigned>(first) * kBlock;
+                    j.lead = first == cf ? kSlot : 0;
+                    // A thread keeps to one row and takes its columns, four at a time, in strides.
+                    constexpr int kJoiners = PAIR ? 128 : 256;
+                    const int joiner = PAIR ? r : s * kTile + r;
+                    const int my_row = joiner & ((1 << shift) - 1), c4_step = kJoiners >> shift;
+                    const int row = min(my_row, rows - 1);  // the threads beyond the rows only load
+                    float top = -INFINITY, z = 0.f;
+                    for (int k0 = 0; k0 < j.count; k0 += 8) {
+                        float pm[8], pl[8];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const float up = fmaxf(top, pm[u]);
-                    z = z * (top == -INFINITY ? 0.f : ex2((top - up) * sc)) + pl[u] * (pm[u] == -INFINITY ? 0.f : ex2((pm[u] - up) * sc));
-                    top = up;
+                        for (int u = 0; u < 8; ++u) {
+                            pm[u] = -INFINITY, pl[u] = 0.f;
+                            if (k0 + u < j.count) {
+                                const float *p = j.part(k0 + u) + size_t(kTile) * j.max_col + row;
+                                pm[u] = __ldcg(p);
+                                pl[u] = __ldcg(p + kTile);
+                            }
+                        }
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const float up = fmaxf(top, pm[u]);
+                            z = z * (top == -INFINITY ? 0.f : ex2((top - up) * sc)) + pl[u] * (pm[u] == -INFINITY ? 0.f : ex2((pm[u] - up) * sc));
+                            top = up;
+                        }
+                    }
+                    const int tk = row / g.group, hd = seg.kv_head * g.group + row - tk * g.group;
+                    const long long qt = seg.q0 + first_token + tk;
+                    const float f = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
+                    unsigned short *to = static_cast<unsigned short *>(g.out) + qt * g.out_token + hd * g.out_head;
+                    if ((joiner >> shift) == 0 && my_row == row) {
+                        if (!final) {
+                            float *p = j.part(0) + size_t(kTile) * (D + 2) + row;
+                            __stcg(p, top);
+                            __stcg(p + kTile, z);
+                        } else if (g.lse) {
+                            g.lse[qt * (c.kv_heads * g.group) + hd] = z == 0.f ? -INFINITY : (top * sc + lg2(z)) * 0.6931471805599453f;
+                        }
+                    }
+                    const int c4 = my_row == row ? joiner >> shift : D / 4;
+                    // Eight to sixteen vectors in flight a thread: two parts are the rule where query tiles fill their rows; with few rows
+                    // there may be many parts.
+                    if (PAIR)
+                        join_columns<BF16, D, 8, 2>(j, row, c4, c4_step, top, f, sc, final, to);
+                    else if (c4_step * 2 <= D / 4)
+                        join_columns<BF16, D, 4, 2>(j, row, c4, c4_step, top, f, sc, final, to);
+                    else
+                        join_columns<BF16, D, 1, 16>(j, row, c4, c4_step, top, f, sc, final, to);
+                    if (!TWO || final) return true;
+                    first = cf;
+                    j.stride = span * kBlock;
+                    j.count = (cl - cf) / span + 1;
+                    j.max_col = D + 2;
                 }
-            }
-            const int tk = row / g.group, hd = seg.kv_head * g.group + row - tk * g.group;
-            const long long qt = seg.q0 + first_token + tk;
-            const float f = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
-            unsigned short *to = static_cast<unsigned short *>(g.out) + qt * g.out_token + hd * g.out_head;
-            if (g.lse && (joiner >> shift) == 0 && my_row == row)
-                g.lse[qt * (c.kv_heads * g.group) + hd] = z == 0.f ? -INFINITY : (top * sc + lg2(z)) * 0.6931471805599453f;
-            const int c4 = my_row == row ? joiner >> shift : D / 4;
-            // Eight to sixteen vectors in flight a thread: two parts are the rule where query tiles fill their rows; with few rows there may be
-            // many parts.
-            if (PAIR)
-                join_columns<BF16, D, S::QT, 8, 2>(parts, cf, cl, row, c4, c4_step, top, f, sc, to);
-            else if (c4_step * 2 <= D / 4)
-                join_columns<BF16, D, S::QT, 4, 2>(parts, cf, cl, row, c4, c4_step, top, f, sc, to);
-            else
-                join_columns<BF16, D, S::QT, 1, 16>(parts, cf, cl, row, c4, c4_step, top, f, sc, to);
+            };
+            ok = ((cl - cf + 1) << shift) < kTwoSteps ? join(std::integral_constant<int, 1>()) : join(std::integral_constant<int, 2>());
+            if (!ok) break;
         }
     }
     tc_fence_before();

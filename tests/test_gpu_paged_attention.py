@@ -102,6 +102,11 @@ CASES = {
     "many": (F16, 64, 2, 1, 16, [(1 + i % 3, 1 + 37 * i % 211) for i in range(70)], True, 0),
     "split_long": (BF16, 128, 4, 1, 64, [(1, 9000)], True, 0),
     "split_ragged": (F16, 128, 2, 1, 16, [(2, 5001), (1, 16), (4, 2500)], True, 0),
+    # cut into so many parts that they are joined in two steps
+    "split_chunk": (BF16, 128, 4, 1, 64, [(32, 9000)], True, 0),
+    "split_pairs": (F16, 128, 3, 1, 128, [(49, 8720)] * 3, True, 0),
+    "split_pairs_one_row": (BF16, 64, 4, 1, 32, [(33, 12001)], False, 0),
+    "split_window": (F16, 64, 8, 2, 16, [(60, 7000), (1, 300)], True, 3000),
 }
 
 
