@@ -471,10 +471,15 @@ __global__ void __launch_bounds__(kBooksThreads, 1)
 // Moves the kept tokens of one row (blockIdx.y) in one (layer, k or v, head) run (blockIdx.x) to the front; one warp.
 //
 // In place and in parallel: token j's new slot is never behind its old one, and both ascend, so a write to slot j only
-// lands on the old slot of a token of the same or an earlier tile.  A tile of 32 tokens is read whole into shared memory, by
+// lands on the old slot of a token of the same or an earlier tile.  A tile is read whole into shared memory, by
 // bulk copies of as many neighbouring tokens as lie together, before it is written; the next tiles' reads are under way
 // meanwhile and need no wait for these writes.
-constexpr int kMoveTokens = 32, kMoveStages = 4;
+//
+// A tile is U times 32 tokens, a lane to a token. A step from tile to tile is a chain of a wait and two trips to memory whatever
+// the tile's size, so few runs take long tiles (a row of 4000 tokens, 64 runs: the whole compaction 65 us, 74 with tiles of
+// 32); of many runs, which memory bounds, short tiles leave room for more blocks on an SM (16 rows of 900-4100 tokens, 64
+// runs each: 230 us, 1.3 GB, 247 with tiles of 128).
+constexpr int kMoveTokens = 32, kMoveLong = 4, kMoveStages = 4, kMoveAhead = 2;  // two stages on their way, two being written
 
 __device__ __forceinline__ void bulk_load(uint32_t to, const void *from, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from), "r"(bytes),
@@ -491,11 +496,13 @@ __device__ __forceinline__ int stretch(unsigned heads, unsigned active, int lane
     return (ends ? __ffs(ends) - 1 : 32) - lane;
 }
 
+template <int U>
 __global__ void __launch_bounds__(32) compact_move_kernel(CacheView c, const int *rows, const int *start, const int *kept, int kept_stride,
                                                           const int *n_kept) {
+    constexpr int kTokens = U * kMoveTokens;
     extern __shared__ __align__(128) unsigned char stages[];
     __shared__ uint64_t full[kMoveStages];
-    __shared__ unsigned char *s_to[kMoveStages][kMoveTokens];
+    __shared__ unsigned char *s_to[kMoveStages][kTokens];
     const int lane = threadIdx.x;
     if (lane == 0) {
         for (int q = 0; q < kMoveStages; ++q) mbar_init(&full[q], 1);
@@ -514,56 +521,86 @@ __global__ void __launch_bounds__(32) compact_move_kernel(CacheView c, const int
     const uint32_t token_b = c.head_dim * 2;
     const size_t run_b = size_t(c.page_size) * token_b, page_b = run_b * c.layers * 2 * c.kv_heads;
     unsigned char *pool = c.pool + run * run_b;
-    const uint32_t base = smem_addr(stages), stage_b = kMoveTokens * token_b;
-    const int first = st & ~mask, tiles = (end - first + kMoveTokens - 1) / kMoveTokens;
-    auto position = [&](int tile) {  // where the lane's token of a tile is now
-        const int j = first + tile * kMoveTokens + lane;
-        return j >= end || j < st ? j : w[j - st];
-    };
-    int ahead = position(0);
-    auto load = [&](int tile) {
-        const int j = first + tile * kMoveTokens + lane, s = ahead, q = tile % kMoveStages;
-        ahead = position(tile + 1);
-        const unsigned char *from = nullptr;
-        unsigned char *to = nullptr;
+    const uint32_t base = smem_addr(stages), stage_b = kTokens * token_b;
+    const int first = st & ~mask, tiles = (end - first + kTokens - 1) / kTokens;
+    // Looked up ahead, as each is a trip to memory: where two tiles' tokens are now, the pages of one.
+    int at[U], next_at[U], from_page[U], to_page[U];
+    auto position = [&](int j) { return j >= end || j < st ? j : w[j - st]; };
+    auto pages = [&](int u, int j) {
         if (j < end) {
-            from = pool + (snap[s >> c.page_shift] & ~kShared) * page_b + size_t(s & mask) * token_b;
-            to = pool + t[j >> c.page_shift] * page_b + size_t(j & mask) * token_b;
-            if (from == to) to = nullptr;  // stays where it is
+            from_page[u] = snap[at[u] >> c.page_shift];
+            to_page[u] = t[j >> c.page_shift];
         }
-        s_to[q][lane] = to;
-        const unsigned active = __ballot_sync(0xffffffffu, to != nullptr);
-        const unsigned long long last = __shfl_up_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), 1);
-        const bool head = to && (lane == 0 || !((active >> (lane - 1)) & 1) || last + token_b != reinterpret_cast<unsigned long long>(from));
-        const unsigned heads = __ballot_sync(0xffffffffu, head);
-        if (lane == 0) mbar_arrive_expect_tx(&full[q], __popc(active) * token_b);
-        __syncwarp();
-        if (head) bulk_load(base + q * stage_b + lane * token_b, from, stretch(heads, active, lane) * token_b, &full[q]);
     };
-    for (int tile = 0; tile < kMoveStages - 1 && tile < tiles; ++tile) load(tile);
-    int loaded = tiles < kMoveStages - 1 ? tiles : kMoveStages - 1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int j = first + u * kMoveTokens + lane;
+        from_page[u] = to_page[u] = 0;
+        at[u] = position(j);
+        next_at[u] = position(j + kTokens);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) pages(u, first + u * kMoveTokens + lane);
+    // stretches of neighbouring tokens that move: whether one begins at the lane, and its length
+    auto stretch_at = [&](bool moves, const unsigned char *p, int *length) {
+        const unsigned active = __ballot_sync(0xffffffffu, moves);
+        const unsigned long long before = __shfl_up_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), 1);
+        const bool head = moves && (lane == 0 || !((active >> (lane - 1)) & 1) || before + token_b != reinterpret_cast<unsigned long long>(p));
+        *length = stretch(__ballot_sync(0xffffffffu, head), active, lane);
+        return head;
+    };
+    auto load = [&](int tile) {
+        const int q = tile % kMoveStages;
+        const unsigned char *from[U];
+        bool moves[U];
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = first + tile * kTokens + u * kMoveTokens + lane;
+            from[u] = pool + (from_page[u] & ~kShared) * page_b + size_t(at[u] & mask) * token_b;
+            unsigned char *to = pool + to_page[u] * page_b + size_t(j & mask) * token_b;
+            moves[u] = j < end && from[u] != to;  // the others stay where they are
+            s_to[q][u * kMoveTokens + lane] = moves[u] ? to : nullptr;
+            bytes += __popc(__ballot_sync(0xffffffffu, moves[u])) * token_b;
+            at[u] = next_at[u];
+            next_at[u] = position(j + 2 * kTokens);
+            pages(u, j + kTokens);
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&full[q], bytes);
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            int length;
+            if (stretch_at(moves[u], from[u], &length))
+                bulk_load(base + q * stage_b + (u * kMoveTokens + lane) * token_b, from[u], length * token_b, &full[q]);
+        }
+    };
+    for (int tile = 0; tile < kMoveAhead && tile < tiles; ++tile) load(tile);
+    int loaded = min(tiles, kMoveAhead);
     for (int tile = 0; tile < tiles; ++tile) {
         const int q = tile % kMoveStages;
         if (!__all_sync(0xffffffffu, mbar_wait(&full[q], (tile / kMoveStages) & 1, kDefaultTimeoutNs))) {
             if (lane == 0) atomicOr(c.status, kStatusTimeout);
             break;
         }
-        unsigned char *to = s_to[q][lane];
-        const unsigned active = __ballot_sync(0xffffffffu, to != nullptr);
-        const unsigned long long last = __shfl_up_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), 1);
-        const bool head = to && (lane == 0 || last + token_b != reinterpret_cast<unsigned long long>(to));
-        const unsigned heads = __ballot_sync(0xffffffffu, head);
-        if (head) bulk_store(to, base + q * stage_b + lane * token_b, stretch(heads, active, lane) * token_b);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            unsigned char *to = s_to[q][u * kMoveTokens + lane];
+            int length;
+            if (stretch_at(to != nullptr, to, &length))
+                bulk_store(to, base + q * stage_b + (u * kMoveTokens + lane) * token_b, length * token_b);
+        }
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        if (tile + kMoveStages - 1 < tiles) {
-            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the slot's last tile has been written from it
+        if (tile + kMoveAhead < tiles) {
+            // the slot's last tile has been written from it
+            asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kMoveStages - kMoveAhead) : "memory");
             __syncwarp();
-            load(tile + kMoveStages - 1);
+            load(tile + kMoveAhead);
             ++loaded;
         }
     }
     // copies in flight end before the block does, also after a wait that gave up
-    for (int tile = loaded > kMoveStages ? loaded - kMoveStages : 0; tile < loaded; ++tile)
+    for (int tile = max(loaded - kMoveStages, 0); tile < loaded; ++tile)
         mbar_wait(&full[tile % kMoveStages], (tile / kMoveStages) & 1, kDefaultTimeoutNs);
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
@@ -593,7 +630,7 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(CacheView c, const int 
 dspark_status launched(cudaError_t e, const char *what) { return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, what); }
 
 // Launches the books of a call that looks through `entries` of lists and tables: a block for each 4096 of them or of the pool's pages, up
-// to eight (1, 2, 4 or 8).  Compacting 16 rows of 2,500 tokens takes 233 us with eight, 245 with one.
+// to eight (1, 2, 4 or 8).  Compacting 16 rows of 2,500 tokens took 233 us with eight, 245 with one.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_books(void (*kernel)(KArgs...), const CacheView &c, long long entries, cudaStream_t stream, Args &&...args) {
     const long long work = entries > c.num_pages ? entries : c.num_pages;
@@ -732,8 +769,24 @@ extern "C" dspark_status dspark_cache_compact(const dspark_cache *cache, const i
     st = launched(launch_books(compact_books_kernel, c, static_cast<long long>(n) * (kept_stride + c.max_pages), stream, c, rows, start, kept, kept_stride, n_kept, n),
                   "cache_compact");
     if (st != DSPARK_OK) return st;
-    return launched(launch_pdl(compact_move_kernel, dim3(c.layers * 2 * c.kv_heads, n), dim3(32), size_t(kMoveStages) * kMoveTokens * c.head_dim * 2,
-                               stream, c, rows, start, kept, kept_stride, n_kept),
+    int sms = 0;
+    if ((st = static_cast<dspark_status>(current_sm_count(&sms))) != DSPARK_OK) return st;
+    const int runs = c.layers * 2 * c.kv_heads;
+    const bool few = static_cast<long long>(runs) * n <= sms;  // an SM to each run
+    auto *kernel = few ? compact_move_kernel<kMoveLong> : compact_move_kernel<1>;
+    const int tile_b = kMoveStages * kMoveTokens * 2;  // for each unit of head_dim
+    if (few) {
+        static int configured = -1;
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess && configured != dev) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveLong * tile_b * 128);
+            if (e == cudaSuccess) configured = dev;
+        }
+        if (e != cudaSuccess) return cuda_fail(e, "cache_compact");
+    }
+    return launched(launch_pdl(kernel, dim3(runs, n), dim3(32), size_t(few ? kMoveLong : 1) * tile_b * c.head_dim, stream, c, rows, start,
+                               kept, kept_stride, n_kept),
                     "cache_compact");
 }
 

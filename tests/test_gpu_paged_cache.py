@@ -110,6 +110,16 @@ def test_long_compaction(page, dim):
     p.call("compact", [3, 0], [100, 0], [sorted(r.sample(range(100, 1781), 900)), list(range(5, 1781))])
 
 
+def test_many_runs():
+    # more runs of layers and heads than there are SMs, and so many forks that several share a block
+    r = random.Random(4)
+    p = Pair(420, 330, 7, page=64, dim=128, layers=6, heads=8)
+    p.call("extend", [0, 1, 2, 3], [400, 129, 64, 333])
+    p.call("compact", [0, 3, 1], [4, 0, 10],
+           [list(range(40, 400)), sorted(r.sample(range(333), 200)), list(range(64, 129))])
+    p.call("fork", [r.choice([0, 0, 0, 1, 2, 3]) for _ in range(7)] + [i // 37 % 4 for i in range(7, 326)], list(range(4, 330)))
+
+
 def test_cut_off_without_a_list():
     p = Pair(20, 3, 8)
     p.call("extend", [0, 1], [50, 33])
