@@ -20,9 +20,9 @@
 // leaves partial sums (32-bit O, maximum, sum) in the workspace; the block that arrives last joins them in
 // block order, many of them in two steps, so the result does not depend on which one that is.
 //
-// Measured (GB300). 8192 tokens after 8192, 32 / 8 heads of 128: 1.02 ms, 1.62 PFLOP/s under the power cap, where the library's
-// matrix product sustains 1.75; one cold launch 0.94 ms with the tensor pipe active for 74 % of it. 1-8 tokens over 16,000-66,000
-// keys: 182 us for 1.2 GB, 98 % of a copy's rate. 16 x 7 tokens over 300-6000 keys: 45 us for 183 MB, of which 32 are that
+// Measured (GB300). 8192 tokens after 8192, 32 / 8 heads of 128: 0.93 ms, 1.77 PFLOP/s, for ten launches after a pause;
+// 1.02 ms, 1.62 PFLOP/s, under the power cap, where the library's matrix product sustains 1.75. 1-8 tokens over 16,000-66,000
+// keys: 182 us for 1.2 GB, 98 % of a copy's rate. 16 x 7 tokens over 300-6000 keys: 42 us for 183 MB, of which about 30 are that
 // stream, the rest start and joins. Chunks of 90-1500 tokens in a window of 1000, 28 / 4 heads of 64: 69 us, where the chain
 // of one stream (scores, softmax, second product) takes 2500 cycles a pair of key tiles and the products 1024. One token
 // over 777 keys: 11 us.
@@ -46,7 +46,7 @@ static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "
 constexpr int kTmemCols = 512;
 constexpr size_t kSmemData = 224 * 1024;      // query tiles and the ring of key and value tiles
 constexpr size_t kSmemBytes = 227 * 1024;
-// An item's fixed cost, in key tiles. With 1, 2, 3, 4, 6: 16 blocks of 7 tokens over 300-6000 keys 44.7, 44.8, 46.0, 46.0, 49.4 us;
+// An item's fixed cost, in key tiles. With 1, 2, 3, 4, 6: 16 blocks of 7 tokens over 300-6000 keys (pages in two copies then) 44.7, 44.8, 46.0, 46.0, 49.4 us;
 // chunks in a window of 1000 70.7, 68.8, 69.0, 68.2, 69.4; 4 chunks of 64 tokens over 3000 keys 36.8, 34.9, 32.7, 33.0, 33.5.
 constexpr int kItemCost = 2;
 // Powers of two by which a row's maximum may lag. With 0, 4, 8: prompt of 8192 tokens after 8192 1176, 1023, 1019 us.
@@ -295,17 +295,26 @@ __device__ __forceinline__ void tma_load_3d_plain(uint32_t dst, const CUtensorMa
         : "memory");
 }
 
-// Descriptor of a value tile as the second product's B operand: N (head elements) is contiguous in 128-byte rows of 64
-// elements, one row a key; 8-key groups are 1024 bytes apart, the 64-element blocks 128 keys apart.
-__device__ __forceinline__ uint64_t smem_desc_values(uint32_t addr) {
+// Key and value tiles lie in shared memory as [8-key group][64-element block][key of the group][64 elements], 128-byte rows
+// with the 128-byte swizzle, so that one copy brings a page whatever its length and the groups are evenly spaced. With a copy for each
+// block of a page ([block][key]) prompts over pages of 16 took a fifth longer: 8192 tokens after 8192 1117
+// against 931 us, where the power cap does not hold it back.
+template <int D>
+__device__ __forceinline__ uint64_t smem_desc_tile(uint32_t addr, uint32_t leading) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>((kTile * 128u) >> 4) << 16;
-    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(leading >> 4) << 16;
+    d |= static_cast<uint64_t>((D * 16u) >> 4) << 32;  // from group to group
     d |= static_cast<uint64_t>(1u) << 46;
     d |= static_cast<uint64_t>(2u) << 61;
     return d;
 }
+// Keys are the first product's B operand, K (head elements) contiguous; values the second's, N (head elements) contiguous, where the
+// leading offset goes from one 64-element block to the next.
+template <int D>
+__device__ __forceinline__ uint64_t smem_desc_keys(uint32_t addr) { return smem_desc_tile<D>(addr, 16); }
+template <int D>
+__device__ __forceinline__ uint64_t smem_desc_values(uint32_t addr) { return smem_desc_tile<D>(addr, 1024); }
 
 // What is joined at once: count parts of one item. A block that an item begins with keeps its part in its second slot, the
 // others in their first, so the parts are a stride apart but for the first one, which may lie `lead` further on. Their maxima stand in
@@ -577,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               token + t * g.tile_tokens, &ctl->q_full);
                 }
                 const int *pages = c.table + static_cast<size_t>(walk.q.row) * c.max_pages;
-                const int run = (g.layer * 2) * c.kv_heads + seg.kv_head;
+                const int run = (g.layer * 2) * c.kv_heads + seg.kv_head, runs = c.layers * 2 * c.kv_heads, page_groups = c.page_size / 8;
                 for (int t = seg.first; ok && t < seg.last; ++t) {
                     const int key = (seg.lo + t) * kTile + lane * box;  // first key of this lane's page
                     const bool mine = lane < per_tile && key < seg.end && key + box > seg.begin;  // pages that no row sees are not looked at
@@ -590,16 +599,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
-                    const int slot = key & (c.page_size - 1);  // pages longer than a tile
+                    const int group = (page * runs + run) * page_groups + (key & (c.page_size - 1)) / 8;  // a page may be longer than a tile
                     for (int w = 0; w < 2; ++w, ++put) {
                         const uint32_t st = put % S::kStages;
                         if (put >= S::kStages && !(ok = warp_wait(ctl, &ctl->empty[st], ((put / S::kStages) & 1) ^ 1, c, g.tries))) break;
                         if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], boxes * static_cast<uint32_t>(box) * D * 2);
                         __syncwarp();
                         if (mine)
-                            for (int h = 0; h < S::kHalves; ++h)
-                                tma_load_4d(ring + st * S::kTileBytes + h * (kTile * 128) + lane * box * 128, &tm_kv, h * 64, slot,
-                                            run + w * c.kv_heads, page, &ctl->full[st]);
+                            tma_load_4d(ring + st * S::kTileBytes + lane * box * (D * 2), &tm_kv, 0, 0, 0, group + w * c.kv_heads * page_groups,
+                                        &ctl->full[st]);
                     }
                 }
             }
@@ -626,21 +634,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto ready = [&](uint64_t *bar, uint32_t phase) { return warp_wait(ctl, bar, phase, c, g.tries); };
             auto issue_scores = [&](const int s, const Entry &e, bool frees_q) {
                 const uint64_t a = smem_desc_sw128(q_smem + (PAIR ? s * S::kTileBytes : 0));
-                const uint64_t b = smem_desc_sw128(ring + e.st * S::kTileBytes);
+                const uint64_t b = smem_desc_keys<D>(ring + e.st * S::kTileBytes);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t o = static_cast<uint64_t>((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
-                    tc_mma_f16(tmem + s * kTile, a + o, b + o, idesc_s, k != 0);
-                }
+                for (int k = 0; k < D / 16; ++k)
+                    tc_mma_f16(tmem + s * kTile, a + (((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4), b + (((k / 4) * 1024 + (k % 4) * 32) >> 4),
+                               idesc_s, k != 0);
                 tc_commit(&ctl->s_full[s]);
                 if (!PAIR || s == 1) tc_commit(&ctl->empty[e.st]);
                 if (frees_q) tc_commit(&ctl->q_empty);  // the segment's last scores free its query tiles
             };
             auto issue_values = [&](const int s, const Entry &e, const int half, bool add) {
-                const uint64_t b = smem_desc_values(ring + e.st * S::kTileBytes);
+                const uint64_t b = smem_desc_values<D>(ring + e.st * S::kTileBytes);
 #pragma unroll
                 for (int k = half * (kTile / 32); k < (half + 1) * (kTile / 32); ++k)
-                    tc_mma_f16_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + k * 8, b + ((k * 2048) >> 4), idesc_o, add || k != 0);
+                    tc_mma_f16_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + k * 8, b + ((k * D * 32) >> 4), idesc_o, add || k != 0);
             };
             // One step of stream s: its second product, then the scores of its next key tile.
             auto advance = [&](const int s, const Entry &v, const Entry &k, bool first, bool more, bool frees_q) {
@@ -748,9 +755,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int first = max(seg.begin - key0, 0) * 8, last = min(seg.end - key0, kTile) * 8;
                     unsigned char *v = ring_ptr + st * S::kTileBytes;
                     for (int h = 0; h < S::kHalves; ++h) {
-                        uint4 *at = reinterpret_cast<uint4 *>(v + h * (kTile * 128));
-                        for (int b = r; b < first; b += kTile) at[b] = make_uint4(0u, 0u, 0u, 0u);
-                        for (int b = last + r; b < kTile * 8; b += kTile) at[b] = make_uint4(0u, 0u, 0u, 0u);
+                        uint4 *at = reinterpret_cast<uint4 *>(v) + h * 64;
+                        for (int b = r; b < first; b += kTile) at[b + (b & ~63) * (S::kHalves - 1)] = make_uint4(0u, 0u, 0u, 0u);
+                        for (int b = last + r; b < kTile * 8; b += kTile) at[b + (b & ~63) * (S::kHalves - 1)] = make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
                 }
@@ -1119,6 +1126,10 @@ dspark_status attend(const dspark_cache *cache, const dspark_attention_args *arg
         return fail(DSPARK_ERR_UNSUPPORTED, "%s: %d tokens of %d sequences over rows of %d pages pass 2^32 key tiles", who, tokens, n_seqs,
                     c.max_pages);
 
+    const cuuint64_t page_groups = 2ull * c.layers * c.kv_heads * (c.page_size / 8), groups = page_groups * c.num_pages;
+    if (groups + page_groups > 0x7fffffffull)
+        return fail(DSPARK_ERR_UNSUPPORTED, "%s: a pool of more than 2^31 groups of 8 slots of a head", who);
+
     Attention g{};
     g.out = out;
     g.lse = lse;
@@ -1156,11 +1167,10 @@ dspark_status attend(const dspark_cache *cache, const dspark_attention_args *arg
         if ((st = make_tmap_nd(&tm_q, bf16, q, 3, dims, strides, box)) != DSPARK_OK) return st;
     }
     {
-        const cuuint64_t runs = 2ull * c.layers * c.kv_heads, run_bytes = 2ull * c.page_size * c.head_dim;
-        const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.page_size), runs,
-                                    static_cast<cuuint64_t>(c.num_pages)};
-        const cuuint64_t strides[3] = {2ull * c.head_dim, run_bytes, runs * run_bytes};
-        const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(c.page_size < kTile ? c.page_size : kTile), 1, 1};
+        // all of the pool as groups of 8 slots of one page, layer, half and head
+        const cuuint64_t dims[4] = {64, 8, static_cast<cuuint64_t>(c.head_dim / 64), groups};
+        const cuuint64_t strides[3] = {2ull * c.head_dim, 128, 16ull * c.head_dim};
+        const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(c.head_dim / 64), static_cast<cuuint32_t>((c.page_size < kTile ? c.page_size : kTile) / 8)};
         if ((st = make_tmap_nd(&tm_kv, bf16, c.pool, 4, dims, strides, box)) != DSPARK_OK) return st;
     }
     const int blocks = sms < kMaxCtas ? sms : kMaxCtas;
