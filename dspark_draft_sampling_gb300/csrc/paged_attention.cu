@@ -15,8 +15,9 @@
 // that rounding.
 //
 // Work.  All (sequence, kv head, query tile) items, each with its own number of 128-key tiles, form one
-// sequence of tiles that the thread blocks, one to an SM, take in equal contiguous ranges.  Every block finds its range
-// from the lengths on the device, so nothing about them has to be known on the host.  An item cut by a range's end
+// sequence of tiles that the thread blocks, one to an SM, take in equal contiguous ranges, or, where cutting would cost more
+// than it gains, an item each.  Every block finds its range from the lengths on the device, so nothing about them has
+// to be known on the host.  An item cut by a range's end
 // leaves partial sums (32-bit O, maximum, sum) in the workspace; the block that arrives last joins them in
 // block order, many of them in two steps, so the result does not depend on which one that is.
 //
@@ -63,6 +64,7 @@ struct Attention {
     const int *rows, *cu_new;
     int tokens, group, n_seqs, layer, causal, window, chunk_tiles;  // chunk_tiles: query tiles of the longest chunk (hint)
     int tile_tokens;    // tokens of a 128-row tile
+    unsigned cut;       // what cutting items costs, in key tiles
     float scale;
     float *partials;
     unsigned *arrivals;
@@ -478,10 +480,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int of_seq = g.chunk_tiles <= 4 ? 1 : 32;  // threads to a sequence
         for (int s = threadIdx.x / of_seq; s < g.n_seqs; s += kThreads / of_seq) {
             const Seq q = load_seq(c, g, s);
-            unsigned w = 0;
-            for (int i = threadIdx.x % of_seq; i * step < q.n; i += of_seq) w += item_cost(g, q, i, step);
-            if (of_seq == 32) w = __reduce_add_sync(0xffffffffu, w);
-            if (threadIdx.x % of_seq == 0) cost[s] = w;
+            unsigned w = 0, most = 0;
+            for (int i = threadIdx.x % of_seq; i * step < q.n; i += of_seq) {
+                const unsigned v = item_cost(g, q, i, step);
+                w += v;
+                most = max(most, v);
+            }
+            if (of_seq == 32) {
+                w = __reduce_add_sync(0xffffffffu, w);
+                most = __reduce_max_sync(0xffffffffu, most);
+            }
+            if (threadIdx.x % of_seq == 0) {
+                cost[s] = w;
+                if (s < 32) cost[kMaxSeqs + s] = most, cost[kMaxSeqs + 32 + s] = (q.n + step - 1) / step;
+            }
         }
         fence_proxy_async_smem();  // the scratch use comes before the copies into the ring
     }
@@ -503,25 +515,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // ---- this block's range of all items' tiles, and the item that it begins with ----
                 // in 32 bits: the host has made sure that the tiles' number fits
                 Seq mine{};
-                unsigned w = 0;
-                if (few && lane < g.n_seqs) {
-                    mine = load_seq(c, g, lane);
-                    for (int i = 0; i * step < mine.n; ++i) w += item_cost(g, mine, i, step);
+                unsigned w = 0, most = 0, items = 0;
+                if (lane < g.n_seqs) {
+                    if (few) {
+                        mine = load_seq(c, g, lane);
+                        for (; static_cast<int>(items) * step < mine.n; ++items) {
+                            const unsigned v = item_cost(g, mine, items, step);
+                            w += v;
+                            most = max(most, v);
+                        }
+                    } else {
+                        w = cost[lane];
+                        most = cost[kMaxSeqs + lane];
+                        items = cost[kMaxSeqs + 32 + lane];
+                    }
                 }
-                unsigned total = few ? w : 0;
-                if (!few)
-                    for (int s = lane; s < g.n_seqs; s += 32) total += cost[s];
+                unsigned total = w;
+                for (int s = 32 + lane; s < g.n_seqs; s += 32) total += cost[s];
                 total = __reduce_add_sync(0xffffffffu, total) * c.kv_heads;
                 // not less than an item's fixed cost: 32 tokens over 1000 keys take 17 us, 21 in ranges of one tile; 7 over 2000 keys 12.0,
                 // 14.2. Ranges of 4 and more pay for some (300 tokens 11.5 against 15.7), but one token over 776 keys takes 14.3 against 10.6.
-                const unsigned per = max((total + gridDim.x - 1) / gridDim.x, static_cast<unsigned>(kItemCost));
+                unsigned per = max((total + gridDim.x - 1) / gridDim.x, static_cast<unsigned>(kItemCost));
+                // Where there are no more items than blocks and whole ones take little longer, a block takes an item: each then counts as
+                // much as the longest. Single tiles are bound by memory, whose share of a block grows when others are done.
+                most = __reduce_max_sync(0xffffffffu, most);
+                const unsigned all = __reduce_add_sync(0xffffffffu, items) * c.kv_heads;
+                const bool whole_items = g.n_seqs <= 32 && all <= gridDim.x && most <= per + (PAIR ? 0 : per / 4) + g.cut;
+                if (whole_items) {
+                    per = most;
+                    w = items * most;
+                    total = all * most;
+                }
                 walk.per = per;
                 walk.pos = min(per * blockIdx.x, total);
                 walk.left = min(per, total - walk.pos);
                 if (walk.left > 0) {
                     unsigned before = 0;
                     for (int s0 = 0;; s0 += 32) {
-                        if (!few) w = s0 + lane < g.n_seqs ? cost[s0 + lane] : 0;
+                        if (s0 > 0) w = s0 + lane < g.n_seqs ? cost[s0 + lane] : 0;
                         const unsigned upto = before + warp_scan(w, lane) * c.kv_heads;
                         const unsigned past = __ballot_sync(0xffffffffu, upto > walk.pos);
                         if (past || s0 + 32 >= g.n_seqs) {  // the range lies within the sequences: found in the last stretch at the latest
@@ -541,7 +572,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     walk.n_tiles = (walk.q.n + step - 1) / step;
                     walk.kv_head = (walk.pos - before) / w;
                     unsigned rem = walk.pos - before - walk.kv_head * w;
-                    for (int i0 = 0; i0 < walk.n_tiles; i0 += 32) {
+                    if (whole_items) {
+                        walk.i = rem / per;
+                        walk.x = 0;
+                        walk.left = item_cost(g, walk.q, walk.i, step);
+                    }
+                    for (int i0 = 0; i0 < walk.n_tiles && !whole_items; i0 += 32) {
                         const unsigned v = i0 + lane < walk.n_tiles ? item_cost(g, walk.q, i0 + lane, step) : 0;
                         const unsigned upto = warp_scan(v, lane);
                         const unsigned past = __ballot_sync(0xffffffffu, upto > rem);
@@ -1152,6 +1188,10 @@ dspark_status attend(const dspark_cache *cache, const dspark_attention_args *arg
     const bool pair = max_new > g.tile_tokens;
     const int step = g.tile_tokens * (pair ? 2 : 1);
     g.chunk_tiles = (max_new + step - 1) / step;
+    // Partial sums, their join and the walk between items take as long as some key tiles, the more rows the more. Every item whole |
+    // all cut into equal ranges: 32 tokens over 1000 keys 13.7 | 17.3 us, 400 tokens of 2 sequences 12.9 | 35.1, 1024 after 4000
+    // 62.9 | 67.9; 9 key tiles of one token 12.0 | 10.8, 17 of 7 tokens 17.8 | 12.1, 4 chunks of 64 tokens over 3000 keys 39.2 | 34.8.
+    g.cut = pair || max_new * group >= kTile ? 16 : 6 + 6 * max_new * group / kTile;
     g.partials = reinterpret_cast<float *>(c.scratch);
     g.arrivals = c.counters;
     g.timeout_ns = kDefaultTimeoutNs;

@@ -107,6 +107,10 @@ CASES = {
     "split_pairs": (F16, 128, 3, 1, 128, [(49, 8720)] * 3, True, 0),
     "split_pairs_one_row": (BF16, 64, 4, 1, 32, [(33, 12001)], False, 0),
     "split_window": (F16, 64, 8, 2, 16, [(60, 7000), (1, 300)], True, 3000),
+    # no more query tiles than SMs: a block to each, the last ones with nothing to do
+    "whole_items": (BF16, 64, 8, 2, 16, [(130, 130), (0, 9), (257, 300), (1, 1), (70, 0), (64, 900)], True, 0),
+    "whole_items_window": (F16, 128, 4, 4, 32, [(200, 700), (90, 90)], True, 50),
+    "whole_items_tokens": (F16, 128, 4, 2, 64, [(1, 900), (1, 1000), (1, 700), (0, 0), (1, 950)], True, 0),
 }
 
 
