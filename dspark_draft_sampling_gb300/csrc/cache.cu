@@ -766,8 +766,8 @@ extern "C" dspark_status dspark_cache_compact(const dspark_cache *cache, const i
     if (kept_stride < 0) return fail(DSPARK_ERR_INVALID, "cache_compact: kept_stride=%d is negative", kept_stride);
     if (n == 0) return DSPARK_OK;
     if (kept_stride > 0 && (!kept || !n_kept)) return fail(DSPARK_ERR_INVALID, "cache_compact: null pointer argument");
-    st = launched(launch_books(compact_books_kernel, c, static_cast<long long>(n) * (kept_stride + c.max_pages), stream, c, rows, start, kept, kept_stride, n_kept, n),
-                  "cache_compact");
+    const long long entries = static_cast<long long>(n) * (kept_stride + c.max_pages);
+    st = launched(launch_books(compact_books_kernel, c, entries, stream, c, rows, start, kept, kept_stride, n_kept, n), "cache_compact");
     if (st != DSPARK_OK) return st;
     int sms = 0;
     if ((st = static_cast<dspark_status>(current_sm_count(&sms))) != DSPARK_OK) return st;
@@ -800,8 +800,8 @@ extern "C" dspark_status dspark_cache_copy_pages(const dspark_cache *cache, cons
     if (!src || !dst) return fail(DSPARK_ERR_INVALID, "cache_copy_pages: null pointer argument");
     const size_t page_v = size_t(c.layers) * 2 * c.kv_heads * c.page_size * c.head_dim / 8;
     const size_t blocks = (page_v + 1023) / 1024;
-    return launched(launch_pdl(copy_pages_kernel, dim3(n, static_cast<unsigned>(blocks < 64 ? blocks : 64)), dim3(256), 0, stream, c, src, dst, page_v),
-                    "cache_copy_pages");
+    const dim3 grid(n, static_cast<unsigned>(blocks < 64 ? blocks : 64));
+    return launched(launch_pdl(copy_pages_kernel, grid, dim3(256), 0, stream, c, src, dst, page_v), "cache_copy_pages");
 }
 
 extern "C" dspark_status dspark_cache_status(const dspark_cache *cache, dspark_stream_t stream) {

@@ -47,8 +47,8 @@ static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "
 constexpr int kTmemCols = 512;
 constexpr size_t kSmemData = 224 * 1024;      // query tiles and the ring of key and value tiles
 constexpr size_t kSmemBytes = 227 * 1024;
-// An item's fixed cost, in key tiles. With 1, 2, 3, 4, 6: 16 blocks of 7 tokens over 300-6000 keys (pages in two copies then) 44.7, 44.8, 46.0, 46.0, 49.4 us;
-// chunks in a window of 1000 70.7, 68.8, 69.0, 68.2, 69.4; 4 chunks of 64 tokens over 3000 keys 36.8, 34.9, 32.7, 33.0, 33.5.
+// An item's fixed cost, in key tiles. With 1, 2, 3, 4, 6: 16 blocks of 7 tokens over 300-6000 keys (pages in two copies then) 44.7,
+// 44.8, 46.0, 46.0, 49.4 us; chunks in a window of 1000 70.7, 68.8, 69.0, 68.2, 69.4; 4 chunks of 64 tokens over 3000 keys 36.8, 34.9, 32.7, 33.0, 33.5.
 constexpr int kItemCost = 2;
 // Powers of two by which a row's maximum may lag. With 0, 4, 8: prompt of 8192 tokens after 8192 1176, 1023, 1019 us.
 constexpr float kRescale = 8.f;
@@ -1064,7 +1064,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
                             const float up = fmaxf(top, pm[u]);
-                            z = z * (top == -INFINITY ? 0.f : ex2((top - up) * sc)) + pl[u] * (pm[u] == -INFINITY ? 0.f : ex2((pm[u] - up) * sc));
+                            const float k = pm[u] == -INFINITY ? 0.f : ex2((pm[u] - up) * sc);
+                            z = z * (top == -INFINITY ? 0.f : ex2((top - up) * sc)) + pl[u] * k;
                             top = up;
                         }
                     }
@@ -1210,16 +1211,16 @@ dspark_status attend(const dspark_cache *cache, const dspark_attention_args *arg
         // all of the pool as groups of 8 slots of one page, layer, half and head
         const cuuint64_t dims[4] = {64, 8, static_cast<cuuint64_t>(c.head_dim / 64), groups};
         const cuuint64_t strides[3] = {2ull * c.head_dim, 128, 16ull * c.head_dim};
-        const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(c.head_dim / 64), static_cast<cuuint32_t>((c.page_size < kTile ? c.page_size : kTile) / 8)};
+        const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(c.head_dim / 64),
+                                   static_cast<cuuint32_t>((c.page_size < kTile ? c.page_size : kTile) / 8)};
         if ((st = make_tmap_nd(&tm_kv, bf16, c.pool, 4, dims, strides, box)) != DSPARK_OK) return st;
     }
     const int blocks = sms < kMaxCtas ? sms : kMaxCtas;
-    if (c.head_dim == 128) {
-        if (bf16) return pair ? launch<true, 128, true>(tm_q, tm_kv, c, g, blocks, stream) : launch<true, 128, false>(tm_q, tm_kv, c, g, blocks, stream);
-        return pair ? launch<false, 128, true>(tm_q, tm_kv, c, g, blocks, stream) : launch<false, 128, false>(tm_q, tm_kv, c, g, blocks, stream);
-    }
-    if (bf16) return pair ? launch<true, 64, true>(tm_q, tm_kv, c, g, blocks, stream) : launch<true, 64, false>(tm_q, tm_kv, c, g, blocks, stream);
-    return pair ? launch<false, 64, true>(tm_q, tm_kv, c, g, blocks, stream) : launch<false, 64, false>(tm_q, tm_kv, c, g, blocks, stream);
+    auto *run = c.head_dim == 128 ? (bf16 ? (pair ? launch<true, 128, true> : launch<true, 128, false>)
+                                          : (pair ? launch<false, 128, true> : launch<false, 128, false>))
+                                  : (bf16 ? (pair ? launch<true, 64, true> : launch<true, 64, false>)
+                                          : (pair ? launch<false, 64, true> : launch<false, 64, false>));
+    return run(tm_q, tm_kv, c, g, blocks, stream);
 }
 
 }  // namespace
