@@ -9,10 +9,12 @@
 // even and odd key tiles of one query tile, joined at the end.
 //
 // Softmax.  A thread owns a row.  The running maximum only moves (and O is only rescaled) when a tile's maximum
-// exceeds it by more than 8 powers of two: P is then at most 256, and sums stay exact enough in 32 bits, as the final
-// division takes the common factor out.  P is rounded to the inputs' type for the second product, which rounds each weight
+// exceeds it by more than 8 powers of two (fp16: 4), and sums stay exact enough in 32 bits, as the final division takes the
+// common factor out.  P is rounded to the inputs' type for the second product, which rounds each weight
 // once (unit roundoff 2^-11 or 2^-8, of the size of the output's own rounding); its sum is taken in 32 bits before
-// that rounding.
+// that rounding.  An fp16 weight below 2^-14 keeps fewer bits and one below 2^-25 none, which many keys would feel: at the maximum
+// 66,000 of 2^-25 are 0.2 % of it.  So fp16's P is 2^7 times as large, at most 2^11 with 5 powers of two to spare for
+// roundings of very large scores: what a weight loses is 2^-32 of the maximum, and a million keys' 2^-12.
 //
 // Work.  All (sequence, kv head, query tile) items, each with its own number of 128-key tiles, form one
 // sequence of tiles that the thread blocks, one to an SM, take in equal contiguous ranges, or, where cutting would cost more
@@ -50,8 +52,12 @@ constexpr size_t kSmemBytes = 227 * 1024;
 // An item's fixed cost, in key tiles. With 1, 2, 3, 4, 6: 16 blocks of 7 tokens over 300-6000 keys (pages in two copies then) 44.7,
 // 44.8, 46.0, 46.0, 49.4 us; chunks in a window of 1000 70.7, 68.8, 69.0, 68.2, 69.4; 4 chunks of 64 tokens over 3000 keys 36.8, 34.9, 32.7, 33.0, 33.5.
 constexpr int kItemCost = 2;
-// Powers of two by which a row's maximum may lag. With 0, 4, 8: prompt of 8192 tokens after 8192 1176, 1023, 1019 us.
-constexpr float kRescale = 8.f;
+// Powers of two by which a row's maximum may lag. With 0, 4, 8: prompt of 8192 tokens after 8192 1176, 1023, 1019 us (bf16).
+template <bool BF16>
+constexpr float kRescale = BF16 ? 8.f : 4.f;
+// Powers of two that P is larger by; a row's sum is, too.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;
 // Rows (rounded up to a power of two) x parts of an item from which its parts are joined in two steps. One step | two: 49 tokens over
 // 8720 keys in 35 parts 52 | 32 us, 64 tokens over 8000 keys in 19 parts 47 | 39; 32 tokens over 1000 keys in 10 parts 21.4 | 22.6.
 constexpr int kTwoSteps = 2048;
@@ -220,6 +226,13 @@ __device__ __forceinline__ float lg2(float x) {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Natural logarithm of a row's sum: sum / 2^kLift times 2^top.
+template <bool BF16>
+__device__ __forceinline__ float log_sum(float top, float sum) {
+    constexpr float back = 1.f / static_cast<float>(1 << static_cast<int>(kLift<BF16>));
+    return sum == 0.f ? -INFINITY : (top + lg2(sum * back)) * 0.6931471805599453f;
 }
 
 template <bool BF16>
@@ -827,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             top[w] = fmaxf(top[w], fmaxf(__uint_as_float(v[q + 2 * w]), __uint_as_float(v[q + 2 * w + 1])));
                     }
                     const float tile_max = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                    const bool moves = real && (tile_max - m) * sc > kRescale;  // also from -infinity
+                    const bool moves = real && (tile_max - m) * sc > kRescale<BF16>;  // also from -infinity
                     if (__any_sync(0xffffffffu, moves)) {
                         const float up = fmaxf(m, tile_max);
                         const float keep = m == -INFINITY ? 0.f : ex2((m - up) * sc);
@@ -845,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         l *= keep;
                         m = up;
                     }
-                    const float shift = m == -INFINITY ? 0.f : -m * sc;
+                    const float shift = m == -INFINITY ? 0.f : kLift<BF16> - m * sc;
                     const unsigned long long sc2 = pair_f32(sc, sc), shift2 = pair_f32(shift, shift);
                     unsigned long long sum2[2] = {0ull, 0ull};
                     // groups of 8 weights: one group's exponentials between the next one's arguments and the last one's sums,
@@ -992,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (whole) {
                 if (real && g.lse && (PAIR || s == 0))
                     g.lse[static_cast<size_t>(seg.q0 + token) * (c.kv_heads * g.group) + out_head] =
-                        l == 0.f ? -INFINITY : (m * sc + lg2(l)) * 0.6931471805599453f;
+                        log_sum<BF16>(m * sc, l);
                 if (!PAIR) {  // the other stream's O has been read before it is written again
                     mbar_arrive(&ctl->sync[0]);
                     if (!(ok = warp_wait(ctl, &ctl->sync[0], n_sync & 1, c, g.tries))) break;
@@ -1079,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __stcg(p, top);
                             __stcg(p + kTile, z);
                         } else if (g.lse) {
-                            g.lse[qt * (c.kv_heads * g.group) + hd] = z == 0.f ? -INFINITY : (top * sc + lg2(z)) * 0.6931471805599453f;
+                            g.lse[qt * (c.kv_heads * g.group) + hd] = log_sum<BF16>(top * sc, z);
                         }
                     }
                     const int c4 = my_row == row ? joiner >> shift : D / 4;
