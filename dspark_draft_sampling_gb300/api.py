@@ -938,7 +938,8 @@ class PagedCache:
 
     def status(self, *, stream=None) -> int:
         """Synchronize, then report and clear what the calls since the last check recorded on the device: 0 (OK),
-        DSPARK_ERR_INDEX, DSPARK_ERR_CAPACITY or DSPARK_ERR_TIMEOUT."""
+        DSPARK_ERR_INDEX, DSPARK_ERR_CAPACITY or DSPARK_ERR_TIMEOUT (a wait on the device gave up: outputs since the last
+        check are undefined; from here on the cache's workspace is sound again)."""
         return int(self._lib.dspark_cache_status(self._ref, _raw_stream(stream, self.device)))
 
 

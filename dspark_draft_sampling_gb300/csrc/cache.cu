@@ -813,7 +813,8 @@ extern "C" dspark_status dspark_cache_status(const dspark_cache *cache, dspark_s
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_fail(e, "cache_status");
     if (bits == 0) return DSPARK_OK;
-    e = cudaMemsetAsync(c.status, 0, 4, stream);
+    // A wait that gave up may have ended attention's blocks between their arrivals at a join: their counts start anew as well.
+    e = cudaMemsetAsync(c.status, 0, bits & kStatusTimeout ? kCacheScratchOffset : 4, stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_fail(e, "cache_status");
     if (bits & kStatusTimeout) return fail(DSPARK_ERR_TIMEOUT, "paged cache: a device-side wait gave up");

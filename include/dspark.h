@@ -558,7 +558,8 @@ void dspark_gated_draft_plan_destroy(dspark_gated_plan *plan);
  *            out of range is skipped and recorded
  * dspark_cache_status synchronizes `stream`, then reports and clears the status word: DSPARK_OK,
  * DSPARK_ERR_INDEX, DSPARK_ERR_CAPACITY, or DSPARK_ERR_TIMEOUT after a device-side wait that gave
- * up (the outputs of that call are undefined and the workspace must be zero-filled again).
+ * up (the outputs of that call, and of those on this workspace between it and this one, are
+ * undefined; the workspace has been zero-filled where it has to be and can be used again).
  * ===================================================================================== */
 typedef enum dspark_dtype { DSPARK_FP16 = 0, DSPARK_BF16 = 1, DSPARK_FP32 = 2 } dspark_dtype;
 

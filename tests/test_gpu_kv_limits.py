@@ -9,10 +9,21 @@ from dspark_draft_sampling_gb300 import api
 pytestmark = pytest.mark.gpu
 
 F16, BF16 = torch.float16, torch.bfloat16
+HEADER, COUNTERS, TIMEOUT = api.CACHE_HEADER_BYTES, 256, 2  # bytes of the workspace's header, its arrival counts, a status bit
 
 
 def ints(v):
     return torch.tensor(v, dtype=torch.int32).cuda()
+
+
+def filled_cache(lens, *, kv_heads, dim, dtype, page=16, seed=0):
+    wide = max(1, max(-(-n // page) for n in lens))
+    cache = api.PagedCache.empty(len(lens) * wide + 1, len(lens), wide, layers=1, kv_heads=kv_heads, page_size=page, head_dim=dim,
+                                 dtype=dtype)
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    cache.pool.copy_(torch.randn(cache.pool.shape, generator=gen, device="cuda"))
+    cache.extend(ints(range(len(lens))), ints(lens))
+    return cache
 
 
 # ---- many keys, each far below the largest -------------------------------------------------
@@ -46,3 +57,20 @@ def test_weights_far_below_the_largest_add_up(dtype, n):
     assert ((out.cpu().double() - want).abs() <= tol).all(), (float(out.max()), float(want.max()))
     assert ((lse.cpu().double() - (top + math.log(2.0 + mass))).abs() <= 2 * 2.0**-20 * (1 + top)).all()
 
+
+# ---- what a wait that gave up leaves behind -----------------------------------------------
+@pytest.mark.parametrize("n", [1, 40])
+def test_status_after_a_wait_that_gave_up_makes_the_workspace_whole(n):
+    # such a call can end between the arrivals of a cut item's blocks; here they are written as it may leave them
+    cache = filled_cache([9000], kv_heads=1, dim=128, dtype=BF16, page=64)
+    q = torch.randn((n, 4, 128), generator=torch.Generator().manual_seed(1)).to(BF16).cuda()
+    cu = ints([0, n])
+    want = api.paged_attention(q, cache, 0, cu)
+    assert cache.status() == 0
+    cache.workspace[COUNTERS:HEADER].fill_(1)
+    cache.workspace[0] = TIMEOUT
+    assert cache.status() == api.DSPARK_ERR_TIMEOUT
+    cache.workspace[HEADER:].fill_(255)  # partial sums of earlier calls are no answer
+    for _ in range(2):
+        assert torch.equal(api.paged_attention(q, cache, 0, cu), want)
+    assert cache.status() == 0 and not cache.workspace[:HEADER].any()
