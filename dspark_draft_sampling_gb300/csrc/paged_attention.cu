@@ -1192,7 +1192,7 @@ dspark_status attend(const dspark_cache *cache, const dspark_attention_args *arg
     g.n_seqs = n_seqs;
     g.layer = layer;
     g.causal = causal != 0;
-    g.window = window;
+    g.window = window < 1 << 30 ? window : 0;  // no row is longer: hides nothing, and differences of positions stay within 32 bits
     g.scale = scale;
     g.tile_tokens = kTile / group;
     // Two query tiles share each key tile where chunks have two; a chunk of one tile splits its keys over the streams. Query tiles

@@ -74,3 +74,17 @@ def test_status_after_a_wait_that_gave_up_makes_the_workspace_whole(n):
     for _ in range(2):
         assert torch.equal(api.paged_attention(q, cache, 0, cu), want)
     assert cache.status() == 0 and not cache.workspace[:HEADER].any()
+
+
+# ---- windows without an end ----------------------------------------------------------------
+@pytest.mark.parametrize("window", [2**30, 2**31 - 1])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_window_longer_than_any_row_hides_nothing(causal, window):
+    # also where a chunk is longer than its row, so that positions are negative
+    cache = filled_cache([40, 300, 3], kv_heads=1, dim=64, dtype=F16)
+    q = torch.randn((340, 2, 64), generator=torch.Generator().manual_seed(3)).half().cuda()
+    cu = ints([0, 50, 150, 340])
+    want, want_lse = api.paged_attention(q, cache, 0, cu, causal=causal, return_lse=True)
+    got, lse = api.paged_attention(q, cache, 0, cu, causal=causal, window=window, return_lse=True)
+    assert cache.status() == 0
+    assert torch.equal(got, want) and torch.equal(lse, want_lse)
