@@ -1162,8 +1162,9 @@ dspark_status attend(const dspark_cache *cache, const dspark_attention_args *arg
     if (n_seqs > kMaxSeqs) return fail(DSPARK_ERR_UNSUPPORTED, "%s: n_seqs %d > %d", who, n_seqs, kMaxSeqs);
     if (tokens == 0 || n_seqs == 0) return DSPARK_OK;
     if (!q || !out || !cu_new) return fail(DSPARK_ERR_INVALID, "%s: null pointer argument", who);
-    if (tokens == 1) q_token_stride = static_cast<long long>(q_heads) * c.head_dim;  // never used: any value will do
-    if (q_heads == 1) q_head_stride = c.head_dim;
+    // strides of axes of one entry are never used: any value will do
+    if (tokens == 1) q_token_stride = out_token_stride = static_cast<long long>(q_heads) * c.head_dim;
+    if (q_heads == 1) q_head_stride = out_head_stride = c.head_dim;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(cu_new, 4) || !aligned(lse, 4) || q_token_stride % 8 ||
         q_head_stride % 8 || out_token_stride % 8 || out_head_stride % 8 || q_token_stride <= 0 || q_head_stride <= 0 ||
         out_token_stride < 0 || out_head_stride < 0)

@@ -309,11 +309,14 @@ dspark_status check_turns(const char *who, const int64_t *turns, int rotary_dim,
     return DSPARK_OK;
 }
 
-dspark_status check_strided(const char *who, const char *name, const void *p, long long token, long long head, int bytes) {
-    if (!p) return fail(DSPARK_ERR_INVALID, "%s: null pointer argument (%s)", who, name);
-    if (!aligned(p, 16) || token * bytes % 16 || head * bytes % 16 || token < 0 || head < 0)
+// Also drops the strides of axes of one entry: nothing moves along them, and tensors come with any value there.
+dspark_status check_strided(const char *who, const char *name, Strided *s, int tokens, int heads, int bytes) {
+    if (!s->p) return fail(DSPARK_ERR_INVALID, "%s: null pointer argument (%s)", who, name);
+    if (tokens == 1) s->token = 0;
+    if (heads == 1) s->head = 0;
+    if (!aligned(s->p, 16) || s->token * bytes % 16 || s->head * bytes % 16 || s->token < 0 || s->head < 0)
         return fail(DSPARK_ERR_INVALID, "%s: %s must be 16-byte aligned, with strides of whole 16 bytes (%lld, %lld)", who, name,
-                    token, head);
+                    s->token, s->head);
     return DSPARK_OK;
 }
 
@@ -336,8 +339,9 @@ extern "C" dspark_status dspark_rotary(const dspark_rotary_args *args, dspark_st
     dspark_status st = check_turns("rotary", turns, rotary_dim, layout, head_dim);
     if (st != DSPARK_OK || tokens == 0 || heads == 0) return st;
     const int bytes = element_bytes(dtype);
-    if ((st = check_strided("rotary", "x", x, x_token_stride, x_head_stride, bytes)) != DSPARK_OK) return st;
-    if ((st = check_strided("rotary", "y", y, y_token_stride, y_head_stride, bytes)) != DSPARK_OK) return st;
+    Strided sx{x, x_token_stride, x_head_stride}, sy{y, y_token_stride, y_head_stride};
+    if ((st = check_strided("rotary", "x", &sx, tokens, heads, bytes)) != DSPARK_OK) return st;
+    if ((st = check_strided("rotary", "y", &sy, tokens, heads, bytes)) != DSPARK_OK) return st;
     if (!positions || !aligned(positions, 4)) return fail(DSPARK_ERR_INVALID, "rotary: positions must be a 4-byte aligned array");
     int sms = 0;
     if ((st = static_cast<dspark_status>(current_sm_count(&sms))) != DSPARK_OK) return st;
@@ -345,7 +349,6 @@ extern "C" dspark_status dspark_rotary(const dspark_rotary_args *args, dspark_st
     int lanes, bx, by;
     shape(tokens, heads, units, sms, &lanes, &bx, &by);
     const Turns t{reinterpret_cast<const long long *>(turns), rotary_dim, layout, amplitude, backward != 0};
-    const Strided sx{x, x_token_stride, x_head_stride}, sy{y, y_token_stride, y_head_stride};
     const dim3 grid(bx, by);
     auto *kernel = dtype == DSPARK_FP32 ? rotary_kernel<float> : dtype == DSPARK_BF16 ? rotary_kernel<__nv_bfloat16> : rotary_kernel<__half>;
     const cudaError_t e = launch_pdl(kernel, grid, dim3(kThreads), 0, stream, sx, sy, tokens, heads, units, lanes, positions, t);
@@ -366,12 +369,17 @@ extern "C" dspark_status dspark_rotary_append(const dspark_cache *cache, const d
         return fail(DSPARK_ERR_INVALID, "%s: bad sizes tokens=%d q_heads=%d n_seqs=%d", who, tokens, q_heads, n_seqs);
     if (n_seqs > kMaxSeqs) return fail(DSPARK_ERR_UNSUPPORTED, "%s: n_seqs %d > %d", who, n_seqs, kMaxSeqs);
     if ((st = check_turns(who, turns, rotary_dim, layout, c.head_dim)) != DSPARK_OK || tokens == 0 || n_seqs == 0) return st;
+    Append g;
+    g.q = Strided{q, q_token_stride, q_head_stride};
+    g.k = Strided{k, k_token_stride, k_head_stride};
+    g.v = Strided{v, v_token_stride, v_head_stride};
+    g.out = Strided{q_out, out_token_stride, out_head_stride};
     if (q_heads > 0) {
-        if ((st = check_strided(who, "q", q, q_token_stride, q_head_stride, 2)) != DSPARK_OK) return st;
-        if ((st = check_strided(who, "q_out", q_out, out_token_stride, out_head_stride, 2)) != DSPARK_OK) return st;
+        if ((st = check_strided(who, "q", &g.q, tokens, q_heads, 2)) != DSPARK_OK) return st;
+        if ((st = check_strided(who, "q_out", &g.out, tokens, q_heads, 2)) != DSPARK_OK) return st;
     }
-    if ((st = check_strided(who, "k", k, k_token_stride, k_head_stride, 2)) != DSPARK_OK) return st;
-    if ((st = check_strided(who, "v", v, v_token_stride, v_head_stride, 2)) != DSPARK_OK) return st;
+    if ((st = check_strided(who, "k", &g.k, tokens, c.kv_heads, 2)) != DSPARK_OK) return st;
+    if ((st = check_strided(who, "v", &g.v, tokens, c.kv_heads, 2)) != DSPARK_OK) return st;
     if (!cu_new || !aligned(cu_new, 4)) return fail(DSPARK_ERR_INVALID, "%s: cu_new must be a 4-byte aligned array", who);
     int sms = 0;
     if ((st = static_cast<dspark_status>(current_sm_count(&sms))) != DSPARK_OK) return st;
@@ -379,11 +387,6 @@ extern "C" dspark_status dspark_rotary_append(const dspark_cache *cache, const d
     int lanes, bx, by;
     shape(tokens, q_heads + 2 * c.kv_heads, units, sms, &lanes, &bx, &by);
     const Turns t{reinterpret_cast<const long long *>(turns), rotary_dim, layout, amplitude, 0};
-    Append g;
-    g.q = Strided{q, q_token_stride, q_head_stride};
-    g.k = Strided{k, k_token_stride, k_head_stride};
-    g.v = Strided{v, v_token_stride, v_head_stride};
-    g.out = Strided{q_out, out_token_stride, out_head_stride};
     g.rows = rows;
     g.cu_new = cu_new;
     g.positions = positions;

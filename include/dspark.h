@@ -618,8 +618,8 @@ dspark_status dspark_cache_status(const dspark_cache *cache, dspark_stream_t str
  *   shorter than the chunk, no page) is rotated but not written, and DSPARK_ERR_INDEX is recorded.
  *   Tokens outside cu_new[0] .. cu_new[n_seqs] are not touched.
  * Supported: rotary_dim a multiple of 16, 16 <= rotary_dim <= head_dim; head_dim a multiple of 16
- *   (fp32: 16) up to 512; pointers and strides multiples of 16 bytes.  tokens == 0 or heads == 0
- *   enqueues nothing.
+ *   (fp32: 16) up to 512; pointers and strides multiples of 16 bytes (the stride of an axis of one
+ *   entry may be anything).  tokens == 0 or heads == 0 enqueues nothing.
  * ===================================================================================== */
 #define DSPARK_ROTARY_HALF 0
 #define DSPARK_ROTARY_INTERLEAVED 1
@@ -665,7 +665,8 @@ dspark_status dspark_rotary_append(const dspark_cache *cache, const dspark_appen
  *
  * Arguments
  *   q, out   [tokens, q_heads, head_dim] in the cache's type; strides in elements, multiples of 8
- *            (the last axis contiguous), 16-byte aligned.  out must not overlap q
+ *            (the last axis contiguous; the stride of an axis of one entry may be anything), 16-byte
+ *            aligned.  out must not overlap q
  *   lse      float [tokens, q_heads] or NULL
  *   scale    positive
  *   max_new  the longest chunk, as far as the caller knows (a hint for the tile shape; wrong values

@@ -88,3 +88,26 @@ def test_a_window_longer_than_any_row_hides_nothing(causal, window):
     got, lse = api.paged_attention(q, cache, 0, cu, causal=causal, window=window, return_lse=True)
     assert cache.status() == 0
     assert torch.equal(got, want) and torch.equal(lse, want_lse)
+
+
+# ---- axes of one entry ---------------------------------------------------------------------
+def test_strides_of_axes_of_one_entry_do_not_matter():
+    # one token, or one head, whose stride is whatever the tensor was made by: it is never used
+    gen = torch.Generator().manual_seed(2)
+    turns = api.RotaryTable(api.rotary_frequencies(64))
+    token = torch.randn((4, 64, 1), generator=gen).half().cuda().permute(2, 0, 1)  # [1, 4, 64], strides (1, 64, 1)
+    head = torch.randn((3, 64, 1), generator=gen).half().cuda().permute(0, 2, 1)   # [3, 1, 64], strides (64, 1, 1)
+    for x in (token, head):
+        pos = ints(range(7, 7 + x.shape[0]))
+        assert torch.equal(api.rotary(x, pos, turns), api.rotary(x.clone(memory_format=torch.contiguous_format), pos, turns))
+    for q, kv in ((token, token[:, :1]), (token, token[:, :2]), (head, head)):
+        n, got = q.shape[0], []
+        for dense in (False, True):
+            cache = filled_cache([20 + n], kv_heads=kv.shape[1], dim=64, dtype=F16)
+            a, b = (x.clone(memory_format=torch.contiguous_format) if dense else x for x in (q, kv))
+            turned = api.rotary_append(a, b, b, cache, 0, ints([0, n]), turns)
+            got.append((turned, cache.pool, api.paged_attention(a, cache, 0, ints([0, n])),
+                        api.paged_attention(a, cache, 0, ints([0, n]), out=torch.empty_like(a))))
+            assert cache.status() == 0
+        for x, y in zip(*got):
+            assert torch.equal(x, y)
