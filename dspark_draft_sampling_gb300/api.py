@@ -805,9 +805,18 @@ def ws_matvec_grouped_host(problems, scratch, *, inputs_copied=None, stream=None
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
-def _raw_stream(stream, device):
-    """The stream's handle; None: the current stream of the tensors' device."""
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+def _launch(call, device: int, stream, *args) -> int:
+    """Status of call(*args, stream) on the GPU that holds the tensors, whichever is current; stream None: that GPU's current one."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    elif stream.device_index != device:
+        raise ValueError(f"the stream is on GPU {stream.device_index}, the tensors on GPU {device}")
+    else:
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == device:
+        return call(*args, raw)
+    with torch.cuda.device(device):
+        return call(*args, raw)
 
 
 def _empty_like(t, stream):
@@ -818,10 +827,10 @@ def _empty_like(t, stream):
         return torch.empty_like(t)
 
 
-def _ints(t, name: str, n=None, *, dtype=torch.int32):
-    """Address of a contiguous CUDA tensor of whole numbers (of n entries)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}")
+def _ints(t, name: str, device: int, n=None, *, dtype=torch.int32):
+    """Address of a contiguous tensor of numbers (of n entries) on the GPU `device`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {dtype} on GPU {device}")
     if n is not None and t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} entries, expected {n}")
     return t.data_ptr()
@@ -833,10 +842,10 @@ _APPEND_ARGS = struct.Struct("@8P8q6if4x")
 _ATTENTION_ARGS = struct.Struct("@5P4q7if")
 
 
-def _heads(t, name: str, dtype, shape=None):
-    """Token and head strides of a CUDA tensor [tokens, heads, head_dim] with a contiguous last axis."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or t.dim() != 3:
-        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, head_dim] of {dtype}")
+def _heads(t, name: str, device: int, dtype, shape=None):
+    """Token and head strides of a tensor [tokens, heads, head_dim] with a contiguous last axis on the GPU `device`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not dtype or t.dim() != 3:
+        raise ValueError(f"{name} must be a tensor [tokens, heads, head_dim] of {dtype} on GPU {device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     a, b, c = t.stride()
@@ -873,9 +882,10 @@ class PagedCache:
         c = CacheStruct(dtype=_DTYPES[pool.dtype], num_pages=pages, layers=layers, kv_heads=kv_heads, page_size=page_size,
                         head_dim=head_dim, max_seqs=table.shape[0], max_pages=table.shape[1])
         c.pool = _ptr(pool, "pool")
-        c.table = _ints(table, "table")
-        c.length = _ints(length, "length", table.shape[0])
-        c.refs = _ints(refs, "refs", pages)
+        device = pool.get_device()
+        c.table = _ints(table, "table", device)
+        c.length = _ints(length, "length", device, table.shape[0])
+        c.refs = _ints(refs, "refs", device, pages)
         if workspace is None:
             n = int(lib.dspark_cache_workspace_bytes(ctypes.byref(c)))
             if n == 0:
@@ -884,10 +894,12 @@ class PagedCache:
             workspace = torch.empty(n, dtype=torch.uint8, device=pool.device)
             workspace[:CACHE_HEADER_BYTES].zero_()
         c.workspace = _ptr(workspace, "workspace")
+        if workspace.get_device() != device:
+            raise ValueError(f"workspace must be on GPU {device}")
         c.workspace_bytes = workspace.numel() * workspace.element_size()
         self.pool, self.table, self.length, self.refs, self.workspace = pool, table, length, refs, workspace
         self.kv_heads, self.page_size, self.head_dim, self.layers = kv_heads, page_size, head_dim, layers
-        self.dtype, self.device = pool.dtype, pool.device
+        self.dtype, self.device, self._index = pool.dtype, pool.device, device
         self._struct, self._ref = c, ctypes.byref(c)
 
     @classmethod
@@ -902,45 +914,43 @@ class PagedCache:
 
     def extend(self, rows, counts, *, stream=None):
         """Row rows[i] becomes counts[i] tokens longer; pages are added where needed."""
-        n = rows.numel()
-        _check(self._lib, self._lib.dspark_cache_extend(self._ref, _ints(rows, "rows"), _ints(counts, "counts", n), n,
-                                                        _raw_stream(stream, self.device)))
+        n, d = rows.numel(), self._index
+        _check(self._lib, _launch(self._lib.dspark_cache_extend, d, stream, self._ref, _ints(rows, "rows", d),
+                                  _ints(counts, "counts", d, n), n))
 
     def fork(self, src, dst, *, stream=None):
         """Row dst[i] becomes a copy of what row src[i] was: full pages are shared, a last page that is not full is
         copied.  Rows can be permuted (beam search)."""
-        n = src.numel()
-        _check(self._lib, self._lib.dspark_cache_fork(self._ref, _ints(src, "src"), _ints(dst, "dst", n), n,
-                                                      _raw_stream(stream, self.device)))
+        n, d = src.numel(), self._index
+        _check(self._lib, _launch(self._lib.dspark_cache_fork, d, stream, self._ref, _ints(src, "src", d), _ints(dst, "dst", d, n), n))
 
     def compact(self, rows, start, kept=None, n_kept=None, *, stream=None):
         """Row rows[i] keeps its first start[i] tokens and the n_kept[i] ones at kept[i, :] (int32 [n, at least
         max n_kept], ascending positions from start[i] on).  Without kept the rows are cut off at start."""
-        n = rows.numel()
+        n, d = rows.numel(), self._index
         stride, kept_p, n_kept_p = 0, None, None
         if kept is not None:
             if kept.dim() != 2 or kept.shape[0] != n:
                 raise ValueError("kept must be int32 [rows, tokens]")
-            stride, kept_p, n_kept_p = kept.shape[1], _ints(kept, "kept"), _ints(n_kept, "n_kept", n)
-        _check(self._lib, self._lib.dspark_cache_compact(self._ref, _ints(rows, "rows"), _ints(start, "start", n), kept_p,
-                                                         stride, n_kept_p, n, _raw_stream(stream, self.device)))
+            stride, kept_p, n_kept_p = kept.shape[1], _ints(kept, "kept", d), _ints(n_kept, "n_kept", d, n)
+        _check(self._lib, _launch(self._lib.dspark_cache_compact, d, stream, self._ref, _ints(rows, "rows", d),
+                                  _ints(start, "start", d, n), kept_p, stride, n_kept_p, n))
 
     def free(self, rows, *, stream=None):
         """The rows release their pages and become empty."""
-        _check(self._lib, self._lib.dspark_cache_free(self._ref, _ints(rows, "rows"), rows.numel(),
-                                                      _raw_stream(stream, self.device)))
+        d = self._index
+        _check(self._lib, _launch(self._lib.dspark_cache_free, d, stream, self._ref, _ints(rows, "rows", d), rows.numel()))
 
     def copy_pages(self, src, dst, *, stream=None):
         """Page dst[i] becomes a copy of page src[i], all layers; table and refs are left alone."""
-        n = src.numel()
-        _check(self._lib, self._lib.dspark_cache_copy_pages(self._ref, _ints(src, "src"), _ints(dst, "dst", n), n,
-                                                            _raw_stream(stream, self.device)))
+        n, d = src.numel(), self._index
+        _check(self._lib, _launch(self._lib.dspark_cache_copy_pages, d, stream, self._ref, _ints(src, "src", d), _ints(dst, "dst", d, n), n))
 
     def status(self, *, stream=None) -> int:
         """Synchronize, then report and clear what the calls since the last check recorded on the device: 0 (OK),
         DSPARK_ERR_INDEX, DSPARK_ERR_CAPACITY or DSPARK_ERR_TIMEOUT (a wait on the device gave up: outputs since the last
         check are undefined; from here on the cache's workspace is sound again)."""
-        return int(self._lib.dspark_cache_status(self._ref, _raw_stream(stream, self.device)))
+        return int(_launch(self._lib.dspark_cache_status, self._index, stream, self._ref))
 
 
 def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
@@ -986,10 +996,19 @@ class RotaryTable:
             raise ValueError(f"layout must be one of {sorted(ROTARY_LAYOUTS)}")
         if not isinstance(turns, torch.Tensor):
             turns = torch.tensor(turns, dtype=torch.int64, device=device or "cuda")
-        self._turns = _ints(turns, "turns", dtype=torch.int64)
+        self._index = turns.get_device()
+        if self._index < 0:
+            raise ValueError("turns must be a CUDA tensor")
+        self._turns = _ints(turns, "turns", self._index, dtype=torch.int64)
         self.turns, self.layout, self.amplitude = turns, layout, float(amplitude)
         self.rotary_dim = 2 * turns.numel()
         self._args = (self._turns, self.rotary_dim, ROTARY_LAYOUTS[layout], self.amplitude)
+
+    def _on(self, device: int):
+        """What the calls pass on, for tensors on the GPU `device`."""
+        if self._index != device:
+            raise ValueError(f"the rotary table is on GPU {self._index}, the tensors on GPU {device}")
+        return self._args
 
 
 def rotary(x, positions, table: RotaryTable, *, backward: bool = False, out=None, stream=None):
@@ -998,19 +1017,22 @@ def rotary(x, positions, table: RotaryTable, *, backward: bool = False, out=None
     lib = load_library()
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
         raise ValueError("x must be an fp16, bf16 or fp32 tensor")
-    a, b = _heads(x, "x", x.dtype)
+    d = x.get_device()
+    if d < 0:
+        raise ValueError("x must be a CUDA tensor")
+    a, b = _heads(x, "x", d, x.dtype)
     shape = x.shape
     if out is None:
         out = _empty_like(x, stream)
         ao, bo, _ = out.stride()
     else:
-        ao, bo = _heads(out, "out", x.dtype, shape)
+        ao, bo = _heads(out, "out", d, x.dtype, shape)
     tokens, heads, dim = shape
-    turns, rotary_dim, layout, amplitude = table._args
-    status = lib.dspark_rotary(
-        _ROTARY_ARGS.pack(x.data_ptr(), out.data_ptr(), _ints(positions, "positions", tokens), turns, a, b, ao, bo,
-                          _DTYPES[x.dtype], tokens, heads, dim, rotary_dim, layout, 1 if backward else 0, amplitude),
-        _raw_stream(stream, x.device))
+    turns, rotary_dim, layout, amplitude = table._on(d)
+    status = _launch(
+        lib.dspark_rotary, d, stream,
+        _ROTARY_ARGS.pack(x.data_ptr(), out.data_ptr(), _ints(positions, "positions", d, tokens), turns, a, b, ao, bo,
+                          _DTYPES[x.dtype], tokens, heads, dim, rotary_dim, layout, 1 if backward else 0, amplitude))
     if status:
         _check(lib, status)
     return out
@@ -1024,29 +1046,28 @@ def rotary_append(q, k, v, cache: PagedCache, layer: int, cu_new, table: RotaryT
     the cache (None: the same number); positions int32 [tokens]: where the angle's position is not the place in the
     cache.  out may be q."""
     lib = cache._lib
-    dtype = cache.dtype
-    qa, qb = _heads(q, "q", dtype)
+    dtype, d = cache.dtype, cache._index
+    qa, qb = _heads(q, "q", d, dtype)
     shape = q.shape
     tokens, q_heads, dim = shape
     if dim != cache.head_dim:
         raise ValueError(f"q has head_dim {dim}, the cache {cache.head_dim}")
     kv_shape = (tokens, cache.kv_heads, dim)
-    ka, kb = _heads(k, "k", dtype, kv_shape)
-    va, vb = _heads(v, "v", dtype, kv_shape)
+    ka, kb = _heads(k, "k", d, dtype, kv_shape)
+    va, vb = _heads(v, "v", d, dtype, kv_shape)
     if out is None:
         out = _empty_like(q, stream)
         oa, ob, _ = out.stride()
     else:
-        oa, ob = _heads(out, "out", dtype, shape)
+        oa, ob = _heads(out, "out", d, dtype, shape)
     seqs = cu_new.numel() - 1
-    turns, rotary_dim, layout, amplitude = table._args
-    status = lib.dspark_rotary_append(
-        cache._ref,
+    turns, rotary_dim, layout, amplitude = table._on(d)
+    status = _launch(
+        lib.dspark_rotary_append, d, stream, cache._ref,
         _APPEND_ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                          0 if rows is None else _ints(rows, "rows", seqs), _ints(cu_new, "cu_new"),
-                          0 if positions is None else _ints(positions, "positions", tokens), turns, qa, qb, ka, kb, va, vb,
-                          oa, ob, layer, tokens, q_heads, seqs, rotary_dim, layout, amplitude),
-        _raw_stream(stream, cache.device))
+                          0 if rows is None else _ints(rows, "rows", d, seqs), _ints(cu_new, "cu_new", d),
+                          0 if positions is None else _ints(positions, "positions", d, tokens), turns, qa, qb, ka, kb, va, vb,
+                          oa, ob, layer, tokens, q_heads, seqs, rotary_dim, layout, amplitude))
     if status:
         _check(lib, status)
     return out
@@ -1059,8 +1080,8 @@ def paged_attention(q, cache: PagedCache, layer: int, cu_new, *, rows=None, max_
     causal=False lets a chunk's tokens see each other; window > 0: only the last window keys; scale: of the scores
     (None: 1 / sqrt(head_dim)).  Returns out, or (out, lse fp32 [tokens, q_heads]) with return_lse."""
     lib = cache._lib
-    dtype = cache.dtype
-    qa, qb = _heads(q, "q", dtype)
+    dtype, d = cache.dtype, cache._index
+    qa, qb = _heads(q, "q", d, dtype)
     shape = q.shape
     tokens, q_heads, dim = shape
     if dim != cache.head_dim:
@@ -1069,7 +1090,7 @@ def paged_attention(q, cache: PagedCache, layer: int, cu_new, *, rows=None, max_
         out = _empty_like(q, stream)
         oa, ob, _ = out.stride()
     else:
-        oa, ob = _heads(out, "out", dtype, shape)
+        oa, ob = _heads(out, "out", d, dtype, shape)
     if lse is None and return_lse:
         if stream is None:
             lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=cache.device)
@@ -1077,14 +1098,13 @@ def paged_attention(q, cache: PagedCache, layer: int, cu_new, *, rows=None, max_
             with torch.cuda.stream(stream):
                 lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=cache.device)
     seqs = cu_new.numel() - 1
-    status = lib.dspark_paged_attention(
-        cache._ref,
+    status = _launch(
+        lib.dspark_paged_attention, d, stream, cache._ref,
         _ATTENTION_ARGS.pack(q.data_ptr(), out.data_ptr(),
-                             0 if lse is None else _ints(lse, "lse", tokens * q_heads, dtype=torch.float32),
-                             0 if rows is None else _ints(rows, "rows", seqs), _ints(cu_new, "cu_new"), qa, qb, oa, ob, layer,
+                             0 if lse is None else _ints(lse, "lse", d, tokens * q_heads, dtype=torch.float32),
+                             0 if rows is None else _ints(rows, "rows", d, seqs), _ints(cu_new, "cu_new", d), qa, qb, oa, ob, layer,
                              tokens, q_heads, seqs, tokens if max_new is None else max_new, 1 if causal else 0, window,
-                             dim ** -0.5 if scale is None else scale),
-        _raw_stream(stream, cache.device))
+                             dim ** -0.5 if scale is None else scale))
     if status:
         _check(lib, status)
     return (out, lse) if return_lse else out
