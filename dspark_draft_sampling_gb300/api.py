@@ -1013,7 +1013,8 @@ class RotaryTable:
 
 def rotary(x, positions, table: RotaryTable, *, backward: bool = False, out=None, stream=None):
     """x [tokens, heads, head_dim] (fp16, bf16 or fp32; strided tokens and heads) turned to positions int32 [tokens].
-    backward: the gradient with respect to x from that of the result.  out may be x."""
+    backward: the gradient with respect to x from that of the result.  out may be x.  Autograd does not see the call, so a tensor that
+    requires a gradient is refused outside torch.no_grad(): an autograd.Function calls this in its forward and backward."""
     lib = load_library()
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
         raise ValueError("x must be an fp16, bf16 or fp32 tensor")
@@ -1027,6 +1028,8 @@ def rotary(x, positions, table: RotaryTable, *, backward: bool = False, out=None
         ao, bo, _ = out.stride()
     else:
         ao, bo = _heads(out, "out", d, x.dtype, shape)
+    if (x.requires_grad or out.requires_grad) and torch.is_grad_enabled():
+        raise ValueError("rotary has no autograd history: call it under torch.no_grad(), and for the gradient with backward=True")
     tokens, heads, dim = shape
     turns, rotary_dim, layout, amplitude = table._on(d)
     status = _launch(
