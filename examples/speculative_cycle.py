@@ -14,7 +14,7 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from dspark_draft_sampling_gb300 import api  # noqa: E402
 
-HIDDEN, Q_HEADS, KV_HEADS, DIM, VOCAB, RANK, BLOCK = 1024, 8, 2, 64, 4096, 64, 7
+HIDDEN, Q_HEADS, KV_HEADS, DIM, VOCAB, RANK, BLOCK, PAGE = 1024, 8, 2, 64, 4096, 64, 7, 16
 
 
 class Layer:
@@ -58,10 +58,13 @@ def main(argv=None):
     gen = torch.Generator().manual_seed(0)
     layer = Layer(gen)
     w1, w2 = ((torch.randn(VOCAB, RANK, generator=gen) * 0.2).to(torch.bfloat16).cuda() for _ in range(2))
-    cache = api.PagedCache.empty(64 * n, 2 * n, 32, layers=1, kv_heads=KV_HEADS, page_size=16, head_dim=DIM, dtype=torch.float16)
+    # a row holds its prompt and a block each cycle; a request has its row's pages, its draft row two or three of its own
+    lens = [20 + 13 * i for i in range(n)]
+    pages = [-(-(length + BLOCK * (a.cycles + 1)) // PAGE) for length in lens]
+    cache = api.PagedCache.empty(sum(pages) + 3 * n, 2 * n, max(pages), layers=1, kv_heads=KV_HEADS, page_size=PAGE, head_dim=DIM,
+                                 dtype=torch.float16)
 
     # the prompts of all requests in one ragged chunk
-    lens = [20 + 13 * i for i in range(n)]
     rows, cu = ints(range(n)), ints([sum(lens[:i]) for i in range(n + 1)])
     cache.extend(rows, ints(lens))
     prompt = torch.randint(VOCAB, (sum(lens),), generator=gen).cuda()
