@@ -49,18 +49,15 @@ def ints(v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
 
 
-def main(argv=None):
-    ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
-    ap.add_argument("--cycles", type=int, default=3)
-    ap.add_argument("--requests", type=int, default=4)
-    a = ap.parse_args(argv)
-    n = a.requests
+def run(n, cycles):
+    """`cycles` cycles of n requests: the cache, the layer, the requests' prompts, and each cycle's verified tokens with how many of them
+    were kept."""
     gen = torch.Generator().manual_seed(0)
     layer = Layer(gen)
     w1, w2 = ((torch.randn(VOCAB, RANK, generator=gen) * 0.2).to(torch.bfloat16).cuda() for _ in range(2))
     # a row holds its prompt and a block each cycle; a request has its row's pages, its draft row two or three of its own
     lens = [20 + 13 * i for i in range(n)]
-    pages = [-(-(length + BLOCK * (a.cycles + 1)) // PAGE) for length in lens]
+    pages = [-(-(length + BLOCK * (cycles + 1)) // PAGE) for length in lens]
     cache = api.PagedCache.empty(sum(pages) + 3 * n, 2 * n, max(pages), layers=1, kv_heads=KV_HEADS, page_size=PAGE, head_dim=DIM,
                                  dtype=torch.float16)
 
@@ -74,7 +71,7 @@ def main(argv=None):
     # a second row for each request: it shares the prompt's pages and takes the draft block, which sees itself whole
     drafts = ints(range(n, 2 * n))
     accepted = []
-    for _ in range(a.cycles):
+    for _ in range(cycles):
         cache.fork(rows, drafts)
         block_cu = ints(range(0, BLOCK * n + 1, BLOCK))
         cache.extend(drafts, ints([BLOCK] * n))
@@ -91,12 +88,21 @@ def main(argv=None):
         keep = (agree + 1).clamp(max=BLOCK)
         last = verdict.gather(1, (keep - 1).long()[:, None])[:, 0]
         cache.compact(rows, (cache.length[:n] - BLOCK + keep).int())
-        accepted.append(keep)
+        accepted.append((chunk, keep))
     cache.free(drafts)
     if cache.status():
         raise SystemExit("the cache refused a call")
-    print("tokens kept a cycle:", torch.stack(accepted, 1).tolist())
-    print("cache lengths:", cache.length[:n].tolist(), "pages in use:", int((cache.refs > 0).sum()))
+    return cache, layer, prompt.split(lens), accepted
+
+
+def main(argv=None):
+    ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
+    ap.add_argument("--cycles", type=int, default=3)
+    ap.add_argument("--requests", type=int, default=4)
+    a = ap.parse_args(argv)
+    cache, _, _, accepted = run(a.requests, a.cycles)
+    print("tokens kept a cycle:", torch.stack([keep for _, keep in accepted], 1).tolist())
+    print("cache lengths:", cache.length[:a.requests].tolist(), "pages in use:", int((cache.refs > 0).sum()))
     return cache
 
 
