@@ -869,7 +869,11 @@ class PagedCache:
 
     pool fp16 or bf16 [num_pages, layers, 2, kv_heads, page_size, head_dim], table int32 [max_seqs, max_pages] (-1: no
     page), length int32 [max_seqs], refs int32 [num_pages].  ``PagedCache.empty`` makes them.  The page operations
-    change table, length and refs on the device, in stream order; ``status`` says whether one of them was refused."""
+    change table, length and refs on the device, in stream order; ``status`` says whether one of them was refused.
+
+    The page operations and ``paged_attention`` also use the cache's one workspace: such calls must not overlap, on whichever
+    streams they are. For attention on several streams at a time, a PagedCache over the same tensors for each (every one makes its own
+    workspace and reports its own status); page operations then have to be ordered against all of them."""
 
     def __init__(self, pool, table, length, refs, *, workspace=None):
         self._lib = lib = load_library()
@@ -1047,7 +1051,7 @@ def rotary_append(q, k, v, cache: PagedCache, layer: int, cu_new, table: RotaryT
     ``cache.extend`` has made room for); returns the queries, turned.  q [tokens, q_heads, head_dim], k, v [tokens,
     kv_heads, head_dim]; cu_new int32 [sequences + 1]: first token of each sequence; rows int32 [sequences]: its row of
     the cache (None: the same number); positions int32 [tokens]: where the angle's position is not the place in the
-    cache.  out may be q."""
+    cache.  out may be q.  Autograd does not see the call."""
     lib = cache._lib
     dtype, d = cache.dtype, cache._index
     qa, qb = _heads(q, "q", d, dtype)
@@ -1079,9 +1083,10 @@ def rotary_append(q, k, v, cache: PagedCache, layer: int, cu_new, table: RotaryT
 def paged_attention(q, cache: PagedCache, layer: int, cu_new, *, rows=None, max_new=None, causal: bool = True,
                     window: int = 0, scale=None, out=None, lse=None, return_lse: bool = False, stream=None):
     """Attention of the last tokens of the cache's rows over all that the rows hold (see dspark_paged_attention).
-    q [tokens, q_heads, head_dim]; cu_new and rows as for rotary_append; max_new: the longest chunk, where known;
-    causal=False lets a chunk's tokens see each other; window > 0: only the last window keys; scale: of the scores
-    (None: 1 / sqrt(head_dim)).  Returns out, or (out, lse fp32 [tokens, q_heads]) with return_lse."""
+    q [tokens, q_heads, head_dim]; cu_new and rows as for rotary_append; max_new: the longest chunk (None: that of one
+    sequence with all tokens, which costs a decode of many requests some percent: there say 1); causal=False lets a chunk's tokens see each other; window > 0: only the last window keys; scale: of the scores
+    (None: 1 / sqrt(head_dim)).  Returns out, or (out, lse fp32 [tokens, q_heads]) with return_lse.  Calls on one cache must not
+    overlap (they share its workspace), and autograd does not see them."""
     lib = cache._lib
     dtype, d = cache.dtype, cache._index
     qa, qb = _heads(q, "q", d, dtype)

@@ -2,8 +2,9 @@
 //
 // The angle of pair j at position p is frac(p * turns[j] / 2^64) of a turn.  The product is taken
 // modulo 2^64, which drops the whole turns exactly; its top 32 bits, read as a signed fraction of
-// half a turn, give sine and cosine.  The error of the angle is 2^-32 turns whatever the position,
-// where p * frequency in fp32 would lose a bit for every doubling of the context.
+// half a turn and rounded to fp32, give sine and cosine.  The error of the angle is that rounding, at most 2^-26 of a turn (near
+// half a turn, where fp32 has 24 of the 31 bits), whatever the position; p * frequency in fp32 would lose a bit for every
+// doubling of the context.
 //
 // Bound by memory: every element is read and written once.  A block first puts the sines and cosines of its tokens into shared
 // memory, one pair to a thread: with every thread computing those of its own unit they took longer than the copies (8190 tokens of

@@ -527,7 +527,7 @@ void dspark_gated_draft_plan_destroy(dspark_gated_plan *plan);
  *   refs    int32 [num_pages]: sequences that hold the page (0: free)
  *   workspace  dspark_cache_workspace_bytes() bytes, 256-byte aligned, the first 2048 of them
  *           ZERO-FILLED before its first use; holds the status word.  Calls that share one must
- *           not overlap.
+ *           not overlap, on one stream or several.
  * Supported: page_size 16, 32, 64, 128 or 256; head_dim 64 or 128; 1 <= kv_heads, layers,
  *   num_pages, max_seqs, max_pages; num_pages < 2^24.
  *
@@ -670,7 +670,8 @@ dspark_status dspark_rotary_append(const dspark_cache *cache, const dspark_appen
  *   lse      float [tokens, q_heads] or NULL
  *   scale    positive
  *   max_new  the longest chunk, as far as the caller knows (a hint for the tile shape; wrong values
- *            cost time, not correctness); tokens where it is not known
+ *            cost time, not correctness: 64 or 256 decoded tokens called one chunk take 2 to 11 %
+ *            longer); tokens where it is not known
  * What lies in the cache where no token of the chunk sees it is never used, whatever it is:
  * behind a row's length, before the window of all, in pages that no row holds (whose table entries
  * are not looked at either).  Keys that only some tokens of a chunk see may hold anything for the
