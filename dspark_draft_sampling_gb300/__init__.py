@@ -1,6 +1,7 @@
 """libdspark: GB300-native DSpark per-cycle draft step (Markov block draft,
 Q8_0 confidence probe, weight-stationary small-M matvec) and its key-value side (paged
-cache, rotary positions, attention of new tokens over the cache).
+cache, rotary positions, attention of new tokens over the cache), and the step from logits to
+kept tokens (drawing them, accepting or replacing drafts).
 
 Every step of the path runs in the CUDA kernels of ``libdspark.so``; this package
 only marshals torch tensors into the C ABI declared in ``include/dspark.h``.
@@ -26,6 +27,8 @@ from .api import (  # noqa: F401
     rotary,
     rotary_append,
     rotary_frequencies,
+    sample,
+    verify_drafts,
     ws_matvec,
     ws_matvec_grouped,
     ws_matvec_host,

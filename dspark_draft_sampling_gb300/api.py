@@ -83,7 +83,10 @@ SIGNATURES = {
     "dspark_rotary": (_I, [_S, _P]),
     "dspark_rotary_append": (_I, [_P, _S, _P]),
     "dspark_paged_attention": (_I, [_P, _S, _P]),
+    "dspark_paged_attention_sinks": (_I, [_P, _S, _I, _P]),
     "dspark_paged_attention_debug": (_I, [_P, _S, _U, _P]),
+    "dspark_sample": (_I, [_S, _P]),
+    "dspark_verify_drafts": (_I, [_S, _P]),
 }
 
 _lock = threading.Lock()
@@ -1081,10 +1084,11 @@ def rotary_append(q, k, v, cache: PagedCache, layer: int, cu_new, table: RotaryT
 
 
 def paged_attention(q, cache: PagedCache, layer: int, cu_new, *, rows=None, max_new=None, causal: bool = True,
-                    window: int = 0, scale=None, out=None, lse=None, return_lse: bool = False, stream=None):
+                    window: int = 0, sinks: int = 0, scale=None, out=None, lse=None, return_lse: bool = False, stream=None):
     """Attention of the last tokens of the cache's rows over all that the rows hold (see dspark_paged_attention).
     q [tokens, q_heads, head_dim]; cu_new and rows as for rotary_append; max_new: the longest chunk (None: that of one
-    sequence with all tokens, which costs a decode of many requests some percent: there say 1); causal=False lets a chunk's tokens see each other; window > 0: only the last window keys; scale: of the scores
+    sequence with all tokens, which costs a decode of many requests some percent: there say 1); causal=False lets a chunk's tokens see each other; window > 0: only the last window keys,
+    and with sinks > 0 the row's first sinks keys too (without a window they change nothing); scale: of the scores
     (None: 1 / sqrt(head_dim)).  Returns out, or (out, lse fp32 [tokens, q_heads]) with return_lse.  Calls on one cache must not
     overlap (they share its workspace), and autograd does not see them."""
     lib = cache._lib
@@ -1106,13 +1110,117 @@ def paged_attention(q, cache: PagedCache, layer: int, cu_new, *, rows=None, max_
             with torch.cuda.stream(stream):
                 lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=cache.device)
     seqs = cu_new.numel() - 1
-    status = _launch(
-        lib.dspark_paged_attention, d, stream, cache._ref,
-        _ATTENTION_ARGS.pack(q.data_ptr(), out.data_ptr(),
-                             0 if lse is None else _ints(lse, "lse", d, tokens * q_heads, dtype=torch.float32),
-                             0 if rows is None else _ints(rows, "rows", d, seqs), _ints(cu_new, "cu_new", d), qa, qb, oa, ob, layer,
-                             tokens, q_heads, seqs, tokens if max_new is None else max_new, 1 if causal else 0, window,
-                             dim ** -0.5 if scale is None else scale))
+    args = _ATTENTION_ARGS.pack(q.data_ptr(), out.data_ptr(),
+                                0 if lse is None else _ints(lse, "lse", d, tokens * q_heads, dtype=torch.float32),
+                                0 if rows is None else _ints(rows, "rows", d, seqs), _ints(cu_new, "cu_new", d), qa, qb, oa, ob, layer,
+                                tokens, q_heads, seqs, tokens if max_new is None else max_new, 1 if causal else 0, window,
+                                dim ** -0.5 if scale is None else scale)
+    if sinks == 0:
+        status = _launch(lib.dspark_paged_attention, d, stream, cache._ref, args)
+    else:
+        status = _launch(lib.dspark_paged_attention_sinks, d, stream, cache._ref, args, sinks)
     if status:
         _check(lib, status)
     return (out, lse) if return_lse else out
+
+
+# ---- drawing tokens, and judging drafted ones ----
+
+_FILTERS = "4P3fi"
+_SAMPLE_ARGS = struct.Struct("@4P2q3i4x" + _FILTERS)
+_VERIFY_ARGS = struct.Struct("@7P2q4i" + _FILTERS)
+
+
+def _filters(n: int, device: int, temperature, top_k, top_p, min_p):
+    """dspark_filters of n rows or sequences: a setting is a number, None (off) or a tensor of n entries."""
+    at, all_of = [], []
+    for name, v, off, dtype in (("temperature", temperature, 1.0, torch.float32), ("top_p", top_p, 1.0, torch.float32),
+                                ("min_p", min_p, 0.0, torch.float32), ("top_k", top_k, 0, torch.int32)):
+        if isinstance(v, torch.Tensor):
+            at.append(_ints(v, name, device, n, dtype=dtype))
+            all_of.append(off)
+        else:
+            at.append(0)
+            all_of.append(off if v is None else v)
+    return (*at, *all_of)
+
+
+def _row_matrix(t, name: str, device: int, dtype, rows=None, columns=None):
+    """Row stride of a matrix with contiguous rows on the GPU `device`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not dtype or t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix of {dtype} on GPU {device}")
+    if (rows is not None and t.shape[0] != rows) or (columns is not None and t.shape[1] != columns):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, columns)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return t.stride(0)
+
+
+def _logits(logits):
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _DTYPES or logits.get_device() < 0:
+        raise ValueError("logits must be an fp16, bf16 or fp32 CUDA tensor [rows, vocab]")
+    d = logits.get_device()
+    return d, _row_matrix(logits, "logits", d, logits.dtype)
+
+
+def _new(shape, dtype, device, stream):
+    """An output in the memory of the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def sample(logits, uniforms, *, temperature=None, top_k=None, top_p=None, min_p=None, out=None, probs=None, return_probs: bool = False,
+           stream=None):
+    """A token of each row of logits [rows, vocab] (fp16, bf16 or fp32; rows may be strided), drawn by uniforms fp32 [rows] in [0, 1)
+    (see dspark_sample).  temperature (None: 1; 0: the largest logit, the lowest of equal ones), top_k (0: all), top_p (1: all) and min_p
+    (0: all) are numbers, None (off) or CUDA tensors with an entry for each row (fp32; top_k int32).  Returns ids int64 [rows], -1 where a
+    row's logits are all -infinity or NaN; with return_probs (ids, probs): what was drawn from, fp32 [rows, vocab], as verify_drafts
+    takes it.  Autograd does not see the call."""
+    lib = load_library()
+    d, stride = _logits(logits)
+    rows, vocab = logits.shape
+    if out is None:
+        out = _new(rows, torch.int64, logits.device, stream)
+    if probs is None and return_probs:
+        probs = _new((rows, vocab), torch.float32, logits.device, stream)
+    status = _launch(
+        lib.dspark_sample, d, stream,
+        _SAMPLE_ARGS.pack(logits.data_ptr(), _ints(uniforms, "uniforms", d, rows, dtype=torch.float32),
+                          _ints(out, "out", d, rows, dtype=torch.int64), 0 if probs is None else probs.data_ptr(), stride,
+                          0 if probs is None else _row_matrix(probs, "probs", d, torch.float32, rows, vocab), _DTYPES[logits.dtype], rows,
+                          vocab, *_filters(rows, d, temperature, top_k, top_p, min_p)))
+    if status:
+        _check(lib, status)
+    return (out, probs) if return_probs else out
+
+
+def verify_drafts(logits, drafts, cu_drafts, uniforms, *, draft_probs=None, temperature=None, top_k=None, top_p=None, min_p=None,
+                  out=None, accepted=None, stream=None):
+    """Accepts or replaces drafted tokens so that the outcome is distributed as the target's own draws (see dspark_verify_drafts).
+    drafts int64 [drafts] of all sequences; cu_drafts int32 [sequences + 1]: first draft of each sequence; logits [drafts + sequences,
+    vocab]: a sequence's rows, one for each of its drafts and one for the token behind them, follow each other; uniforms fp32 [drafts +
+    sequences, 2]; draft_probs fp32 [drafts, vocab]: what each draft was drawn from (None: they were picked, as by markov_draft).  The
+    settings are as for sample, an entry for each sequence.  Returns (ids int64 [drafts + sequences], accepted int32 [sequences]): a
+    sequence's rows of ids hold its accepted drafts, the token drawn behind them, then -1.  Autograd does not see the call."""
+    lib = load_library()
+    d, stride = _logits(logits)
+    seqs, n = cu_drafts.numel() - 1, drafts.numel()
+    rows, vocab = logits.shape
+    if seqs < 0 or rows != n + seqs:
+        raise ValueError(f"logits has {rows} rows, expected {n} drafts' and {seqs} sequences'")
+    if out is None:
+        out = _new(rows, torch.int64, logits.device, stream)
+    if accepted is None:
+        accepted = _new(seqs, torch.int32, logits.device, stream)
+    status = _launch(
+        lib.dspark_verify_drafts, d, stream,
+        _VERIFY_ARGS.pack(logits.data_ptr(), _ints(uniforms, "uniforms", d, 2 * rows, dtype=torch.float32), _ints(cu_drafts, "cu_drafts", d),
+                          _ints(drafts, "drafts", d, dtype=torch.int64), 0 if draft_probs is None else draft_probs.data_ptr(),
+                          _ints(out, "out", d, rows, dtype=torch.int64), _ints(accepted, "accepted", d, seqs), stride,
+                          0 if draft_probs is None else _row_matrix(draft_probs, "draft_probs", d, torch.float32, n, vocab),
+                          _DTYPES[logits.dtype], vocab, seqs, n, *_filters(seqs, d, temperature, top_k, top_p, min_p)))
+    if status:
+        _check(lib, status)
+    return out, accepted

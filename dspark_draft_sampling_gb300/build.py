@@ -19,7 +19,7 @@ INCLUDE_DIR = os.path.join(REPO_DIR, "include")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_NAME = "libdspark.so"
 SOURCES = ["common.cu", "markov.cu", "markov_tc.cu", "markov_cluster.cu", "probe.cu", "ws_matvec.cu", "draft_plan.cu", "gated_plan.cu", "ws_q8.cu", "host_api.cu",
-           "cache.cu", "rotary.cu", "paged_attention.cu"]
+           "cache.cu", "rotary.cu", "paged_attention.cu", "sample.cu"]
 BENCH_LIB_NAME = "libdspark_bench.so"
 BENCH_SOURCES = ["bench_kernels.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

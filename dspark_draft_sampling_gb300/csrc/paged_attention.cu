@@ -69,6 +69,7 @@ struct Attention {
     long long out_token, out_head;
     const int *rows, *cu_new;
     int tokens, group, n_seqs, layer, causal, window, chunk_tiles;  // chunk_tiles: query tiles of the longest chunk (hint)
+    int sinks;          // first keys that stay visible; 0 without a window
     int tile_tokens;    // tokens of a 128-row tile
     unsigned cut;       // what cutting items costs, in key tiles
     float scale;
@@ -113,9 +114,11 @@ __device__ __forceinline__ Seq load_seq(const CacheView &c, const Attention &g, 
     return q;
 }
 
-// Keys [begin, end) that some token of query tile i (of `step` tokens) of a sequence sees, and the key tiles [lo, hi) they lie in.
+// Keys [0, sinks) and [begin, end) that some token of query tile i (of `step` tokens) of a sequence sees, and the key tiles [0, split) and
+// [lo, hi) they lie in.
 struct Keys {
-    int begin, end, lo, hi;
+    int sinks, begin, end, split, lo, hi;
+    __device__ __forceinline__ int tiles() const { return split + hi - lo; }
 };
 
 __device__ __forceinline__ Keys keys_of(const Attention &g, const Seq &q, int i, int step) {
@@ -125,23 +128,26 @@ __device__ __forceinline__ Keys keys_of(const Attention &g, const Seq &q, int i,
     k.begin = g.window > 0 ? max(0, off + first - g.window + 1) : 0;
     k.hi = (k.end + kTile - 1) / kTile;
     k.lo = k.begin < k.end ? k.begin / kTile : k.hi;
+    k.sinks = min(min(g.sinks, k.begin), k.end);
+    k.split = min((k.sinks + kTile - 1) / kTile, k.lo);
     return k;
 }
 
 // What an item counts among all tiles.
 __device__ __forceinline__ int item_cost(const Attention &g, const Seq &q, int i, int step) {
-    const Keys k = keys_of(g, q, i, step);
-    return kItemCost + k.hi - k.lo;
+    return kItemCost + keys_of(g, q, i, step).tiles();
 }
 
 // One stretch of an item that a block works on, as the copying warp hands it to the others.
 struct Segment {
     int kv_head, tile;        // query tile of the sequence
-    int lo, first, last;      // the item's first key tile; the stretch's, relative to it
+    int first, last;          // the stretch among the item's key tiles
+    int split, gap;           // the item's tile t is the row's key tile t, or from `split` on t + gap
     int tiles;                // of the whole item; -1: no more segments
-    int begin, end;           // keys that some row of the item sees
+    int sinks, begin, end;    // keys [0, sinks) and [begin, end) that some row of the item sees
     int q0, n, length;        // the sequence's first query token, its new tokens, its tokens
     int cf, cl;               // first and last block that work on the item (where that is more than one)
+    __device__ __forceinline__ int key(int t) const { return (t < split ? t : t + gap) * kTile; }  // first one of the item's tile t
 };
 
 // Walks a block's range.
@@ -164,11 +170,13 @@ struct Walk {
                 }
             }
             const Keys k = keys_of(g, q, i, step);
-            const int tiles = k.hi - k.lo;
+            const int tiles = k.tiles();
             const unsigned take = min(left, kItemCost + tiles - x);
             out->kv_head = kv_head;
             out->tile = i;
-            out->lo = k.lo;
+            out->split = k.split;
+            out->gap = k.lo - k.split;
+            out->sinks = k.sinks;
             out->begin = k.begin;
             out->end = k.end;
             out->tiles = tiles;
@@ -637,8 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int *pages = c.table + static_cast<size_t>(walk.q.row) * c.max_pages;
                 const int run = (g.layer * 2) * c.kv_heads + seg.kv_head, runs = c.layers * 2 * c.kv_heads, page_groups = c.page_size / 8;
                 for (int t = seg.first; ok && t < seg.last; ++t) {
-                    const int key = (seg.lo + t) * kTile + lane * box;  // first key of this lane's page
-                    const bool mine = lane < per_tile && key < seg.end && key + box > seg.begin;  // pages that no row sees are not looked at
+                    const int key = seg.key(t) + lane * box;  // first key of this lane's page
+                    // pages that no row sees are not looked at
+                    const bool mine = lane < per_tile && key < seg.end && (key + box > seg.begin || key < seg.sinks);
                     int page = 0;
                     if (mine) {
                         page = pages[key >> c.page_shift];
@@ -792,20 +801,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool warp_real = __any_sync(0xffffffffu, real);
             for (int i = 0; i < steps && ok; ++i) {
                 const int t = PAIR ? i : 2 * i + s;
-                const int key0 = (seg.lo + seg.first + t) * kTile;
+                const int key0 = seg.key(seg.first + t);
                 if (!(ok = warp_wait(ctl, &ctl->s_full[s], n_s & 1, c, g.tries))) break;
                 ++n_s;
                 tc_fence_after();
-                if (key0 < seg.begin || key0 + kTile > seg.end) {
+                if ((key0 < seg.begin && key0 + kTile > seg.sinks) || key0 + kTile > seg.end) {
                     // Values that no row of the item sees are whatever the pages hold, or were not copied: zeros, so that weights of 0
                     // stay 0.
                     const uint32_t p = 2 * (base + t) + 1, st = p % S::kStages;
                     if (!(ok = warp_wait(ctl, &ctl->full[st], (p / S::kStages) & 1, c, g.tries))) break;
-                    const int first = max(seg.begin - key0, 0) * 8, last = min(seg.end - key0, kTile) * 8;
+                    const int skip = max(seg.sinks - key0, 0) * 8;
+                    const int first = min(max(seg.begin - key0, 0), kTile) * 8, last = min(seg.end - key0, kTile) * 8;
                     unsigned char *v = ring_ptr + st * S::kTileBytes;
                     for (int h = 0; h < S::kHalves; ++h) {
                         uint4 *at = reinterpret_cast<uint4 *>(v) + h * 64;
-                        for (int b = r; b < first; b += kTile) at[b + (b & ~63) * (S::kHalves - 1)] = make_uint4(0u, 0u, 0u, 0u);
+                        for (int b = skip + r; b < first; b += kTile) at[b + (b & ~63) * (S::kHalves - 1)] = make_uint4(0u, 0u, 0u, 0u);
                         for (int b = last + r; b < kTile * 8; b += kTile) at[b + (b & ~63) * (S::kHalves - 1)] = make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
@@ -813,19 +823,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (warp_real) {
                     uint32_t v[kTile];
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    const bool edge = __any_sync(0xffffffffu, key0 < see_lo || key0 + kTile > see_hi);
+                    const bool edge = __any_sync(0xffffffffu, (key0 < see_lo && key0 + kTile > g.sinks) || key0 + kTile > see_hi);
                     if (edge) {
                         // masked in place, a quarter at a time: few tiles have an edge, and their code stands here once
 #pragma unroll 1
                         for (int q = 0; q < 4; ++q) {
-                            const int lo = see_lo - key0 - q * 32, hi = see_hi - key0 - q * 32;
+                            const int lo = see_lo - key0 - q * 32, hi = see_hi - key0 - q * 32, sinks = g.sinks - key0 - q * 32;
                             if (!__any_sync(0xffffffffu, lo > 0 || hi < 32)) continue;
                             uint32_t w[32];
                             tmem_ld_32(t_s + q * 32, w);
                             tmem_wait_ld();
 #pragma unroll
                             for (int u = 0; u < 32; ++u)
-                                if (u < lo || u >= hi) w[u] = 0xff800000u;
+                                if ((u < lo && u >= sinks) || u >= hi) w[u] = 0xff800000u;
                             tmem_st_32(t_s + q * 32, w);
                         }
                         tmem_wait_st();
@@ -1143,7 +1153,7 @@ dspark_status launch(const CUtensorMap &tm_q, const CUtensorMap &tm_kv, const Ca
     return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "paged_attention");
 }
 
-dspark_status attend(const dspark_cache *cache, const dspark_attention_args *args, unsigned stall_us, cudaStream_t stream) {
+dspark_status attend(const dspark_cache *cache, const dspark_attention_args *args, int sinks, unsigned stall_us, cudaStream_t stream) {
     const char *who = "paged_attention";
     CacheView c;
     dspark_status st = cache_view(cache, who, &c);
@@ -1152,9 +1162,9 @@ dspark_status attend(const dspark_cache *cache, const dspark_attention_args *arg
     auto [q, out, lse, rows, cu_new, q_token_stride, q_head_stride, out_token_stride, out_head_stride, layer, tokens, q_heads, n_seqs,
           max_new, causal, window, scale] = *args;
     if (layer < 0 || layer >= c.layers) return fail(DSPARK_ERR_INVALID, "%s: layer %d of %d", who, layer, c.layers);
-    if (tokens < 0 || q_heads < 1 || n_seqs < 0 || max_new < 0 || window < 0)
-        return fail(DSPARK_ERR_INVALID, "%s: bad sizes tokens=%d q_heads=%d n_seqs=%d max_new=%d window=%d", who, tokens,
-                    q_heads, n_seqs, max_new, window);
+    if (tokens < 0 || q_heads < 1 || n_seqs < 0 || max_new < 0 || window < 0 || sinks < 0)
+        return fail(DSPARK_ERR_INVALID, "%s: bad sizes tokens=%d q_heads=%d n_seqs=%d max_new=%d window=%d sinks=%d", who, tokens,
+                    q_heads, n_seqs, max_new, window, sinks);
     if (q_heads % c.kv_heads) return fail(DSPARK_ERR_INVALID, "%s: %d query heads over %d kv heads", who, q_heads, c.kv_heads);
     if (!(scale > 0.f) || scale > 3.0e38f) return fail(DSPARK_ERR_INVALID, "%s: scale %g is not positive and finite", who, scale);
     const int group = q_heads / c.kv_heads;
@@ -1194,6 +1204,7 @@ dspark_status attend(const dspark_cache *cache, const dspark_attention_args *arg
     g.layer = layer;
     g.causal = causal != 0;
     g.window = window < 1 << 30 ? window : 0;  // no row is longer: hides nothing, and differences of positions stay within 32 bits
+    g.sinks = g.window > 0 ? (sinks < 1 << 30 ? sinks : 1 << 30) : 0;
     g.scale = scale;
     g.tile_tokens = kTile / group;
     // Two query tiles share each key tile where chunks have two; a chunk of one tile splits its keys over the streams. Query tiles
@@ -1245,10 +1256,15 @@ size_t attention_scratch_bytes(int head_dim) { return size_t(kMaxCtas) * 2 * 2 *
 }  // namespace dspark
 
 extern "C" dspark_status dspark_paged_attention(const dspark_cache *cache, const dspark_attention_args *args, dspark_stream_t stream) {
-    return dspark::attend(cache, args, 0, stream);
+    return dspark::attend(cache, args, 0, 0, stream);
+}
+
+extern "C" dspark_status dspark_paged_attention_sinks(const dspark_cache *cache, const dspark_attention_args *args, int sinks,
+                                                      dspark_stream_t stream) {
+    return dspark::attend(cache, args, sinks, 0, stream);
 }
 
 extern "C" dspark_status dspark_paged_attention_debug(const dspark_cache *cache, const dspark_attention_args *args, unsigned stall_us,
                                                       dspark_stream_t stream) {
-    return dspark::attend(cache, args, stall_us, stream);
+    return dspark::attend(cache, args, 0, stall_us, stream);
 }

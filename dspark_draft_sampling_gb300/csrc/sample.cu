@@ -1,0 +1,857 @@
+// Drawing tokens from logits (temperature, top-k, top-p, min-p), and judging drafted tokens against the target's logits.
+//
+// Weights.  A row's token v weighs w_v = exp((l_v - m) / T), m the largest logit.  Sums over a vocabulary decide which token a
+// uniform number falls on and where a nucleus ends, so they have to come out the same whatever their order: weights are whole
+// numbers of 2^-44, sums 64-bit integers.  With y = (l - m) log2(e) / T in two 32-bit parts, 2^y of the tokens that matter (y >= -8) comes
+// from a table of 2^(j/64) and a cubic in the rest |r| <= 2^-7, whose next term is 4e-11: 28 bits.  Lighter tokens take the fast
+// exponential (2^-22) of a difference rounded to 32 bits (2^-24 of |ln w|): 2^-28 of the heaviest token's weight at most.
+//
+// Work.  A row belongs to a cluster of thread blocks, each of which keeps its slice in shared memory, so the logits are read from
+// memory once whatever the settings ask for.  The blocks exchange maxima, sums and histograms through distributed shared memory.
+#include <atomic>
+#include <cmath>
+#include <cstddef>
+#include <cstring>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBins = kThreads;           // of a histogram: a thread looks after one
+constexpr int kMaxBlocks = 16;            // of a cluster
+constexpr int kMaxVocab = 1 << 19;        // 2^19 weights of 2^44 stay below 2^64
+constexpr long long kAccepted = -2;       // in ids until the second kernel has run: the row's draft is accepted
+
+using u64 = unsigned long long;
+
+struct Draw {
+    const void *logits;
+    const float *uniforms, *temperature, *top_p, *min_p, *draft_probs;
+    const int *top_k, *cu_drafts;
+    const long long *drafts;
+    long long *ids;
+    int *accepted;
+    float *probs;
+    long long logits_stride, probs_stride, draft_probs_stride;
+    float temperature_all, top_p_all, min_p_all;
+    int top_k_all;
+    int rows, vocab, slice, n_seqs, n_drafts;
+    uint2 table[64];  // 2^(28 + j/64): rounded, and as a float
+};
+
+// What a row is drawn by: the cluster's first block reads it and hands it to the others, so that all of them take the same branches
+// whatever happens to those arrays meanwhile.
+struct Given {
+    float hi, lo;              // log2(e) / T in two parts
+    float floor_hi, floor_lo;  // log2 of min_p
+    float top_p, u;
+    int top_k;                 // 0: all
+    int state;                 // one of the below
+    int token;                 // the draft that the row judges; -1: none that can be accepted
+    float logit, share, accept;  // its logit, its probability when it was drawn, the number that decides
+    int draft;                 // its place among all drafts
+};
+enum { kNotDrawn, kGreedy, kDrawn };
+
+struct alignas(16) Shared {
+    uint2 table[64];
+    Given given;
+    unsigned count[2][kBins];    // histograms, read by the cluster's other blocks
+    alignas(8) unsigned mass[2][kBins][2];  // low and high half of 64 bits
+    u64 slot[2][kMaxBlocks];     // [parity][block]: what the blocks exchange
+    u64 warp[kWarps];            // sums over the warps' stretches of the slice
+    u64 scan[2][kWarps];
+    u64 inverse;
+    int found, sequence;
+};
+
+static_assert(offsetof(Shared, mass) % 8 == 0 && offsetof(Shared, slot) % 8 == 0 && sizeof(Shared) % 16 == 0, "64-bit words and vectors are aligned");
+
+__device__ __forceinline__ uint32_t at_block(const void *p, int block) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(block));
+    return r;
+}
+__device__ __forceinline__ unsigned ld_block_u32(uint32_t at) {
+    unsigned v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ u64 ld_block_u64(uint32_t at) {
+    u64 v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_block_u32(uint32_t at, unsigned v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_block_u64(uint32_t at, u64 v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+}
+// Every thread of the cluster; orders their memory accesses.
+__device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ u64 warp_sum(u64 v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <typename N>
+__device__ __forceinline__ N warp_prefix(N v, int lane) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const N y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    return v;
+}
+
+// floor(z * f), or its ceiling, exactly; f in [0, 1).
+__device__ __forceinline__ u64 part_of(u64 z, float f, bool up) {
+    const unsigned bits = __float_as_uint(f), e = max(bits >> 23, 1u);
+    const unsigned mantissa = (bits & 0x7fffffu) | (bits >> 23 ? 0x800000u : 0u);
+    const unsigned __int128 product = static_cast<unsigned __int128>(z) * mantissa;
+    const unsigned shift = 150 - e;
+    if (shift > 100) return up && product != 0 ? 1 : 0;
+    const unsigned __int128 rest = up ? (static_cast<unsigned __int128>(1) << shift) - 1 : 0;
+    return static_cast<u64>((product + rest) >> shift);
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <typename T>
+struct Type;
+template <>
+struct Type<float> {
+    static constexpr int kPer = 4;
+    static __device__ __forceinline__ void spread(uint4 v, float *x) {
+        x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ float one(const void *p, long long i) { return static_cast<const float *>(p)[i]; }
+    static constexpr unsigned kMasked = 0xff800000u;
+};
+template <>
+struct Type<__nv_bfloat16> {
+    static constexpr int kPer = 8;
+    static __device__ __forceinline__ void spread(uint4 v, float *x) {
+        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    static __device__ __forceinline__ float one(const void *p, long long i) {
+        return __uint_as_float(static_cast<unsigned>(static_cast<const unsigned short *>(p)[i]) << 16);
+    }
+    static constexpr unsigned kMasked = 0xff80ff80u;
+};
+template <>
+struct Type<__half> {
+    static constexpr int kPer = 8;
+    static __device__ __forceinline__ void spread(uint4 v, float *x) {
+        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        }
+    }
+    static __device__ __forceinline__ float one(const void *p, long long i) { return __half2float(static_cast<const __half *>(p)[i]); }
+    static constexpr unsigned kMasked = 0xfc00fc00u;
+};
+
+// The weights of a row's tokens.
+template <typename T>
+struct Weights {
+    float top, hi, lo, least;   // m; log2(e) / T in two parts; the difference of logits whose weight is nothing
+    const uint2 *table;
+
+    __device__ __forceinline__ Weights(float m, const Given &g, const uint2 *t) : top(m), hi(g.hi), lo(g.lo), least(-100.f / g.hi), table(t) {}
+    // y of a logit that is not NaN, as two parts
+    __device__ __forceinline__ void exponent(float l, float *p, float *e) const {
+        const float diff = l - top, d = l >= top ? 0.f : fmaxf(diff, least);
+        *p = d * hi;
+        *e = __fmaf_rn(d, lo, __fmaf_rn(d, hi, -*p));
+        if (heavy(*p) && d < 0.f) {  // and what the difference lost
+            const float back = diff - l, lost = (l - (diff - back)) + (-top - back);
+            *e = __fmaf_rn(lost, hi, *e);
+        }
+    }
+    __device__ __forceinline__ static bool heavy(float p) { return p >= -8.f; }
+    // 2^(28 + fraction) in whole numbers and the power of two that it is to be divided by
+    __device__ __forceinline__ unsigned significand(float p, float e, int *shift) const {
+        const float t = p + 196608.f;  // 1.5 * 2^17: rounded to 64ths
+        const int n = __float_as_int(t) - 0x48400000;
+        const float r = (p - (t - 196608.f)) + e;
+        const float q = r * __fmaf_rn(r, __fmaf_rn(r, 0.0555041087f, 0.2402265070f), 0.6931471806f);
+        const uint2 entry = table[n & 63];
+        *shift = -(n >> 6);
+        return entry.x + (__float_as_int(__fmaf_rn(q, __uint_as_float(entry.y), 12582912.f)) - 0x4b400000);
+    }
+    __device__ __forceinline__ u64 heavy_weight(float p, float e) const {
+        int shift;
+        const unsigned s = significand(p, e, &shift);
+        return static_cast<u64>(s) << (16 - shift);
+    }
+    __device__ __forceinline__ static float light_weight(float p, float e) {  // of 2^-44
+        const float w = fast_exp2(p) * 17592186044416.f;
+        return __fmaf_rn(w * 0.6931471806f, e, w);
+    }
+    __device__ __forceinline__ u64 weight(float l) const {
+        float p, e;
+        exponent(l, &p, &e);
+        return heavy(p) ? heavy_weight(p, e) : __float2ull_rn(light_weight(p, e));
+    }
+};
+
+// Which tokens are left: those before and with the last one of the order, and of at least a weight.
+struct Kept {
+    float value;  // the last token's logit, and the last index of its ties that stays
+    int index;
+    float floor_hi, floor_lo;  // log2 of the least weight
+
+    __device__ __forceinline__ bool order(float l, int i) const { return l > value || (l == value && i <= index); }
+    __device__ __forceinline__ bool weight(float p, float e) const { return (p - floor_hi) + (e - floor_lo) >= 0.f; }
+};
+
+// Sums over a vector's tokens, in index order: the sum up to a token never falls, and the sum over the vector is the same whenever it is
+// taken.
+template <typename T>
+struct MassSum {
+    const Weights<T> &w;
+    const Kept &kept;
+    u64 h = 0;
+    float c = 0.f;
+    __device__ __forceinline__ MassSum(const Weights<T> &a, const Kept &b) : w(a), kept(b) {}
+    __device__ __forceinline__ void add(float l, int i) {
+        if (!kept.order(l, i)) return;
+        float p, e;
+        w.exponent(l, &p, &e);
+        if (!kept.weight(p, e)) return;
+        if (w.heavy(p)) h += w.heavy_weight(p, e);
+        else c += w.light_weight(p, e);
+    }
+    __device__ __forceinline__ u64 sum() const { return h + __float2ull_rn(c); }
+};
+
+struct TieSum {
+    float value;
+    const Kept &kept;
+    u64 n = 0;
+    __device__ __forceinline__ TieSum(float v, const Kept &b) : value(v), kept(b) {}
+    __device__ __forceinline__ void add(float l, int i) { n += l == value && kept.order(l, i) ? 1 : 0; }
+    __device__ __forceinline__ u64 sum() const { return n; }
+};
+
+// Leading zeros of a row's sum: 0 to 19, as 2^44 <= z.
+__device__ __forceinline__ int lead_of(u64 z) { return __clzll(static_cast<long long>(z)); }
+
+// max(0, p - q) in 2^-62 over the kept tokens; without q, p without the draft.
+template <typename T>
+struct RestSum {
+    const Weights<T> &w;
+    const Kept &kept;
+    const float *q;
+    int draft, shift;
+    u64 inverse;
+    u64 n = 0;
+    // of the row's sum z: 2^127 / (z 2^lead), the last bits of which do not matter, as it is the same for all tokens
+    static __device__ u64 invert(u64 z) {
+        const int lead = lead_of(z);
+        const double r = 9223372036854775808.0 / static_cast<double>(z << lead) * 18446744073709551616.0;
+        return r >= 18446744073709549568.0 ? ~0ull : static_cast<u64>(r);
+    }
+    __device__ __forceinline__ RestSum(const Weights<T> &a, const Kept &b, const float *draft_probs, int x, u64 z, u64 inverted)
+        : w(a), kept(b), q(draft_probs), draft(x), shift(20 - lead_of(z)), inverse(inverted) {}
+    __device__ __forceinline__ void add(float l, int i) {
+        if (!kept.order(l, i)) return;
+        float p, e;
+        w.exponent(l, &p, &e);
+        if (!kept.weight(p, e)) return;
+        const u64 mine = __umul64hi((w.heavy(p) ? w.heavy_weight(p, e) : __float2ull_rn(w.light_weight(p, e))) << 19, inverse) >> shift;
+        u64 theirs = i == draft ? ~0ull : 0ull;
+        if (q) {
+            const unsigned bits = __float_as_uint(fminf(fmaxf(q[i], 0.f), 1.f));
+            const int up = static_cast<int>(bits >> 23) - 88;  // 2^62 of a 24-bit significand
+            const u64 s = (bits & 0x7fffffu) | 0x800000u;
+            theirs = up >= 0 ? s << up : up > -24 ? s >> -up : 0;
+        }
+        n += mine > theirs ? mine - theirs : 0;
+    }
+    __device__ __forceinline__ u64 sum() const { return n; }
+};
+
+// A row's slice in this block, and the cluster around it.
+template <typename T>
+struct Row {
+    static constexpr int kPer = Type<T>::kPer;
+    Shared *s;
+    const uint4 *data;
+    int warp, lane, block, blocks;
+    int vectors, rounds, first;  // vectors of the slice, of a thread; index of the first vector's first element (which may lie before the slice)
+    int parity, histogram;
+
+    // Warp w takes a stretch of neighbouring vectors, so that index order is the order of warps, rounds, lanes and elements.
+    __device__ __forceinline__ int vector(int round) const { return (warp * rounds + round) * 32 + lane; }
+
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+#pragma unroll 1
+        for (int k = 0; k < rounds; ++k) {
+            const int v = vector(k);
+            if (v >= vectors) break;
+            float x[kPer];
+            Type<T>::spread(data[v], x);
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) f(x[u], first + v * kPer + u);
+        }
+    }
+    // The blocks' values: their sum, and that over the blocks before this one.
+    __device__ __forceinline__ u64 exchange_sum(u64 mine, u64 *before) {
+        u64 all = 0;
+        *before = 0;
+        exchange(mine);
+        for (int b = 0; b < blocks; ++b) {
+            const u64 v = s->slot[parity][b];
+            if (b < block) *before += v;
+            all += v;
+        }
+        return all;
+    }
+    __device__ __forceinline__ void exchange(u64 a) {
+        parity ^= 1;
+        if (static_cast<int>(threadIdx.x) < blocks) {
+            st_block_u64(at_block(&s->slot[parity][block], threadIdx.x), a);
+        }
+        cluster_barrier();
+    }
+    // The block's sum of `make()` over its slice; the warps' sums stay in s->warp.
+    template <typename M>
+    __device__ __forceinline__ u64 sum(M make) {
+        u64 n = 0;
+#pragma unroll 1
+        for (int k = 0; k < rounds; ++k) n += vector_sum(make, vector(k));
+        n = warp_sum(n);
+        __syncthreads();
+        if (lane == 0) s->warp[warp] = n;
+        __syncthreads();
+        n = 0;
+        for (int w = 0; w < kWarps; ++w) n += s->warp[w];
+        return n;
+    }
+    template <typename M>
+    __device__ __forceinline__ u64 vector_sum(M make, int v) const {
+        auto a = make();
+        if (v < vectors) {
+            float x[kPer];
+            Type<T>::spread(data[v], x);
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) a.add(x[u], first + v * kPer + u);
+        }
+        return a.sum();
+    }
+    // The first token at which the sum over the slice, taken just before by sum(), exceeds `target` (less than it): its index, in s->found.
+    template <typename M>
+    __device__ __forceinline__ void find(M make, u64 target) {
+        u64 before = 0;
+        int w = 0;
+        while (w < kWarps - 1 && before + s->warp[w] <= target) before += s->warp[w++];
+        if (w != warp) return;
+#pragma unroll 1
+        for (int k = 0; k < rounds; ++k) {
+            const int v = vector(k);
+            const u64 mine = vector_sum(make, v), upto = before + warp_prefix(mine, lane);
+            const unsigned past = __ballot_sync(0xffffffffu, upto > target);
+            if (past == 0) {
+                before = __shfl_sync(0xffffffffu, upto, 31);
+                continue;
+            }
+            if (lane == __ffs(past) - 1) {
+                auto a = make();
+                float x[kPer];
+                Type<T>::spread(data[v], x);
+                int u = 0;
+                for (; u < kPer; ++u) {
+                    a.add(x[u], first + v * kPer + u);
+                    if (upto - mine + a.sum() > target) break;
+                }
+                s->found = first + v * kPer + u;
+            }
+            return;
+        }
+    }
+
+    // Narrows `kept` to the tokens up to the one at which their number (MASS: weight) in descending order reaches `target`.
+    template <bool MASS>
+    __device__ __forceinline__ void select(Kept *kept, const Weights<T> &w, u64 target, float from) {
+        const Kept prior = *kept;
+        unsigned c0 = float_order_code(from), c1 = float_order_code(w.top);
+        u64 above = 0;
+        for (;;) {
+            const int bits = 32 - __clz(static_cast<int>(c1 - c0)), shift = max(bits - 9, 0);
+            histogram ^= 1;
+            s->count[histogram][threadIdx.x] = 0;
+            s->mass[histogram][threadIdx.x][0] = s->mass[histogram][threadIdx.x][1] = 0;
+            __syncthreads();
+            each([&](float l, int i) {
+                if (!prior.order(l, i)) return;
+                const unsigned c = float_order_code(l);
+                if (c < c0 || c > c1) return;
+                const unsigned b = (c1 - c) >> shift;
+                if (MASS) {
+                    const u64 v = w.weight(l);
+                    const unsigned low = static_cast<unsigned>(v), was = atomicAdd(&s->mass[histogram][b][0], low);
+                    const unsigned high = static_cast<unsigned>(v >> 32) + (was + low < low ? 1 : 0);
+                    if (high) atomicAdd(&s->mass[histogram][b][1], high);
+                } else {
+                    atomicAdd(&s->count[histogram][b], 1u);
+                }
+            });
+            cluster_barrier();
+            u64 n = 0;
+            for (int b = 0; b < blocks; ++b)
+                n += MASS ? ld_block_u64(at_block(&s->mass[histogram][threadIdx.x][0], b)) : ld_block_u32(at_block(&s->count[histogram][threadIdx.x], b));
+            // the first bin that reaches the target
+            u64 upto = warp_prefix(n, lane);
+            if (lane == 31) s->scan[0][warp] = upto;
+            if (threadIdx.x == 0) s->found = kBins;
+            __syncthreads();
+            for (int k = 0; k < warp; ++k) upto += s->scan[0][k];
+            upto += above;
+            if (upto >= target && upto - n < target) {
+                s->found = threadIdx.x;
+                s->scan[1][0] = upto - n;
+            }
+            __syncthreads();
+            const int bin = s->found;
+            if (bin == kBins) return;  // all of them do not reach it: nothing is dropped
+            above = s->scan[1][0];
+            __syncthreads();
+            c1 -= static_cast<unsigned>(bin) << shift;
+            c0 = max(c0, c1 - ((1u << shift) - 1));
+            if (shift == 0) break;
+        }
+        // all tokens of one logit: how many of them stay, and which one is the last
+        const unsigned back = c1 & 0x80000000u ? c1 & 0x7fffffffu : ~c1;
+        const float value = __uint_as_float(back);
+        u64 left = target - above;
+        if (MASS) {
+            const u64 each_one = w.weight(value);
+            left = (left + each_one - 1) / each_one;
+        }
+        auto ties = [&] { return TieSum(value, prior); };
+        const u64 mine = sum(ties);
+        u64 before;
+        const u64 all = exchange_sum(mine, &before);
+        kept->value = value;
+        kept->index = value == prior.value ? prior.index : 0x7fffffff;
+        if (left >= all) return;
+        if (left - 1 >= before && left - 1 < before + mine) find(ties, left - 1 - before);
+        __syncthreads();
+        exchange(left - 1 >= before && left - 1 < before + mine ? s->found : 0);
+        u64 index = 0;
+        for (int b = 0; b < blocks; ++b) index += s->slot[parity][b];
+        kept->index = static_cast<int>(index);
+    }
+
+    // The token of the weights `make()` at u of their sum; true if any weighs something.
+    template <typename M>
+    __device__ __forceinline__ bool pick(M make, float u, long long *id) {
+        const u64 mine = sum(make);
+        u64 before;
+        const u64 all = exchange_sum(mine, &before);
+        if (all == 0) return false;
+        const u64 target = !(u > 0.f) ? 0 : u < 1.f ? part_of(all, u, false) : all - 1;
+        if (target >= before && target < before + mine) {
+            find(make, target - before);
+            __syncthreads();
+            if (threadIdx.x == 0) *id = s->found;
+        }
+        return true;
+    }
+};
+
+template <typename T, bool VERIFY>
+__global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant__ Draw g) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    Row<T> row;
+    Shared *s = row.s = reinterpret_cast<Shared *>(smem);
+    row.data = reinterpret_cast<const uint4 *>(smem + sizeof(Shared));
+    {
+        unsigned r, n;
+        asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+        asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+        row.block = r;
+        row.blocks = n;
+    }
+    row.warp = threadIdx.x >> 5;
+    row.lane = threadIdx.x & 31;
+    row.parity = row.histogram = 0;
+    const long long r = blockIdx.x / row.blocks;
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (threadIdx.x < 64) s->table[threadIdx.x] = g.table[threadIdx.x];
+    if (VERIFY && threadIdx.x == 0) s->sequence = g.n_seqs;
+    __syncthreads();
+    pdl_launch_dependents();
+    pdl_wait();  // no global-memory access before this point
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all blocks run: their shared memory may be written to
+
+    const size_t row_at = static_cast<size_t>(r) * g.logits_stride;
+    if (row.block == 0) {
+        // ---- whose row it is, and what it is to be drawn by ----
+        if (VERIFY) {
+            for (int q = threadIdx.x; q < g.n_seqs; q += kThreads) {
+                const int a = g.cu_drafts[q], b = g.cu_drafts[q + 1];
+                if (a >= 0 && b >= a && b <= g.n_drafts && r >= a + q && r <= b + q) atomicMin(&s->sequence, q);
+            }
+            __syncthreads();
+        }
+        if (row.warp == 0) {
+            if (row.lane == 0) {
+                const int setting = VERIFY ? s->sequence : static_cast<int>(r);
+                Given v{};
+                v.token = v.draft = -1;
+                if (!VERIFY || setting < g.n_seqs) {
+                    v.u = g.uniforms[VERIFY ? 2 * r + 1 : r];
+                    if (VERIFY && r < g.cu_drafts[setting + 1] + setting) {
+                        const int d = static_cast<int>(r) - setting;
+                        const long long x = g.drafts[d];
+                        if (x >= 0 && x < g.vocab) {
+                            v.draft = d;
+                            v.token = static_cast<int>(x);
+                            v.logit = Type<T>::one(g.logits, row_at + x);
+                            v.accept = g.uniforms[2 * r];
+                            v.share = g.draft_probs ? fmaxf(g.draft_probs[static_cast<size_t>(d) * g.draft_probs_stride + x], 0.f) : 1.f;
+                        }
+                    }
+                    const float temperature = g.temperature ? g.temperature[setting] : g.temperature_all;
+                    v.state = temperature > 0.f ? kDrawn : kGreedy;
+                    v.top_p = g.top_p ? g.top_p[setting] : g.top_p_all;
+                    v.top_k = g.top_k ? g.top_k[setting] : g.top_k_all;
+                    const float min_p = g.min_p ? g.min_p[setting] : g.min_p_all;
+                    // within these temperatures neither part leaves the range of 32 bits; beyond them a weight is one or nothing
+                    const double c = v.state == kDrawn ? 1.4426950408889634074 / fmin(fmax(static_cast<double>(temperature), 1e-30), 1e30) : 1.0;
+                    v.hi = static_cast<float>(c);
+                    v.lo = static_cast<float>(c - v.hi);
+                    v.floor_hi = -INFINITY;
+                    if (v.state == kDrawn && min_p > 0.f) {
+                        const double least = log2(fmin(static_cast<double>(min_p), 1.0));
+                        v.floor_hi = static_cast<float>(least);
+                        v.floor_lo = static_cast<float>(least - v.floor_hi);
+                    }
+                    if (v.state == kGreedy) v.top_k = 1;
+                    if (v.state == kGreedy || !(v.top_p < 1.f)) v.top_p = 1.f;
+                    if (v.top_k < 0 || v.top_k >= g.vocab) v.top_k = 0;
+                    if (v.state == kGreedy && g.vocab == 1) v.top_k = 1;
+                }
+                s->given = v;
+            }
+            __syncwarp();
+            const unsigned *v = reinterpret_cast<const unsigned *>(&s->given);
+            for (int i = row.lane; i < row.blocks * static_cast<int>(sizeof(Given) / 4); i += 32) {
+                const int to = i / static_cast<int>(sizeof(Given) / 4), at = i % static_cast<int>(sizeof(Given) / 4);
+                if (to > 0) st_block_u32(at_block(v + at, to), v[at]);
+            }
+        }
+    }
+
+    // ---- the slice into shared memory, and the largest logit ----
+    float top = -INFINITY;
+    {
+        constexpr int P = Row<T>::kPer;
+        const int begin = min(row.block * g.slice, g.vocab), n = min(g.slice, g.vocab - begin);
+        const T *from = static_cast<const T *>(g.logits) + row_at + begin;
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15) / static_cast<int>(sizeof(T));
+        row.first = begin - off;
+        row.vectors = n > 0 ? (off + n + P - 1) / P : 0;
+        row.rounds = (row.vectors + kThreads - 1) / kThreads;
+        const uint4 *whole = reinterpret_cast<const uint4 *>(from - off);
+        uint4 *data = reinterpret_cast<uint4 *>(smem + sizeof(Shared));
+        const int full0 = off ? 1 : 0, full1 = (off + n) / P;
+        for (int k0 = 0; k0 < row.rounds; k0 += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = row.vector(k0 + j);
+                v[j] = make_uint4(Type<T>::kMasked, Type<T>::kMasked, Type<T>::kMasked, Type<T>::kMasked);
+                if (k0 + j < row.rounds && at >= full0 && at < full1) v[j] = ldg_nc_v4(whole + at);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = row.vector(k0 + j);
+                if (k0 + j >= row.rounds || at >= row.vectors) break;
+                if (at < full0 || at >= full1) {  // the slice's ends: element by element
+                    alignas(16) T part[P];
+                    *reinterpret_cast<uint4 *>(part) = v[j];
+                    for (int e = 0; e < P; ++e)
+                        if (at * P + e >= off && at * P + e < off + n) part[e] = from[at * P + e - off];
+                    v[j] = *reinterpret_cast<uint4 *>(part);
+                }
+                data[at] = v[j];
+                float x[P];
+                Type<T>::spread(v[j], x);
+#pragma unroll
+                for (int e = 0; e < P; ++e) top = fmaxf(top, x[e]);
+            }
+        }
+    }
+    {
+        const unsigned m = __reduce_max_sync(0xffffffffu, float_order_code(top));
+        if (row.lane == 0) s->warp[row.warp] = m;
+        __syncthreads();
+        u64 most = 0;
+        for (int w = 0; w < kWarps; ++w) most = max(most, s->warp[w]);
+        row.exchange(most);
+        most = 0;
+        for (int b = 0; b < row.blocks; ++b) most = max(most, s->slot[row.parity][b]);
+        const unsigned c = static_cast<unsigned>(most);
+        top = __uint_as_float(c & 0x80000000u ? c & 0x7fffffffu : ~c);
+    }
+
+    // ---- what is left of the row ----
+    const Given &given = s->given;  // here since the exchange of the maxima
+    if (given.state == kNotDrawn) return;  // a row behind the sequences: left as it is
+    long long *id = g.ids + r;
+    if (top == -INFINITY) {
+        if (row.block == 0 && threadIdx.x == 0) *id = -1;
+        if (!VERIFY && g.probs) {
+            float *to = g.probs + r * g.probs_stride;
+            for (int i = row.block * g.slice + threadIdx.x; i < min((row.block + 1) * g.slice, g.vocab); i += kThreads) to[i] = 0.f;
+        }
+        return;
+    }
+    const Weights<T> weights(top, given, s->table);
+    Kept kept{-INFINITY, -1, -INFINITY, 0.f};
+    auto mass = [&] { return MassSum<T>(weights, kept); };
+    auto total = [&] {
+        u64 before;
+        return row.exchange_sum(row.sum(mass), &before);
+    };
+    if (given.top_k > 0) row.template select<false>(&kept, weights, given.top_k, -3.402823466e38f);
+    if (given.top_p < 1.f)
+        row.template select<true>(&kept, weights, max(part_of(total(), fmaxf(given.top_p, 0.f), true), 1ull), -3.402823466e38f);
+    kept.floor_hi = given.floor_hi;
+    kept.floor_lo = given.floor_lo;
+    u64 z = 0;
+    if (VERIFY || g.probs) z = total();
+
+    // ---- the distribution ----
+    if (!VERIFY && g.probs) {
+        float *to = g.probs + r * g.probs_stride;
+        const float scale = 1.f / static_cast<float>(z);
+        row.each([&](float l, int i) {
+            if (i < row.block * g.slice || i >= min((row.block + 1) * g.slice, g.vocab)) return;
+            float p, e, v = 0.f;
+            if (kept.order(l, i)) {
+                weights.exponent(l, &p, &e);
+                if (kept.weight(p, e)) v = weights.heavy(p) ? static_cast<float>(weights.heavy_weight(p, e)) : weights.light_weight(p, e);
+            }
+            to[i] = v * scale;
+        });
+    }
+
+    // ---- the token ----
+    bool done = false;
+    if (VERIFY && given.token >= 0) {
+        if (threadIdx.x == 0) {
+            u64 w = 0;
+            if (kept.order(given.logit, given.token)) {
+                float p, e;
+                weights.exponent(given.logit, &p, &e);
+                if (kept.weight(p, e)) w = weights.weight(given.logit);
+            }
+            const bool yes = static_cast<double>(given.accept) * static_cast<double>(given.share) * static_cast<double>(z) < static_cast<double>(w);
+            if (yes && row.block == 0) *id = kAccepted;
+            s->found = yes;
+            if (!yes) s->inverse = RestSum<T>::invert(z);
+        }
+        __syncthreads();
+        done = s->found;
+        __syncthreads();
+        const float *q = g.draft_probs ? g.draft_probs + static_cast<size_t>(given.draft) * g.draft_probs_stride : nullptr;
+        if (!done) done = row.pick([&] { return RestSum<T>(weights, kept, q, given.token, z, s->inverse); }, given.u, id);
+    }
+    if (!done) row.pick(mass, given.u, id);
+    cluster_barrier();  // no block leaves while another may read its shared memory
+}
+
+// Each sequence's accepted drafts, the token drawn at its first row that did not accept, and -1 behind it.  A warp to a sequence.
+__global__ void __launch_bounds__(128) settle_kernel(const Draw g) {
+    const int q = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (q >= g.n_seqs) return;
+    const int a = g.cu_drafts[q], b = g.cu_drafts[q + 1];
+    if (a < 0 || b < a || b > g.n_drafts) return;
+    long long *ids = g.ids + a + q;
+    const int n = b - a;
+    int taken = n;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const unsigned no = __ballot_sync(0xffffffffu, i0 + lane < n && ids[i0 + lane] != kAccepted);
+        if (no) {
+            taken = i0 + __ffs(no) - 1;
+            break;
+        }
+    }
+    for (int i = lane; i <= n; i += 32)
+        if (i != taken) ids[i] = i < taken ? g.drafts[a + i] : -1;
+    if (lane == 0) g.accepted[q] = taken;
+}
+
+template <typename... Args>
+cudaError_t launch_cluster(void (*kernel)(Args...), int grid, int cluster, int threads, size_t smem, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+constexpr int kMostSlice = 128 * 1024;  // bytes; kMaxVocab fp32 logits over kMaxBlocks blocks
+
+template <typename T, bool VERIFY>
+dspark_status launch(Draw g, int sms, cudaStream_t stream) {
+    auto *kernel = draw_kernel<T, VERIFY>;
+    static std::atomic<unsigned long long> configured{0};  // a bit a device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (dev >= 64 || !(configured.load() >> dev & 1)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Shared)) + kMostSlice + 16);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(sample)");
+        if (dev < 64) configured.fetch_or(1ull << dev);
+    }
+    int blocks = 1;
+    const long long size = sizeof(T);
+    while (blocks < kMaxBlocks && (g.vocab * size > 64 * 1024ll * blocks || (2ll * g.rows * blocks <= sms && g.vocab > 2048 * blocks)))
+        blocks *= 2;
+    const int per = 16 / static_cast<int>(size);
+    g.slice = ((g.vocab + blocks - 1) / blocks + per - 1) / per * per;
+    const size_t smem = sizeof(Shared) + (g.slice + per) * size;
+    e = launch_cluster(kernel, g.rows * blocks, blocks, kThreads, smem, stream, g);
+    return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, VERIFY ? "verify_drafts" : "sample");
+}
+
+dspark_status check(const char *who, const void *logits, int dtype, int rows, int vocab, long long stride, const dspark_filters &f) {
+    if (rows < 0 || vocab < 1) return fail(DSPARK_ERR_INVALID, "%s: bad sizes rows=%d vocab=%d", who, rows, vocab);
+    if (vocab > kMaxVocab) return fail(DSPARK_ERR_UNSUPPORTED, "%s: vocab %d > %d", who, vocab, kMaxVocab);
+    if (rows > 0x7fffffff / kMaxBlocks) return fail(DSPARK_ERR_UNSUPPORTED, "%s: %d rows", who, rows);
+    if (dtype < DSPARK_FP16 || dtype > DSPARK_FP32) return fail(DSPARK_ERR_INVALID, "%s: unknown type %d", who, dtype);
+    if (rows > 1 && stride < 0) return fail(DSPARK_ERR_INVALID, "%s: negative row stride", who);
+    if (!f.temperature && !(f.temperature_all >= 0.f))
+        return fail(DSPARK_ERR_INVALID, "%s: temperature %g is negative or not a number", who, f.temperature_all);
+    if (!f.top_p && !(f.top_p_all >= 0.f && f.top_p_all <= 1.f)) return fail(DSPARK_ERR_INVALID, "%s: top_p %g is not in 0..1", who, f.top_p_all);
+    if (!f.min_p && !(f.min_p_all >= 0.f && f.min_p_all <= 1.f)) return fail(DSPARK_ERR_INVALID, "%s: min_p %g is not in 0..1", who, f.min_p_all);
+    if (!f.top_k && f.top_k_all < 0) return fail(DSPARK_ERR_INVALID, "%s: top_k %d is negative", who, f.top_k_all);
+    if (!aligned(f.temperature, 4) || !aligned(f.top_p, 4) || !aligned(f.min_p, 4) || !aligned(f.top_k, 4) ||
+        !aligned(logits, dtype == DSPARK_FP32 ? 4 : 2))
+        return fail(DSPARK_ERR_INVALID, "%s: misaligned pointer", who);
+    return DSPARK_OK;
+}
+
+template <bool VERIFY>
+dspark_status run(Draw g, int dtype, const dspark_filters &f, cudaStream_t stream) {
+    g.temperature = f.temperature;
+    g.top_p = f.top_p;
+    g.min_p = f.min_p;
+    g.top_k = f.top_k;
+    g.temperature_all = f.temperature_all;
+    g.top_p_all = f.top_p_all;
+    g.min_p_all = f.min_p_all;
+    g.top_k_all = f.top_k_all;
+    for (int j = 0; j < 64; ++j) {
+        const double x = std::exp2(28.0 + j / 64.0);
+        const float as_float = static_cast<float>(x);
+        g.table[j].x = static_cast<unsigned>(std::llrint(x));
+        std::memcpy(&g.table[j].y, &as_float, 4);
+    }
+    int sms = 0;
+    const dspark_status st = static_cast<dspark_status>(current_sm_count(&sms));
+    if (st != DSPARK_OK) return st;
+    return dtype == DSPARK_FP32   ? launch<float, VERIFY>(g, sms, stream)
+           : dtype == DSPARK_BF16 ? launch<__nv_bfloat16, VERIFY>(g, sms, stream)
+                                  : launch<__half, VERIFY>(g, sms, stream);
+}
+
+}  // namespace
+
+}  // namespace dspark
+
+extern "C" dspark_status dspark_sample(const dspark_sample_args *a, dspark_stream_t stream) {
+    using namespace dspark;
+    const char *who = "sample";
+    if (!a) return fail(DSPARK_ERR_INVALID, "%s: null arguments", who);
+    const dspark_status st = check(who, a->logits, a->dtype, a->rows, a->vocab, a->logits_stride, a->filters);
+    if (st != DSPARK_OK || a->rows == 0) return st;
+    if (!a->logits || !a->uniforms || !a->ids) return fail(DSPARK_ERR_INVALID, "%s: null pointer argument", who);
+    if (!aligned(a->uniforms, 4) || !aligned(a->ids, 8) || !aligned(a->probs, 4))
+        return fail(DSPARK_ERR_INVALID, "%s: misaligned pointer", who);
+    if (a->probs && a->rows > 1 && a->probs_stride < a->vocab)
+        return fail(DSPARK_ERR_INVALID, "%s: rows of probs overlap (stride %lld, vocab %d)", who, a->probs_stride, a->vocab);
+    Draw g{};
+    g.logits = a->logits;
+    g.uniforms = a->uniforms;
+    g.ids = reinterpret_cast<long long *>(a->ids);
+    g.probs = a->probs;
+    g.logits_stride = a->logits_stride;
+    g.probs_stride = a->probs_stride;
+    g.rows = a->rows;
+    g.vocab = a->vocab;
+    return run<false>(g, a->dtype, a->filters, stream);
+}
+
+extern "C" dspark_status dspark_verify_drafts(const dspark_verify_args *a, dspark_stream_t stream) {
+    using namespace dspark;
+    const char *who = "verify_drafts";
+    if (!a) return fail(DSPARK_ERR_INVALID, "%s: null arguments", who);
+    if (a->n_seqs < 0 || a->n_drafts < 0) return fail(DSPARK_ERR_INVALID, "%s: bad sizes n_seqs=%d n_drafts=%d", who, a->n_seqs, a->n_drafts);
+    if (a->n_drafts > 0x7fffffff - a->n_seqs) return fail(DSPARK_ERR_UNSUPPORTED, "%s: %d drafts", who, a->n_drafts);
+    const int rows = a->n_drafts + a->n_seqs;
+    const dspark_status st = check(who, a->logits, a->dtype, rows, a->vocab, a->logits_stride, a->filters);
+    if (st != DSPARK_OK || a->n_seqs == 0) return st;
+    if (!a->logits || !a->uniforms || !a->ids || !a->accepted || !a->cu_drafts || (a->n_drafts > 0 && !a->drafts))
+        return fail(DSPARK_ERR_INVALID, "%s: null pointer argument", who);
+    if (!aligned(a->uniforms, 4) || !aligned(a->ids, 8) || !aligned(a->drafts, 8) || !aligned(a->accepted, 4) || !aligned(a->cu_drafts, 4) ||
+        !aligned(a->draft_probs, 4))
+        return fail(DSPARK_ERR_INVALID, "%s: misaligned pointer", who);
+    if (a->draft_probs && a->n_drafts > 1 && a->draft_probs_stride < 0) return fail(DSPARK_ERR_INVALID, "%s: negative row stride", who);
+    Draw g{};
+    g.logits = a->logits;
+    g.uniforms = a->uniforms;
+    g.cu_drafts = a->cu_drafts;
+    g.drafts = reinterpret_cast<const long long *>(a->drafts);
+    g.draft_probs = a->draft_probs;
+    g.ids = reinterpret_cast<long long *>(a->ids);
+    g.accepted = a->accepted;
+    g.logits_stride = a->logits_stride;
+    g.draft_probs_stride = a->draft_probs_stride;
+    g.rows = rows;
+    g.vocab = a->vocab;
+    g.n_seqs = a->n_seqs;
+    g.n_drafts = a->n_drafts;
+    dspark_status done = run<true>(g, a->dtype, a->filters, stream);
+    if (done != DSPARK_OK) return done;
+    const cudaError_t e = launch_pdl(settle_kernel, dim3((g.n_seqs + 3) / 4), dim3(128), 0, stream, g);
+    return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, "verify_drafts (settle)");
+}

@@ -10,6 +10,9 @@
  *   dspark_cache_*         a paged cache's pages: allocate, fork, compact, free, copy
  *   dspark_rotary(_append) rotary positions, alone (with gradient) or on the way into the cache
  *   dspark_paged_attention attention of the new tokens over the cache
+ * and the step from logits to kept tokens where they are sampled:
+ *   dspark_sample          tokens drawn with temperature, top-k, top-p and min-p
+ *   dspark_verify_drafts   drafted tokens accepted or replaced by the target's logits
  *
  * Conventions shared by every entry point
  *   - Tensor pointers are DEVICE pointers (cudaMalloc / PyTorch allocations), owned
@@ -694,12 +697,104 @@ typedef struct dspark_attention_args {
 dspark_status dspark_paged_attention(const dspark_cache *cache, const dspark_attention_args *args,
                                      dspark_stream_t stream);
 
+/* The same with a row's first tokens visible beside the window: a token of position p sees the keys
+ *   0 <= j < L,   j <= p if causal,   j > p - window or j < sinks if window > 0
+ * What lies between the first `sinks` tokens and the window of a chunk's first token is neither looked
+ * at nor read, so a drafter's view of a long row costs what the window and the sinks hold.  sinks >= 0;
+ * with 0, or without a window, it is dspark_paged_attention. */
+dspark_status dspark_paged_attention_sinks(const dspark_cache *cache, const dspark_attention_args *args,
+                                           int sinks, dspark_stream_t stream);
+
 /* Fault-injection hook for testing the device-side wait limit: the same launch as
  * dspark_paged_attention, except that the softmax threads first wait `stall_us` microseconds on a
  * barrier that nothing signals; the wait gives up, DSPARK_ERR_TIMEOUT is recorded and the kernel
  * finishes normally.  Not for production use. */
 dspark_status dspark_paged_attention_debug(const dspark_cache *cache, const dspark_attention_args *args,
                                            unsigned stall_us, dspark_stream_t stream);
+
+/* =====================================================================================
+ * Drawing tokens, and judging drafted ones
+ *
+ * A row of logits l, its largest m, a temperature T > 0: token v weighs w_v = exp((l_v - m) / T).
+ * Three settings drop tokens, in this order; tokens stand in the order of their logits, largest
+ * first, equal ones by index:
+ *   top_k  the first top_k stay (0 or at least vocab: all)
+ *   top_p  of those, a token stays if what stands before it weighs less than top_p times what they
+ *          weigh together; the first one always does (1: all)
+ *   min_p  of those, the ones stay that weigh at least min_p (the first one weighs 1; 0: all)
+ * p_v = w_v over the sum of what is left, 0 for what is not.  T = 0 leaves the first token only.  A
+ * uniform number u in [0, 1) draws the lowest token whose p, added up in index order to it, exceeds u.
+ * Logits of -infinity and NaN are not tokens; where one is +infinity, those of +infinity weigh the
+ * same and the others nothing.  A row without tokens draws -1 and has p = 0.
+ * Sums are taken in 64-bit fixed point and do not depend on their order: the same inputs give the
+ * same tokens, whatever the number of rows or SMs.  Weights are off by less than 2^-27 of themselves,
+ * those below 2^-8 by 2^-28 of the heaviest one.
+ *
+ * Filters: each setting is an array, an entry for each row (dspark_sample) or sequence
+ * (dspark_verify_drafts), or where that is NULL the number for all.  The numbers are checked
+ * (temperature >= 0, top_p and min_p in 0..1, top_k >= 0); the arrays' entries, which only the
+ * device sees, are taken as temperature 0 where they are negative or NaN, top_p and min_p as their
+ * bounds where they lie beyond them and as off where they are NaN, top_k as off where it is negative.
+ *
+ * dspark_sample
+ *   logits    [rows, vocab] of dtype, the rows logits_stride elements apart
+ *   uniforms  float [rows] (below 0 or NaN is taken as 0, 1 and above as just below 1)
+ *   ids       int64 [rows], out
+ *   probs     float [rows, vocab], out, the rows probs_stride elements apart, or NULL: the p of all
+ *             tokens, rounded to fp32; must not overlap logits
+ *
+ * dspark_verify_drafts: the speculative acceptance that leaves the target's distribution as it is.
+ * Sequence s has the drafts cu_drafts[s] .. cu_drafts[s + 1] - 1, n of them (0 is fine), and n + 1 rows
+ * of logits from row cu_drafts[s] + s on: row i holds the target's logits where draft i stands, the
+ * last one those behind all drafts.  With a row's p as above, and its draft x drawn from q (or q = 1 at
+ * x and 0 elsewhere, where draft_probs is NULL: a draft picked greedily):
+ *   x is accepted if u0 q_x < p_x.  At the first row that does not accept, a token is drawn with u1
+ *   from max(0, p - q) (from p, where that is nothing); where all accept, from the last row's p.
+ *   logits       [n_drafts + n_seqs, vocab] of dtype
+ *   uniforms     float [n_drafts + n_seqs, 2]: u0 and u1 of each row (the last rows' u0 is not used)
+ *   cu_drafts    int32 [n_seqs + 1], from 0, ascending, at most n_drafts
+ *   drafts       int64 [n_drafts]; one outside 0 .. vocab - 1 is not accepted, and the token drawn from p
+ *   draft_probs  float [n_drafts, vocab], the rows draft_probs_stride apart, or NULL
+ *   ids          int64 [n_drafts + n_seqs], out: each sequence's accepted drafts, then the token
+ *                drawn, then -1
+ *   accepted     int32 [n_seqs], out: how many drafts that are
+ * Rows of ids that belong to no sequence, and accepted of a sequence whose bounds are out of range, are
+ * left as they are.  Supported: vocab <= 2^19; pointers aligned to their elements; ids must not overlap
+ * the inputs.  rows == 0 (n_seqs == 0) enqueues nothing.  No workspace: calls may overlap.
+ * ===================================================================================== */
+typedef struct dspark_filters {
+    const float *temperature, *top_p, *min_p; /* each may be NULL */
+    const int32_t *top_k;                     /* may be NULL */
+    float temperature_all, top_p_all, min_p_all;
+    int top_k_all;
+} dspark_filters;
+
+typedef struct dspark_sample_args {
+    const void *logits;
+    const float *uniforms;
+    int64_t *ids;
+    float *probs;
+    long long logits_stride, probs_stride;
+    int dtype, rows, vocab;
+    dspark_filters filters;
+} dspark_sample_args;
+
+dspark_status dspark_sample(const dspark_sample_args *args, dspark_stream_t stream);
+
+typedef struct dspark_verify_args {
+    const void *logits;
+    const float *uniforms;
+    const int32_t *cu_drafts;
+    const int64_t *drafts;
+    const float *draft_probs;
+    int64_t *ids;
+    int32_t *accepted;
+    long long logits_stride, draft_probs_stride;
+    int dtype, vocab, n_seqs, n_drafts;
+    dspark_filters filters;
+} dspark_verify_args;
+
+dspark_status dspark_verify_drafts(const dspark_verify_args *args, dspark_stream_t stream);
 
 #ifdef __cplusplus
 }
