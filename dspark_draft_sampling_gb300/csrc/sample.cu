@@ -24,7 +24,9 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = kThreads;           // of a histogram: a thread looks after one
+constexpr int kList = kThreads;           // tokens that one block sorts: a thread to each
 constexpr int kMaxBlocks = 16;            // of a cluster
+constexpr float kLowest = -3.402823466e38f;
 constexpr int kMaxVocab = 1 << 19;        // 2^19 weights of 2^44 stay below 2^64
 constexpr long long kAccepted = -2;       // in ids until the second kernel has run: the row's draft is accepted
 
@@ -65,10 +67,15 @@ struct alignas(16) Shared {
     unsigned count[2][kBins];    // histograms, read by the cluster's other blocks
     alignas(8) unsigned mass[2][kBins][2];  // low and high half of 64 bits
     u64 slot[2][kMaxBlocks];     // [parity][block]: what the blocks exchange
+    u64 list[kList];             // this block's tokens of a list, read by the first block: order code and what is left of 2^32 behind the index
+    u64 sort[2][kList];
     u64 warp[kWarps];            // sums over the warps' stretches of the slice
     u64 scan[2][kWarps];
-    u64 inverse;
-    int found, sequence;
+    u64 inverse, last;           // last: of the kept tokens, as in the list
+    u64 z;
+    u64 count_before, mass_before, count_in, drafted;
+    int found;
+    unsigned listed;
 };
 
 static_assert(offsetof(Shared, mass) % 8 == 0 && offsetof(Shared, slot) % 8 == 0 && sizeof(Shared) % 16 == 0, "64-bit words and vectors are aligned");
@@ -100,6 +107,12 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The logit of an order code in the upper half.
+__device__ __forceinline__ float value_of(u64 key) {
+    const unsigned c = static_cast<unsigned>(key >> 32);
+    return __uint_as_float(c & 0x80000000u ? c & 0x7fffffffu : ~c);
+}
+
 __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -125,6 +138,9 @@ __device__ __forceinline__ u64 part_of(u64 z, float f, bool up) {
     const unsigned __int128 rest = up ? (static_cast<unsigned __int128>(1) << shift) - 1 : 0;
     return static_cast<u64>((product + rest) >> shift);
 }
+
+// Where a uniform number falls among z.
+__device__ __forceinline__ u64 place_of(float u, u64 z) { return !(u > 0.f) ? 0 : u < 1.f ? part_of(z, u, false) : z - 1; }
 
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
@@ -274,12 +290,8 @@ struct RestSum {
     }
     __device__ __forceinline__ RestSum(const Weights<T> &a, const Kept &b, const float *draft_probs, int x, u64 z, u64 inverted)
         : w(a), kept(b), q(draft_probs), draft(x), shift(20 - lead_of(z)), inverse(inverted) {}
-    __device__ __forceinline__ void add(float l, int i) {
-        if (!kept.order(l, i)) return;
-        float p, e;
-        w.exponent(l, &p, &e);
-        if (!kept.weight(p, e)) return;
-        const u64 mine = __umul64hi((w.heavy(p) ? w.heavy_weight(p, e) : __float2ull_rn(w.light_weight(p, e))) << 19, inverse) >> shift;
+    __device__ __forceinline__ u64 rest(u64 weight, int i) const {
+        const u64 mine = __umul64hi(weight << 19, inverse) >> shift;
         u64 theirs = i == draft ? ~0ull : 0ull;
         if (q) {
             const unsigned bits = __float_as_uint(fminf(fmaxf(q[i], 0.f), 1.f));
@@ -287,7 +299,13 @@ struct RestSum {
             const u64 s = (bits & 0x7fffffu) | 0x800000u;
             theirs = up >= 0 ? s << up : up > -24 ? s >> -up : 0;
         }
-        n += mine > theirs ? mine - theirs : 0;
+        return mine > theirs ? mine - theirs : 0;
+    }
+    __device__ __forceinline__ void add(float l, int i) {
+        if (!kept.order(l, i)) return;
+        float p, e;
+        w.exponent(l, &p, &e);
+        if (kept.weight(p, e)) n += rest(w.heavy(p) ? w.heavy_weight(p, e) : __float2ull_rn(w.light_weight(p, e)), i);
     }
     __device__ __forceinline__ u64 sum() const { return n; }
 };
@@ -392,59 +410,160 @@ struct Row {
         }
     }
 
-    // Narrows `kept` to the tokens up to the one at which their number (MASS: weight) in descending order reaches `target`.
+    // Inclusive sums over the block's threads.
+    __device__ __forceinline__ u64 block_prefix(u64 v) {
+        u64 upto = warp_prefix(v, lane);
+        __syncthreads();
+        if (lane == 31) s->scan[0][warp] = upto;
+        __syncthreads();
+        for (int k = 0; k < warp; ++k) upto += s->scan[0][k];
+        return upto;
+    }
+
+    // A histogram over the cluster's tokens (bin(l, i) < 0: not counted) and the first bin at which the number (MASS: weight) of tokens from
+    // bin 0 on reaches `target`; kBins if none does.  What comes before it and lies in it is left in shared memory.
+    template <bool MASS, typename B>
+    __device__ __forceinline__ int reach(const Weights<T> &w, u64 target, B bin) {
+        histogram ^= 1;
+        s->count[histogram][threadIdx.x] = 0;
+        s->mass[histogram][threadIdx.x][0] = s->mass[histogram][threadIdx.x][1] = 0;
+        __syncthreads();
+        each([&](float l, int i) {
+            const int b = bin(l, i);
+            if (b < 0) return;
+            atomicAdd(&s->count[histogram][b], 1u);
+            if (MASS) {
+                const u64 v = w.weight(l);
+                const unsigned low = static_cast<unsigned>(v), was = atomicAdd(&s->mass[histogram][b][0], low);
+                const unsigned high = static_cast<unsigned>(v >> 32) + (was + low < low ? 1 : 0);
+                if (high) atomicAdd(&s->mass[histogram][b][1], high);
+            }
+        });
+        return reached<MASS>(target);
+    }
     template <bool MASS>
-    __device__ __forceinline__ void select(Kept *kept, const Weights<T> &w, u64 target, float from) {
+    __device__ __forceinline__ int reached(u64 target) {
+        cluster_barrier();
+        u64 n = 0, m = 0;
+        for (int b = 0; b < blocks; ++b) {
+            n += ld_block_u32(at_block(&s->count[histogram][threadIdx.x], b));
+            if (MASS) m += ld_block_u64(at_block(&s->mass[histogram][threadIdx.x][0], b));
+        }
+        if (threadIdx.x == 0) s->found = kBins;
+        const u64 count = block_prefix(n), mass = MASS ? block_prefix(m) : 0;
+        const u64 upto = MASS ? mass : count, in = MASS ? m : n;
+        if (upto >= target && upto - in < target) {
+            s->found = threadIdx.x;
+            s->count_before = count - n;
+            s->count_in = n;
+            s->mass_before = mass - m;
+        }
+        __syncthreads();
+        return s->found;
+    }
+
+    // The tokens for which `wanted` holds into the blocks' lists; how many there are in all.
+    template <typename W>
+    __device__ __forceinline__ int gather(W wanted) {
+        if (threadIdx.x == 0) s->listed = 0;
+        __syncthreads();
+        each([&](float l, int i) {
+            if (!wanted(l, i)) return;
+            const unsigned at = atomicAdd(&s->listed, 1u);
+            if (at < kList) s->list[at] = static_cast<u64>(float_order_code(l)) << 32 | (0xffffffffu - static_cast<unsigned>(i));
+        });
+        cluster_barrier();
+        int n = 0;
+        for (int b = 0; b < blocks; ++b) n += ld_block_u32(at_block(&s->listed, b));
+        return n;
+    }
+    // The first block's threads get a token each of the n (at most kList) in all lists, in their order; 0 behind them.
+    __device__ __forceinline__ u64 sorted_list(int n) {
+        u64 key = 0;
+        int at = threadIdx.x;
+        for (int b = 0; b < blocks && at >= 0; ++b) {
+            const int here = ld_block_u32(at_block(&s->listed, b));
+            if (at < here) key = ld_block_u64(at_block(&s->list[at], b));
+            at -= here;
+        }
+        return sort(key, n);
+    }
+    // Bitonic, descending, of the threads' keys, of which those from n on are 0.
+    __device__ __forceinline__ u64 sort(u64 key, int n) {
+        int side = 0;
+        for (int k = 2; k < 2 * n; k *= 2)
+            for (int j = k / 2; j > 0; j /= 2) {
+                u64 other;
+                if (j >= 32) {
+                    s->sort[side][threadIdx.x] = key;
+                    __syncthreads();
+                    other = s->sort[side][threadIdx.x ^ j];
+                    side ^= 1;
+                } else {
+                    other = __shfl_xor_sync(0xffffffffu, key, j);
+                }
+                const bool large = ((threadIdx.x & k) == 0) == ((threadIdx.x & j) == 0);
+                key = large == (key > other) ? key : other;
+            }
+        __syncthreads();
+        return key;
+    }
+
+    // Narrows `kept` to the tokens up to the one at which their number (MASS: weight) in descending order reaches `target`. `from`: a
+    // logit below which none of them lies. Where WHOLE and they are few, they and the ones up to a bin's end behind them are listed
+    // instead, and their number returned; else 0.
+    template <bool MASS, bool WHOLE = false>
+    __device__ __forceinline__ int select(Kept *kept, const Weights<T> &w, u64 target, float from) {
         const Kept prior = *kept;
-        unsigned c0 = float_order_code(from), c1 = float_order_code(w.top);
-        u64 above = 0;
+        // bins of equal width first, which spread the logits best
+        const float range = w.top - from, scale = range > 0.f && range < 3e38f ? 511.9f / range : 0.f;
+        auto linear = [&](float l, int i) {
+            return l >= from && prior.order(l, i) ? min(static_cast<int>((w.top - l) * scale), kBins - 1) : -1;
+        };
+        const int bin = reach<MASS>(w, target, linear);
+        if (bin == kBins) return 0;  // all of them do not reach it: nothing is dropped
+        if (WHOLE && s->count_before + s->count_in <= kList)
+            return gather([&](float l, int i) { return l >= from && linear(l, i) <= bin; });
+        u64 above = MASS ? s->mass_before : s->count_before;
+        if (s->count_in <= kList) {
+            const int n = gather([&](float l, int i) { return linear(l, i) == bin; });
+            if (block == 0) {
+                const u64 key = sorted_list(n);
+                const u64 in = MASS ? (key ? w.weight(value_of(key)) : 0) : (key ? 1 : 0);
+                const u64 upto = above + block_prefix(in);
+                if (in && upto >= target && upto - in < target) s->last = key;
+                __syncthreads();
+                if (static_cast<int>(threadIdx.x) < blocks) st_block_u64(at_block(&s->last, threadIdx.x), s->last);
+            }
+            cluster_barrier();
+            kept->value = value_of(s->last);
+            kept->index = 0xffffffffu - static_cast<unsigned>(s->last);
+            return 0;
+        }
+        // then of equal numbers of codes, until a bin is one logit
+        unsigned c0, c1;
+        {
+            unsigned least = 0xffffffffu, most = 0;
+            each([&](float l, int i) {
+                if (linear(l, i) != bin) return;
+                least = min(least, float_order_code(l));
+                most = max(most, float_order_code(l));
+            });
+            exchange_range(least, most, &c0, &c1);
+        }
         for (;;) {
             const int bits = 32 - __clz(static_cast<int>(c1 - c0)), shift = max(bits - 9, 0);
-            histogram ^= 1;
-            s->count[histogram][threadIdx.x] = 0;
-            s->mass[histogram][threadIdx.x][0] = s->mass[histogram][threadIdx.x][1] = 0;
-            __syncthreads();
-            each([&](float l, int i) {
-                if (!prior.order(l, i)) return;
+            const int b = reach<MASS>(w, target - above, [&](float l, int i) {
                 const unsigned c = float_order_code(l);
-                if (c < c0 || c > c1) return;
-                const unsigned b = (c1 - c) >> shift;
-                if (MASS) {
-                    const u64 v = w.weight(l);
-                    const unsigned low = static_cast<unsigned>(v), was = atomicAdd(&s->mass[histogram][b][0], low);
-                    const unsigned high = static_cast<unsigned>(v >> 32) + (was + low < low ? 1 : 0);
-                    if (high) atomicAdd(&s->mass[histogram][b][1], high);
-                } else {
-                    atomicAdd(&s->count[histogram][b], 1u);
-                }
+                return prior.order(l, i) && c >= c0 && c <= c1 ? static_cast<int>((c1 - c) >> shift) : -1;
             });
-            cluster_barrier();
-            u64 n = 0;
-            for (int b = 0; b < blocks; ++b)
-                n += MASS ? ld_block_u64(at_block(&s->mass[histogram][threadIdx.x][0], b)) : ld_block_u32(at_block(&s->count[histogram][threadIdx.x], b));
-            // the first bin that reaches the target
-            u64 upto = warp_prefix(n, lane);
-            if (lane == 31) s->scan[0][warp] = upto;
-            if (threadIdx.x == 0) s->found = kBins;
-            __syncthreads();
-            for (int k = 0; k < warp; ++k) upto += s->scan[0][k];
-            upto += above;
-            if (upto >= target && upto - n < target) {
-                s->found = threadIdx.x;
-                s->scan[1][0] = upto - n;
-            }
-            __syncthreads();
-            const int bin = s->found;
-            if (bin == kBins) return;  // all of them do not reach it: nothing is dropped
-            above = s->scan[1][0];
-            __syncthreads();
-            c1 -= static_cast<unsigned>(bin) << shift;
+            above += MASS ? s->mass_before : s->count_before;
+            c1 -= static_cast<unsigned>(b) << shift;
             c0 = max(c0, c1 - ((1u << shift) - 1));
             if (shift == 0) break;
         }
         // all tokens of one logit: how many of them stay, and which one is the last
-        const unsigned back = c1 & 0x80000000u ? c1 & 0x7fffffffu : ~c1;
-        const float value = __uint_as_float(back);
+        const float value = value_of(static_cast<u64>(c1) << 32);
         u64 left = target - above;
         if (MASS) {
             const u64 each_one = w.weight(value);
@@ -456,13 +575,35 @@ struct Row {
         const u64 all = exchange_sum(mine, &before);
         kept->value = value;
         kept->index = value == prior.value ? prior.index : 0x7fffffff;
-        if (left >= all) return;
-        if (left - 1 >= before && left - 1 < before + mine) find(ties, left - 1 - before);
+        if (left >= all) return 0;
+        const bool here = left - 1 >= before && left - 1 < before + mine;
+        if (here) find(ties, left - 1 - before);
         __syncthreads();
-        exchange(left - 1 >= before && left - 1 < before + mine ? s->found : 0);
+        exchange(here ? s->found : 0);
         u64 index = 0;
         for (int b = 0; b < blocks; ++b) index += s->slot[parity][b];
         kept->index = static_cast<int>(index);
+        return 0;
+    }
+    // The least and the largest of the cluster's codes.
+    __device__ __forceinline__ void exchange_range(unsigned least, unsigned most, unsigned *c0, unsigned *c1) {
+        least = __reduce_min_sync(0xffffffffu, least);
+        most = __reduce_max_sync(0xffffffffu, most);
+        __syncthreads();
+        if (lane == 0) s->scan[0][warp] = static_cast<u64>(most) << 32 | (0xffffffffu - least);
+        __syncthreads();
+        unsigned a = 0, b = 0;
+        for (int k = 0; k < kWarps; ++k) {
+            a = max(a, static_cast<unsigned>(s->scan[0][k] >> 32));
+            b = max(b, static_cast<unsigned>(s->scan[0][k]));
+        }
+        exchange(static_cast<u64>(a) << 32 | b);
+        for (int k = 0; k < blocks; ++k) {
+            a = max(a, static_cast<unsigned>(s->slot[parity][k] >> 32));
+            b = max(b, static_cast<unsigned>(s->slot[parity][k]));
+        }
+        *c0 = 0xffffffffu - b;
+        *c1 = a;
     }
 
     // The token of the weights `make()` at u of their sum; true if any weighs something.
@@ -472,7 +613,7 @@ struct Row {
         u64 before;
         const u64 all = exchange_sum(mine, &before);
         if (all == 0) return false;
-        const u64 target = !(u > 0.f) ? 0 : u < 1.f ? part_of(all, u, false) : all - 1;
+        const u64 target = place_of(u, all);
         if (target >= before && target < before + mine) {
             find(make, target - before);
             __syncthreads();
@@ -481,6 +622,73 @@ struct Row {
         return true;
     }
 };
+
+// What row r is drawn by, into this block's shared memory.  One warp.
+template <typename T, bool VERIFY>
+__device__ __forceinline__ void give(const Draw &g, long long r, size_t row_at, Shared *s, int lane) {
+    int setting = static_cast<int>(r), draft = -1;
+    if (VERIFY) {  // the first sequence whose rows r is among
+        setting = g.n_seqs;
+        for (int q0 = 0; q0 < g.n_seqs && setting == g.n_seqs; q0 += 32) {
+            const int q = q0 + lane;
+            int a = 0, b = -1;
+            if (q < g.n_seqs) a = g.cu_drafts[q], b = g.cu_drafts[q + 1];
+            const bool here = q < g.n_seqs && a >= 0 && b >= a && b <= g.n_drafts && r >= a + q && r <= b + q;
+            const unsigned found = __ballot_sync(0xffffffffu, here);
+            if (found) {
+                setting = q0 + __ffs(found) - 1;
+                draft = __shfl_sync(0xffffffffu, r < b + q ? static_cast<int>(r) - q : -1, __ffs(found) - 1);
+            }
+        }
+    }
+    if (lane == 0) {
+        Given v{};
+        v.token = v.draft = -1;
+        if (!VERIFY || setting < g.n_seqs) {
+            v.u = g.uniforms[VERIFY ? 2 * r + 1 : r];
+            const float temperature = g.temperature ? g.temperature[setting] : g.temperature_all;
+            const float min_p = g.min_p ? g.min_p[setting] : g.min_p_all;
+            const float top_p = g.top_p ? g.top_p[setting] : g.top_p_all;
+            v.top_k = g.top_k ? g.top_k[setting] : g.top_k_all;
+            if (VERIFY && draft >= 0) {
+                const long long x = g.drafts[draft];
+                if (x >= 0 && x < g.vocab) {
+                    v.draft = draft;
+                    v.token = static_cast<int>(x);
+                    v.logit = Type<T>::one(g.logits, row_at + x);
+                    v.accept = g.uniforms[2 * r];
+                    v.share = g.draft_probs ? fmaxf(g.draft_probs[static_cast<size_t>(draft) * g.draft_probs_stride + x], 0.f) : 1.f;
+                }
+            }
+            v.state = temperature > 0.f ? kDrawn : kGreedy;
+            // within these temperatures neither part leaves the range of 32 bits; beyond them a weight is one or nothing
+            const double c = v.state == kDrawn ? 1.4426950408889634074 / fmin(fmax(static_cast<double>(temperature), 1e-30), 1e30) : 1.0;
+            v.hi = static_cast<float>(c);
+            v.lo = static_cast<float>(c - v.hi);
+            v.floor_hi = -INFINITY;
+            if (v.state == kDrawn && min_p > 0.f) {
+                const double least = log2(fmin(static_cast<double>(min_p), 1.0));
+                v.floor_hi = static_cast<float>(least);
+                v.floor_lo = static_cast<float>(least - v.floor_hi);
+            }
+            v.top_p = v.state == kGreedy || !(top_p < 1.f) ? 1.f : fmaxf(top_p, 0.f);
+            if (v.top_k < 0 || v.top_k >= g.vocab) v.top_k = 0;
+            if (v.state == kGreedy) v.top_k = 1;
+        }
+        s->given = v;
+    }
+    __syncwarp();
+}
+
+// Whether the draft is accepted, of s->drafted and the sum s->z; if not, what its rest is taken by.  Called by all threads.
+template <typename T>
+__device__ __forceinline__ void judge(const Given &given, Shared *s) {
+    if (threadIdx.x != 0) return;
+    const bool yes = static_cast<double>(given.accept) * static_cast<double>(given.share) * static_cast<double>(s->z) <
+                     static_cast<double>(s->drafted);
+    s->found = yes;
+    if (!yes) s->inverse = RestSum<T>::invert(s->z);
+}
 
 template <typename T, bool VERIFY>
 __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant__ Draw g) {
@@ -501,134 +709,78 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
     const long long r = blockIdx.x / row.blocks;
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (threadIdx.x < 64) s->table[threadIdx.x] = g.table[threadIdx.x];
-    if (VERIFY && threadIdx.x == 0) s->sequence = g.n_seqs;
-    __syncthreads();
     pdl_launch_dependents();
     pdl_wait();  // no global-memory access before this point
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all blocks run: their shared memory may be written to
 
     const size_t row_at = static_cast<size_t>(r) * g.logits_stride;
-    if (row.block == 0) {
-        // ---- whose row it is, and what it is to be drawn by ----
-        if (VERIFY) {
-            for (int q = threadIdx.x; q < g.n_seqs; q += kThreads) {
-                const int a = g.cu_drafts[q], b = g.cu_drafts[q + 1];
-                if (a >= 0 && b >= a && b <= g.n_drafts && r >= a + q && r <= b + q) atomicMin(&s->sequence, q);
-            }
-            __syncthreads();
+    constexpr int P = Row<T>::kPer, kBatch = 4;
+    const int begin = min(row.block * g.slice, g.vocab), n = min(g.slice, g.vocab - begin);
+    const T *from = static_cast<const T *>(g.logits) + row_at + begin;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15) / static_cast<int>(sizeof(T));
+    row.first = begin - off;
+    row.vectors = n > 0 ? (off + n + P - 1) / P : 0;
+    row.rounds = (row.vectors + kThreads - 1) / kThreads;
+    const uint4 *whole = reinterpret_cast<const uint4 *>(from - off);
+    const int full0 = off ? 1 : 0, full1 = (off + n) / P;
+    uint4 v[kBatch];
+    auto request = [&](int k0) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int at = row.vector(k0 + j);
+            v[j] = make_uint4(Type<T>::kMasked, Type<T>::kMasked, Type<T>::kMasked, Type<T>::kMasked);
+            if (k0 + j < row.rounds && at >= full0 && at < full1) v[j] = ldg_nc_v4(whole + at);
         }
-        if (row.warp == 0) {
-            if (row.lane == 0) {
-                const int setting = VERIFY ? s->sequence : static_cast<int>(r);
-                Given v{};
-                v.token = v.draft = -1;
-                if (!VERIFY || setting < g.n_seqs) {
-                    v.u = g.uniforms[VERIFY ? 2 * r + 1 : r];
-                    if (VERIFY && r < g.cu_drafts[setting + 1] + setting) {
-                        const int d = static_cast<int>(r) - setting;
-                        const long long x = g.drafts[d];
-                        if (x >= 0 && x < g.vocab) {
-                            v.draft = d;
-                            v.token = static_cast<int>(x);
-                            v.logit = Type<T>::one(g.logits, row_at + x);
-                            v.accept = g.uniforms[2 * r];
-                            v.share = g.draft_probs ? fmaxf(g.draft_probs[static_cast<size_t>(d) * g.draft_probs_stride + x], 0.f) : 1.f;
-                        }
-                    }
-                    const float temperature = g.temperature ? g.temperature[setting] : g.temperature_all;
-                    v.state = temperature > 0.f ? kDrawn : kGreedy;
-                    v.top_p = g.top_p ? g.top_p[setting] : g.top_p_all;
-                    v.top_k = g.top_k ? g.top_k[setting] : g.top_k_all;
-                    const float min_p = g.min_p ? g.min_p[setting] : g.min_p_all;
-                    // within these temperatures neither part leaves the range of 32 bits; beyond them a weight is one or nothing
-                    const double c = v.state == kDrawn ? 1.4426950408889634074 / fmin(fmax(static_cast<double>(temperature), 1e-30), 1e30) : 1.0;
-                    v.hi = static_cast<float>(c);
-                    v.lo = static_cast<float>(c - v.hi);
-                    v.floor_hi = -INFINITY;
-                    if (v.state == kDrawn && min_p > 0.f) {
-                        const double least = log2(fmin(static_cast<double>(min_p), 1.0));
-                        v.floor_hi = static_cast<float>(least);
-                        v.floor_lo = static_cast<float>(least - v.floor_hi);
-                    }
-                    if (v.state == kGreedy) v.top_k = 1;
-                    if (v.state == kGreedy || !(v.top_p < 1.f)) v.top_p = 1.f;
-                    if (v.top_k < 0 || v.top_k >= g.vocab) v.top_k = 0;
-                    if (v.state == kGreedy && g.vocab == 1) v.top_k = 1;
-                }
-                s->given = v;
-            }
-            __syncwarp();
-            const unsigned *v = reinterpret_cast<const unsigned *>(&s->given);
-            for (int i = row.lane; i < row.blocks * static_cast<int>(sizeof(Given) / 4); i += 32) {
-                const int to = i / static_cast<int>(sizeof(Given) / 4), at = i % static_cast<int>(sizeof(Given) / 4);
-                if (to > 0) st_block_u32(at_block(v + at, to), v[at]);
-            }
-        }
+    };
+    request(0);
+    if (row.block == 0 && row.warp == 0) {
+        give<T, VERIFY>(g, r, row_at, s, row.lane);
+        const unsigned *from_here = reinterpret_cast<const unsigned *>(&s->given);
+        constexpr int kWords = static_cast<int>(sizeof(Given) / 4);
+        for (int i = row.lane; i < (row.blocks - 1) * kWords; i += 32)
+            st_block_u32(at_block(from_here + i % kWords, i / kWords + 1), from_here[i % kWords]);
     }
-
     // ---- the slice into shared memory, and the largest logit ----
     float top = -INFINITY;
-    {
-        constexpr int P = Row<T>::kPer;
-        const int begin = min(row.block * g.slice, g.vocab), n = min(g.slice, g.vocab - begin);
-        const T *from = static_cast<const T *>(g.logits) + row_at + begin;
-        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15) / static_cast<int>(sizeof(T));
-        row.first = begin - off;
-        row.vectors = n > 0 ? (off + n + P - 1) / P : 0;
-        row.rounds = (row.vectors + kThreads - 1) / kThreads;
-        const uint4 *whole = reinterpret_cast<const uint4 *>(from - off);
-        uint4 *data = reinterpret_cast<uint4 *>(smem + sizeof(Shared));
-        const int full0 = off ? 1 : 0, full1 = (off + n) / P;
-        for (int k0 = 0; k0 < row.rounds; k0 += 4) {
-            uint4 v[4];
+    for (int k0 = 0; k0 < row.rounds; k0 += kBatch) {
+        if (k0 > 0) request(k0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int at = row.vector(k0 + j);
-                v[j] = make_uint4(Type<T>::kMasked, Type<T>::kMasked, Type<T>::kMasked, Type<T>::kMasked);
-                if (k0 + j < row.rounds && at >= full0 && at < full1) v[j] = ldg_nc_v4(whole + at);
+        for (int j = 0; j < kBatch; ++j) {
+            const int at = row.vector(k0 + j);
+            if (k0 + j >= row.rounds || at >= row.vectors) break;
+            if (at < full0 || at >= full1) {  // the slice's ends: element by element
+                alignas(16) T part[P];
+                *reinterpret_cast<uint4 *>(part) = v[j];
+                for (int e = 0; e < P; ++e)
+                    if (at * P + e >= off && at * P + e < off + n) part[e] = from[at * P + e - off];
+                v[j] = *reinterpret_cast<uint4 *>(part);
             }
+            const_cast<uint4 *>(row.data)[at] = v[j];
+            float x[P];
+            Type<T>::spread(v[j], x);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int at = row.vector(k0 + j);
-                if (k0 + j >= row.rounds || at >= row.vectors) break;
-                if (at < full0 || at >= full1) {  // the slice's ends: element by element
-                    alignas(16) T part[P];
-                    *reinterpret_cast<uint4 *>(part) = v[j];
-                    for (int e = 0; e < P; ++e)
-                        if (at * P + e >= off && at * P + e < off + n) part[e] = from[at * P + e - off];
-                    v[j] = *reinterpret_cast<uint4 *>(part);
-                }
-                data[at] = v[j];
-                float x[P];
-                Type<T>::spread(v[j], x);
-#pragma unroll
-                for (int e = 0; e < P; ++e) top = fmaxf(top, x[e]);
-            }
+            for (int e = 0; e < P; ++e) top = fmaxf(top, x[e]);
         }
     }
+    const float mine = top;  // this thread's
+    unsigned least;
     {
-        const unsigned m = __reduce_max_sync(0xffffffffu, float_order_code(top));
-        if (row.lane == 0) s->warp[row.warp] = m;
-        __syncthreads();
-        u64 most = 0;
-        for (int w = 0; w < kWarps; ++w) most = max(most, s->warp[w]);
-        row.exchange(most);
-        most = 0;
-        for (int b = 0; b < row.blocks; ++b) most = max(most, s->slot[row.parity][b]);
-        const unsigned c = static_cast<unsigned>(most);
-        top = __uint_as_float(c & 0x80000000u ? c & 0x7fffffffu : ~c);
+        unsigned most;
+        row.exchange_range(mine > -INFINITY ? float_order_code(mine) : 0xffffffffu, float_order_code(mine), &least, &most);
+        top = value_of(static_cast<u64>(most) << 32);
     }
 
     // ---- what is left of the row ----
-    const Given &given = s->given;  // here since the exchange of the maxima
+    const Given &given = s->given;  // here since the exchange
     if (given.state == kNotDrawn) return;  // a row behind the sequences: left as it is
     long long *id = g.ids + r;
+    const bool probs = !VERIFY && g.probs;
+    float *probs_to = probs ? g.probs + r * g.probs_stride : nullptr;
+    const int end = begin + max(n, 0);
     if (top == -INFINITY) {
         if (row.block == 0 && threadIdx.x == 0) *id = -1;
-        if (!VERIFY && g.probs) {
-            float *to = g.probs + r * g.probs_stride;
-            for (int i = row.block * g.slice + threadIdx.x; i < min((row.block + 1) * g.slice, g.vocab); i += kThreads) to[i] = 0.f;
-        }
+        if (probs)
+            for (int i = begin + threadIdx.x; i < end; i += kThreads) probs_to[i] = 0.f;
         return;
     }
     const Weights<T> weights(top, given, s->table);
@@ -638,27 +790,142 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
         u64 before;
         return row.exchange_sum(row.sum(mass), &before);
     };
-    if (given.top_k > 0) row.template select<false>(&kept, weights, given.top_k, -3.402823466e38f);
-    if (given.top_p < 1.f)
-        row.template select<true>(&kept, weights, max(part_of(total(), fmaxf(given.top_p, 0.f), true), 1ull), -3.402823466e38f);
-    kept.floor_hi = given.floor_hi;
-    kept.floor_lo = given.floor_lo;
+    const int top_k = given.top_k;
+    const bool by_p = given.top_p < 1.f, by_floor = given.floor_hi > -INFINITY;
     u64 z = 0;
-    if (VERIFY || g.probs) z = total();
+    float cut = kLowest;  // a logit below which none of the kept tokens lies
+    if (by_floor && !(top_k > 0 && by_p)) cut = fmaxf(cut, top + (given.floor_hi - 0.01f) / weights.hi - 4.8e-7f * fabsf(top));
+    bool finish = false;
+    int candidates = 0;
+    auto list_all = [&] {
+        candidates = row.gather([&](float l, int) { return l >= cut; });
+        finish = candidates <= kList;
+    };
+    auto drop_light = [&] { return max(part_of(z, given.top_p, true), 1ull); };  // what the nucleus has to weigh, of the sum z
+    if (top_k > 0) {
+        // The top_k-th largest of the threads' maxima is a bound from below.
+        bool bounded = g.vocab <= kList;
+        if (top < 3.4e38f) {
+            row.histogram ^= 1;
+            s->count[row.histogram][threadIdx.x] = 0;
+            __syncthreads();
+            const float range = top - value_of(static_cast<u64>(least) << 32), scale = range > 0.f && range < 3e38f ? 511.9f / range : 0.f;
+            if (mine > -INFINITY) atomicAdd(&s->count[row.histogram][min(static_cast<int>((top - mine) * scale), kBins - 1)], 1u);
+            const int bin = row.template reached<false>(top_k);
+            if (bin < kBins) {
+                cut = fmaxf(cut, top - (static_cast<float>(bin) + 1.001f) * (range / 511.9f) - 4.8e-7f * fabsf(top));
+                bounded = true;
+            }
+        }
+        if (bounded) list_all();
+    } else if (by_p) {
+        z = total();
+        // Tokens lighter than an even share of what may be dropped are dropped, all together.
+        const float share = (1.f - given.top_p) * static_cast<float>(z) / (17592186044416.f * static_cast<float>(g.vocab));
+        if (share > 1e-30f) cut = fmaxf(cut, top + (log2f(share) - 0.01f) / weights.hi - 4.8e-7f * fabsf(top));
+        candidates = row.template select<true, true>(&kept, weights, drop_light(), cut);
+        finish = candidates > 0;
+    } else if (by_floor) {
+        list_all();
+    } else if (VERIFY || probs) {
+        z = total();
+    }
+    if (finish) {
+        // ---- few tokens: the first block goes on with them alone ----
+        if (row.block == 0) {
+            const u64 key = row.sorted_list(candidates);
+            if (!probs) cluster_barrier();  // the others leave
+            const int i = 0xffffffffu - static_cast<unsigned>(key), rank = threadIdx.x;
+            const float l = value_of(key);
+            bool stays = key != 0 && (top_k == 0 || rank < top_k);
+            float p, e;
+            weights.exponent(l, &p, &e);
+            u64 w = stays ? weights.weight(l) : 0;
+            if (by_p) {
+                const u64 upto = row.block_prefix(w);
+                __syncthreads();
+                if (threadIdx.x == kThreads - 1) s->z = upto;
+                __syncthreads();
+                if (top_k > 0) z = s->z;  // else that of all tokens
+                stays = stays && upto - w < drop_light();
+            }
+            kept.floor_hi = given.floor_hi;
+            kept.floor_lo = given.floor_lo;
+            stays = stays && kept.weight(p, e);
+            if (!stays) w = 0;
+            // the kept ones come first: their number, and their sum
+            const int left = __syncthreads_count(stays);
+            if (VERIFY || probs) {
+                const u64 upto = row.block_prefix(w);
+                if (threadIdx.x == kThreads - 1) s->z = upto;
+                if (VERIFY && threadIdx.x == 0) s->drafted = 0;
+                if (rank == left - 1) s->last = key;
+                __syncthreads();
+            }
+            if (probs) {
+                if (static_cast<int>(threadIdx.x) < row.blocks && threadIdx.x > 0) {
+                    st_block_u64(at_block(&s->last, threadIdx.x), s->last);
+                    st_block_u64(at_block(&s->z, threadIdx.x), s->z);
+                }
+                cluster_barrier();
+            }
+            u64 weight = w;
+            if (VERIFY && given.token >= 0) {
+                if (stays && i == given.token) s->drafted = w;
+                __syncthreads();
+                judge<T>(given, s);
+                __syncthreads();
+                if (s->found) {
+                    if (threadIdx.x == 0) *id = kAccepted;
+                    return;
+                }
+                const float *q = g.draft_probs ? g.draft_probs + static_cast<size_t>(given.draft) * g.draft_probs_stride : nullptr;
+                const RestSum<T> rest(weights, kept, q, given.token, s->z, s->inverse);
+                const u64 over = stays ? rest.rest(w, i) >> 18 : 0;  // in 2^-44
+                if (__syncthreads_or(over != 0)) weight = over;
+            }
+            // in index order, with the weights of 45 bits behind the indices
+            const u64 by_index = row.sort(stays ? static_cast<u64>(kMaxVocab - 1 - i) << 45 | weight : 0, left);
+            weight = by_index & ((1ull << 45) - 1);
+            const u64 upto = row.block_prefix(weight);
+            if (threadIdx.x == kThreads - 1) s->z = upto;
+            __syncthreads();
+            const u64 target = place_of(given.u, s->z);
+            if (upto > target && upto - weight <= target) *id = kMaxVocab - 1 - static_cast<int>(by_index >> 45);
+        } else {
+            cluster_barrier();
+        }
+        if (!probs) return;
+        kept.value = value_of(s->last);
+        kept.index = 0xffffffffu - static_cast<unsigned>(s->last);
+        z = s->z;
+    }
+    if (!finish) {
+        if (top_k > 0) {
+            row.template select<false>(&kept, weights, top_k, cut);
+            if (by_p) {
+                z = total();
+                row.template select<true>(&kept, weights, drop_light(), cut);
+            }
+        }
+        kept.floor_hi = given.floor_hi;
+        kept.floor_lo = given.floor_lo;
+        if ((VERIFY || probs) && (top_k > 0 || by_p || by_floor)) z = total();
+    }
 
     // ---- the distribution ----
-    if (!VERIFY && g.probs) {
-        float *to = g.probs + r * g.probs_stride;
+    if (probs) {
         const float scale = 1.f / static_cast<float>(z);
         row.each([&](float l, int i) {
-            if (i < row.block * g.slice || i >= min((row.block + 1) * g.slice, g.vocab)) return;
+            if (i < begin || i >= end) return;
             float p, e, v = 0.f;
             if (kept.order(l, i)) {
                 weights.exponent(l, &p, &e);
                 if (kept.weight(p, e)) v = weights.heavy(p) ? static_cast<float>(weights.heavy_weight(p, e)) : weights.light_weight(p, e);
             }
-            to[i] = v * scale;
+            probs_to[i] = v * scale;
         });
+        if (finish) return;
     }
 
     // ---- the token ----
@@ -671,14 +938,14 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
                 weights.exponent(given.logit, &p, &e);
                 if (kept.weight(p, e)) w = weights.weight(given.logit);
             }
-            const bool yes = static_cast<double>(given.accept) * static_cast<double>(given.share) * static_cast<double>(z) < static_cast<double>(w);
-            if (yes && row.block == 0) *id = kAccepted;
-            s->found = yes;
-            if (!yes) s->inverse = RestSum<T>::invert(z);
+            s->drafted = w;
+            s->z = z;
         }
         __syncthreads();
-        done = s->found;
+        judge<T>(given, s);
         __syncthreads();
+        done = s->found;
+        if (done && row.block == 0 && threadIdx.x == 0) *id = kAccepted;
         const float *q = g.draft_probs ? g.draft_probs + static_cast<size_t>(given.draft) * g.draft_probs_stride : nullptr;
         if (!done) done = row.pick([&] { return RestSum<T>(weights, kept, q, given.token, z, s->inverse); }, given.u, id);
     }
