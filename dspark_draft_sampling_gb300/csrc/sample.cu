@@ -190,10 +190,10 @@ struct Type<__half> {
 // The weights of a row's tokens.
 template <typename T>
 struct Weights {
-    float top, hi, lo, least;   // m; log2(e) / T in two parts; the difference of logits whose weight is nothing
+    float top, hi, lo, least;   // m; log2(e) / T in two parts; a difference of logits whose weight is 0
     const uint2 *table;
 
-    __device__ __forceinline__ Weights(float m, const Given &g, const uint2 *t) : top(m), hi(g.hi), lo(g.lo), least(-100.f / g.hi), table(t) {}
+    __device__ __forceinline__ Weights(float m, const Given &g, const uint2 *t) : top(m), hi(g.hi), lo(g.lo), least(-200.f / g.hi), table(t) {}
     // y of a logit that is not NaN, as two parts
     __device__ __forceinline__ void exponent(float l, float *p, float *e) const {
         const float diff = l - top, d = l >= top ? 0.f : fmaxf(diff, least);
@@ -224,22 +224,62 @@ struct Weights {
         const float w = fast_exp2(p) * 17592186044416.f;
         return __fmaf_rn(w * 0.6931471806f, e, w);
     }
+    // Light weights in whole numbers. The fast exponential falls short by 5.1e-8 on average (rms 5.9e-8, at most 1.42e-7, over -40..-8 on
+    // this GPU), which would shift light tokens against heavy ones: 2^-24 is added back.
+    __device__ __forceinline__ static u64 whole(float c) {
+        const u64 v = __float2ull_rn(c);
+        return v + (v >> 24);
+    }
     __device__ __forceinline__ u64 weight(float l) const {
         float p, e;
         exponent(l, &p, &e);
-        return heavy(p) ? heavy_weight(p, e) : __float2ull_rn(light_weight(p, e));
+        return heavy(p) ? heavy_weight(p, e) : whole(light_weight(p, e));
     }
 };
 
-// Which tokens are left: those before and with the last one of the order, and of at least a weight.
+// Which tokens are left: those before and with the last one of the order.
 struct Kept {
     float value;  // the last token's logit, and the last index of its ties that stays
     int index;
-    float floor_hi, floor_lo;  // log2 of the least weight
 
     __device__ __forceinline__ bool order(float l, int i) const { return l > value || (l == value && i <= index); }
-    __device__ __forceinline__ bool weight(float p, float e) const { return (p - floor_hi) + (e - floor_lo) >= 0.f; }
 };
+
+// The weights of a vector's tokens in 32 bits, two at a time, where all of them are light: false where one is not, or is as large as the
+// last kept one, of which indices decide. 8 instructions a token (the general form takes 40 and more), and as many cycles of the exponential's unit.
+template <typename T>
+__device__ __forceinline__ bool light_weights(const Weights<T> &w, const Kept &kept, float (&x)[Type<T>::kPer]) {
+    constexpr int P = Type<T>::kPer;
+    bool odd = !(w.top < 3.4e38f);
+    if (kept.value > -INFINITY) {
+#pragma unroll
+        for (int u = 0; u < P; ++u) {
+            odd = odd || x[u] == kept.value;
+            x[u] = x[u] >= kept.value ? x[u] : -INFINITY;
+        }
+    }
+    u64 d[P / 2], p[P / 2];
+    float most = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < P / 2; ++u) {
+        float a, b;
+        split_f32(add_f32x2(pair_f32(x[2 * u], x[2 * u + 1]), pair_f32(-w.top, -w.top)), &a, &b);
+        d[u] = pair_f32(fmaxf(a, w.least), fmaxf(b, w.least));  // also from NaN
+        p[u] = mul_f32x2(d[u], pair_f32(w.hi, w.hi));
+        split_f32(p[u], &a, &b);
+        most = fmaxf(most, fmaxf(a, b));
+    }
+    if (odd || w.heavy(most)) return false;
+#pragma unroll
+    for (int u = 0; u < P / 2; ++u) {
+        float a, b;
+        split_f32(p[u], &a, &b);
+        const u64 e = fma_f32x2(d[u], pair_f32(-w.lo, -w.lo), fma_f32x2(d[u], pair_f32(-w.hi, -w.hi), p[u]));  // what p lacks, negative
+        const u64 v = pair_f32(fast_exp2(a), fast_exp2(b));
+        split_f32(fma_f32x2(mul_f32x2(v, pair_f32(-0.6931471806f, -0.6931471806f)), e, v), &x[2 * u], &x[2 * u + 1]);
+    }
+    return true;
+}
 
 // Sums over a vector's tokens, in index order: the sum up to a token never falls, and the sum over the vector is the same whenever it is
 // taken.
@@ -254,13 +294,35 @@ struct MassSum {
         if (!kept.order(l, i)) return;
         float p, e;
         w.exponent(l, &p, &e);
-        if (!kept.weight(p, e)) return;
         if (w.heavy(p)) h += w.heavy_weight(p, e);
         else c += w.light_weight(p, e);
     }
-    __device__ __forceinline__ u64 sum() const { return h + __float2ull_rn(c); }
+    __device__ __forceinline__ u64 sum() const { return h + w.whole(c); }
+    __device__ __forceinline__ u64 vector(uint4 v, int first) {
+        constexpr int P = Type<T>::kPer;
+        float x[P];
+        Type<T>::spread(v, x);
+        if (light_weights(w, kept, x)) {
+            u64 s = pair_f32(x[0], x[1]);
+#pragma unroll
+            for (int u = 1; u < P / 2; ++u) s = add_f32x2(s, pair_f32(x[2 * u], x[2 * u + 1]));
+            float a, b;
+            split_f32(s, &a, &b);
+            c = (a + b) * 17592186044416.f;
+        } else {
+            Type<T>::spread(v, x);
+#pragma unroll 1
+            for (int u = 0; u < P; ++u) {
+                add(x[0], first + u);
+#pragma unroll
+                for (int k = 0; k + 1 < P; ++k) x[k] = x[k + 1];
+            }
+        }
+        return sum();
+    }
 };
 
+template <typename T>
 struct TieSum {
     float value;
     const Kept &kept;
@@ -268,6 +330,13 @@ struct TieSum {
     __device__ __forceinline__ TieSum(float v, const Kept &b) : value(v), kept(b) {}
     __device__ __forceinline__ void add(float l, int i) { n += l == value && kept.order(l, i) ? 1 : 0; }
     __device__ __forceinline__ u64 sum() const { return n; }
+    __device__ __forceinline__ u64 vector(uint4 v, int first) {
+        float x[Type<T>::kPer];
+        Type<T>::spread(v, x);
+#pragma unroll
+        for (int u = 0; u < Type<T>::kPer; ++u) add(x[u], first + u);
+        return n;
+    }
 };
 
 // Leading zeros of a row's sum: 0 to 19, as 2^44 <= z.
@@ -290,24 +359,38 @@ struct RestSum {
     }
     __device__ __forceinline__ RestSum(const Weights<T> &a, const Kept &b, const float *draft_probs, int x, u64 z, u64 inverted)
         : w(a), kept(b), q(draft_probs), draft(x), shift(20 - lead_of(z)), inverse(inverted) {}
-    __device__ __forceinline__ u64 rest(u64 weight, int i) const {
+    __device__ __forceinline__ u64 rest(u64 weight, int i, float share) const {
         const u64 mine = __umul64hi(weight << 19, inverse) >> shift;
         u64 theirs = i == draft ? ~0ull : 0ull;
         if (q) {
-            const unsigned bits = __float_as_uint(fminf(fmaxf(q[i], 0.f), 1.f));
+            const unsigned bits = __float_as_uint(fminf(fmaxf(share, 0.f), 1.f));
             const int up = static_cast<int>(bits >> 23) - 88;  // 2^62 of a 24-bit significand
             const u64 s = (bits & 0x7fffffu) | 0x800000u;
             theirs = up >= 0 ? s << up : up > -24 ? s >> -up : 0;
         }
         return mine > theirs ? mine - theirs : 0;
     }
+    __device__ __forceinline__ void add(float l, int i, float share) {
+        if (kept.order(l, i)) n += rest(w.weight(l), i, share);
+    }
     __device__ __forceinline__ void add(float l, int i) {
-        if (!kept.order(l, i)) return;
-        float p, e;
-        w.exponent(l, &p, &e);
-        if (kept.weight(p, e)) n += rest(w.heavy(p) ? w.heavy_weight(p, e) : __float2ull_rn(w.light_weight(p, e)), i);
+        if (kept.order(l, i)) n += rest(w.weight(l), i, q ? q[i] : 0.f);
     }
     __device__ __forceinline__ u64 sum() const { return n; }
+    __device__ __forceinline__ u64 vector(uint4 v, int first) {
+        constexpr int P = Type<T>::kPer;
+        float x[P], share[P];
+        Type<T>::spread(v, x);
+        bool some = false;
+#pragma unroll
+        for (int u = 0; u < P; ++u) some = some || x[u] >= kept.value;
+        if (!some) return 0;
+#pragma unroll
+        for (int u = 0; u < P; ++u) share[u] = q && kept.order(x[u], first + u) ? q[first + u] : 0.f;
+#pragma unroll
+        for (int u = 0; u < P; ++u) add(x[u], first + u, share[u]);
+        return n;
+    }
 };
 
 // A row's slice in this block, and the cluster around it.
@@ -371,41 +454,46 @@ struct Row {
     template <typename M>
     __device__ __forceinline__ u64 vector_sum(M make, int v) const {
         auto a = make();
-        if (v < vectors) {
-            float x[kPer];
-            Type<T>::spread(data[v], x);
-#pragma unroll
-            for (int u = 0; u < kPer; ++u) a.add(x[u], first + v * kPer + u);
-        }
-        return a.sum();
+        return v < vectors ? a.vector(data[v], first + v * kPer) : 0;
     }
     // The first token at which the sum over the slice, taken just before by sum(), exceeds `target` (less than it): its index, in s->found.
+    // Called by the whole block. The stretch of the warp that it falls to is looked at by all warps, a round each.
     template <typename M>
     __device__ __forceinline__ void find(M make, u64 target) {
         u64 before = 0;
         int w = 0;
         while (w < kWarps - 1 && before + s->warp[w] <= target) before += s->warp[w++];
-        if (w != warp) return;
-#pragma unroll 1
-        for (int k = 0; k < rounds; ++k) {
-            const int v = vector(k);
-            const u64 mine = vector_sum(make, v), upto = before + warp_prefix(mine, lane);
-            const unsigned past = __ballot_sync(0xffffffffu, upto > target);
-            if (past == 0) {
-                before = __shfl_sync(0xffffffffu, upto, 31);
+        for (int k0 = 0; k0 < rounds; k0 += kWarps) {
+            const int k = k0 + warp, v = k < rounds ? (w * rounds + k) * 32 + lane : vectors;
+            const u64 mine = vector_sum(make, v), all = warp_sum(mine);
+            __syncthreads();
+            if (lane == 0) s->scan[1][warp] = all;
+            __syncthreads();
+            int j = 0;  // the round among these
+            u64 upto = before;
+            while (j < kWarps - 1 && upto + s->scan[1][j] <= target) upto += s->scan[1][j++];
+            const bool last = k0 + kWarps >= rounds;
+            if (upto + s->scan[1][j] <= target && !last) {
+                before = upto + s->scan[1][j];
                 continue;
             }
-            if (lane == __ffs(past) - 1) {
-                auto a = make();
-                float x[kPer];
-                Type<T>::spread(data[v], x);
-                int u = 0;
-                for (; u < kPer; ++u) {
-                    a.add(x[u], first + v * kPer + u);
-                    if (upto - mine + a.sum() > target) break;
-                }
-                s->found = first + v * kPer + u;
-            }
+            if (warp != j) return;
+            const u64 prefix = upto + warp_prefix(mine, lane);
+            const unsigned past = __ballot_sync(0xffffffffu, prefix > target);
+            if (past == 0) return;  // not the case, as the sums are the same ones
+            const int owner = __ffs(past) - 1;
+            upto = __shfl_sync(0xffffffffu, prefix - mine, owner);
+            const int at = first + __shfl_sync(0xffffffffu, v, owner) * kPer;
+            // a lane to each of its tokens; their sum may be a rounding less than the vector's: then the last that weighs anything
+            float x[kPer];
+            Type<T>::spread(data[__shfl_sync(0xffffffffu, v, owner)], x);
+            auto a = make();
+#pragma unroll
+            for (int u = 0; u < kPer; ++u)
+                if (lane == u) a.add(x[u], at + u);
+            const u64 one = a.sum(), here_upto = upto + warp_prefix(one, lane);
+            const unsigned any = __ballot_sync(0xffffffffu, one > 0), here = any & __ballot_sync(0xffffffffu, here_upto > target);
+            if (lane == 0) s->found = at + (here ? __ffs(here) - 1 : any ? 31 - __clz(any) : 0);
             return;
         }
     }
@@ -569,7 +657,7 @@ struct Row {
             const u64 each_one = w.weight(value);
             left = (left + each_one - 1) / each_one;
         }
-        auto ties = [&] { return TieSum(value, prior); };
+        auto ties = [&] { return TieSum<T>(value, prior); };
         const u64 mine = sum(ties);
         u64 before;
         const u64 all = exchange_sum(mine, &before);
@@ -584,6 +672,25 @@ struct Row {
         for (int b = 0; b < blocks; ++b) index += s->slot[parity][b];
         kept->index = static_cast<int>(index);
         return 0;
+    }
+    // Narrows `kept` to tokens of at least min_p. Weights never fall with the logits, so there is a largest one that is too small: each
+    // warp looks for its code, in 31 places at a time.
+    __device__ __forceinline__ void drop_below(Kept *kept, const Weights<T> &w, const Given &given) const {
+        unsigned low = float_order_code(kLowest), high = float_order_code(w.top);  // the first may be too small, the last is not
+        auto stays = [&](unsigned c) {
+            float p, e;
+            w.exponent(value_of(static_cast<u64>(c) << 32), &p, &e);
+            return (p - given.floor_hi) + (e - given.floor_lo) >= 0.f;
+        };
+        if (stays(low)) return;
+        while (high - low > 1) {
+            const unsigned step = (high - low + 31) / 32, at = min(low + (lane + 1) * step, high);
+            const int first = __ffs(__ballot_sync(0xffffffffu, at == high || stays(at))) - 1;
+            high = __shfl_sync(0xffffffffu, at, first);
+            low += first * step;
+        }
+        const float value = value_of(static_cast<u64>(low) << 32);
+        if (value > kept->value) *kept = {value, -1};
     }
     // The least and the largest of the cluster's codes.
     __device__ __forceinline__ void exchange_range(unsigned least, unsigned most, unsigned *c0, unsigned *c1) {
@@ -714,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all blocks run: their shared memory may be written to
 
     const size_t row_at = static_cast<size_t>(r) * g.logits_stride;
-    constexpr int P = Row<T>::kPer, kBatch = 4;
+    constexpr int P = Row<T>::kPer, kBatch = 8;
     const int begin = min(row.block * g.slice, g.vocab), n = min(g.slice, g.vocab - begin);
     const T *from = static_cast<const T *>(g.logits) + row_at + begin;
     const int off = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15) / static_cast<int>(sizeof(T));
@@ -784,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
         return;
     }
     const Weights<T> weights(top, given, s->table);
-    Kept kept{-INFINITY, -1, -INFINITY, 0.f};
+    Kept kept{-INFINITY, -1};
     auto mass = [&] { return MassSum<T>(weights, kept); };
     auto total = [&] {
         u64 before;
@@ -849,9 +956,7 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
                 if (top_k > 0) z = s->z;  // else that of all tokens
                 stays = stays && upto - w < drop_light();
             }
-            kept.floor_hi = given.floor_hi;
-            kept.floor_lo = given.floor_lo;
-            stays = stays && kept.weight(p, e);
+            stays = stays && (p - given.floor_hi) + (e - given.floor_lo) >= 0.f;
             if (!stays) w = 0;
             // the kept ones come first: their number, and their sum
             const int left = __syncthreads_count(stays);
@@ -881,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
                 }
                 const float *q = g.draft_probs ? g.draft_probs + static_cast<size_t>(given.draft) * g.draft_probs_stride : nullptr;
                 const RestSum<T> rest(weights, kept, q, given.token, s->z, s->inverse);
-                const u64 over = stays ? rest.rest(w, i) >> 18 : 0;  // in 2^-44
+                const u64 over = stays ? rest.rest(w, i, q ? q[i] : 0.f) >> 18 : 0;  // in 2^-44
                 if (__syncthreads_or(over != 0)) weight = over;
             }
             // in index order, with the weights of 45 bits behind the indices
@@ -908,23 +1013,48 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
                 row.template select<true>(&kept, weights, drop_light(), cut);
             }
         }
-        kept.floor_hi = given.floor_hi;
-        kept.floor_lo = given.floor_lo;
+        if (by_floor) row.drop_below(&kept, weights, given);
         if ((VERIFY || probs) && (top_k > 0 || by_p || by_floor)) z = total();
     }
 
     // ---- the distribution ----
     if (probs) {
         const float scale = 1.f / static_cast<float>(z);
-        row.each([&](float l, int i) {
-            if (i < begin || i >= end) return;
-            float p, e, v = 0.f;
-            if (kept.order(l, i)) {
-                weights.exponent(l, &p, &e);
-                if (kept.weight(p, e)) v = weights.heavy(p) ? static_cast<float>(weights.heavy_weight(p, e)) : weights.light_weight(p, e);
+        const bool wide = (reinterpret_cast<uintptr_t>(probs_to + row.first) & 15) == 0;
+#pragma unroll 1
+        for (int k = 0; k < row.rounds; ++k) {
+            const int at = row.vector(k), i0 = row.first + at * P;
+            if (at >= row.vectors) break;
+            float x[P], y[P];
+            Type<T>::spread(row.data[at], x);
+            bool some = false;
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                y[e] = x[e];
+                some = some || x[e] >= kept.value;
             }
-            probs_to[i] = v * scale;
-        });
+            if (some && light_weights(weights, kept, y)) {
+#pragma unroll
+                for (int e = 0; e < P; ++e) y[e] *= 17592186044416.f * scale;
+            } else {
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    y[e] = 0.f;
+                    if (!some || !kept.order(x[e], i0 + e)) continue;
+                    float p, rest;
+                    weights.exponent(x[e], &p, &rest);
+                    y[e] = (weights.heavy(p) ? static_cast<float>(weights.heavy_weight(p, rest)) : weights.light_weight(p, rest)) * scale;
+                }
+            }
+            if (wide && i0 >= begin && i0 + P <= end) {
+#pragma unroll
+                for (int e = 0; e < P; e += 4) __stcs(reinterpret_cast<float4 *>(probs_to + i0 + e), make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < P; ++e)
+                    if (i0 + e >= begin && i0 + e < end) probs_to[i0 + e] = y[e];
+            }
+        }
         if (finish) return;
     }
 
@@ -933,11 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
     if (VERIFY && given.token >= 0) {
         if (threadIdx.x == 0) {
             u64 w = 0;
-            if (kept.order(given.logit, given.token)) {
-                float p, e;
-                weights.exponent(given.logit, &p, &e);
-                if (kept.weight(p, e)) w = weights.weight(given.logit);
-            }
+            if (kept.order(given.logit, given.token)) w = weights.weight(given.logit);
             s->drafted = w;
             s->z = z;
         }
@@ -950,7 +1076,6 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
         if (!done) done = row.pick([&] { return RestSum<T>(weights, kept, q, given.token, z, s->inverse); }, given.u, id);
     }
     if (!done) row.pick(mass, given.u, id);
-    cluster_barrier();  // no block leaves while another may read its shared memory
 }
 
 // Each sequence's accepted drafts, the token drawn at its first row that did not accept, and -1 behind it.  A warp to a sequence.
@@ -1037,6 +1162,18 @@ dspark_status check(const char *who, const void *logits, int dtype, int rows, in
     return DSPARK_OK;
 }
 
+struct Table {
+    uint2 entry[64];
+    Table() {
+        for (int j = 0; j < 64; ++j) {
+            const double x = std::exp2(28.0 + j / 64.0);
+            const float as_float = static_cast<float>(x);
+            entry[j].x = static_cast<unsigned>(std::llrint(x));
+            std::memcpy(&entry[j].y, &as_float, 4);
+        }
+    }
+};
+
 template <bool VERIFY>
 dspark_status run(Draw g, int dtype, const dspark_filters &f, cudaStream_t stream) {
     g.temperature = f.temperature;
@@ -1047,12 +1184,8 @@ dspark_status run(Draw g, int dtype, const dspark_filters &f, cudaStream_t strea
     g.top_p_all = f.top_p_all;
     g.min_p_all = f.min_p_all;
     g.top_k_all = f.top_k_all;
-    for (int j = 0; j < 64; ++j) {
-        const double x = std::exp2(28.0 + j / 64.0);
-        const float as_float = static_cast<float>(x);
-        g.table[j].x = static_cast<unsigned>(std::llrint(x));
-        std::memcpy(&g.table[j].y, &as_float, 4);
-    }
+    static const Table table;
+    std::memcpy(g.table, table.entry, sizeof g.table);
     int sms = 0;
     const dspark_status st = static_cast<dspark_status>(current_sm_count(&sms));
     if (st != DSPARK_OK) return st;
