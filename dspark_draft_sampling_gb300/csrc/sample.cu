@@ -148,20 +148,34 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// 16 bytes of logits of a type.
 template <typename T>
 struct Type;
 template <>
 struct Type<float> {
     static constexpr int kPer = 4;
+    static constexpr unsigned kMasked = 0xff800000u;  // -infinity
     static __device__ __forceinline__ void spread(uint4 v, float *x) {
         x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
     }
     static __device__ __forceinline__ float one(const void *p, long long i) { return static_cast<const float *>(p)[i]; }
-    static constexpr unsigned kMasked = 0xff800000u;
+    // The larger ones of two vectors, and the largest of one, NaN left aside.
+    static __device__ __forceinline__ uint4 larger(uint4 a, uint4 b) {
+        auto most = [](unsigned x, unsigned y) { return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y))); };
+        return make_uint4(most(a.x, b.x), most(a.y, b.y), most(a.z, b.z), most(a.w, b.w));
+    }
+    static __device__ __forceinline__ float largest(uint4 v) {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+    // One value throughout, rounded down; that value; about the lowest one.
+    static __device__ __forceinline__ unsigned down(float x) { return __float_as_uint(x); }
+    static __device__ __forceinline__ float low(unsigned v) { return __uint_as_float(v); }
+    static constexpr float kLeast = -3.0e38f;
 };
 template <>
 struct Type<__nv_bfloat16> {
     static constexpr int kPer = 8;
+    static constexpr unsigned kMasked = 0xff80ff80u;
     static __device__ __forceinline__ void spread(uint4 v, float *x) {
         const unsigned w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -170,11 +184,27 @@ struct Type<__nv_bfloat16> {
     static __device__ __forceinline__ float one(const void *p, long long i) {
         return __uint_as_float(static_cast<unsigned>(static_cast<const unsigned short *>(p)[i]) << 16);
     }
-    static constexpr unsigned kMasked = 0xff80ff80u;
+    static __device__ __forceinline__ unsigned most(unsigned a, unsigned b) {
+        unsigned r;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint4 larger(uint4 a, uint4 b) { return make_uint4(most(a.x, b.x), most(a.y, b.y), most(a.z, b.z), most(a.w, b.w)); }
+    static __device__ __forceinline__ float largest(uint4 v) {
+        const unsigned m = most(most(v.x, v.y), most(v.z, v.w));
+        return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
+    static __device__ __forceinline__ unsigned down(float x) {
+        const unsigned b = __float_as_uint(x), up = (b & 0x80000000u ? b + 0xffffu : b) >> 16;
+        return up | up << 16;
+    }
+    static __device__ __forceinline__ float low(unsigned v) { return __uint_as_float(v << 16); }
+    static constexpr float kLeast = -3.0e38f;
 };
 template <>
 struct Type<__half> {
     static constexpr int kPer = 8;
+    static constexpr unsigned kMasked = 0xfc00fc00u;
     static __device__ __forceinline__ void spread(uint4 v, float *x) {
         const unsigned w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -184,16 +214,38 @@ struct Type<__half> {
         }
     }
     static __device__ __forceinline__ float one(const void *p, long long i) { return __half2float(static_cast<const __half *>(p)[i]); }
-    static constexpr unsigned kMasked = 0xfc00fc00u;
+    static __device__ __forceinline__ unsigned most(unsigned a, unsigned b) {
+        unsigned r;
+        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint4 larger(uint4 a, uint4 b) { return make_uint4(most(a.x, b.x), most(a.y, b.y), most(a.z, b.z), most(a.w, b.w)); }
+    static __device__ __forceinline__ float largest(uint4 v) {
+        const unsigned m = most(most(v.x, v.y), most(v.z, v.w));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&m));
+        return fmaxf(f.x, f.y);
+    }
+    static __device__ __forceinline__ unsigned down(float x) {
+        const unsigned h = __half_as_ushort(__float2half_rd(x));
+        return h | h << 16;
+    }
+    static __device__ __forceinline__ float low(unsigned v) { return __half2float(__ushort_as_half(static_cast<unsigned short>(v))); }
+    static constexpr float kLeast = -6.0e4f;
 };
 
 // The weights of a row's tokens.
 template <typename T>
 struct Weights {
     float top, hi, lo, least;   // m; log2(e) / T in two parts; a difference of logits whose weight is 0
+    unsigned clamp;             // a logit of that difference or a larger one, in the logits' type
+    bool simple;                // whether there is one that weighs nothing and leaves all numbers finite
     const uint2 *table;
 
-    __device__ __forceinline__ Weights(float m, const Given &g, const uint2 *t) : top(m), hi(g.hi), lo(g.lo), least(-200.f / g.hi), table(t) {}
+    __device__ __forceinline__ Weights(float m, const Given &g, const uint2 *t) : top(m), hi(g.hi), lo(g.lo), least(-200.f / g.hi), table(t) {
+        clamp = Type<T>::down(top + least);
+        const float y = (Type<T>::low(clamp) - top) * hi;
+        simple = y <= -100.f && y > -1.0e4f && top + least > Type<T>::kLeast && top < 1.0e37f;
+    }
     // y of a logit that is not NaN, as two parts
     __device__ __forceinline__ void exponent(float l, float *p, float *e) const {
         const float diff = l - top, d = l >= top ? 0.f : fmaxf(diff, least);
@@ -245,40 +297,39 @@ struct Kept {
     __device__ __forceinline__ bool order(float l, int i) const { return l > value || (l == value && i <= index); }
 };
 
-// The weights of a vector's tokens in 32 bits, two at a time, where all of them are light: false where one is not, or is as large as the
-// last kept one, of which indices decide. 8 instructions a token (the general form takes 40 and more), and as many cycles of the exponential's unit.
+// The weights of a vector's tokens in 32 bits, two at a time, where all of them are light: kGeneral where one is not, or is as large as the
+// last kept one, of which indices decide; kNothing where none is kept. Some 9 instructions a token where the general form takes 40 and more.
+enum { kGeneral, kNothing, kLight };
 template <typename T>
-__device__ __forceinline__ bool light_weights(const Weights<T> &w, const Kept &kept, float (&x)[Type<T>::kPer]) {
+__device__ __forceinline__ int light_weights(const Weights<T> &w, const Kept &kept, uint4 v, float (&x)[Type<T>::kPer]) {
     constexpr int P = Type<T>::kPer;
-    bool odd = !(w.top < 3.4e38f);
+    const float most = Type<T>::largest(v);
+    if (most < kept.value) return kNothing;
+    if (!w.simple || w.heavy((most - w.top) * w.hi)) return kGeneral;
+    const uint4 c = make_uint4(w.clamp, w.clamp, w.clamp, w.clamp);
+    Type<T>::spread(Type<T>::larger(v, c), x);  // also from NaN and -infinity
     if (kept.value > -INFINITY) {
+        bool tie = false;
+        const float none = w.top + w.least;
 #pragma unroll
         for (int u = 0; u < P; ++u) {
-            odd = odd || x[u] == kept.value;
-            x[u] = x[u] >= kept.value ? x[u] : -INFINITY;
+            tie = tie || x[u] == kept.value;
+            x[u] = x[u] >= kept.value ? x[u] : none;
         }
+        if (tie) return kGeneral;
     }
-    u64 d[P / 2], p[P / 2];
-    float most = -INFINITY;
+    const u64 top = pair_f32(-w.top, -w.top), hi = pair_f32(w.hi, w.hi), less_hi = pair_f32(-w.hi, -w.hi), less_lo = pair_f32(-w.lo, -w.lo),
+              less_ln2 = pair_f32(-0.6931471806f, -0.6931471806f);
 #pragma unroll
     for (int u = 0; u < P / 2; ++u) {
+        const u64 d = add_f32x2(pair_f32(x[2 * u], x[2 * u + 1]), top), p = mul_f32x2(d, hi);
+        const u64 e = fma_f32x2(d, less_lo, fma_f32x2(d, less_hi, p));  // what p lacks, negative
         float a, b;
-        split_f32(add_f32x2(pair_f32(x[2 * u], x[2 * u + 1]), pair_f32(-w.top, -w.top)), &a, &b);
-        d[u] = pair_f32(fmaxf(a, w.least), fmaxf(b, w.least));  // also from NaN
-        p[u] = mul_f32x2(d[u], pair_f32(w.hi, w.hi));
-        split_f32(p[u], &a, &b);
-        most = fmaxf(most, fmaxf(a, b));
+        split_f32(p, &a, &b);
+        const u64 two = pair_f32(fast_exp2(a), fast_exp2(b));
+        split_f32(fma_f32x2(mul_f32x2(two, less_ln2), e, two), &x[2 * u], &x[2 * u + 1]);
     }
-    if (odd || w.heavy(most)) return false;
-#pragma unroll
-    for (int u = 0; u < P / 2; ++u) {
-        float a, b;
-        split_f32(p[u], &a, &b);
-        const u64 e = fma_f32x2(d[u], pair_f32(-w.lo, -w.lo), fma_f32x2(d[u], pair_f32(-w.hi, -w.hi), p[u]));  // what p lacks, negative
-        const u64 v = pair_f32(fast_exp2(a), fast_exp2(b));
-        split_f32(fma_f32x2(mul_f32x2(v, pair_f32(-0.6931471806f, -0.6931471806f)), e, v), &x[2 * u], &x[2 * u + 1]);
-    }
-    return true;
+    return kLight;
 }
 
 // Sums over a vector's tokens, in index order: the sum up to a token never falls, and the sum over the vector is the same whenever it is
@@ -301,22 +352,22 @@ struct MassSum {
     __device__ __forceinline__ u64 vector(uint4 v, int first) {
         constexpr int P = Type<T>::kPer;
         float x[P];
-        Type<T>::spread(v, x);
-        if (light_weights(w, kept, x)) {
+        const int kind = light_weights(w, kept, v, x);
+        if (kind == kNothing) return 0;
+        if (kind == kLight) {
             u64 s = pair_f32(x[0], x[1]);
 #pragma unroll
             for (int u = 1; u < P / 2; ++u) s = add_f32x2(s, pair_f32(x[2 * u], x[2 * u + 1]));
             float a, b;
             split_f32(s, &a, &b);
-            c = (a + b) * 17592186044416.f;
-        } else {
-            Type<T>::spread(v, x);
+            return w.whole((a + b) * 17592186044416.f);
+        }
+        Type<T>::spread(v, x);
 #pragma unroll 1
-            for (int u = 0; u < P; ++u) {
-                add(x[0], first + u);
+        for (int u = 0; u < P; ++u) {
+            add(x[0], first + u);
 #pragma unroll
-                for (int k = 0; k + 1 < P; ++k) x[k] = x[k + 1];
-            }
+            for (int k = 0; k + 1 < P; ++k) x[k] = x[k + 1];
         }
         return sum();
     }
@@ -379,12 +430,9 @@ struct RestSum {
     __device__ __forceinline__ u64 sum() const { return n; }
     __device__ __forceinline__ u64 vector(uint4 v, int first) {
         constexpr int P = Type<T>::kPer;
+        if (!(Type<T>::largest(v) >= kept.value)) return 0;
         float x[P], share[P];
         Type<T>::spread(v, x);
-        bool some = false;
-#pragma unroll
-        for (int u = 0; u < P; ++u) some = some || x[u] >= kept.value;
-        if (!some) return 0;
 #pragma unroll
         for (int u = 0; u < P; ++u) share[u] = q && kept.order(x[u], first + u) ? q[first + u] : 0.f;
 #pragma unroll
@@ -848,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
             st_block_u32(at_block(from_here + i % kWords, i / kWords + 1), from_here[i % kWords]);
     }
     // ---- the slice into shared memory, and the largest logit ----
-    float top = -INFINITY;
+    uint4 most = make_uint4(Type<T>::kMasked, Type<T>::kMasked, Type<T>::kMasked, Type<T>::kMasked);
     for (int k0 = 0; k0 < row.rounds; k0 += kBatch) {
         if (k0 > 0) request(k0);
 #pragma unroll
@@ -863,19 +911,13 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
                 v[j] = *reinterpret_cast<uint4 *>(part);
             }
             const_cast<uint4 *>(row.data)[at] = v[j];
-            float x[P];
-            Type<T>::spread(v[j], x);
-#pragma unroll
-            for (int e = 0; e < P; ++e) top = fmaxf(top, x[e]);
+            most = Type<T>::larger(most, v[j]);
         }
     }
-    const float mine = top;  // this thread's
-    unsigned least;
-    {
-        unsigned most;
-        row.exchange_range(mine > -INFINITY ? float_order_code(mine) : 0xffffffffu, float_order_code(mine), &least, &most);
-        top = value_of(static_cast<u64>(most) << 32);
-    }
+    const float mine = Type<T>::largest(most);  // this thread's
+    unsigned least, largest;
+    row.exchange_range(mine > -INFINITY ? float_order_code(mine) : 0xffffffffu, float_order_code(mine), &least, &largest);
+    const float top = value_of(static_cast<u64>(largest) << 32);
 
     // ---- what is left of the row ----
     const Given &given = s->given;  // here since the exchange
@@ -1025,24 +1067,23 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
         for (int k = 0; k < row.rounds; ++k) {
             const int at = row.vector(k), i0 = row.first + at * P;
             if (at >= row.vectors) break;
-            float x[P], y[P];
-            Type<T>::spread(row.data[at], x);
-            bool some = false;
-#pragma unroll
-            for (int e = 0; e < P; ++e) {
-                y[e] = x[e];
-                some = some || x[e] >= kept.value;
-            }
-            if (some && light_weights(weights, kept, y)) {
+            float y[P];
+            const int kind = light_weights(weights, kept, row.data[at], y);
+            if (kind == kLight) {
 #pragma unroll
                 for (int e = 0; e < P; ++e) y[e] *= 17592186044416.f * scale;
+            } else if (kind == kNothing) {
+#pragma unroll
+                for (int e = 0; e < P; ++e) y[e] = 0.f;
             } else {
+                Type<T>::spread(row.data[at], y);
 #pragma unroll
                 for (int e = 0; e < P; ++e) {
+                    const float l = y[e];
                     y[e] = 0.f;
-                    if (!some || !kept.order(x[e], i0 + e)) continue;
+                    if (!kept.order(l, i0 + e)) continue;
                     float p, rest;
-                    weights.exponent(x[e], &p, &rest);
+                    weights.exponent(l, &p, &rest);
                     y[e] = (weights.heavy(p) ? static_cast<float>(weights.heavy_weight(p, rest)) : weights.light_weight(p, rest)) * scale;
                 }
             }
