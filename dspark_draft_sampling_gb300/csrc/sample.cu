@@ -43,6 +43,7 @@ struct Draw {
     long long logits_stride, probs_stride, draft_probs_stride;
     float temperature_all, top_p_all, min_p_all;
     int top_k_all;
+    float floor_hi_all, floor_lo_all;  // log2(min_p_all)
     int rows, vocab, slice, n_seqs, n_drafts;
     uint2 table[64];  // 2^(28 + j/64): rounded, and as a float
 };
@@ -50,7 +51,7 @@ struct Draw {
 // What a row is drawn by: the cluster's first block reads it and hands it to the others, so that all of them take the same branches
 // whatever happens to those arrays meanwhile.
 struct Given {
-    float hi, lo;              // log2(e) / T in two parts
+    float hi, lo, least;       // log2(e) / T in two parts; a difference of logits whose weight is 0
     float floor_hi, floor_lo;  // log2 of min_p
     float top_p, u;
     int top_k;                 // 0: all
@@ -67,6 +68,7 @@ struct alignas(16) Shared {
     unsigned count[2][kBins];    // histograms, read by the cluster's other blocks
     alignas(8) unsigned mass[2][kBins][2];  // low and high half of 64 bits
     u64 slot[2][kMaxBlocks];     // [parity][block]: what the blocks exchange
+    float profile[2][kMaxBlocks][16], part[kWarps][16];
     u64 list[kList];             // this block's tokens of a list, read by the first block: order code and what is left of 2^32 behind the index
     u64 sort[2][kList];
     u64 warp[kWarps];            // sums over the warps' stretches of the slice
@@ -74,6 +76,7 @@ struct alignas(16) Shared {
     u64 inverse, last;           // last: of the kept tokens, as in the list
     u64 z;
     u64 count_before, mass_before, count_in, drafted;
+    float share_hi, share_lo;    // what turns a light weight into a probability
     int found;
     unsigned listed;
 };
@@ -130,13 +133,18 @@ __device__ __forceinline__ N warp_prefix(N v, int lane) {  // inclusive
 
 // floor(z * f), or its ceiling, exactly; f in [0, 1).
 __device__ __forceinline__ u64 part_of(u64 z, float f, bool up) {
-    const unsigned bits = __float_as_uint(f), e = max(bits >> 23, 1u);
-    const unsigned mantissa = (bits & 0x7fffffu) | (bits >> 23 ? 0x800000u : 0u);
-    const unsigned __int128 product = static_cast<unsigned __int128>(z) * mantissa;
-    const unsigned shift = 150 - e;
-    if (shift > 100) return up && product != 0 ? 1 : 0;
-    const unsigned __int128 rest = up ? (static_cast<unsigned __int128>(1) << shift) - 1 : 0;
-    return static_cast<u64>((product + rest) >> shift);
+    const unsigned bits = __float_as_uint(f), mantissa = (bits & 0x7fffffu) | (bits >> 23 ? 0x800000u : 0u);
+    const unsigned shift = 150 - max(bits >> 23, 1u);  // 24 to 149
+    const u64 high = __umul64hi(z, mantissa), low = z * mantissa;
+    u64 whole = 0, rest = high | low;
+    if (shift < 64) {
+        whole = high << (64 - shift) | low >> shift;
+        rest = low << (64 - shift);
+    } else if (shift < 128) {
+        whole = high >> (shift - 64);
+        rest = low | (high & ((1ull << (shift - 64)) - 1));
+    }
+    return whole + (up && rest != 0 ? 1 : 0);
 }
 
 // Where a uniform number falls among z.
@@ -241,7 +249,7 @@ struct Weights {
     bool simple;                // whether there is one that weighs nothing and leaves all numbers finite
     const uint2 *table;
 
-    __device__ __forceinline__ Weights(float m, const Given &g, const uint2 *t) : top(m), hi(g.hi), lo(g.lo), least(-200.f / g.hi), table(t) {
+    __device__ __forceinline__ Weights(float m, const Given &g, const uint2 *t) : top(m), hi(g.hi), lo(g.lo), least(g.least), table(t) {
         clamp = Type<T>::down(top + least);
         const float y = (Type<T>::low(clamp) - top) * hi;
         simple = y <= -100.f && y > -1.0e4f && top + least > Type<T>::kLeast && top < 1.0e37f;
@@ -258,7 +266,8 @@ struct Weights {
     }
     __device__ __forceinline__ static bool heavy(float p) { return p >= -8.f; }
     // 2^(28 + fraction) in whole numbers and the power of two that it is to be divided by
-    __device__ __forceinline__ unsigned significand(float p, float e, int *shift) const {
+    __device__ __forceinline__ unsigned significand(float p, float e, int *shift) const { return significand(p, e, table, shift); }
+    __device__ __forceinline__ static unsigned significand(float p, float e, const uint2 *table, int *shift) {
         const float t = p + 196608.f;  // 1.5 * 2^17: rounded to 64ths
         const int n = __float_as_int(t) - 0x48400000;
         const float r = (p - (t - 196608.f)) + e;
@@ -338,11 +347,12 @@ template <typename T>
 struct MassSum {
     const Weights<T> &w;
     const Kept &kept;
+    int skip;  // a token left out, or -1
     u64 h = 0;
     float c = 0.f;
-    __device__ __forceinline__ MassSum(const Weights<T> &a, const Kept &b) : w(a), kept(b) {}
+    __device__ __forceinline__ MassSum(const Weights<T> &a, const Kept &b, int without = -1) : w(a), kept(b), skip(without) {}
     __device__ __forceinline__ void add(float l, int i) {
-        if (!kept.order(l, i)) return;
+        if (!kept.order(l, i) || i == skip) return;
         float p, e;
         w.exponent(l, &p, &e);
         if (w.heavy(p)) h += w.heavy_weight(p, e);
@@ -354,7 +364,7 @@ struct MassSum {
         float x[P];
         const int kind = light_weights(w, kept, v, x);
         if (kind == kNothing) return 0;
-        if (kind == kLight) {
+        if (kind == kLight && static_cast<unsigned>(skip - first) >= P) {
             u64 s = pair_f32(x[0], x[1]);
 #pragma unroll
             for (int u = 1; u < P / 2; ++u) s = add_f32x2(s, pair_f32(x[2 * u], x[2 * u + 1]));
@@ -393,51 +403,74 @@ struct TieSum {
 // Leading zeros of a row's sum: 0 to 19, as 2^44 <= z.
 __device__ __forceinline__ int lead_of(u64 z) { return __clzll(static_cast<long long>(z)); }
 
-// max(0, p - q) in 2^-62 over the kept tokens; without q, p without the draft.
+// max(0, p - q) in 2^-62 over the kept tokens. Of light ones p and the difference are taken in 32 bits, p with a share in two parts.
 template <typename T>
 struct RestSum {
     const Weights<T> &w;
     const Kept &kept;
     const float *q;
-    int draft, shift;
+    int vocab, shift;
     u64 inverse;
-    u64 n = 0;
-    // of the row's sum z: 2^127 / (z 2^lead), the last bits of which do not matter, as it is the same for all tokens
-    static __device__ u64 invert(u64 z) {
+    float share_hi, share_lo;
+    u64 h = 0;
+    float c = 0.f;
+    // What p is taken by, of the row's sum z: 2^127 / (z 2^lead), the last bits of which do not matter, as it is the same for all tokens, and
+    // 2^44 / z with what the fast exponential lacks.
+    static __device__ void prepare(Shared *s, u64 z) {
         const int lead = lead_of(z);
-        const double r = 9223372036854775808.0 / static_cast<double>(z << lead) * 18446744073709551616.0;
-        return r >= 18446744073709549568.0 ? ~0ull : static_cast<u64>(r);
+        const double r = 9223372036854775808.0 / static_cast<double>(z << lead);
+        s->inverse = r >= 0.9999999999999999 ? ~0ull : static_cast<u64>(r * 18446744073709551616.0);
+        const double share = ldexp(r, lead - 19) * (1.0 + 5.1e-8);
+        s->share_hi = static_cast<float>(share);
+        s->share_lo = static_cast<float>(share - s->share_hi);
     }
-    __device__ __forceinline__ RestSum(const Weights<T> &a, const Kept &b, const float *draft_probs, int x, u64 z, u64 inverted)
-        : w(a), kept(b), q(draft_probs), draft(x), shift(20 - lead_of(z)), inverse(inverted) {}
-    __device__ __forceinline__ u64 rest(u64 weight, int i, float share) const {
+    __device__ __forceinline__ RestSum(const Weights<T> &a, const Kept &b, const float *draft_probs, int tokens, u64 z, const Shared *s)
+        : w(a), kept(b), q(draft_probs), vocab(tokens), shift(20 - lead_of(z)), inverse(s->inverse), share_hi(s->share_hi), share_lo(s->share_lo) {}
+    __device__ __forceinline__ u64 rest(u64 weight, int i) const {
         const u64 mine = __umul64hi(weight << 19, inverse) >> shift;
-        u64 theirs = i == draft ? ~0ull : 0ull;
-        if (q) {
-            const unsigned bits = __float_as_uint(fminf(fmaxf(share, 0.f), 1.f));
-            const int up = static_cast<int>(bits >> 23) - 88;  // 2^62 of a 24-bit significand
-            const u64 s = (bits & 0x7fffffu) | 0x800000u;
-            theirs = up >= 0 ? s << up : up > -24 ? s >> -up : 0;
-        }
+        const unsigned bits = __float_as_uint(fminf(fmaxf(q[i], 0.f), 1.f));
+        const int up = static_cast<int>(bits >> 23) - 88;  // 2^62 of a 24-bit significand
+        const u64 s = (bits & 0x7fffffu) | 0x800000u, theirs = up >= 0 ? s << up : up > -24 ? s >> -up : 0;
         return mine > theirs ? mine - theirs : 0;
     }
-    __device__ __forceinline__ void add(float l, int i, float share) {
-        if (kept.order(l, i)) n += rest(w.weight(l), i, share);
+    __device__ __forceinline__ float light_rest(float weight, float share) const {  // weight: as light_weights gives it
+        return fmaxf(__fmaf_rn(weight, share_hi, weight * share_lo) - fmaxf(share, 0.f), 0.f);
     }
     __device__ __forceinline__ void add(float l, int i) {
-        if (kept.order(l, i)) n += rest(w.weight(l), i, q ? q[i] : 0.f);
+        if (!kept.order(l, i)) return;
+        float p, e;
+        w.exponent(l, &p, &e);
+        if (w.heavy(p)) h += rest(w.heavy_weight(p, e), i);
+        else c += light_rest(w.light_weight(p, e) * 0x1p-44f, q[i]);
     }
-    __device__ __forceinline__ u64 sum() const { return n; }
+    __device__ __forceinline__ u64 sum() const { return h + __float2ull_rn(c * 0x1p62f); }
     __device__ __forceinline__ u64 vector(uint4 v, int first) {
         constexpr int P = Type<T>::kPer;
-        if (!(Type<T>::largest(v) >= kept.value)) return 0;
-        float x[P], share[P];
-        Type<T>::spread(v, x);
+        float x[P];
+        const int kind = light_weights(w, kept, v, x);
+        if (kind == kNothing) return 0;
+        if (kind == kLight && first >= 0 && first + P <= vocab) {
+            alignas(16) float share[P];
+            if ((reinterpret_cast<uintptr_t>(q + first) & 15) == 0) {
 #pragma unroll
-        for (int u = 0; u < P; ++u) share[u] = q && kept.order(x[u], first + u) ? q[first + u] : 0.f;
+                for (int u = 0; u < P; u += 4)
+                    *reinterpret_cast<float4 *>(&share[u]) = *reinterpret_cast<const float4 *>(q + first + u);
+            } else {
 #pragma unroll
-        for (int u = 0; u < P; ++u) add(x[u], first + u, share[u]);
-        return n;
+                for (int u = 0; u < P; ++u) share[u] = q[first + u];
+            }
+#pragma unroll
+            for (int u = 0; u < P; ++u) c += light_rest(x[u], share[u]);
+        } else {
+            Type<T>::spread(v, x);
+#pragma unroll 1
+            for (int u = 0; u < P; ++u) {
+                add(x[0], first + u);
+#pragma unroll
+                for (int k = 0; k + 1 < P; ++k) x[k] = x[k + 1];
+            }
+        }
+        return sum();
     }
 };
 
@@ -466,28 +499,25 @@ struct Row {
             for (int u = 0; u < kPer; ++u) f(x[u], first + v * kPer + u);
         }
     }
+    // Every block's value to all of them; a lane then reads one.
+    __device__ __forceinline__ u64 exchange(u64 mine) {
+        parity ^= 1;
+        if (static_cast<int>(threadIdx.x) < blocks) st_block_u64(at_block(&s->slot[parity][block], threadIdx.x), mine);
+        cluster_barrier();
+        return lane < blocks ? s->slot[parity][lane] : 0;
+    }
     // The blocks' values: their sum, and that over the blocks before this one.
     __device__ __forceinline__ u64 exchange_sum(u64 mine, u64 *before) {
-        u64 all = 0;
-        *before = 0;
-        exchange(mine);
-        for (int b = 0; b < blocks; ++b) {
-            const u64 v = s->slot[parity][b];
-            if (b < block) *before += v;
-            all += v;
-        }
-        return all;
+        const u64 v = exchange(mine), upto = warp_prefix(v, lane);
+        *before = __shfl_sync(0xffffffffu, upto - v, block);
+        return __shfl_sync(0xffffffffu, upto, 31);
     }
-    __device__ __forceinline__ void exchange(u64 a) {
-        parity ^= 1;
-        if (static_cast<int>(threadIdx.x) < blocks) {
-            st_block_u64(at_block(&s->slot[parity][block], threadIdx.x), a);
-        }
-        cluster_barrier();
-    }
-    // The block's sum of `make()` over its slice; the warps' sums stay in s->warp.
+    // The sum of `make()` over this block's slice, which leaves those over the warps' stretches in s->warp, over the blocks before it, and over all.
+    struct Total {
+        u64 mine, before, all;
+    };
     template <typename M>
-    __device__ __forceinline__ u64 sum(M make) {
+    __device__ __forceinline__ Total total(M make) {
         u64 n = 0;
 #pragma unroll 1
         for (int k = 0; k < rounds; ++k) n += vector_sum(make, vector(k));
@@ -495,33 +525,31 @@ struct Row {
         __syncthreads();
         if (lane == 0) s->warp[warp] = n;
         __syncthreads();
-        n = 0;
-        for (int w = 0; w < kWarps; ++w) n += s->warp[w];
-        return n;
+        Total t;
+        t.mine = warp_sum(lane < kWarps ? s->warp[lane] : 0);
+        t.all = exchange_sum(t.mine, &t.before);
+        return t;
     }
     template <typename M>
     __device__ __forceinline__ u64 vector_sum(M make, int v) const {
         auto a = make();
         return v < vectors ? a.vector(data[v], first + v * kPer) : 0;
     }
-    // The first token at which the sum over the slice, taken just before by sum(), exceeds `target` (less than it): its index, in s->found.
+    // The first token at which the sum over the slice, taken just before by total(), exceeds `target` (less than it): its index, in s->found.
     // Called by the whole block. The stretch of the warp that it falls to is looked at by all warps, a round each.
     template <typename M>
     __device__ __forceinline__ void find(M make, u64 target) {
-        u64 before = 0;
-        int w = 0;
-        while (w < kWarps - 1 && before + s->warp[w] <= target) before += s->warp[w++];
+        u64 before;
+        const int w = first_past(s->warp, 0, target, &before);
         for (int k0 = 0; k0 < rounds; k0 += kWarps) {
             const int k = k0 + warp, v = k < rounds ? (w * rounds + k) * 32 + lane : vectors;
             const u64 mine = vector_sum(make, v), all = warp_sum(mine);
             __syncthreads();
             if (lane == 0) s->scan[1][warp] = all;
             __syncthreads();
-            int j = 0;  // the round among these
-            u64 upto = before;
-            while (j < kWarps - 1 && upto + s->scan[1][j] <= target) upto += s->scan[1][j++];
-            const bool last = k0 + kWarps >= rounds;
-            if (upto + s->scan[1][j] <= target && !last) {
+            u64 upto;
+            const int j = first_past(s->scan[1], before, target, &upto);  // the round among these
+            if (upto + s->scan[1][j] <= target) {
                 before = upto + s->scan[1][j];
                 continue;
             }
@@ -546,14 +574,22 @@ struct Row {
         }
     }
 
+    // The first of kWarps numbers at which their sum, with `before`, exceeds `target` (the last one if none does), and the sum before it.
+    __device__ __forceinline__ int first_past(const u64 *n, u64 before, u64 target, u64 *sum_before) const {
+        const u64 v = lane < kWarps ? n[lane] : 0, upto = before + warp_prefix(v, lane);
+        const unsigned past = __ballot_sync(0xffffffffu, upto > target && lane < kWarps) | 1u << (kWarps - 1);
+        const int at = __ffs(past) - 1;
+        *sum_before = __shfl_sync(0xffffffffu, upto - v, at);
+        return at;
+    }
     // Inclusive sums over the block's threads.
     __device__ __forceinline__ u64 block_prefix(u64 v) {
-        u64 upto = warp_prefix(v, lane);
+        const u64 upto = warp_prefix(v, lane);
         __syncthreads();
         if (lane == 31) s->scan[0][warp] = upto;
         __syncthreads();
-        for (int k = 0; k < warp; ++k) upto += s->scan[0][k];
-        return upto;
+        const u64 w = lane < kWarps ? s->scan[0][lane] : 0;
+        return upto + __shfl_sync(0xffffffffu, warp_prefix(w, lane) - w, warp);
     }
 
     // A histogram over the cluster's tokens (bin(l, i) < 0: not counted) and the first bin at which the number (MASS: weight) of tokens from
@@ -581,9 +617,19 @@ struct Row {
     __device__ __forceinline__ int reached(u64 target) {
         cluster_barrier();
         u64 n = 0, m = 0;
-        for (int b = 0; b < blocks; ++b) {
-            n += ld_block_u32(at_block(&s->count[histogram][threadIdx.x], b));
-            if (MASS) m += ld_block_u64(at_block(&s->mass[histogram][threadIdx.x][0], b));
+        {
+            unsigned v[kMaxBlocks];  // all on their way before the first is used
+#pragma unroll
+            for (int b = 0; b < kMaxBlocks; ++b) v[b] = b < blocks ? ld_block_u32(at_block(&s->count[histogram][threadIdx.x], b)) : 0;
+#pragma unroll
+            for (int b = 0; b < kMaxBlocks; ++b) n += v[b];
+        }
+        if (MASS) {
+            u64 v[kMaxBlocks];
+#pragma unroll
+            for (int b = 0; b < kMaxBlocks; ++b) v[b] = b < blocks ? ld_block_u64(at_block(&s->mass[histogram][threadIdx.x][0], b)) : 0;
+#pragma unroll
+            for (int b = 0; b < kMaxBlocks; ++b) m += v[b];
         }
         if (threadIdx.x == 0) s->found = kBins;
         const u64 count = block_prefix(n), mass = MASS ? block_prefix(m) : 0;
@@ -608,17 +654,16 @@ struct Row {
             const unsigned at = atomicAdd(&s->listed, 1u);
             if (at < kList) s->list[at] = static_cast<u64>(float_order_code(l)) << 32 | (0xffffffffu - static_cast<unsigned>(i));
         });
-        cluster_barrier();
-        int n = 0;
-        for (int b = 0; b < blocks; ++b) n += ld_block_u32(at_block(&s->listed, b));
-        return n;
+        __syncthreads();
+        u64 before;
+        return static_cast<int>(exchange_sum(s->listed, &before));
     }
     // The first block's threads get a token each of the n (at most kList) in all lists, in their order; 0 behind them.
     __device__ __forceinline__ u64 sorted_list(int n) {
         u64 key = 0;
         int at = threadIdx.x;
         for (int b = 0; b < blocks && at >= 0; ++b) {
-            const int here = ld_block_u32(at_block(&s->listed, b));
+            const int here = static_cast<int>(s->slot[parity][b]);  // from gather()'s exchange
             if (at < here) key = ld_block_u64(at_block(&s->list[at], b));
             at -= here;
         }
@@ -651,16 +696,65 @@ struct Row {
     template <bool MASS, bool WHOLE = false>
     __device__ __forceinline__ int select(Kept *kept, const Weights<T> &w, u64 target, float from) {
         const Kept prior = *kept;
-        // bins of equal width first, which spread the logits best
-        const float range = w.top - from, scale = range > 0.f && range < 3e38f ? 511.9f / range : 0.f;
+        // Atomics on shared memory take about a cycle each, so the tokens that a histogram counts are narrowed down to from <= l < to first.
+        const float lowest = from;
+        float to = INFINITY;
+        u64 above = 0;  // what the tokens from `to` on weigh
+        int many = 0;   // how many they are
+        if (MASS && w.simple) {
+            const float goal = static_cast<float>(target) * 0x1p-44f;
+            for (int stage = 0; stage < 2; ++stage) {
+                const float from_here = from, high = fminf(to, w.top), step = (high - from) / 8.f;
+                if (!(step > 4.8e-7f * fabsf(high))) break;
+                float mass, count;  // lane j: of the tokens from high - (j + 1) * step on, the last one: from `from` on
+                profile(w, high, step, from, &mass, &count);
+                const unsigned less = __ballot_sync(0xffffffffu, lane < 8 && mass < goal * 0.99999f), more = __ballot_sync(0xffffffffu, lane < 8 && mass > goal * 1.00001f);
+                int in = 0x7fffffff;
+                if (more) {
+                    const int j = __ffs(more) - 1;
+                    if (j < 7) from = high - static_cast<float>(j + 1) * step;
+                    in = static_cast<int>(__shfl_sync(0xffffffffu, count, j));
+                }
+                if (less & 0x7fu) {
+                    const int j = 31 - __clz(less & 0x7fu);
+                    to = high - static_cast<float>(j + 1) * step;
+                    many = static_cast<int>(__shfl_sync(0xffffffffu, count, j));
+                }
+                if (!(from < to && from >= from_here)) {  // not with such rounding
+                    from = lowest;
+                    to = INFINITY;
+                    many = 0;
+                    break;
+                }
+                if (in - many <= 256 * blocks) break;
+            }
+            if (to < INFINITY) {
+                const Kept upper{to, 0x7fffffff};
+                above = total([&] { return MassSum<T>(w, upper); }).all;
+            }
+        }
+        float high, scale;
         auto linear = [&](float l, int i) {
-            return l >= from && prior.order(l, i) ? min(static_cast<int>((w.top - l) * scale), kBins - 1) : -1;
+            return l >= from && (l < to || to == INFINITY) && prior.order(l, i) ? min(static_cast<int>((high - l) * scale), kBins - 1) : -1;
         };
-        const int bin = reach<MASS>(w, target, linear);
-        if (bin == kBins) return 0;  // all of them do not reach it: nothing is dropped
-        if (WHOLE && s->count_before + s->count_in <= kList)
-            return gather([&](float l, int i) { return l >= from && linear(l, i) <= bin; });
-        u64 above = MASS ? s->mass_before : s->count_before;
+        int bin = kBins;
+        for (;;) {
+            if (above < target) {
+                high = fminf(to, w.top);
+                const float range = high - from;
+                scale = range > 0.f && range < 3e38f ? 511.9f / range : 0.f;
+                bin = reach<MASS>(w, target - above, linear);
+            }
+            if (bin < kBins) break;
+            if (to == INFINITY && from == lowest) return 0;  // all of them do not reach it: nothing is dropped
+            from = lowest;  // a border of the narrowed range was a rounding off
+            to = INFINITY;
+            above = 0;
+            many = 0;
+        }
+        if (WHOLE && many + s->count_before + s->count_in <= kList)
+            return gather([&](float l, int i) { return (l >= to && to < INFINITY) || (l >= from && linear(l, i) <= bin); });
+        above += MASS ? s->mass_before : s->count_before;
         if (s->count_in <= kList) {
             const int n = gather([&](float l, int i) { return linear(l, i) == bin; });
             if (block == 0) {
@@ -706,19 +800,15 @@ struct Row {
             left = (left + each_one - 1) / each_one;
         }
         auto ties = [&] { return TieSum<T>(value, prior); };
-        const u64 mine = sum(ties);
-        u64 before;
-        const u64 all = exchange_sum(mine, &before);
+        const Total n = total(ties);
         kept->value = value;
         kept->index = value == prior.value ? prior.index : 0x7fffffff;
-        if (left >= all) return 0;
-        const bool here = left - 1 >= before && left - 1 < before + mine;
-        if (here) find(ties, left - 1 - before);
+        if (left >= n.all) return 0;
+        const bool here = left - 1 >= n.before && left - 1 < n.before + n.mine;
+        if (here) find(ties, left - 1 - n.before);
         __syncthreads();
-        exchange(here ? s->found : 0);
-        u64 index = 0;
-        for (int b = 0; b < blocks; ++b) index += s->slot[parity][b];
-        kept->index = static_cast<int>(index);
+        u64 before;
+        kept->index = static_cast<int>(exchange_sum(here ? s->found : 0, &before));
         return 0;
     }
     // Narrows `kept` to tokens of at least min_p. Weights never fall with the logits, so there is a largest one that is too small: each
@@ -740,6 +830,65 @@ struct Row {
         const float value = value_of(static_cast<u64>(low) << 32);
         if (value > kept->value) *kept = {value, -1};
     }
+    // About the weight (in units of the heaviest one) and the number of the tokens with l >= high - (j + 1) step, in lane j < 7, and with
+    // l >= low, in lane 7.
+    __device__ __forceinline__ void profile(const Weights<T> &w, float high, float step, float low, float *mass, float *count) {
+        float t[8];
+        u64 acc[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            t[j] = j < 7 ? high - static_cast<float>(j + 1) * step : low;
+            acc[j] = 0;
+        }
+        const uint4 clamp = make_uint4(w.clamp, w.clamp, w.clamp, w.clamp);
+#pragma unroll 1
+        for (int k = 0; k < rounds; ++k) {
+            const int v = vector(k);
+            if (v >= vectors) break;
+            const uint4 d = data[v];
+            if (!(Type<T>::largest(d) >= low)) continue;
+            float x[kPer];
+            Type<T>::spread(Type<T>::larger(d, clamp), x);
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) {
+                const u64 one = pair_f32(fast_exp2((x[u] - w.top) * w.hi), 1.f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (x[u] >= t[j]) acc[j] = add_f32x2(acc[j], one);
+            }
+        }
+        // sixteen sums over the warp: halves change hands, so that lane 2k ends with sum k
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) split_f32(acc[j], &v[j], &v[8 + j]);
+#pragma unroll
+        for (int h = 8; h >= 1; h /= 2) {
+            const bool upper = (lane & (2 * h)) != 0;
+#pragma unroll
+            for (int j = 0; j < h; ++j) {
+                const float got = __shfl_xor_sync(0xffffffffu, upper ? v[j] : v[j + h], 2 * h);
+                v[j] = (upper ? v[j + h] : v[j]) + got;
+            }
+        }
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+        __syncthreads();
+        if ((lane & 1) == 0) s->part[warp][lane >> 1] = v[0];
+        __syncthreads();
+        parity ^= 1;
+        if (static_cast<int>(threadIdx.x) < 16 * blocks) {
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) sum += s->part[k][threadIdx.x & 15];
+            st_block_u32(at_block(&s->profile[parity][block][threadIdx.x & 15], threadIdx.x >> 4), __float_as_uint(sum));
+        }
+        cluster_barrier();
+        float sum = 0.f;
+#pragma unroll
+        for (int b = 0; b < kMaxBlocks; ++b)
+            if (b < blocks) sum += s->profile[parity][b][lane & 15];
+        *mass = sum;
+        *count = __shfl_sync(0xffffffffu, sum, (lane & 7) + 8);
+    }
     // The least and the largest of the cluster's codes.
     __device__ __forceinline__ void exchange_range(unsigned least, unsigned most, unsigned *c0, unsigned *c1) {
         least = __reduce_min_sync(0xffffffffu, least);
@@ -747,36 +896,34 @@ struct Row {
         __syncthreads();
         if (lane == 0) s->scan[0][warp] = static_cast<u64>(most) << 32 | (0xffffffffu - least);
         __syncthreads();
-        unsigned a = 0, b = 0;
-        for (int k = 0; k < kWarps; ++k) {
-            a = max(a, static_cast<unsigned>(s->scan[0][k] >> 32));
-            b = max(b, static_cast<unsigned>(s->scan[0][k]));
-        }
-        exchange(static_cast<u64>(a) << 32 | b);
-        for (int k = 0; k < blocks; ++k) {
-            a = max(a, static_cast<unsigned>(s->slot[parity][k] >> 32));
-            b = max(b, static_cast<unsigned>(s->slot[parity][k]));
-        }
-        *c0 = 0xffffffffu - b;
-        *c1 = a;
+        auto join = [&](u64 v) {
+            return static_cast<u64>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(v >> 32))) << 32 |
+                   __reduce_max_sync(0xffffffffu, static_cast<unsigned>(v));
+        };
+        const u64 all = join(exchange(join(lane < kWarps ? s->scan[0][lane] : 0)));
+        *c0 = 0xffffffffu - static_cast<unsigned>(all);
+        *c1 = static_cast<unsigned>(all >> 32);
     }
 
-    // The token of the weights `make()` at u of their sum; true if any weighs something.
+    // The token of the weights `make()`, of which `t` is the total taken just before, at u of their sum.
     template <typename M>
-    __device__ __forceinline__ bool pick(M make, float u, long long *id) {
-        const u64 mine = sum(make);
-        u64 before;
-        const u64 all = exchange_sum(mine, &before);
-        if (all == 0) return false;
-        const u64 target = place_of(u, all);
-        if (target >= before && target < before + mine) {
-            find(make, target - before);
-            __syncthreads();
-            if (threadIdx.x == 0) *id = s->found;
-        }
-        return true;
+    __device__ __forceinline__ void pick(M make, const Total &t, float u, long long *id) {
+        const u64 target = place_of(u, t.all);
+        if (target < t.before || target >= t.before + t.mine) return;
+        find(make, target - t.before);
+        __syncthreads();
+        if (threadIdx.x == 0) *id = s->found;
     }
 };
+
+// log2 of a number in (0, 1] in two parts: the logarithm in 32 bits, and what is missing from 2^hi to the number.
+__device__ __forceinline__ void log2_of(float x, const uint2 *table, float *hi, float *lo) {
+    *hi = fmaxf(fminf(log2f(x), 0.f), -140.f);
+    int shift;
+    const unsigned s = Weights<float>::significand(*hi, 0.f, table, &shift);
+    const float scaled = ldexpf(x, 28 + shift);  // exact
+    *lo = (scaled - static_cast<float>(s & ~127u) - static_cast<float>(s & 127u)) / static_cast<float>(s) * 1.4426950409f;
+}
 
 // What row r is drawn by, into this block's shared memory.  One warp.
 template <typename T, bool VERIFY>
@@ -816,15 +963,20 @@ __device__ __forceinline__ void give(const Draw &g, long long r, size_t row_at, 
                 }
             }
             v.state = temperature > 0.f ? kDrawn : kGreedy;
-            // within these temperatures neither part leaves the range of 32 bits; beyond them a weight is one or nothing
-            const double c = v.state == kDrawn ? 1.4426950408889634074 / fmin(fmax(static_cast<double>(temperature), 1e-30), 1e30) : 1.0;
-            v.hi = static_cast<float>(c);
-            v.lo = static_cast<float>(c - v.hi);
+            v.hi = 1.f;
+            if (v.state == kDrawn) {
+                // log2(e) / T by one step of a division in two parts. Within these temperatures neither part leaves the range of 32 bits; beyond
+                // them a weight is one or nothing.
+                const float d = fminf(fmaxf(temperature, 1e-30f), 1e30f);
+                v.hi = 1.4426950216f / d;
+                v.lo = (__fmaf_rn(-v.hi, d, 1.4426950216f) + 1.9259629e-8f) / d;
+            }
+            v.least = -200.f / v.hi;
             v.floor_hi = -INFINITY;
             if (v.state == kDrawn && min_p > 0.f) {
-                const double least = log2(fmin(static_cast<double>(min_p), 1.0));
-                v.floor_hi = static_cast<float>(least);
-                v.floor_lo = static_cast<float>(least - v.floor_hi);
+                v.floor_hi = g.floor_hi_all;
+                v.floor_lo = g.floor_lo_all;
+                if (g.min_p) log2_of(fminf(min_p, 1.f), s->table, &v.floor_hi, &v.floor_lo);
             }
             v.top_p = v.state == kGreedy || !(top_p < 1.f) ? 1.f : fmaxf(top_p, 0.f);
             if (v.top_k < 0 || v.top_k >= g.vocab) v.top_k = 0;
@@ -837,12 +989,15 @@ __device__ __forceinline__ void give(const Draw &g, long long r, size_t row_at, 
 
 // Whether the draft is accepted, of s->drafted and the sum s->z; if not, what its rest is taken by.  Called by all threads.
 template <typename T>
-__device__ __forceinline__ void judge(const Given &given, Shared *s) {
-    if (threadIdx.x != 0) return;
-    const bool yes = static_cast<double>(given.accept) * static_cast<double>(given.share) * static_cast<double>(s->z) <
-                     static_cast<double>(s->drafted);
-    s->found = yes;
-    if (!yes) s->inverse = RestSum<T>::invert(s->z);
+__device__ __forceinline__ bool judge(const Given &given, Shared *s) {
+    if (threadIdx.x == 0) {
+        const bool yes = static_cast<double>(given.accept) * static_cast<double>(given.share) * static_cast<double>(s->z) <
+                         static_cast<double>(s->drafted);
+        s->found = yes;
+        if (!yes) RestSum<T>::prepare(s, s->z);
+    }
+    __syncthreads();
+    return s->found;
 }
 
 template <typename T, bool VERIFY>
@@ -935,15 +1090,12 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
     const Weights<T> weights(top, given, s->table);
     Kept kept{-INFINITY, -1};
     auto mass = [&] { return MassSum<T>(weights, kept); };
-    auto total = [&] {
-        u64 before;
-        return row.exchange_sum(row.sum(mass), &before);
-    };
     const int top_k = given.top_k;
     const bool by_p = given.top_p < 1.f, by_floor = given.floor_hi > -INFINITY;
     u64 z = 0;
     float cut = kLowest;  // a logit below which none of the kept tokens lies
     if (by_floor && !(top_k > 0 && by_p)) cut = fmaxf(cut, top + (given.floor_hi - 0.01f) / weights.hi - 4.8e-7f * fabsf(top));
+    typename Row<T>::Total sums{};
     bool finish = false;
     int candidates = 0;
     auto list_all = [&] {
@@ -951,6 +1103,11 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
         finish = candidates <= kList;
     };
     auto drop_light = [&] { return max(part_of(z, given.top_p, true), 1ull); };  // what the nucleus has to weigh, of the sum z
+    // Of n tokens that weigh z, those lighter than an even share of what may be dropped are dropped all together: a bound from below.
+    auto above_share = [&](int n) {
+        const float share = (1.f - given.top_p) * static_cast<float>(z) * 0x1p-44f / static_cast<float>(n);
+        return share > 1e-30f ? fmaxf(cut, top + (log2f(share) - 0.01f) / weights.hi - 4.8e-7f * fabsf(top)) : cut;
+    };
     if (top_k > 0) {
         // The top_k-th largest of the threads' maxima is a bound from below.
         bool bounded = g.vocab <= kList;
@@ -968,16 +1125,12 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
         }
         if (bounded) list_all();
     } else if (by_p) {
-        z = total();
-        // Tokens lighter than an even share of what may be dropped are dropped, all together.
-        const float share = (1.f - given.top_p) * static_cast<float>(z) / (17592186044416.f * static_cast<float>(g.vocab));
-        if (share > 1e-30f) cut = fmaxf(cut, top + (log2f(share) - 0.01f) / weights.hi - 4.8e-7f * fabsf(top));
-        candidates = row.template select<true, true>(&kept, weights, drop_light(), cut);
+        z = row.total(mass).all;
+        const u64 goal = drop_light();
+        candidates = row.template select<true, true>(&kept, weights, goal, above_share(g.vocab));
         finish = candidates > 0;
     } else if (by_floor) {
         list_all();
-    } else if (VERIFY || probs) {
-        z = total();
     }
     if (finish) {
         // ---- few tokens: the first block goes on with them alone ----
@@ -1020,15 +1173,15 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
             if (VERIFY && given.token >= 0) {
                 if (stays && i == given.token) s->drafted = w;
                 __syncthreads();
-                judge<T>(given, s);
-                __syncthreads();
-                if (s->found) {
+                if (judge<T>(given, s)) {
                     if (threadIdx.x == 0) *id = kAccepted;
                     return;
                 }
-                const float *q = g.draft_probs ? g.draft_probs + static_cast<size_t>(given.draft) * g.draft_probs_stride : nullptr;
-                const RestSum<T> rest(weights, kept, q, given.token, s->z, s->inverse);
-                const u64 over = stays ? rest.rest(w, i, q ? q[i] : 0.f) >> 18 : 0;  // in 2^-44
+                u64 over = stays && i != given.token ? w : 0;
+                if (g.draft_probs) {
+                    const RestSum<T> rest(weights, kept, g.draft_probs + static_cast<size_t>(given.draft) * g.draft_probs_stride, g.vocab, s->z, s);
+                    over = stays ? rest.rest(w, i) >> 18 : 0;  // in 2^-44
+                }
                 if (__syncthreads_or(over != 0)) weight = over;
             }
             // in index order, with the weights of 45 bits behind the indices
@@ -1051,12 +1204,13 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
         if (top_k > 0) {
             row.template select<false>(&kept, weights, top_k, cut);
             if (by_p) {
-                z = total();
-                row.template select<true>(&kept, weights, drop_light(), cut);
+                z = row.total(mass).all;
+                row.template select<true>(&kept, weights, drop_light(), above_share(top_k));
             }
         }
         if (by_floor) row.drop_below(&kept, weights, given);
-        if ((VERIFY || probs) && (top_k > 0 || by_p || by_floor)) z = total();
+        sums = row.total(mass);
+        z = sums.all;
     }
 
     // ---- the distribution ----
@@ -1100,23 +1254,34 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
     }
 
     // ---- the token ----
-    bool done = false;
     if (VERIFY && given.token >= 0) {
         if (threadIdx.x == 0) {
-            u64 w = 0;
-            if (kept.order(given.logit, given.token)) w = weights.weight(given.logit);
-            s->drafted = w;
+            s->drafted = kept.order(given.logit, given.token) ? weights.weight(given.logit) : 0;
             s->z = z;
         }
-        __syncthreads();
-        judge<T>(given, s);
-        __syncthreads();
-        done = s->found;
-        if (done && row.block == 0 && threadIdx.x == 0) *id = kAccepted;
-        const float *q = g.draft_probs ? g.draft_probs + static_cast<size_t>(given.draft) * g.draft_probs_stride : nullptr;
-        if (!done) done = row.pick([&] { return RestSum<T>(weights, kept, q, given.token, z, s->inverse); }, given.u, id);
+        if (judge<T>(given, s)) {
+            if (row.block == 0 && threadIdx.x == 0) *id = kAccepted;
+            return;
+        }
+        if (g.draft_probs) {
+            const float *q = g.draft_probs + static_cast<size_t>(given.draft) * g.draft_probs_stride;
+            auto rest = [&] { return RestSum<T>(weights, kept, q, g.vocab, z, s); };
+            const typename Row<T>::Total t = row.total(rest);
+            if (t.all > 0) {
+                row.pick(rest, t, given.u, id);
+                return;
+            }
+        } else {
+            auto others = [&] { return MassSum<T>(weights, kept, given.token); };
+            const typename Row<T>::Total t = row.total(others);
+            if (t.all > 0) {
+                row.pick(others, t, given.u, id);
+                return;
+            }
+        }
+        sums = row.total(mass);  // the warps' sums are wanted again
     }
-    if (!done) row.pick(mass, given.u, id);
+    row.pick(mass, sums, given.u, id);
 }
 
 // Each sequence's accepted drafts, the token drawn at its first row that did not accept, and -1 behind it.  A warp to a sequence.
@@ -1225,6 +1390,11 @@ dspark_status run(Draw g, int dtype, const dspark_filters &f, cudaStream_t strea
     g.top_p_all = f.top_p_all;
     g.min_p_all = f.min_p_all;
     g.top_k_all = f.top_k_all;
+    if (!f.min_p && f.min_p_all > 0.f) {
+        const double least = std::log2(static_cast<double>(f.min_p_all));
+        g.floor_hi_all = static_cast<float>(least);
+        g.floor_lo_all = static_cast<float>(least - g.floor_hi_all);
+    }
     static const Table table;
     std::memcpy(g.table, table.entry, sizeof g.table);
     int sms = 0;
