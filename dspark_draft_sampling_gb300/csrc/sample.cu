@@ -27,6 +27,7 @@ constexpr int kBins = kThreads;           // of a histogram: a thread looks afte
 constexpr int kList = kThreads;           // tokens that one block sorts: a thread to each
 constexpr int kMaxBlocks = 16;            // of a cluster
 constexpr float kLowest = -3.402823466e38f;
+constexpr int kNoIndex = -0x7fffffff;      // before all indices, also those of what pads a slice
 constexpr int kMaxVocab = 1 << 19;        // 2^19 weights of 2^44 stay below 2^64
 constexpr long long kAccepted = -2;       // in ids until the second kernel has run: the row's draft is accepted
 
@@ -282,7 +283,7 @@ struct Weights {
         return static_cast<u64>(s) << (16 - shift);
     }
     __device__ __forceinline__ static float light_weight(float p, float e) {  // of 2^-44
-        const float w = fast_exp2(p) * 17592186044416.f;
+        const float w = fast_exp2(p) * 0x1p44f;
         return __fmaf_rn(w * 0.6931471806f, e, w);
     }
     // Light weights in whole numbers. The fast exponential falls short by 5.1e-8 on average (rms 5.9e-8, at most 1.42e-7, over -40..-8 on
@@ -306,26 +307,36 @@ struct Kept {
     __device__ __forceinline__ bool order(float l, int i) const { return l > value || (l == value && i <= index); }
 };
 
-// The weights of a vector's tokens in 32 bits, two at a time, where all of them are light: kGeneral where one is not, or is as large as the
-// last kept one, of which indices decide; kNothing where none is kept. Some 9 instructions a token where the general form takes 40 and more.
-enum { kGeneral, kNothing, kLight };
+// The weights of a vector's light tokens in 32 bits (in units of the heaviest one), two at a time: some 10 instructions a token where the
+// general form takes 40 and more. 0 for those that are not kept, and for the ones whose bits are returned: tokens that are not light, or
+// as large as the last kept one, of which indices decide. They are few, and looked at one by one.
 template <typename T>
-__device__ __forceinline__ int light_weights(const Weights<T> &w, const Kept &kept, uint4 v, float (&x)[Type<T>::kPer]) {
+__device__ __forceinline__ unsigned light_weights(const Weights<T> &w, const Kept &kept, uint4 v, float (&x)[Type<T>::kPer]) {
     constexpr int P = Type<T>::kPer;
     const float most = Type<T>::largest(v);
-    if (most < kept.value) return kNothing;
-    if (!w.simple || w.heavy((most - w.top) * w.hi)) return kGeneral;
+    if (most < kept.value || !w.simple) {
+#pragma unroll
+        for (int u = 0; u < P; ++u) x[u] = 0.f;
+        return w.simple ? 0u : (1u << P) - 1u;
+    }
     const uint4 c = make_uint4(w.clamp, w.clamp, w.clamp, w.clamp);
     Type<T>::spread(Type<T>::larger(v, c), x);  // also from NaN and -infinity
+    const float none = w.top + w.least;
+    unsigned special = 0;
+    if (w.heavy((most - w.top) * w.hi)) {
+#pragma unroll
+        for (int u = 0; u < P; ++u)
+            if (w.heavy((x[u] - w.top) * w.hi)) {
+                special |= 1u << u;
+                x[u] = none;
+            }
+    }
     if (kept.value > -INFINITY) {
-        bool tie = false;
-        const float none = w.top + w.least;
 #pragma unroll
         for (int u = 0; u < P; ++u) {
-            tie = tie || x[u] == kept.value;
-            x[u] = x[u] >= kept.value ? x[u] : none;
+            if (x[u] == kept.value) special |= 1u << u;
+            x[u] = x[u] > kept.value ? x[u] : none;
         }
-        if (tie) return kGeneral;
     }
     const u64 top = pair_f32(-w.top, -w.top), hi = pair_f32(w.hi, w.hi), less_hi = pair_f32(-w.hi, -w.hi), less_lo = pair_f32(-w.lo, -w.lo),
               less_ln2 = pair_f32(-0.6931471806f, -0.6931471806f);
@@ -338,7 +349,7 @@ __device__ __forceinline__ int light_weights(const Weights<T> &w, const Kept &ke
         const u64 two = pair_f32(fast_exp2(a), fast_exp2(b));
         split_f32(fma_f32x2(mul_f32x2(two, less_ln2), e, two), &x[2 * u], &x[2 * u + 1]);
     }
-    return kLight;
+    return special;
 }
 
 // Sums over a vector's tokens, in index order: the sum up to a token never falls, and the sum over the vector is the same whenever it is
@@ -359,25 +370,24 @@ struct MassSum {
         else c += w.light_weight(p, e);
     }
     __device__ __forceinline__ u64 sum() const { return h + w.whole(c); }
-    __device__ __forceinline__ u64 vector(uint4 v, int first) {
+    __device__ __forceinline__ u64 vector(const uint4 *at, int first) {
         constexpr int P = Type<T>::kPer;
         float x[P];
-        const int kind = light_weights(w, kept, v, x);
-        if (kind == kNothing) return 0;
-        if (kind == kLight && static_cast<unsigned>(skip - first) >= P) {
-            u64 s = pair_f32(x[0], x[1]);
+        unsigned special = light_weights(w, kept, *at, x);
+        if (static_cast<unsigned>(skip - first) < P) {
 #pragma unroll
-            for (int u = 1; u < P / 2; ++u) s = add_f32x2(s, pair_f32(x[2 * u], x[2 * u + 1]));
-            float a, b;
-            split_f32(s, &a, &b);
-            return w.whole((a + b) * 17592186044416.f);
+            for (int u = 0; u < P; ++u)
+                if (first + u == skip) x[u] = 0.f;
         }
-        Type<T>::spread(v, x);
-#pragma unroll 1
-        for (int u = 0; u < P; ++u) {
-            add(x[0], first + u);
+        u64 s = pair_f32(x[0], x[1]);
 #pragma unroll
-            for (int k = 0; k + 1 < P; ++k) x[k] = x[k + 1];
+        for (int u = 1; u < P / 2; ++u) s = add_f32x2(s, pair_f32(x[2 * u], x[2 * u + 1]));
+        float a, b;
+        split_f32(s, &a, &b);
+        c = (a + b) * 0x1p44f;
+        for (; special; special &= special - 1) {
+            const int u = __ffs(special) - 1;
+            add(Type<T>::one(at, u), first + u);
         }
         return sum();
     }
@@ -391,9 +401,9 @@ struct TieSum {
     __device__ __forceinline__ TieSum(float v, const Kept &b) : value(v), kept(b) {}
     __device__ __forceinline__ void add(float l, int i) { n += l == value && kept.order(l, i) ? 1 : 0; }
     __device__ __forceinline__ u64 sum() const { return n; }
-    __device__ __forceinline__ u64 vector(uint4 v, int first) {
+    __device__ __forceinline__ u64 vector(const uint4 *at, int first) {
         float x[Type<T>::kPer];
-        Type<T>::spread(v, x);
+        Type<T>::spread(*at, x);
 #pragma unroll
         for (int u = 0; u < Type<T>::kPer; ++u) add(x[u], first + u);
         return n;
@@ -444,31 +454,24 @@ struct RestSum {
         else c += light_rest(w.light_weight(p, e) * 0x1p-44f, q[i]);
     }
     __device__ __forceinline__ u64 sum() const { return h + __float2ull_rn(c * 0x1p62f); }
-    __device__ __forceinline__ u64 vector(uint4 v, int first) {
+    __device__ __forceinline__ u64 vector(const uint4 *at, int first) {
         constexpr int P = Type<T>::kPer;
+        if (Type<T>::largest(*at) < kept.value) return 0;
         float x[P];
-        const int kind = light_weights(w, kept, v, x);
-        if (kind == kNothing) return 0;
-        if (kind == kLight && first >= 0 && first + P <= vocab) {
-            alignas(16) float share[P];
-            if ((reinterpret_cast<uintptr_t>(q + first) & 15) == 0) {
+        unsigned special = light_weights(w, kept, *at, x);
+        alignas(16) float share[P];
+        if (first >= 0 && first + P <= vocab && (reinterpret_cast<uintptr_t>(q + first) & 15) == 0) {
 #pragma unroll
-                for (int u = 0; u < P; u += 4)
-                    *reinterpret_cast<float4 *>(&share[u]) = *reinterpret_cast<const float4 *>(q + first + u);
-            } else {
-#pragma unroll
-                for (int u = 0; u < P; ++u) share[u] = q[first + u];
-            }
-#pragma unroll
-            for (int u = 0; u < P; ++u) c += light_rest(x[u], share[u]);
+            for (int u = 0; u < P; u += 4) *reinterpret_cast<float4 *>(&share[u]) = *reinterpret_cast<const float4 *>(q + first + u);
         } else {
-            Type<T>::spread(v, x);
-#pragma unroll 1
-            for (int u = 0; u < P; ++u) {
-                add(x[0], first + u);
 #pragma unroll
-                for (int k = 0; k + 1 < P; ++k) x[k] = x[k + 1];
-            }
+            for (int u = 0; u < P; ++u) share[u] = first + u >= 0 && first + u < vocab ? q[first + u] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < P; ++u) c += light_rest(x[u], share[u]);
+        for (; special; special &= special - 1) {
+            const int u = __ffs(special) - 1;
+            add(Type<T>::one(at, u), first + u);
         }
         return sum();
     }
@@ -533,7 +536,7 @@ struct Row {
     template <typename M>
     __device__ __forceinline__ u64 vector_sum(M make, int v) const {
         auto a = make();
-        return v < vectors ? a.vector(data[v], first + v * kPer) : 0;
+        return v < vectors ? a.vector(data + v, first + v * kPer) : 0;
     }
     // The first token at which the sum over the slice, taken just before by total(), exceeds `target` (less than it): its index, in s->found.
     // Called by the whole block. The stretch of the warp that it falls to is looked at by all warps, a round each.
@@ -828,7 +831,7 @@ struct Row {
             low += first * step;
         }
         const float value = value_of(static_cast<u64>(low) << 32);
-        if (value > kept->value) *kept = {value, -1};
+        if (value > kept->value) *kept = {value, kNoIndex};
     }
     // About the weight (in units of the heaviest one) and the number of the tokens with l >= high - (j + 1) step, in lane j < 7, and with
     // l >= low, in lane 7.
@@ -1088,7 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
         return;
     }
     const Weights<T> weights(top, given, s->table);
-    Kept kept{-INFINITY, -1};
+    Kept kept{-INFINITY, kNoIndex};
     auto mass = [&] { return MassSum<T>(weights, kept); };
     const int top_k = given.top_k;
     const bool by_p = given.top_p < 1.f, by_floor = given.floor_hi > -INFINITY;
@@ -1222,25 +1225,9 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
             const int at = row.vector(k), i0 = row.first + at * P;
             if (at >= row.vectors) break;
             float y[P];
-            const int kind = light_weights(weights, kept, row.data[at], y);
-            if (kind == kLight) {
+            unsigned special = light_weights(weights, kept, row.data[at], y);
 #pragma unroll
-                for (int e = 0; e < P; ++e) y[e] *= 17592186044416.f * scale;
-            } else if (kind == kNothing) {
-#pragma unroll
-                for (int e = 0; e < P; ++e) y[e] = 0.f;
-            } else {
-                Type<T>::spread(row.data[at], y);
-#pragma unroll
-                for (int e = 0; e < P; ++e) {
-                    const float l = y[e];
-                    y[e] = 0.f;
-                    if (!kept.order(l, i0 + e)) continue;
-                    float p, rest;
-                    weights.exponent(l, &p, &rest);
-                    y[e] = (weights.heavy(p) ? static_cast<float>(weights.heavy_weight(p, rest)) : weights.light_weight(p, rest)) * scale;
-                }
-            }
+            for (int e = 0; e < P; ++e) y[e] *= 0x1p44f * scale;
             if (wide && i0 >= begin && i0 + P <= end) {
 #pragma unroll
                 for (int e = 0; e < P; e += 4) __stcs(reinterpret_cast<float4 *>(probs_to + i0 + e), make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]));
@@ -1248,6 +1235,14 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
 #pragma unroll
                 for (int e = 0; e < P; ++e)
                     if (i0 + e >= begin && i0 + e < end) probs_to[i0 + e] = y[e];
+            }
+            for (; special; special &= special - 1) {
+                const int e = __ffs(special) - 1;
+                const float l = Type<T>::one(row.data + at, e);
+                if (!kept.order(l, i0 + e) || i0 + e < begin || i0 + e >= end) continue;
+                float p, rest;
+                weights.exponent(l, &p, &rest);
+                probs_to[i0 + e] = (weights.heavy(p) ? static_cast<float>(weights.heavy_weight(p, rest)) : weights.light_weight(p, rest)) * scale;
             }
         }
         if (finish) return;
