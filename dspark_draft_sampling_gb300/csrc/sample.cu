@@ -2,9 +2,9 @@
 //
 // Weights.  A row's token v weighs w_v = exp((l_v - m) / T), m the largest logit.  Sums over a vocabulary decide which token a
 // uniform number falls on and where a nucleus ends, so they have to come out the same whatever their order: weights are whole
-// numbers of 2^-44, sums 64-bit integers.  With y = (l - m) log2(e) / T in two 32-bit parts, 2^y of the tokens that matter (y >= -8) comes
+// numbers of 2^-44, sums 64-bit integers.  With y = (l - m) log2(e) / T in two 32-bit parts, 2^y of the tokens that matter (y >= -6) comes
 // from a table of 2^(j/64) and a cubic in the rest |r| <= 2^-7, whose next term is 4e-11: 28 bits.  Lighter tokens take the fast
-// exponential (2^-22) of a difference rounded to 32 bits (2^-24 of |ln w|): 2^-28 of the heaviest token's weight at most.
+// exponential (2^-22) of a difference rounded to 32 bits (2^-24 of |ln w|): 2^-27 of the heaviest token's weight at most.
 //
 // Work.  A row belongs to a cluster of thread blocks, each of which keeps its slice in shared memory, so the logits are read from
 // memory once whatever the settings ask for.  The blocks exchange maxima, sums and histograms through distributed shared memory.
@@ -25,7 +25,9 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = kThreads;           // of a histogram: a thread looks after one
 constexpr int kList = kThreads;           // tokens that one block sorts: a thread to each
+constexpr int kNear = 1024;               // tokens of a block's slice around a nucleus' end
 constexpr int kMaxBlocks = 16;            // of a cluster
+constexpr int kHeavy = 6;                 // powers of two below the heaviest token down to which weights are exact to 28 bits
 constexpr float kLowest = -3.402823466e38f;
 constexpr int kNoIndex = -0x7fffffff;      // before all indices, also those of what pads a slice
 constexpr int kMaxVocab = 1 << 19;        // 2^19 weights of 2^44 stay below 2^64
@@ -68,9 +70,9 @@ struct alignas(16) Shared {
     Given given;
     unsigned count[2][kBins];    // histograms, read by the cluster's other blocks
     alignas(8) unsigned mass[2][kBins][2];  // low and high half of 64 bits
-    u64 slot[2][kMaxBlocks];     // [parity][block]: what the blocks exchange
-    float profile[2][kMaxBlocks][16], part[kWarps][16];
+    u64 slot[2][3][kMaxBlocks];  // [parity][value][block]: what the blocks exchange
     u64 list[kList];             // this block's tokens of a list, read by the first block: order code and what is left of 2^32 behind the index
+    u64 near_end[kNear];         // tokens in the same form, this block's own
     u64 sort[2][kList];
     u64 warp[kWarps];            // sums over the warps' stretches of the slice
     u64 scan[2][kWarps];
@@ -78,8 +80,9 @@ struct alignas(16) Shared {
     u64 z;
     u64 count_before, mass_before, count_in, drafted;
     float share_hi, share_lo;    // what turns a light weight into a probability
-    int found;
-    unsigned listed;
+    int found, to_bin, from_bin, likely;
+    float at_anchor[2], at_to, at_from;
+    unsigned listed, nears, heavies;
 };
 
 static_assert(offsetof(Shared, mass) % 8 == 0 && offsetof(Shared, slot) % 8 == 0 && sizeof(Shared) % 16 == 0, "64-bit words and vectors are aligned");
@@ -242,6 +245,14 @@ struct Type<__half> {
     static constexpr float kLeast = -6.0e4f;
 };
 
+// A number of 0 to 2^63 rounded down, by shifts: the conversion instruction runs at the rate of 64-bit floating point, 15 cycles a warp.
+__device__ __forceinline__ u64 to_whole(float x) {
+    const unsigned bits = __float_as_uint(x);
+    const int shift = static_cast<int>(bits >> 23) - 150;
+    const u64 m = (bits & 0x7fffffu) | 0x800000u;
+    return shift >= 0 ? m << shift : shift > -24 ? m >> -shift : 0;
+}
+
 // The weights of a row's tokens.
 template <typename T>
 struct Weights {
@@ -265,7 +276,7 @@ struct Weights {
             *e = __fmaf_rn(lost, hi, *e);
         }
     }
-    __device__ __forceinline__ static bool heavy(float p) { return p >= -8.f; }
+    __device__ __forceinline__ static bool heavy(float p) { return p >= -static_cast<float>(kHeavy); }
     // 2^(28 + fraction) in whole numbers and the power of two that it is to be divided by
     __device__ __forceinline__ unsigned significand(float p, float e, int *shift) const { return significand(p, e, table, shift); }
     __device__ __forceinline__ static unsigned significand(float p, float e, const uint2 *table, int *shift) {
@@ -289,7 +300,7 @@ struct Weights {
     // Light weights in whole numbers. The fast exponential falls short by 5.1e-8 on average (rms 5.9e-8, at most 1.42e-7, over -40..-8 on
     // this GPU), which would shift light tokens against heavy ones: 2^-24 is added back.
     __device__ __forceinline__ static u64 whole(float c) {
-        const u64 v = __float2ull_rn(c);
+        const u64 v = to_whole(c);
         return v + (v >> 24);
     }
     __device__ __forceinline__ u64 weight(float l) const {
@@ -453,7 +464,7 @@ struct RestSum {
         if (w.heavy(p)) h += rest(w.heavy_weight(p, e), i);
         else c += light_rest(w.light_weight(p, e) * 0x1p-44f, q[i]);
     }
-    __device__ __forceinline__ u64 sum() const { return h + __float2ull_rn(c * 0x1p62f); }
+    __device__ __forceinline__ u64 sum() const { return h + to_whole(c * 0x1p62f); }
     __device__ __forceinline__ u64 vector(const uint4 *at, int first) {
         constexpr int P = Type<T>::kPer;
         if (Type<T>::largest(*at) < kept.value) return 0;
@@ -502,18 +513,32 @@ struct Row {
             for (int u = 0; u < kPer; ++u) f(x[u], first + v * kPer + u);
         }
     }
-    // Every block's value to all of them; a lane then reads one.
-    __device__ __forceinline__ u64 exchange(u64 mine) {
+    // Every block's values to all of them; a lane then reads one of each.
+    template <int N = 1>
+    __device__ __forceinline__ u64 exchange(u64 a, u64 b = 0, u64 c = 0) {
         parity ^= 1;
-        if (static_cast<int>(threadIdx.x) < blocks) st_block_u64(at_block(&s->slot[parity][block], threadIdx.x), mine);
+        if (static_cast<int>(threadIdx.x) < blocks) {
+            st_block_u64(at_block(&s->slot[parity][0][block], threadIdx.x), a);
+            if (N > 1) st_block_u64(at_block(&s->slot[parity][1][block], threadIdx.x), b);
+            if (N > 2) st_block_u64(at_block(&s->slot[parity][2][block], threadIdx.x), c);
+        }
         cluster_barrier();
-        return lane < blocks ? s->slot[parity][lane] : 0;
+        return exchanged(0);
     }
+    __device__ __forceinline__ u64 exchanged(int value) const { return lane < blocks ? s->slot[parity][value][lane] : 0; }
     // The blocks' values: their sum, and that over the blocks before this one.
     __device__ __forceinline__ u64 exchange_sum(u64 mine, u64 *before) {
         const u64 v = exchange(mine), upto = warp_prefix(v, lane);
         *before = __shfl_sync(0xffffffffu, upto - v, block);
         return __shfl_sync(0xffffffffu, upto, 31);
+    }
+    // The block's sum, in all threads.
+    __device__ __forceinline__ u64 block_sum(u64 n, u64 *by_warp) {
+        n = warp_sum(n);
+        __syncthreads();
+        if (lane == 0) by_warp[warp] = n;
+        __syncthreads();
+        return warp_sum(lane < kWarps ? by_warp[lane] : 0);
     }
     // The sum of `make()` over this block's slice, which leaves those over the warps' stretches in s->warp, over the blocks before it, and over all.
     struct Total {
@@ -524,12 +549,8 @@ struct Row {
         u64 n = 0;
 #pragma unroll 1
         for (int k = 0; k < rounds; ++k) n += vector_sum(make, vector(k));
-        n = warp_sum(n);
-        __syncthreads();
-        if (lane == 0) s->warp[warp] = n;
-        __syncthreads();
         Total t;
-        t.mine = warp_sum(lane < kWarps ? s->warp[lane] : 0);
+        t.mine = block_sum(n, s->warp);
         t.all = exchange_sum(t.mine, &t.before);
         return t;
     }
@@ -586,24 +607,23 @@ struct Row {
         return at;
     }
     // Inclusive sums over the block's threads.
-    __device__ __forceinline__ u64 block_prefix(u64 v) {
-        const u64 upto = warp_prefix(v, lane);
+    template <typename N>
+    __device__ __forceinline__ N block_prefix(N v) {
+        N *scan = reinterpret_cast<N *>(s->scan[0]);
+        const N upto = warp_prefix(v, lane);
         __syncthreads();
-        if (lane == 31) s->scan[0][warp] = upto;
+        if (lane == 31) scan[warp] = upto;
         __syncthreads();
-        const u64 w = lane < kWarps ? s->scan[0][lane] : 0;
+        const N w = lane < kWarps ? scan[lane] : 0;
         return upto + __shfl_sync(0xffffffffu, warp_prefix(w, lane) - w, warp);
     }
 
     // A histogram over the cluster's tokens (bin(l, i) < 0: not counted) and the first bin at which the number (MASS: weight) of tokens from
     // bin 0 on reaches `target`; kBins if none does.  What comes before it and lies in it is left in shared memory.
     template <bool MASS, typename B>
-    __device__ __forceinline__ int reach(const Weights<T> &w, u64 target, B bin) {
-        histogram ^= 1;
-        s->count[histogram][threadIdx.x] = 0;
-        s->mass[histogram][threadIdx.x][0] = s->mass[histogram][threadIdx.x][1] = 0;
-        __syncthreads();
-        each([&](float l, int i) {
+    __device__ __forceinline__ int reach(const Weights<T> &w, u64 target, bool near_end, B bin) {
+        new_histogram();
+        over(near_end, [&](float l, int i) {
             const int b = bin(l, i);
             if (b < 0) return;
             atomicAdd(&s->count[histogram][b], 1u);
@@ -615,6 +635,22 @@ struct Row {
             }
         });
         return reached<MASS>(target);
+    }
+    __device__ __forceinline__ void new_histogram() {
+        histogram ^= 1;
+        s->count[histogram][threadIdx.x] = 0;
+        s->mass[histogram][threadIdx.x][0] = s->mass[histogram][threadIdx.x][1] = 0;
+        __syncthreads();
+    }
+    // Each token of the slice, or of those near a nucleus' end.
+    template <typename F>
+    __device__ __forceinline__ void over(bool near_end, F f) const {
+        if (near_end) {
+            for (int i = threadIdx.x; i < static_cast<int>(s->nears); i += kThreads)
+                f(value_of(s->near_end[i]), static_cast<int>(0xffffffffu - static_cast<unsigned>(s->near_end[i])));
+        } else {
+            each(f);
+        }
     }
     template <bool MASS>
     __device__ __forceinline__ int reached(u64 target) {
@@ -649,10 +685,10 @@ struct Row {
 
     // The tokens for which `wanted` holds into the blocks' lists; how many there are in all.
     template <typename W>
-    __device__ __forceinline__ int gather(W wanted) {
+    __device__ __forceinline__ int gather(W wanted, bool near_end = false) {
         if (threadIdx.x == 0) s->listed = 0;
         __syncthreads();
-        each([&](float l, int i) {
+        over(near_end, [&](float l, int i) {
             if (!wanted(l, i)) return;
             const unsigned at = atomicAdd(&s->listed, 1u);
             if (at < kList) s->list[at] = static_cast<u64>(float_order_code(l)) << 32 | (0xffffffffu - static_cast<unsigned>(i));
@@ -666,7 +702,7 @@ struct Row {
         u64 key = 0;
         int at = threadIdx.x;
         for (int b = 0; b < blocks && at >= 0; ++b) {
-            const int here = static_cast<int>(s->slot[parity][b]);  // from gather()'s exchange
+            const int here = static_cast<int>(s->slot[parity][0][b]);  // from gather()'s exchange
             if (at < here) key = ld_block_u64(at_block(&s->list[at], b));
             at -= here;
         }
@@ -693,91 +729,29 @@ struct Row {
         return key;
     }
 
-    // Narrows `kept` to the tokens up to the one at which their number (MASS: weight) in descending order reaches `target`. `from`: a
-    // logit below which none of them lies. Where WHOLE and they are few, they and the ones up to a bin's end behind them are listed
-    // instead, and their number returned; else 0.
-    template <bool MASS, bool WHOLE = false>
-    __device__ __forceinline__ int select(Kept *kept, const Weights<T> &w, u64 target, float from) {
+    // Narrows `kept` to the tokens up to the one at which their number (MASS: weight) in descending order reaches `target`, which has `above` from
+    // the tokens with l >= to. `from`: a logit below which none of them lies. False if what is left from there on does not reach it.
+    // near_end: all tokens of from <= l < to are in the lists of those.
+    template <bool MASS>
+    __device__ __forceinline__ bool select(Kept *kept, const Weights<T> &w, u64 target, float from, float to = INFINITY, u64 above = 0, bool near_end = false) {
         const Kept prior = *kept;
-        // Atomics on shared memory take about a cycle each, so the tokens that a histogram counts are narrowed down to from <= l < to first.
-        const float lowest = from;
-        float to = INFINITY;
-        u64 above = 0;  // what the tokens from `to` on weigh
-        int many = 0;   // how many they are
-        if (MASS && w.simple) {
-            const float goal = static_cast<float>(target) * 0x1p-44f;
-            for (int stage = 0; stage < 2; ++stage) {
-                const float from_here = from, high = fminf(to, w.top), step = (high - from) / 8.f;
-                if (!(step > 4.8e-7f * fabsf(high))) break;
-                float mass, count;  // lane j: of the tokens from high - (j + 1) * step on, the last one: from `from` on
-                profile(w, high, step, from, &mass, &count);
-                const unsigned less = __ballot_sync(0xffffffffu, lane < 8 && mass < goal * 0.99999f), more = __ballot_sync(0xffffffffu, lane < 8 && mass > goal * 1.00001f);
-                int in = 0x7fffffff;
-                if (more) {
-                    const int j = __ffs(more) - 1;
-                    if (j < 7) from = high - static_cast<float>(j + 1) * step;
-                    in = static_cast<int>(__shfl_sync(0xffffffffu, count, j));
-                }
-                if (less & 0x7fu) {
-                    const int j = 31 - __clz(less & 0x7fu);
-                    to = high - static_cast<float>(j + 1) * step;
-                    many = static_cast<int>(__shfl_sync(0xffffffffu, count, j));
-                }
-                if (!(from < to && from >= from_here)) {  // not with such rounding
-                    from = lowest;
-                    to = INFINITY;
-                    many = 0;
-                    break;
-                }
-                if (in - many <= 256 * blocks) break;
-            }
-            if (to < INFINITY) {
-                const Kept upper{to, 0x7fffffff};
-                above = total([&] { return MassSum<T>(w, upper); }).all;
-            }
-        }
-        float high, scale;
+        // bins of equal width first, which spread the logits best
+        const float high = fminf(to, w.top), range = high - from, scale = range > 0.f && range < 3e38f ? 511.9f / range : 0.f;
         auto linear = [&](float l, int i) {
             return l >= from && (l < to || to == INFINITY) && prior.order(l, i) ? min(static_cast<int>((high - l) * scale), kBins - 1) : -1;
         };
-        int bin = kBins;
-        for (;;) {
-            if (above < target) {
-                high = fminf(to, w.top);
-                const float range = high - from;
-                scale = range > 0.f && range < 3e38f ? 511.9f / range : 0.f;
-                bin = reach<MASS>(w, target - above, linear);
-            }
-            if (bin < kBins) break;
-            if (to == INFINITY && from == lowest) return 0;  // all of them do not reach it: nothing is dropped
-            from = lowest;  // a border of the narrowed range was a rounding off
-            to = INFINITY;
-            above = 0;
-            many = 0;
-        }
-        if (WHOLE && many + s->count_before + s->count_in <= kList)
-            return gather([&](float l, int i) { return (l >= to && to < INFINITY) || (l >= from && linear(l, i) <= bin); });
+        const int bin = reach<MASS>(w, target - above, near_end, linear);
+        if (bin == kBins) return false;
         above += MASS ? s->mass_before : s->count_before;
         if (s->count_in <= kList) {
-            const int n = gather([&](float l, int i) { return linear(l, i) == bin; });
-            if (block == 0) {
-                const u64 key = sorted_list(n);
-                const u64 in = MASS ? (key ? w.weight(value_of(key)) : 0) : (key ? 1 : 0);
-                const u64 upto = above + block_prefix(in);
-                if (in && upto >= target && upto - in < target) s->last = key;
-                __syncthreads();
-                if (static_cast<int>(threadIdx.x) < blocks) st_block_u64(at_block(&s->last, threadIdx.x), s->last);
-            }
-            cluster_barrier();
-            kept->value = value_of(s->last);
-            kept->index = 0xffffffffu - static_cast<unsigned>(s->last);
-            return 0;
+            narrow<MASS>(kept, w, target, above, gather([&](float l, int i) { return linear(l, i) == bin; }, near_end));
+            return true;
         }
         // then of equal numbers of codes, until a bin is one logit
         unsigned c0, c1;
         {
             unsigned least = 0xffffffffu, most = 0;
-            each([&](float l, int i) {
+            over(near_end, [&](float l, int i) {
                 if (linear(l, i) != bin) return;
                 least = min(least, float_order_code(l));
                 most = max(most, float_order_code(l));
@@ -786,10 +760,11 @@ struct Row {
         }
         for (;;) {
             const int bits = 32 - __clz(static_cast<int>(c1 - c0)), shift = max(bits - 9, 0);
-            const int b = reach<MASS>(w, target - above, [&](float l, int i) {
+            const int b = reach<MASS>(w, target - above, near_end, [&](float l, int i) {
                 const unsigned c = float_order_code(l);
                 return prior.order(l, i) && c >= c0 && c <= c1 ? static_cast<int>((c1 - c) >> shift) : -1;
             });
+            if (b == kBins) return false;  // not the case: the sums are whole numbers
             above += MASS ? s->mass_before : s->count_before;
             c1 -= static_cast<unsigned>(b) << shift;
             c0 = max(c0, c1 - ((1u << shift) - 1));
@@ -806,12 +781,162 @@ struct Row {
         const Total n = total(ties);
         kept->value = value;
         kept->index = value == prior.value ? prior.index : 0x7fffffff;
-        if (left >= n.all) return 0;
+        if (left >= n.all) return true;
         const bool here = left - 1 >= n.before && left - 1 < n.before + n.mine;
         if (here) find(ties, left - 1 - n.before);
         __syncthreads();
         u64 before;
         kept->index = static_cast<int>(exchange_sum(here ? s->found : 0, &before));
+        return true;
+    }
+    // The same of the n tokens just gathered, which the target is reached among.
+    template <bool MASS>
+    __device__ __forceinline__ void narrow(Kept *kept, const Weights<T> &w, u64 target, u64 above, int n) {
+        if (block == 0) {
+            const u64 key = sorted_list(n);
+            const u64 in = MASS ? (key ? w.weight(value_of(key)) : 0) : (key ? 1 : 0);
+            const u64 upto = above + block_prefix(in);
+            if (in && upto >= target && upto - in < target) s->last = key;
+            __syncthreads();
+            if (static_cast<int>(threadIdx.x) < blocks) st_block_u64(at_block(&s->last, threadIdx.x), s->last);
+        }
+        cluster_barrier();
+        kept->value = value_of(s->last);
+        kept->index = 0xffffffffu - static_cast<unsigned>(s->last);
+    }
+
+    // The kept tokens' sum z, and the nucleus of top_p of it. Returns the number of tokens listed, among which is the nucleus and all tokens
+    // before its end, where they are few (LIST; at most n are kept); else narrows `kept` and returns 0.
+    //
+    // Where the nucleus ends is looked for with as few instructions a token as there are: the sum's pass notes an eighth (fp32: a quarter) of the tokens in a
+    // histogram of eighths of powers of two, which gives that place within some percent; the next pass weighs what is before and
+    // lists what is near it, exactly. (A histogram with weights of all tokens took 100 instructions and 3 atomics, of a cycle each, a token.)
+    template <bool LIST>
+    __device__ __forceinline__ int nucleus(Kept *kept, const Weights<T> &w, float top_p, int most, u64 *z) {
+        const Kept prior = *kept;
+        if (threadIdx.x == 0) s->heavies = s->nears = 0;
+        new_histogram();
+        u64 n = 0, h = 0;
+        {
+            unsigned heavies = 0;
+#pragma unroll 1
+            for (int k = 0; k < rounds; ++k) {
+                const int v = vector(k);
+                if (v >= vectors) break;
+                MassSum<T> m(w, prior);
+                n += m.vector(data + v, first + v * kPer);
+                h += m.h;
+                heavies += m.h > 0 ? 1 : 0;
+                const float l = Type<T>::one(data + v, lane % kPer), y = (l - w.top) * w.hi;
+                if (y > -60.f && l > prior.value) atomicAdd(&s->count[histogram][min(static_cast<int>(-8.f * y), kBins - 1)], 1u);
+            }
+            heavies = __reduce_add_sync(0xffffffffu, heavies);
+            if (lane == 0 && heavies) atomicAdd(&s->heavies, heavies);
+        }
+        n = block_sum(n, s->warp);
+        h = block_sum(h, s->warp);
+        exchange<3>(n, h, s->heavies);
+        *z = warp_sum(exchanged(0));
+        h = warp_sum(exchanged(1));
+        const unsigned heavies = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(exchanged(2)));  // vectors with some
+        unsigned counted = 0;
+        {
+            unsigned v[kMaxBlocks];
+#pragma unroll
+            for (int b = 0; b < kMaxBlocks; ++b) v[b] = b < blocks ? ld_block_u32(at_block(&s->count[histogram][threadIdx.x], b)) : 0;
+#pragma unroll
+            for (int b = 0; b < kMaxBlocks; ++b) counted += v[b];
+        }
+        const u64 target = max(part_of(*z, top_p, true), 1ull);
+        const float share = (1.f - top_p) * static_cast<float>(*z) * 0x1p-44f / static_cast<float>(most);
+        // of at most `most` tokens, those lighter than an even share of what may be dropped are dropped all together
+        const float lowest = share > 1e-30f ? w.top + (log2f(share) - 0.01f) / w.hi - 4.8e-7f * fabsf(w.top) : kLowest;
+        const bool in_heavy = target <= h;
+        if (in_heavy && heavies <= kList) {
+            const int listed = gather([&](float l, int i) { return (l >= w.top || w.heavy((l - w.top) * w.hi)) && prior.order(l, i); });
+            if (listed <= kList && LIST) return listed;
+            if (listed <= kList) {
+                narrow<true>(kept, w, target, 0, listed);
+                return 0;
+            }
+        }
+        // The place by what was noted: the weight up to each bin's end from the nearest place whose weight is known (`anchor`), and four times
+        // how far that may be off. Where too many tokens lie within, the most likely place's weight is taken and the others' from there.
+        const int bin = threadIdx.x;
+        const float one = exp2f(-0.125f * (static_cast<float>(bin) + 0.5f)), c = kPer * static_cast<float>(counted);
+        const float noted = block_prefix(c * one), square = kPer * block_prefix(c * one * one), number = block_prefix(c);
+        const float goal = static_cast<float>(target) * 0x1p-44f;
+        int anchor = in_heavy ? -1 : 8 * kHeavy - 1;
+        float known = in_heavy ? 0.f : static_cast<float>(h) * 0x1p-44f;
+        auto edge = [&](int b) { return w.top - static_cast<float>(b + 1) * 0.125f / w.hi; };
+        int to_bin, from_bin;
+        for (int step = 0;; ++step) {
+            __syncthreads();
+            if (bin == 0) {
+                s->to_bin = -1;
+                s->from_bin = s->likely = kBins;
+                s->at_to = 0.f;
+                if (anchor < 0) s->at_anchor[0] = s->at_anchor[1] = 0.f;
+            }
+            __syncthreads();
+            if (bin == anchor) {
+                s->at_anchor[0] = noted;
+                s->at_anchor[1] = square;
+            }
+            __syncthreads();
+            const float from_there = noted - s->at_anchor[0];
+            const float off = 4.f * sqrtf(fabsf(square - s->at_anchor[1])) + 0.004f * fabsf(from_there) + kPer * one;
+            if (known + from_there + off < goal) atomicMax(&s->to_bin, bin);
+            if (known + from_there - off >= goal) atomicMin(&s->from_bin, bin);
+            if (known + from_there >= goal) atomicMin(&s->likely, bin);
+            __syncthreads();
+            to_bin = s->to_bin;
+            from_bin = s->from_bin;
+            if (bin == to_bin) s->at_to = number;
+            if (bin == min(from_bin, kBins - 1)) s->at_from = number;
+            __syncthreads();
+            if (step == 1 || s->at_from - s->at_to <= static_cast<float>(kNear / 2) * blocks || !w.simple) break;
+            anchor = min(s->likely, kBins - 1);
+            const Kept upper{edge(anchor), 0x7fffffff};
+            if (!(upper.value > prior.value)) break;
+            known = static_cast<float>(total([&] { return MassSum<T>(w, upper); }).all) * 0x1p-44f;
+        }
+        const float to = to_bin >= 0 ? edge(to_bin) : INFINITY, from = from_bin < kBins ? fmaxf(lowest, edge(from_bin)) : lowest;
+        const bool narrowed = w.simple && from < to && to > prior.value;
+        if (narrowed) {
+            // what weighs before `to`, and a list of what lies from there to `from`
+            const Kept upper{to, 0x7fffffff};
+            n = 0;
+#pragma unroll 1
+            for (int k = 0; k < rounds; ++k) {
+                const int v = vector(k);
+                if (v >= vectors) break;
+                const float largest = Type<T>::largest(data[v]);
+                if (largest >= to) n += MassSum<T>(w, upper).vector(data + v, first + v * kPer);
+                if (largest < from) continue;
+                float x[kPer];
+                Type<T>::spread(data[v], x);
+                unsigned some = 0;
+#pragma unroll
+                for (int u = 0; u < kPer; ++u)
+                    if (x[u] >= from && x[u] < to) some |= 1u << u;
+                for (; some; some &= some - 1) {
+                    const int i = first + v * kPer + __ffs(some) - 1;
+                    const float l = Type<T>::one(data + v, __ffs(some) - 1);
+                    if (!prior.order(l, i)) continue;
+                    const unsigned at = atomicAdd(&s->nears, 1u);
+                    if (at < kNear) s->near_end[at] = static_cast<u64>(float_order_code(l)) << 32 | (0xffffffffu - static_cast<unsigned>(i));
+                }
+            }
+            n = block_sum(n, s->warp);
+            exchange<2>(n, s->nears);
+            const u64 above = warp_sum(exchanged(0));
+            const unsigned nears = static_cast<unsigned>(exchanged(1));
+            if (above < target && __reduce_max_sync(0xffffffffu, nears) <= kNear) {
+                if (select<true>(kept, w, target, from, to, above, true)) return 0;
+            }
+        }
+        select<true>(kept, w, target, lowest);
         return 0;
     }
     // Narrows `kept` to tokens of at least min_p. Weights never fall with the logits, so there is a largest one that is too small: each
@@ -832,65 +957,6 @@ struct Row {
         }
         const float value = value_of(static_cast<u64>(low) << 32);
         if (value > kept->value) *kept = {value, kNoIndex};
-    }
-    // About the weight (in units of the heaviest one) and the number of the tokens with l >= high - (j + 1) step, in lane j < 7, and with
-    // l >= low, in lane 7.
-    __device__ __forceinline__ void profile(const Weights<T> &w, float high, float step, float low, float *mass, float *count) {
-        float t[8];
-        u64 acc[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            t[j] = j < 7 ? high - static_cast<float>(j + 1) * step : low;
-            acc[j] = 0;
-        }
-        const uint4 clamp = make_uint4(w.clamp, w.clamp, w.clamp, w.clamp);
-#pragma unroll 1
-        for (int k = 0; k < rounds; ++k) {
-            const int v = vector(k);
-            if (v >= vectors) break;
-            const uint4 d = data[v];
-            if (!(Type<T>::largest(d) >= low)) continue;
-            float x[kPer];
-            Type<T>::spread(Type<T>::larger(d, clamp), x);
-#pragma unroll
-            for (int u = 0; u < kPer; ++u) {
-                const u64 one = pair_f32(fast_exp2((x[u] - w.top) * w.hi), 1.f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (x[u] >= t[j]) acc[j] = add_f32x2(acc[j], one);
-            }
-        }
-        // sixteen sums over the warp: halves change hands, so that lane 2k ends with sum k
-        float v[16];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) split_f32(acc[j], &v[j], &v[8 + j]);
-#pragma unroll
-        for (int h = 8; h >= 1; h /= 2) {
-            const bool upper = (lane & (2 * h)) != 0;
-#pragma unroll
-            for (int j = 0; j < h; ++j) {
-                const float got = __shfl_xor_sync(0xffffffffu, upper ? v[j] : v[j + h], 2 * h);
-                v[j] = (upper ? v[j + h] : v[j]) + got;
-            }
-        }
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
-        __syncthreads();
-        if ((lane & 1) == 0) s->part[warp][lane >> 1] = v[0];
-        __syncthreads();
-        parity ^= 1;
-        if (static_cast<int>(threadIdx.x) < 16 * blocks) {
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) sum += s->part[k][threadIdx.x & 15];
-            st_block_u32(at_block(&s->profile[parity][block][threadIdx.x & 15], threadIdx.x >> 4), __float_as_uint(sum));
-        }
-        cluster_barrier();
-        float sum = 0.f;
-#pragma unroll
-        for (int b = 0; b < kMaxBlocks; ++b)
-            if (b < blocks) sum += s->profile[parity][b][lane & 15];
-        *mass = sum;
-        *count = __shfl_sync(0xffffffffu, sum, (lane & 7) + 8);
     }
     // The least and the largest of the cluster's codes.
     __device__ __forceinline__ void exchange_range(unsigned least, unsigned most, unsigned *c0, unsigned *c1) {
@@ -1106,11 +1172,6 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
         finish = candidates <= kList;
     };
     auto drop_light = [&] { return max(part_of(z, given.top_p, true), 1ull); };  // what the nucleus has to weigh, of the sum z
-    // Of n tokens that weigh z, those lighter than an even share of what may be dropped are dropped all together: a bound from below.
-    auto above_share = [&](int n) {
-        const float share = (1.f - given.top_p) * static_cast<float>(z) * 0x1p-44f / static_cast<float>(n);
-        return share > 1e-30f ? fmaxf(cut, top + (log2f(share) - 0.01f) / weights.hi - 4.8e-7f * fabsf(top)) : cut;
-    };
     if (top_k > 0) {
         // The top_k-th largest of the threads' maxima is a bound from below.
         bool bounded = g.vocab <= kList;
@@ -1128,9 +1189,7 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
         }
         if (bounded) list_all();
     } else if (by_p) {
-        z = row.total(mass).all;
-        const u64 goal = drop_light();
-        candidates = row.template select<true, true>(&kept, weights, goal, above_share(g.vocab));
+        candidates = row.template nucleus<true>(&kept, weights, given.top_p, g.vocab, &z);
         finish = candidates > 0;
     } else if (by_floor) {
         list_all();
@@ -1206,10 +1265,7 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
     if (!finish) {
         if (top_k > 0) {
             row.template select<false>(&kept, weights, top_k, cut);
-            if (by_p) {
-                z = row.total(mass).all;
-                row.template select<true>(&kept, weights, drop_light(), above_share(top_k));
-            }
+            if (by_p) row.template nucleus<false>(&kept, weights, given.top_p, top_k, &z);
         }
         if (by_floor) row.drop_below(&kept, weights, given);
         sums = row.total(mass);

@@ -728,7 +728,7 @@ dspark_status dspark_paged_attention_debug(const dspark_cache *cache, const dspa
  * same and the others nothing.  A row without tokens draws -1 and has p = 0.
  * Sums are taken in 64-bit fixed point and do not depend on their order: the same inputs give the
  * same tokens, whatever the number of rows or SMs.  Weights are off by less than 2^-27 of themselves,
- * those below 2^-8 by 2^-28 of the heaviest one.
+ * those below 2^-6 by less than 2^-27 of the heaviest one.
  *
  * Filters: each setting is an array, an entry for each row (dspark_sample) or sequence
  * (dspark_verify_drafts), or where that is NULL the number for all.  The numbers are checked

@@ -1,7 +1,7 @@
 """Drawing tokens and judging drafts against the 64-bit reference, at the sizes, types and settings where they can go wrong.
 
 Ids have to be equal.  A uniform number closer than 1e-7 of the row's mass to a border between two tokens says nothing (weights are off by
-2^-27, or 2^-28 of the heaviest one's, and the reference's own sums by 1e-16): such numbers are moved before the first run, in `away`.
+2^-27, or 2^-27 of the heaviest one's, and the reference's own sums by 1e-16): such numbers are moved before the first run, in `away`.
 The distribution is rounded to fp32: the light weights' fast exponential is off by 2^-22, their product, the sum's and its reciprocal's
 rounding and the last product by 2^-24 each, so less than 2^-21 of a value together; and a light weight's difference of logits d is rounded
 to 32 bits, |d| 2^-24, so its weight exp(d / T) by 2^-24 of |d / T| = |ln w| of itself."""
