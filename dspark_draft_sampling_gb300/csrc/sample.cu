@@ -72,8 +72,10 @@ struct alignas(16) Shared {
     alignas(8) unsigned mass[2][kBins][2];  // low and high half of 64 bits
     u64 slot[2][3][kMaxBlocks];  // [parity][value][block]: what the blocks exchange
     u64 list[kList];             // this block's tokens of a list, read by the first block: order code and what is left of 2^32 behind the index
-    u64 near_end[kNear];         // tokens in the same form, this block's own
-    u64 sort[2][kList];
+    union {                      // lists are sorted when what lies near a nucleus' end is no longer wanted
+        u64 near_end[kNear];     // tokens in the same form, this block's own
+        u64 sort[2][kList];
+    };
     u64 warp[kWarps];            // sums over the warps' stretches of the slice
     u64 scan[2][kWarps];
     u64 inverse, last;           // last: of the kept tokens, as in the list
@@ -1376,6 +1378,7 @@ cudaError_t launch_cluster(void (*kernel)(Args...), int grid, int cluster, int t
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+constexpr long long kGoodSlice = 84 * 1024;  // two blocks to an SM
 constexpr int kMostSlice = 128 * 1024;  // bytes; kMaxVocab fp32 logits over kMaxBlocks blocks
 
 template <typename T, bool VERIFY>
@@ -1391,10 +1394,18 @@ dspark_status launch(Draw g, int sms, cudaStream_t stream) {
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(sample)");
         if (dev < 64) configured.fetch_or(1ull << dev);
     }
-    int blocks = 1;
-    const long long size = sizeof(T);
-    while (blocks < kMaxBlocks && (g.vocab * size > 64 * 1024ll * blocks || (2ll * g.rows * blocks <= sms && g.vocab > 2048 * blocks)))
-        blocks *= 2;
+    // Blocks of a row's cluster: a block takes some time whatever its slice, about that of 8 KB of it, and two of them share an SM. 96 rows of
+    // 151936 (bf16, nuclei) over 4 | 8 | 16 blocks 227 | 186 | 212 us, 28 of them (fp32) over 8 | 16 61 | 83.
+    const long long size = sizeof(T), bytes = g.vocab * size, slots = 2ll * sms;
+    int blocks = 0;
+    long long least = 0;
+    for (int b = 1; b <= kMaxBlocks; b *= 2) {
+        const long long slice = (bytes + b - 1) / b, cost = (g.rows * static_cast<long long>(b) + slots - 1) / slots * (slice + 8 * 1024);
+        if (slice <= (b < kMaxBlocks ? kGoodSlice : kMostSlice) && (blocks == 0 || cost < least)) {
+            blocks = b;
+            least = cost;
+        }
+    }
     const int per = 16 / static_cast<int>(size);
     g.slice = ((g.vocab + blocks - 1) / blocks + per - 1) / per * per;
     const size_t smem = sizeof(Shared) + (g.slice + per) * size;
