@@ -24,6 +24,10 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = kThreads;           // of a histogram: a thread looks after one
+constexpr int kBinBits = kBins == 512 ? 9 : 8;
+static_assert(1 << kBinBits == kBins, "");
+constexpr int kOctave = kBins / 64;       // of them to a power of two, where they divide weights
+constexpr float kSpread = kBins - 0.1f;   // bins of equal width over a range, short of the end
 constexpr int kList = kThreads;           // tokens that one block sorts: a thread to each
 constexpr int kNear = 1024;               // tokens of a block's slice around a nucleus' end
 constexpr int kMaxBlocks = 16;            // of a cluster
@@ -167,7 +171,7 @@ template <typename T>
 struct Type;
 template <>
 struct Type<float> {
-    static constexpr int kPer = 4;
+    static constexpr int kVector = 4, kPer = 2 * kVector;  // tokens of 16 bytes, and of the 32 that a thread takes at a time
     static constexpr unsigned kMasked = 0xff800000u;  // -infinity
     static __device__ __forceinline__ void spread(uint4 v, float *x) {
         x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
@@ -188,7 +192,7 @@ struct Type<float> {
 };
 template <>
 struct Type<__nv_bfloat16> {
-    static constexpr int kPer = 8;
+    static constexpr int kVector = 8, kPer = 2 * kVector;
     static constexpr unsigned kMasked = 0xff80ff80u;
     static __device__ __forceinline__ void spread(uint4 v, float *x) {
         const unsigned w[4] = {v.x, v.y, v.z, v.w};
@@ -217,7 +221,7 @@ struct Type<__nv_bfloat16> {
 };
 template <>
 struct Type<__half> {
-    static constexpr int kPer = 8;
+    static constexpr int kVector = 8, kPer = 2 * kVector;
     static constexpr unsigned kMasked = 0xfc00fc00u;
     static __device__ __forceinline__ void spread(uint4 v, float *x) {
         const unsigned w[4] = {v.x, v.y, v.z, v.w};
@@ -320,23 +324,22 @@ struct Kept {
     __device__ __forceinline__ bool order(float l, int i) const { return l > value || (l == value && i <= index); }
 };
 
-// The weights of a vector's light tokens in 32 bits (in units of the heaviest one), two at a time: some 10 instructions a token where the
-// general form takes 40 and more. 0 for those that are not kept, and for the ones whose bits are returned: tokens that are not light, or
+// take(u, weights of tokens 2u and 2u + 1) for a vector's light tokens, in 32 bits and units of the heaviest one: some 10 instructions a token where the
+// general form takes 40 and more. 0 (or not called) for those that are not kept, and for the ones whose bits are returned: tokens that are not light, or
 // as large as the last kept one, of which indices decide. They are few, and looked at one by one.
-template <typename T>
-__device__ __forceinline__ unsigned light_weights(const Weights<T> &w, const Kept &kept, uint4 v, float (&x)[Type<T>::kPer]) {
+template <typename T, typename F>
+__device__ __forceinline__ unsigned light_weights(const Weights<T> &w, const Kept &kept, const uint4 *at, F take) {
     constexpr int P = Type<T>::kPer;
-    const float most = Type<T>::largest(v);
-    if (most < kept.value || !w.simple) {
-#pragma unroll
-        for (int u = 0; u < P; ++u) x[u] = 0.f;
-        return w.simple ? 0u : (1u << P) - 1u;
-    }
+    const uint4 v0 = at[0], v1 = at[1];
+    const float most = Type<T>::largest(Type<T>::larger(v0, v1));
+    if (most < kept.value || !w.simple) return w.simple ? 0u : (1u << P) - 1u;
     const uint4 c = make_uint4(w.clamp, w.clamp, w.clamp, w.clamp);
-    Type<T>::spread(Type<T>::larger(v, c), x);  // also from NaN and -infinity
-    const float none = w.top + w.least;
+    float x[P];
+    Type<T>::spread(Type<T>::larger(v0, c), x);  // also from NaN and -infinity
+    Type<T>::spread(Type<T>::larger(v1, c), x + P / 2);
     unsigned special = 0;
     if (w.heavy((most - w.top) * w.hi)) {
+        const float none = w.top + w.least;
 #pragma unroll
         for (int u = 0; u < P; ++u)
             if (w.heavy((x[u] - w.top) * w.hi)) {
@@ -345,6 +348,7 @@ __device__ __forceinline__ unsigned light_weights(const Weights<T> &w, const Kep
             }
     }
     if (kept.value > -INFINITY) {
+        const float none = w.top + w.least;
 #pragma unroll
         for (int u = 0; u < P; ++u) {
             if (x[u] == kept.value) special |= 1u << u;
@@ -360,7 +364,7 @@ __device__ __forceinline__ unsigned light_weights(const Weights<T> &w, const Kep
         float a, b;
         split_f32(p, &a, &b);
         const u64 two = pair_f32(fast_exp2(a), fast_exp2(b));
-        split_f32(fma_f32x2(mul_f32x2(two, less_ln2), e, two), &x[2 * u], &x[2 * u + 1]);
+        take(u, fma_f32x2(mul_f32x2(two, less_ln2), e, two));
     }
     return special;
 }
@@ -385,18 +389,18 @@ struct MassSum {
     __device__ __forceinline__ u64 sum() const { return h + w.whole(c); }
     __device__ __forceinline__ u64 vector(const uint4 *at, int first) {
         constexpr int P = Type<T>::kPer;
-        float x[P];
-        unsigned special = light_weights(w, kept, *at, x);
-        if (static_cast<unsigned>(skip - first) < P) {
-#pragma unroll
-            for (int u = 0; u < P; ++u)
-                if (first + u == skip) x[u] = 0.f;
-        }
-        u64 s = pair_f32(x[0], x[1]);
-#pragma unroll
-        for (int u = 1; u < P / 2; ++u) s = add_f32x2(s, pair_f32(x[2 * u], x[2 * u + 1]));
+        u64 s[2] = {0, 0};
+        const bool skips = static_cast<unsigned>(skip - first) < P;
+        unsigned special = light_weights(w, kept, at, [&](int u, u64 two) {
+            if (skips && (skip - first) >> 1 == u) {
+                float a, b;
+                split_f32(two, &a, &b);
+                two = (skip - first) & 1 ? pair_f32(a, 0.f) : pair_f32(0.f, b);
+            }
+            s[u & 1] = add_f32x2(s[u & 1], two);
+        });
         float a, b;
-        split_f32(s, &a, &b);
+        split_f32(add_f32x2(s[0], s[1]), &a, &b);
         c = (a + b) * 0x1p44f;
         for (; special; special &= special - 1) {
             const int u = __ffs(special) - 1;
@@ -416,7 +420,8 @@ struct TieSum {
     __device__ __forceinline__ u64 sum() const { return n; }
     __device__ __forceinline__ u64 vector(const uint4 *at, int first) {
         float x[Type<T>::kPer];
-        Type<T>::spread(*at, x);
+        Type<T>::spread(at[0], x);
+        Type<T>::spread(at[1], x + Type<T>::kVector);
 #pragma unroll
         for (int u = 0; u < Type<T>::kPer; ++u) add(x[u], first + u);
         return n;
@@ -469,9 +474,7 @@ struct RestSum {
     __device__ __forceinline__ u64 sum() const { return h + to_whole(c * 0x1p62f); }
     __device__ __forceinline__ u64 vector(const uint4 *at, int first) {
         constexpr int P = Type<T>::kPer;
-        if (Type<T>::largest(*at) < kept.value) return 0;
-        float x[P];
-        unsigned special = light_weights(w, kept, *at, x);
+        if (Type<T>::largest(Type<T>::larger(at[0], at[1])) < kept.value) return 0;
         alignas(16) float share[P];
         if (first >= 0 && first + P <= vocab && (reinterpret_cast<uintptr_t>(q + first) & 15) == 0) {
 #pragma unroll
@@ -480,8 +483,11 @@ struct RestSum {
 #pragma unroll
             for (int u = 0; u < P; ++u) share[u] = first + u >= 0 && first + u < vocab ? q[first + u] : 0.f;
         }
-#pragma unroll
-        for (int u = 0; u < P; ++u) c += light_rest(x[u], share[u]);
+        unsigned special = light_weights(w, kept, at, [&](int u, u64 two) {
+            float a, b;
+            split_f32(two, &a, &b);
+            c += light_rest(a, share[2 * u]) + light_rest(b, share[2 * u + 1]);
+        });
         for (; special; special &= special - 1) {
             const int u = __ffs(special) - 1;
             add(Type<T>::one(at, u), first + u);
@@ -500,6 +506,10 @@ struct Row {
     int vectors, rounds, first;  // vectors of the slice, of a thread; index of the first vector's first element (which may lie before the slice)
     int parity, histogram;
 
+    __device__ __forceinline__ void spread(int v, float *x) const {
+        Type<T>::spread(data[2 * v], x);
+        Type<T>::spread(data[2 * v + 1], x + Type<T>::kVector);
+    }
     // Warp w takes a stretch of neighbouring vectors, so that index order is the order of warps, rounds, lanes and elements.
     __device__ __forceinline__ int vector(int round) const { return (warp * rounds + round) * 32 + lane; }
 
@@ -510,7 +520,7 @@ struct Row {
             const int v = vector(k);
             if (v >= vectors) break;
             float x[kPer];
-            Type<T>::spread(data[v], x);
+            spread(v, x);
 #pragma unroll
             for (int u = 0; u < kPer; ++u) f(x[u], first + v * kPer + u);
         }
@@ -559,7 +569,7 @@ struct Row {
     template <typename M>
     __device__ __forceinline__ u64 vector_sum(M make, int v) const {
         auto a = make();
-        return v < vectors ? a.vector(data + v, first + v * kPer) : 0;
+        return v < vectors ? a.vector(data + 2 * v, first + v * kPer) : 0;
     }
     // The first token at which the sum over the slice, taken just before by total(), exceeds `target` (less than it): its index, in s->found.
     // Called by the whole block. The stretch of the warp that it falls to is looked at by all warps, a round each.
@@ -588,7 +598,7 @@ struct Row {
             const int at = first + __shfl_sync(0xffffffffu, v, owner) * kPer;
             // a lane to each of its tokens; their sum may be a rounding less than the vector's: then the last that weighs anything
             float x[kPer];
-            Type<T>::spread(data[__shfl_sync(0xffffffffu, v, owner)], x);
+            spread(__shfl_sync(0xffffffffu, v, owner), x);
             auto a = make();
 #pragma unroll
             for (int u = 0; u < kPer; ++u)
@@ -738,7 +748,7 @@ struct Row {
     __device__ __forceinline__ bool select(Kept *kept, const Weights<T> &w, u64 target, float from, float to = INFINITY, u64 above = 0, bool near_end = false) {
         const Kept prior = *kept;
         // bins of equal width first, which spread the logits best
-        const float high = fminf(to, w.top), range = high - from, scale = range > 0.f && range < 3e38f ? 511.9f / range : 0.f;
+        const float high = fminf(to, w.top), range = high - from, scale = range > 0.f && range < 3e38f ? kSpread / range : 0.f;
         auto linear = [&](float l, int i) {
             return l >= from && (l < to || to == INFINITY) && prior.order(l, i) ? min(static_cast<int>((high - l) * scale), kBins - 1) : -1;
         };
@@ -761,7 +771,7 @@ struct Row {
             exchange_range(least, most, &c0, &c1);
         }
         for (;;) {
-            const int bits = 32 - __clz(static_cast<int>(c1 - c0)), shift = max(bits - 9, 0);
+            const int bits = 32 - __clz(static_cast<int>(c1 - c0)), shift = max(bits - kBinBits, 0);
             const int b = reach<MASS>(w, target - above, near_end, [&](float l, int i) {
                 const unsigned c = float_order_code(l);
                 return prior.order(l, i) && c >= c0 && c <= c1 ? static_cast<int>((c1 - c) >> shift) : -1;
@@ -815,6 +825,7 @@ struct Row {
     // lists what is near it, exactly. (A histogram with weights of all tokens took 100 instructions and 3 atomics, of a cycle each, a token.)
     template <bool LIST>
     __device__ __forceinline__ int nucleus(Kept *kept, const Weights<T> &w, float top_p, int most, u64 *z) {
+        constexpr int kNoted = Type<T>::kVector;  // one of so many
         const Kept prior = *kept;
         if (threadIdx.x == 0) s->heavies = s->nears = 0;
         new_histogram();
@@ -826,11 +837,14 @@ struct Row {
                 const int v = vector(k);
                 if (v >= vectors) break;
                 MassSum<T> m(w, prior);
-                n += m.vector(data + v, first + v * kPer);
+                n += m.vector(data + 2 * v, first + v * kPer);
                 h += m.h;
                 heavies += m.h > 0 ? 1 : 0;
-                const float l = Type<T>::one(data + v, lane % kPer), y = (l - w.top) * w.hi;
-                if (y > -60.f && l > prior.value) atomicAdd(&s->count[histogram][min(static_cast<int>(-8.f * y), kBins - 1)], 1u);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float l = Type<T>::one(data + 2 * v + half, lane % kNoted), y = (l - w.top) * w.hi;
+                    if (y > -60.f && l > prior.value) atomicAdd(&s->count[histogram][min(static_cast<int>(-static_cast<float>(kOctave) * y), kBins - 1)], 1u);
+                }
             }
             heavies = __reduce_add_sync(0xffffffffu, heavies);
             if (lane == 0 && heavies) atomicAdd(&s->heavies, heavies);
@@ -865,12 +879,12 @@ struct Row {
         // The place by what was noted: the weight up to each bin's end from the nearest place whose weight is known (`anchor`), and four times
         // how far that may be off. Where too many tokens lie within, the most likely place's weight is taken and the others' from there.
         const int bin = threadIdx.x;
-        const float one = exp2f(-0.125f * (static_cast<float>(bin) + 0.5f)), c = kPer * static_cast<float>(counted);
-        const float noted = block_prefix(c * one), square = kPer * block_prefix(c * one * one), number = block_prefix(c);
+        const float one = exp2f(-(static_cast<float>(bin) + 0.5f) / kOctave), c = kNoted * static_cast<float>(counted);
+        const float noted = block_prefix(c * one), square = kNoted * block_prefix(c * one * one), number = block_prefix(c);
         const float goal = static_cast<float>(target) * 0x1p-44f;
-        int anchor = in_heavy ? -1 : 8 * kHeavy - 1;
+        int anchor = in_heavy ? -1 : kOctave * kHeavy - 1;
         float known = in_heavy ? 0.f : static_cast<float>(h) * 0x1p-44f;
-        auto edge = [&](int b) { return w.top - static_cast<float>(b + 1) * 0.125f / w.hi; };
+        auto edge = [&](int b) { return w.top - static_cast<float>(b + 1) / (kOctave * w.hi); };
         int to_bin, from_bin;
         for (int step = 0;; ++step) {
             __syncthreads();
@@ -887,7 +901,7 @@ struct Row {
             }
             __syncthreads();
             const float from_there = noted - s->at_anchor[0];
-            const float off = 4.f * sqrtf(fabsf(square - s->at_anchor[1])) + 0.004f * fabsf(from_there) + kPer * one;
+            const float off = 4.f * sqrtf(fabsf(square - s->at_anchor[1])) + 0.004f * fabsf(from_there) + kNoted * one;
             if (known + from_there + off < goal) atomicMax(&s->to_bin, bin);
             if (known + from_there - off >= goal) atomicMin(&s->from_bin, bin);
             if (known + from_there >= goal) atomicMin(&s->likely, bin);
@@ -913,18 +927,18 @@ struct Row {
             for (int k = 0; k < rounds; ++k) {
                 const int v = vector(k);
                 if (v >= vectors) break;
-                const float largest = Type<T>::largest(data[v]);
-                if (largest >= to) n += MassSum<T>(w, upper).vector(data + v, first + v * kPer);
+                const float largest = Type<T>::largest(Type<T>::larger(data[2 * v], data[2 * v + 1]));
+                if (largest >= to) n += MassSum<T>(w, upper).vector(data + 2 * v, first + v * kPer);
                 if (largest < from) continue;
                 float x[kPer];
-                Type<T>::spread(data[v], x);
+                spread(v, x);
                 unsigned some = 0;
 #pragma unroll
                 for (int u = 0; u < kPer; ++u)
                     if (x[u] >= from && x[u] < to) some |= 1u << u;
                 for (; some; some &= some - 1) {
                     const int i = first + v * kPer + __ffs(some) - 1;
-                    const float l = Type<T>::one(data + v, __ffs(some) - 1);
+                    const float l = Type<T>::one(data + 2 * v, __ffs(some) - 1);
                     if (!prior.order(l, i)) continue;
                     const unsigned at = atomicAdd(&s->nears, 1u);
                     if (at < kNear) s->near_end[at] = static_cast<u64>(float_order_code(l)) << 32 | (0xffffffffu - static_cast<unsigned>(i));
@@ -1095,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all blocks run: their shared memory may be written to
 
     const size_t row_at = static_cast<size_t>(r) * g.logits_stride;
-    constexpr int P = Row<T>::kPer, kBatch = 8;
+    constexpr int P = Row<T>::kPer, V = Type<T>::kVector, kBatch = 8;
     const int begin = min(row.block * g.slice, g.vocab), n = min(g.slice, g.vocab - begin);
     const T *from = static_cast<const T *>(g.logits) + row_at + begin;
     const int off = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15) / static_cast<int>(sizeof(T));
@@ -1103,14 +1117,14 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
     row.vectors = n > 0 ? (off + n + P - 1) / P : 0;
     row.rounds = (row.vectors + kThreads - 1) / kThreads;
     const uint4 *whole = reinterpret_cast<const uint4 *>(from - off);
-    const int full0 = off ? 1 : 0, full1 = (off + n) / P;
+    const int full0 = off ? 1 : 0, full1 = (off + n) / V, loads = 2 * row.vectors;
     uint4 v[kBatch];
     auto request = [&](int k0) {
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const int at = row.vector(k0 + j);
+            const int at = (k0 + j) * kThreads + threadIdx.x;
             v[j] = make_uint4(Type<T>::kMasked, Type<T>::kMasked, Type<T>::kMasked, Type<T>::kMasked);
-            if (k0 + j < row.rounds && at >= full0 && at < full1) v[j] = ldg_nc_v4(whole + at);
+            if (at >= full0 && at < full1) v[j] = ldg_nc_v4(whole + at);
         }
     };
     request(0);
@@ -1123,17 +1137,17 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
     }
     // ---- the slice into shared memory, and the largest logit ----
     uint4 most = make_uint4(Type<T>::kMasked, Type<T>::kMasked, Type<T>::kMasked, Type<T>::kMasked);
-    for (int k0 = 0; k0 < row.rounds; k0 += kBatch) {
+    for (int k0 = 0; k0 * kThreads < loads; k0 += kBatch) {
         if (k0 > 0) request(k0);
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const int at = row.vector(k0 + j);
-            if (k0 + j >= row.rounds || at >= row.vectors) break;
+            const int at = (k0 + j) * kThreads + threadIdx.x;
+            if (at >= loads) break;
             if (at < full0 || at >= full1) {  // the slice's ends: element by element
-                alignas(16) T part[P];
+                alignas(16) T part[V];
                 *reinterpret_cast<uint4 *>(part) = v[j];
-                for (int e = 0; e < P; ++e)
-                    if (at * P + e >= off && at * P + e < off + n) part[e] = from[at * P + e - off];
+                for (int e = 0; e < V; ++e)
+                    if (at * V + e >= off && at * V + e < off + n) part[e] = from[at * V + e - off];
                 v[j] = *reinterpret_cast<uint4 *>(part);
             }
             const_cast<uint4 *>(row.data)[at] = v[j];
@@ -1181,11 +1195,11 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
             row.histogram ^= 1;
             s->count[row.histogram][threadIdx.x] = 0;
             __syncthreads();
-            const float range = top - value_of(static_cast<u64>(least) << 32), scale = range > 0.f && range < 3e38f ? 511.9f / range : 0.f;
+            const float range = top - value_of(static_cast<u64>(least) << 32), scale = range > 0.f && range < 3e38f ? kSpread / range : 0.f;
             if (mine > -INFINITY) atomicAdd(&s->count[row.histogram][min(static_cast<int>((top - mine) * scale), kBins - 1)], 1u);
             const int bin = row.template reached<false>(top_k);
             if (bin < kBins) {
-                cut = fmaxf(cut, top - (static_cast<float>(bin) + 1.001f) * (range / 511.9f) - 4.8e-7f * fabsf(top));
+                cut = fmaxf(cut, top - (static_cast<float>(bin) + 1.001f) * (range / kSpread) - 4.8e-7f * fabsf(top));
                 bounded = true;
             }
         }
@@ -1283,9 +1297,11 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
             const int at = row.vector(k), i0 = row.first + at * P;
             if (at >= row.vectors) break;
             float y[P];
-            unsigned special = light_weights(weights, kept, row.data[at], y);
 #pragma unroll
-            for (int e = 0; e < P; ++e) y[e] *= 0x1p44f * scale;
+            for (int e = 0; e < P; ++e) y[e] = 0.f;
+            unsigned special = light_weights(weights, kept, row.data + 2 * at, [&](int u, u64 two) {
+                split_f32(mul_f32x2(two, pair_f32(0x1p44f * scale, 0x1p44f * scale)), &y[2 * u], &y[2 * u + 1]);
+            });
             if (wide && i0 >= begin && i0 + P <= end) {
 #pragma unroll
                 for (int e = 0; e < P; e += 4) __stcs(reinterpret_cast<float4 *>(probs_to + i0 + e), make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]));
@@ -1296,7 +1312,7 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
             }
             for (; special; special &= special - 1) {
                 const int e = __ffs(special) - 1;
-                const float l = Type<T>::one(row.data + at, e);
+                const float l = Type<T>::one(row.data + 2 * at, e);
                 if (!kept.order(l, i0 + e) || i0 + e < begin || i0 + e >= end) continue;
                 float p, rest;
                 weights.exponent(l, &p, &rest);
@@ -1389,7 +1405,7 @@ dspark_status launch(Draw g, int sms, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     if (dev >= 64 || !(configured.load() >> dev & 1)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Shared)) + kMostSlice + 16);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Shared)) + kMostSlice + 128);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(sample)");
         if (dev < 64) configured.fetch_or(1ull << dev);
@@ -1406,9 +1422,9 @@ dspark_status launch(Draw g, int sms, cudaStream_t stream) {
             least = cost;
         }
     }
-    const int per = 16 / static_cast<int>(size);
+    const int per = 16 / static_cast<int>(size);  // whole vectors: all slices begin at the same place of one
     g.slice = ((g.vocab + blocks - 1) / blocks + per - 1) / per * per;
-    const size_t smem = sizeof(Shared) + (g.slice + per) * size;
+    const size_t smem = sizeof(Shared) + g.slice * size + 64;  // what stands before the slice's first vector and fills its last one
     e = launch_cluster(kernel, g.rows * blocks, blocks, kThreads, smem, stream, g);
     return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, VERIFY ? "verify_drafts" : "sample");
 }
