@@ -32,6 +32,7 @@ constexpr int kList = kThreads;           // tokens that one block sorts: a thre
 constexpr int kNear = 1024;               // tokens of a block's slice around a nucleus' end
 constexpr int kMaxBlocks = 16;            // of a cluster
 constexpr int kHeavy = 6;                 // powers of two below the heaviest token down to which weights are exact to 28 bits
+constexpr int kCounted = 10;               // powers of two below it down to which a nucleus' end is looked for among all tokens
 constexpr float kLowest = -3.402823466e38f;
 constexpr int kNoIndex = -0x7fffffff;      // before all indices, also those of what pads a slice
 constexpr int kMaxVocab = 1 << 19;        // 2^19 weights of 2^44 stay below 2^64
@@ -371,16 +372,16 @@ __device__ __forceinline__ unsigned light_weights(const Weights<T> &w, const Kep
 
 // Sums over a vector's tokens, in index order: the sum up to a token never falls, and the sum over the vector is the same whenever it is
 // taken.
-template <typename T>
+template <typename T, bool SKIP = false>
 struct MassSum {
     const Weights<T> &w;
     const Kept &kept;
-    int skip;  // a token left out, or -1
+    int skip;  // a token left out
     u64 h = 0;
     float c = 0.f;
     __device__ __forceinline__ MassSum(const Weights<T> &a, const Kept &b, int without = -1) : w(a), kept(b), skip(without) {}
     __device__ __forceinline__ void add(float l, int i) {
-        if (!kept.order(l, i) || i == skip) return;
+        if (!kept.order(l, i) || (SKIP && i == skip)) return;
         float p, e;
         w.exponent(l, &p, &e);
         if (w.heavy(p)) h += w.heavy_weight(p, e);
@@ -392,7 +393,7 @@ struct MassSum {
         u64 s[2] = {0, 0};
         const bool skips = static_cast<unsigned>(skip - first) < P;
         unsigned special = light_weights(w, kept, at, [&](int u, u64 two) {
-            if (skips && (skip - first) >> 1 == u) {
+            if (SKIP && skips && (skip - first) >> 1 == u) {
                 float a, b;
                 split_f32(two, &a, &b);
                 two = (skip - first) & 1 ? pair_f32(a, 0.f) : pair_f32(0.f, b);
@@ -820,9 +821,10 @@ struct Row {
     // The kept tokens' sum z, and the nucleus of top_p of it. Returns the number of tokens listed, among which is the nucleus and all tokens
     // before its end, where they are few (LIST; at most n are kept); else narrows `kept` and returns 0.
     //
-    // Where the nucleus ends is looked for with as few instructions a token as there are: the sum's pass notes an eighth (fp32: a quarter) of the tokens in a
-    // histogram of eighths of powers of two, which gives that place within some percent; the next pass weighs what is before and
-    // lists what is near it, exactly. (A histogram with weights of all tokens took 100 instructions and 3 atomics, of a cycle each, a token.)
+    // Where the nucleus ends is looked for with as few instructions a token as there are. The sum's pass counts tokens in a histogram of
+    // eighths of powers of two: the heavier ones, and of the lighter ones an eighth (fp32: a quarter). That gives the place within some percent
+    // or less; the next pass weighs what is before it and lists what is near it, exactly. (A histogram with weights of all tokens took 100
+    // instructions and 3 atomics, of a cycle each, a token: 96 rows at temperature 1.6 326 us instead of 180.)
     template <bool LIST>
     __device__ __forceinline__ int nucleus(Kept *kept, const Weights<T> &w, float top_p, int most, u64 *z) {
         constexpr int kNoted = Type<T>::kVector;  // one of so many
@@ -830,6 +832,7 @@ struct Row {
         if (threadIdx.x == 0) s->heavies = s->nears = 0;
         new_histogram();
         u64 n = 0, h = 0;
+        const float counted_from = w.top - (static_cast<float>(kCounted) + 0.01f) / w.hi - 4.8e-7f * fabsf(w.top);
         {
             unsigned heavies = 0;
 #pragma unroll 1
@@ -840,10 +843,21 @@ struct Row {
                 n += m.vector(data + 2 * v, first + v * kPer);
                 h += m.h;
                 heavies += m.h > 0 ? 1 : 0;
+                auto note = [&](float l, bool every) {
+                    const float y = (l - w.top) * w.hi;
+                    const int bin = min(static_cast<int>(-static_cast<float>(kOctave) * y), kBins - 1);
+                    if (y > -60.f && l > prior.value && (bin < kOctave * kCounted) == every) atomicAdd(&s->count[histogram][bin], 1u);
+                };
+                note(Type<T>::one(data + 2 * v, lane % kNoted), false);
+                note(Type<T>::one(data + 2 * v + 1, lane % kNoted), false);
+                if (Type<T>::largest(Type<T>::larger(data[2 * v], data[2 * v + 1])) >= counted_from) {
+                    float x[kPer];
+                    spread(v, x);
+                    unsigned some = 0;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const float l = Type<T>::one(data + 2 * v + half, lane % kNoted), y = (l - w.top) * w.hi;
-                    if (y > -60.f && l > prior.value) atomicAdd(&s->count[histogram][min(static_cast<int>(-static_cast<float>(kOctave) * y), kBins - 1)], 1u);
+                    for (int u = 0; u < kPer; ++u)
+                        if (x[u] >= counted_from) some |= 1u << u;
+                    for (; some; some &= some - 1) note(Type<T>::one(data + 2 * v, __ffs(some) - 1), true);
                 }
             }
             heavies = __reduce_add_sync(0xffffffffu, heavies);
@@ -876,22 +890,25 @@ struct Row {
                 return 0;
             }
         }
-        // The place by what was noted: the weight up to each bin's end from the nearest place whose weight is known (`anchor`), and four times
-        // how far that may be off. Where too many tokens lie within, the most likely place's weight is taken and the others' from there.
+        // The place by what was counted: the weight up to each bin's end from the nearest place whose weight is known (`anchor`), and four times
+        // how far that may be off: a token's place in its bin, and how many stand for how many. Where too many tokens lie within, the most likely
+        // place's weight is taken and the others' from there.
         const int bin = threadIdx.x;
-        const float one = exp2f(-(static_cast<float>(bin) + 0.5f) / kOctave), c = kNoted * static_cast<float>(counted);
-        const float noted = block_prefix(c * one), square = kNoted * block_prefix(c * one * one), number = block_prefix(c);
+        const bool every = bin < kOctave * kCounted;
+        const float one = exp2f(-(static_cast<float>(bin) + 0.5f) / kOctave), c = (every ? 1 : kNoted) * static_cast<float>(counted);
+        const float noted = block_prefix(c * one), number = block_prefix(c);
+        const float square = block_prefix(c * one * one * (every ? 1e-3f : kNoted));
         const float goal = static_cast<float>(target) * 0x1p-44f;
         int anchor = in_heavy ? -1 : kOctave * kHeavy - 1;
         float known = in_heavy ? 0.f : static_cast<float>(h) * 0x1p-44f;
         auto edge = [&](int b) { return w.top - static_cast<float>(b + 1) / (kOctave * w.hi); };
-        int to_bin, from_bin;
-        for (int step = 0;; ++step) {
+        for (int attempt = 0; attempt < 4 && w.simple; ++attempt) {
             __syncthreads();
             if (bin == 0) {
                 s->to_bin = -1;
                 s->from_bin = s->likely = kBins;
                 s->at_to = 0.f;
+                s->nears = 0;
                 if (anchor < 0) s->at_anchor[0] = s->at_anchor[1] = 0.f;
             }
             __syncthreads();
@@ -901,25 +918,24 @@ struct Row {
             }
             __syncthreads();
             const float from_there = noted - s->at_anchor[0];
-            const float off = 4.f * sqrtf(fabsf(square - s->at_anchor[1])) + 0.004f * fabsf(from_there) + kNoted * one;
+            const float off = 4.f * sqrtf(fabsf(square - s->at_anchor[1])) + 0.004f * fabsf(from_there) + 0.1f * one;
             if (known + from_there + off < goal) atomicMax(&s->to_bin, bin);
             if (known + from_there - off >= goal) atomicMin(&s->from_bin, bin);
             if (known + from_there >= goal) atomicMin(&s->likely, bin);
             __syncthreads();
-            to_bin = s->to_bin;
-            from_bin = s->from_bin;
+            const int to_bin = s->to_bin, from_bin = s->from_bin;
             if (bin == to_bin) s->at_to = number;
             if (bin == min(from_bin, kBins - 1)) s->at_from = number;
             __syncthreads();
-            if (step == 1 || s->at_from - s->at_to <= static_cast<float>(kNear / 2) * blocks || !w.simple) break;
-            anchor = min(s->likely, kBins - 1);
-            const Kept upper{edge(anchor), 0x7fffffff};
-            if (!(upper.value > prior.value)) break;
-            known = static_cast<float>(total([&] { return MassSum<T>(w, upper); }).all) * 0x1p-44f;
-        }
-        const float to = to_bin >= 0 ? edge(to_bin) : INFINITY, from = from_bin < kBins ? fmaxf(lowest, edge(from_bin)) : lowest;
-        const bool narrowed = w.simple && from < to && to > prior.value;
-        if (narrowed) {
+            if (attempt < 3 && s->at_from - s->at_to > static_cast<float>(kNear / 2) * blocks) {
+                anchor = min(s->likely, kBins - 1);
+                const Kept upper{edge(anchor), 0x7fffffff};
+                if (!(upper.value > prior.value)) break;
+                known = static_cast<float>(total([&] { return MassSum<T>(w, upper); }).all) * 0x1p-44f;
+                continue;
+            }
+            const float to = to_bin >= 0 ? edge(to_bin) : INFINITY, from = from_bin < kBins ? fmaxf(lowest, edge(from_bin)) : lowest;
+            if (!(from < to && to > prior.value)) break;
             // what weighs before `to`, and a list of what lies from there to `from`
             const Kept upper{to, 0x7fffffff};
             n = 0;
@@ -948,9 +964,10 @@ struct Row {
             exchange<2>(n, s->nears);
             const u64 above = warp_sum(exchanged(0));
             const unsigned nears = static_cast<unsigned>(exchanged(1));
-            if (above < target && __reduce_max_sync(0xffffffffu, nears) <= kNear) {
-                if (select<true>(kept, w, target, from, to, above, true)) return 0;
-            }
+            if (__reduce_max_sync(0xffffffffu, nears) <= kNear && above < target && select<true>(kept, w, target, from, to, above, true)) return 0;
+            if (to_bin < 0) break;
+            anchor = to_bin;  // not between these: once more, from a place whose weight is known now
+            known = static_cast<float>(above) * 0x1p-44f;
         }
         select<true>(kept, w, target, lowest);
         return 0;
@@ -1341,7 +1358,7 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
                 return;
             }
         } else {
-            auto others = [&] { return MassSum<T>(weights, kept, given.token); };
+            auto others = [&] { return MassSum<T, true>(weights, kept, given.token); };
             const typename Row<T>::Total t = row.total(others);
             if (t.all > 0) {
                 row.pick(others, t, given.u, id);
