@@ -1133,16 +1133,17 @@ _VERIFY_ARGS = struct.Struct("@7P2q4i" + _FILTERS)
 
 def _filters(n: int, device: int, temperature, top_k, top_p, min_p):
     """dspark_filters of n rows or sequences: a setting is a number, None (off) or a tensor of n entries."""
-    at, all_of = [], []
-    for name, v, off, dtype in (("temperature", temperature, 1.0, torch.float32), ("top_p", top_p, 1.0, torch.float32),
-                                ("min_p", min_p, 0.0, torch.float32), ("top_k", top_k, 0, torch.int32)):
-        if isinstance(v, torch.Tensor):
-            at.append(_ints(v, name, device, n, dtype=dtype))
-            all_of.append(off)
-        else:
-            at.append(0)
-            all_of.append(off if v is None else v)
-    return (*at, *all_of)
+    t = p = m = k = 0  # addresses, where there are any
+    if isinstance(temperature, torch.Tensor):
+        t, temperature = _ints(temperature, "temperature", device, n, dtype=torch.float32), 1.0
+    if isinstance(top_p, torch.Tensor):
+        p, top_p = _ints(top_p, "top_p", device, n, dtype=torch.float32), 1.0
+    if isinstance(min_p, torch.Tensor):
+        m, min_p = _ints(min_p, "min_p", device, n, dtype=torch.float32), 0.0
+    if isinstance(top_k, torch.Tensor):
+        k, top_k = _ints(top_k, "top_k", device, n), 0
+    return (t, p, m, k, 1.0 if temperature is None else temperature, 1.0 if top_p is None else top_p, 0.0 if min_p is None else min_p,
+            0 if top_k is None else top_k)
 
 
 def _row_matrix(t, name: str, device: int, dtype, rows=None, columns=None):

@@ -993,18 +993,43 @@ struct Row {
     }
     // The least and the largest of the cluster's codes.
     __device__ __forceinline__ void exchange_range(unsigned least, unsigned most, unsigned *c0, unsigned *c1) {
+        const u64 all = join(exchange(join(by_warp(least, most))));
+        *c0 = 0xffffffffu - static_cast<unsigned>(all);
+        *c1 = static_cast<unsigned>(all >> 32);
+    }
+    // The same of the threads' largest logits, and bounds from below for the 2 * blocks-th, 4 * blocks-th and 8 * blocks-th largest logit of all: what so
+    // many of each block's warps have a logit of.
+    __device__ __forceinline__ void exchange_largest(unsigned code, bool some, unsigned *least, unsigned *most, unsigned (&nth)[3]) {
+        const u64 mine = by_warp(some ? code : 0xffffffffu, code);
+        unsigned c = static_cast<unsigned>(mine >> 32);  // a warp's to a lane of 16: sorted, the largest first
+#pragma unroll
+        for (int k = 2; k <= kWarps; k *= 2)
+#pragma unroll
+            for (int j = k / 2; j > 0; j /= 2) {
+                const unsigned other = __shfl_xor_sync(0xffffffffu, c, j);
+                c = ((lane & k) == 0) == ((lane & j) == 0) ? max(c, other) : min(c, other);
+            }
+        const unsigned second = __shfl_sync(0xffffffffu, c, 1), fourth = __shfl_sync(0xffffffffu, c, 3), eighth = __shfl_sync(0xffffffffu, c, 7);
+        const u64 all = join(exchange<3>(join(mine), static_cast<u64>(second) << 32 | fourth, eighth));
+        *least = 0xffffffffu - static_cast<unsigned>(all);
+        *most = static_cast<unsigned>(all >> 32);
+        const u64 none = ~0ull, b = lane < blocks ? exchanged(1) : none, d = lane < blocks ? exchanged(2) : none;
+        nth[0] = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(b >> 32));
+        nth[1] = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(b));
+        nth[2] = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(d));
+    }
+    // A warp's largest and (turned round) least code to each of kWarps lanes.
+    __device__ __forceinline__ u64 by_warp(unsigned least, unsigned most) {
         least = __reduce_min_sync(0xffffffffu, least);
         most = __reduce_max_sync(0xffffffffu, most);
         __syncthreads();
         if (lane == 0) s->scan[0][warp] = static_cast<u64>(most) << 32 | (0xffffffffu - least);
         __syncthreads();
-        auto join = [&](u64 v) {
-            return static_cast<u64>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(v >> 32))) << 32 |
-                   __reduce_max_sync(0xffffffffu, static_cast<unsigned>(v));
-        };
-        const u64 all = join(exchange(join(lane < kWarps ? s->scan[0][lane] : 0)));
-        *c0 = 0xffffffffu - static_cast<unsigned>(all);
-        *c1 = static_cast<unsigned>(all >> 32);
+        return lane < kWarps ? s->scan[0][lane] : 0;
+    }
+    __device__ __forceinline__ static u64 join(u64 v) {
+        return static_cast<u64>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(v >> 32))) << 32 |
+               __reduce_max_sync(0xffffffffu, static_cast<unsigned>(v));
     }
 
     // The token of the weights `make()`, of which `t` is the total taken just before, at u of their sum.
@@ -1172,8 +1197,8 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
         }
     }
     const float mine = Type<T>::largest(most);  // this thread's
-    unsigned least, largest;
-    row.exchange_range(mine > -INFINITY ? float_order_code(mine) : 0xffffffffu, float_order_code(mine), &least, &largest);
+    unsigned least, largest, nth[3];
+    row.exchange_largest(float_order_code(mine), mine > -INFINITY, &least, &largest, nth);
     const float top = value_of(static_cast<u64>(largest) << 32);
 
     // ---- what is left of the row ----
@@ -1206,12 +1231,18 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
     };
     auto drop_light = [&] { return max(part_of(z, given.top_p, true), 1ull); };  // what the nucleus has to weigh, of the sum z
     if (top_k > 0) {
-        // The top_k-th largest of the threads' maxima is a bound from below.
+        // A bound from below: what each block has enough of, or the top_k-th largest of the threads' maxima.
         bool bounded = g.vocab <= kList;
-        if (top < 3.4e38f) {
-            row.histogram ^= 1;
-            s->count[row.histogram][threadIdx.x] = 0;
-            __syncthreads();
+        unsigned code = 0;
+        if (top_k == 1) code = largest;
+        else if (top_k <= 128)
+            for (int j = 2; j >= 0; --j)
+                if (top_k <= (2 << j) * row.blocks && (2 << j) * row.blocks <= 128) code = nth[j];
+        if (code > float_order_code(-INFINITY)) {
+            cut = fmaxf(cut, value_of(static_cast<u64>(code) << 32));
+            bounded = true;
+        } else if (top < 3.4e38f) {
+            row.new_histogram();
             const float range = top - value_of(static_cast<u64>(least) << 32), scale = range > 0.f && range < 3e38f ? kSpread / range : 0.f;
             if (mine > -INFINITY) atomicAdd(&s->count[row.histogram][min(static_cast<int>((top - mine) * scale), kBins - 1)], 1u);
             const int bin = row.template reached<false>(top_k);
