@@ -190,6 +190,7 @@ struct Type<float> {
     static __device__ __forceinline__ unsigned down(float x) { return __float_as_uint(x); }
     static __device__ __forceinline__ float low(unsigned v) { return __uint_as_float(v); }
     static constexpr float kLeast = -3.0e38f;
+    static constexpr bool kFine = true;
 };
 template <>
 struct Type<__nv_bfloat16> {
@@ -219,6 +220,7 @@ struct Type<__nv_bfloat16> {
     }
     static __device__ __forceinline__ float low(unsigned v) { return __uint_as_float(v << 16); }
     static constexpr float kLeast = -3.0e38f;
+    static constexpr bool kFine = false;  // differences of 8-bit significands are exact but for the smallest logits'
 };
 template <>
 struct Type<__half> {
@@ -250,6 +252,7 @@ struct Type<__half> {
     }
     static __device__ __forceinline__ float low(unsigned v) { return __half2float(__ushort_as_half(static_cast<unsigned short>(v))); }
     static constexpr float kLeast = -6.0e4f;
+    static constexpr bool kFine = true;
 };
 
 // A number of 0 to 2^63 rounded down, by shifts: the conversion instruction runs at the rate of 64-bit floating point, 15 cycles a warp.
@@ -278,7 +281,7 @@ struct Weights {
         const float diff = l - top, d = l >= top ? 0.f : fmaxf(diff, least);
         *p = d * hi;
         *e = __fmaf_rn(d, lo, __fmaf_rn(d, hi, -*p));
-        if (heavy(*p) && d < 0.f) {  // and what the difference lost
+        if ((heavy(*p) || Type<T>::kFine) && d < 0.f && d > least) {  // and what the difference lost
             const float back = diff - l, lost = (l - (diff - back)) + (-top - back);
             *e = __fmaf_rn(lost, hi, *e);
         }
@@ -357,11 +360,13 @@ __device__ __forceinline__ unsigned light_weights(const Weights<T> &w, const Kep
         }
     }
     const u64 top = pair_f32(-w.top, -w.top), hi = pair_f32(w.hi, w.hi), less_hi = pair_f32(-w.hi, -w.hi), less_lo = pair_f32(-w.lo, -w.lo),
-              less_ln2 = pair_f32(-0.6931471806f, -0.6931471806f);
+              less_ln2 = pair_f32(-0.6931471806f, -0.6931471806f), back = pair_f32(w.top, w.top), minus = pair_f32(-1.f, -1.f);
 #pragma unroll
     for (int u = 0; u < P / 2; ++u) {
         const u64 d = add_f32x2(pair_f32(x[2 * u], x[2 * u + 1]), top), p = mul_f32x2(d, hi);
-        const u64 e = fma_f32x2(d, less_lo, fma_f32x2(d, less_hi, p));  // what p lacks, negative
+        u64 e = fma_f32x2(d, less_lo, fma_f32x2(d, less_hi, p));  // what p lacks, negative
+        if (Type<T>::kFine)  // and what the difference lost: that of 24 bits, or of small logits, is not exact
+            e = fma_f32x2(fma_f32x2(add_f32x2(d, back), minus, pair_f32(x[2 * u], x[2 * u + 1])), less_hi, e);
         float a, b;
         split_f32(p, &a, &b);
         const u64 two = pair_f32(fast_exp2(a), fast_exp2(b));
