@@ -73,26 +73,29 @@ enum { kNotDrawn, kGreedy, kDrawn };
 struct alignas(16) Shared {
     uint2 table[64];
     Given given;
-    unsigned count[2][kBins];    // histograms, read by the cluster's other blocks
-    alignas(8) unsigned mass[2][kBins][2];  // low and high half of 64 bits
+    int found, to_bin, from_bin, likely;
+    float share_hi, share_lo;    // what turns a light weight into a probability
+    float at_anchor[2], at_to, at_from;
+    unsigned listed, nears, heavies;
     u64 slot[2][3][kMaxBlocks];  // [parity][value][block]: what the blocks exchange
+    u64 warp[kWarps];            // sums over the warps' stretches of the slice
+    u64 scan[2][kWarps];
+    u64 inverse, last;           // last: of the kept tokens, as in the list
+    u64 z, drafted;
+    u64 count_before, mass_before, count_in;
+    // from here on not used, and not there, where nothing is dropped
+    alignas(16) unsigned count[2][kBins];  // histograms, read by the cluster's other blocks
+    unsigned mass[2][kBins][2];  // low and high half of 64 bits
     u64 list[kList];             // this block's tokens of a list, read by the first block: order code and what is left of 2^32 behind the index
     union {                      // lists are sorted when what lies near a nucleus' end is no longer wanted
         u64 near_end[kNear];     // tokens in the same form, this block's own
         u64 sort[2][kList];
     };
-    u64 warp[kWarps];            // sums over the warps' stretches of the slice
-    u64 scan[2][kWarps];
-    u64 inverse, last;           // last: of the kept tokens, as in the list
-    u64 z;
-    u64 count_before, mass_before, count_in, drafted;
-    float share_hi, share_lo;    // what turns a light weight into a probability
-    int found, to_bin, from_bin, likely;
-    float at_anchor[2], at_to, at_from;
-    unsigned listed, nears, heavies;
 };
 
-static_assert(offsetof(Shared, mass) % 8 == 0 && offsetof(Shared, slot) % 8 == 0 && sizeof(Shared) % 16 == 0, "64-bit words and vectors are aligned");
+constexpr size_t shared_bytes(bool whole) { return whole ? offsetof(Shared, count) : sizeof(Shared); }
+static_assert(offsetof(Shared, mass) % 8 == 0 && offsetof(Shared, slot) % 8 == 0 && shared_bytes(true) % 16 == 0 && shared_bytes(false) % 16 == 0,
+              "64-bit words and vectors are aligned");
 
 __device__ __forceinline__ uint32_t at_block(const void *p, int block) {
     uint32_t r;
@@ -1132,12 +1135,13 @@ __device__ __forceinline__ bool judge(const Given &given, Shared *s) {
     return s->found;
 }
 
-template <typename T, bool VERIFY>
-__global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant__ Draw g) {
+// WHOLE: no row has a setting that drops tokens. What that needs fits 40 registers, so three blocks share an SM instead of two.
+template <typename T, bool VERIFY, bool WHOLE>
+__global__ void __launch_bounds__(kThreads, WHOLE ? 3 : 2) draw_kernel(const __grid_constant__ Draw g) {
     extern __shared__ __align__(16) unsigned char smem[];
     Row<T> row;
     Shared *s = row.s = reinterpret_cast<Shared *>(smem);
-    row.data = reinterpret_cast<const uint4 *>(smem + sizeof(Shared));
+    row.data = reinterpret_cast<const uint4 *>(smem + shared_bytes(WHOLE));
     {
         unsigned r, n;
         asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -1156,7 +1160,7 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all blocks run: their shared memory may be written to
 
     const size_t row_at = static_cast<size_t>(r) * g.logits_stride;
-    constexpr int P = Row<T>::kPer, V = Type<T>::kVector, kBatch = 8;
+    constexpr int P = Row<T>::kPer, V = Type<T>::kVector, kBatch = WHOLE ? 4 : 8;
     const int begin = min(row.block * g.slice, g.vocab), n = min(g.slice, g.vocab - begin);
     const T *from = static_cast<const T *>(g.logits) + row_at + begin;
     const int off = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15) / static_cast<int>(sizeof(T));
@@ -1203,7 +1207,8 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
     }
     const float mine = Type<T>::largest(most);  // this thread's
     unsigned least, largest, nth[3];
-    row.exchange_largest(float_order_code(mine), mine > -INFINITY, &least, &largest, nth);
+    if (WHOLE) row.exchange_range(0u, float_order_code(mine), &least, &largest);
+    else row.exchange_largest(float_order_code(mine), mine > -INFINITY, &least, &largest, nth);
     const float top = value_of(static_cast<u64>(largest) << 32);
 
     // ---- what is left of the row ----
@@ -1222,8 +1227,8 @@ __global__ void __launch_bounds__(kThreads, 2) draw_kernel(const __grid_constant
     const Weights<T> weights(top, given, s->table);
     Kept kept{-INFINITY, kNoIndex};
     auto mass = [&] { return MassSum<T>(weights, kept); };
-    const int top_k = given.top_k;
-    const bool by_p = given.top_p < 1.f, by_floor = given.floor_hi > -INFINITY;
+    const int top_k = WHOLE ? 0 : given.top_k;
+    const bool by_p = !WHOLE && given.top_p < 1.f, by_floor = !WHOLE && given.floor_hi > -INFINITY;
     u64 z = 0;
     float cut = kLowest;  // a logit below which none of the kept tokens lies
     if (by_floor && !(top_k > 0 && by_p)) cut = fmaxf(cut, top + (given.floor_hi - 0.01f) / weights.hi - 4.8e-7f * fabsf(top));
@@ -1447,25 +1452,26 @@ cudaError_t launch_cluster(void (*kernel)(Args...), int grid, int cluster, int t
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-constexpr long long kGoodSlice = 84 * 1024;  // two blocks to an SM
 constexpr int kMostSlice = 128 * 1024;  // bytes; kMaxVocab fp32 logits over kMaxBlocks blocks
 
-template <typename T, bool VERIFY>
+template <typename T, bool VERIFY, bool WHOLE>
 dspark_status launch(Draw g, int sms, cudaStream_t stream) {
-    auto *kernel = draw_kernel<T, VERIFY>;
+    auto *kernel = draw_kernel<T, VERIFY, WHOLE>;
     static std::atomic<unsigned long long> configured{0};  // a bit a device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     if (dev >= 64 || !(configured.load() >> dev & 1)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Shared)) + kMostSlice + 128);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared_bytes(WHOLE)) + kMostSlice + 128);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(sample)");
         if (dev < 64) configured.fetch_or(1ull << dev);
     }
-    // Blocks of a row's cluster: a block takes some time whatever its slice, about that of 8 KB of it, and two of them share an SM. 96 rows of
-    // 151936 (bf16, nuclei) over 4 | 8 | 16 blocks 227 | 186 | 212 us, 28 of them (fp32) over 8 | 16 61 | 83.
-    const long long size = sizeof(T), bytes = g.vocab * size, slots = 2ll * sms;
+    // Blocks of a row's cluster: a block takes some time whatever its slice, about that of 8 KB of it, and two of them (three, where nothing is
+    // dropped) share an SM. 96 rows of 151936 (bf16, nuclei) over 4 | 8 | 16 blocks 227 | 186 | 212 us, 28 of them (fp32) over 8 | 16 61 | 83.
+    constexpr int kShare = WHOLE ? 3 : 2;
+    constexpr long long kGoodSlice = 227 * 1024 / kShare - 1024 - static_cast<long long>(shared_bytes(WHOLE)) - 64;
+    const long long size = sizeof(T), bytes = g.vocab * size, slots = static_cast<long long>(kShare) * sms;
     int blocks = 0;
     long long least = 0;
     for (int b = 1; b <= kMaxBlocks; b *= 2) {
@@ -1477,7 +1483,7 @@ dspark_status launch(Draw g, int sms, cudaStream_t stream) {
     }
     const int per = 16 / static_cast<int>(size);  // whole vectors: all slices begin at the same place of one
     g.slice = ((g.vocab + blocks - 1) / blocks + per - 1) / per * per;
-    const size_t smem = sizeof(Shared) + g.slice * size + 64;  // what stands before the slice's first vector and fills its last one
+    const size_t smem = shared_bytes(WHOLE) + g.slice * size + 64;  // what stands before the slice's first vector and fills its last one
     e = launch_cluster(kernel, g.rows * blocks, blocks, kThreads, smem, stream, g);
     return e == cudaSuccess ? DSPARK_OK : cuda_fail(e, VERIFY ? "verify_drafts" : "sample");
 }
@@ -1531,9 +1537,12 @@ dspark_status run(Draw g, int dtype, const dspark_filters &f, cudaStream_t strea
     int sms = 0;
     const dspark_status st = static_cast<dspark_status>(current_sm_count(&sms));
     if (st != DSPARK_OK) return st;
-    return dtype == DSPARK_FP32   ? launch<float, VERIFY>(g, sms, stream)
-           : dtype == DSPARK_BF16 ? launch<__nv_bfloat16, VERIFY>(g, sms, stream)
-                                  : launch<__half, VERIFY>(g, sms, stream);
+    const bool whole = !f.temperature && f.temperature_all > 0.f && !f.top_k && (f.top_k_all == 0 || f.top_k_all >= g.vocab) && !f.top_p &&
+                       f.top_p_all >= 1.f && !f.min_p && f.min_p_all <= 0.f;
+    auto *go = dtype == DSPARK_FP32   ? (whole ? launch<float, VERIFY, true> : launch<float, VERIFY, false>)
+               : dtype == DSPARK_BF16 ? (whole ? launch<__nv_bfloat16, VERIFY, true> : launch<__nv_bfloat16, VERIFY, false>)
+                                      : (whole ? launch<__half, VERIFY, true> : launch<__half, VERIFY, false>);
+    return go(g, sms, stream);
 }
 
 }  // namespace
