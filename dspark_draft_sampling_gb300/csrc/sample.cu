@@ -888,7 +888,7 @@ struct Row {
         const u64 target = max(part_of(*z, top_p, true), 1ull);
         const float share = (1.f - top_p) * static_cast<float>(*z) * 0x1p-44f / static_cast<float>(most);
         // of at most `most` tokens, those lighter than an even share of what may be dropped are dropped all together
-        const float lowest = share > 1e-30f ? w.top + (log2f(share) - 0.01f) / w.hi - 4.8e-7f * fabsf(w.top) : kLowest;
+        const float lowest = share > 1e-30f ? fmaxf(w.top + (log2f(share) - 0.01f) / w.hi - 4.8e-7f * fabsf(w.top), kLowest) : kLowest;
         const bool in_heavy = target <= h;
         if (in_heavy && heavies <= kList) {
             const int listed = gather([&](float l, int i) { return (l >= w.top || w.heavy((l - w.top) * w.hi)) && prior.order(l, i); });
@@ -1153,8 +1153,9 @@ __global__ void __launch_bounds__(kThreads, WHOLE ? 3 : 2) draw_kernel(const __g
     row.lane = threadIdx.x & 31;
     row.parity = row.histogram = 0;
     const long long r = blockIdx.x / row.blocks;
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (threadIdx.x < 64) s->table[threadIdx.x] = g.table[threadIdx.x];
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     pdl_launch_dependents();
     pdl_wait();  // no global-memory access before this point
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all blocks run: their shared memory may be written to

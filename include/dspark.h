@@ -722,7 +722,8 @@ dspark_status dspark_paged_attention_debug(const dspark_cache *cache, const dspa
  *   top_p  of those, a token stays if what stands before it weighs less than top_p times what they
  *          weigh together; the first one always does (1: all)
  *   min_p  of those, the ones stay that weigh at least min_p (the first one weighs 1; 0: all)
- * p_v = w_v over the sum of what is left, 0 for what is not.  T = 0 leaves the first token only.  A
+ * p_v = w_v over the sum of what is left, 0 for what is not.  T = 0 leaves the first token only;
+ * one above 0 and beyond 1e-30 .. 1e30 is taken as that bound.  A
  * uniform number u in [0, 1) draws the lowest token whose p, added up in index order to it, exceeds u.
  * Logits of -infinity and NaN are not tokens; where one is +infinity, those of +infinity weigh the
  * same and the others nothing.  A row without tokens draws -1 and has p = 0.

@@ -153,6 +153,20 @@ def test_masks(dtype):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
+def test_many_infinities_and_highest_values(dtype):
+    """More equal largest logits than one block lists, beyond where differences are finite."""
+    gen = torch.Generator().manual_seed(6)
+    t, vocab = TYPES[dtype], 6007
+    x = logits_of(gen, 3, vocab, t)
+    x[0, 1::3] = math.inf
+    x[1, ::2] = torch.finfo(t).max
+    x[2, ::5] = math.inf
+    x[2, 1::5] = torch.finfo(t).min
+    for setting in ((1.0, 0, 0.7071, 0.0), (0.5, 900, 1.0, 0.0), (1.0, 700, 0.3333, 0.5), (1.0, 0, 1.0, 0.5), (0.0, 0, 1.0, 0.0)):
+        check(x, setting, gen, probs=True, scalar=True)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
 def test_ties(dtype):
     """Few distinct logits: equal ones stay by index, wherever the last one of them lies."""
     gen = torch.Generator().manual_seed(8)
