@@ -78,6 +78,7 @@ struct alignas(16) Shared {
     float at_anchor[2], at_to, at_from;
     unsigned listed, nears, heavies;
     u64 slot[2][3][kMaxBlocks];  // [parity][value][block]: what the blocks exchange
+    u64 said[2][4];              // [parity][value]: what the first warp makes of it
     u64 warp[kWarps];            // sums over the warps' stretches of the slice
     u64 scan[2][kWarps];
     u64 inverse, last;           // last: of the kept tokens, as in the list
@@ -534,9 +535,10 @@ struct Row {
             for (int u = 0; u < kPer; ++u) f(x[u], first + v * kPer + u);
         }
     }
-    // Every block's values to all of them; a lane then reads one of each.
+    // The first warp's values to every block; its lanes then read one of each.  What they make of them it tells the others: a warp less to issue
+    // the same for.
     template <int N = 1>
-    __device__ __forceinline__ u64 exchange(u64 a, u64 b = 0, u64 c = 0) {
+    __device__ __forceinline__ void exchange(u64 a, u64 b = 0, u64 c = 0) {
         parity ^= 1;
         if (static_cast<int>(threadIdx.x) < blocks) {
             st_block_u64(at_block(&s->slot[parity][0][block], threadIdx.x), a);
@@ -544,23 +546,33 @@ struct Row {
             if (N > 2) st_block_u64(at_block(&s->slot[parity][2][block], threadIdx.x), c);
         }
         cluster_barrier();
-        return exchanged(0);
     }
     __device__ __forceinline__ u64 exchanged(int value) const { return lane < blocks ? s->slot[parity][value][lane] : 0; }
-    // The blocks' values: their sum, and that over the blocks before this one.
-    __device__ __forceinline__ u64 exchange_sum(u64 mine, u64 *before) {
-        const u64 v = exchange(mine), upto = warp_prefix(v, lane);
-        *before = __shfl_sync(0xffffffffu, upto - v, block);
-        return __shfl_sync(0xffffffffu, upto, 31);
+    __device__ __forceinline__ void say(u64 a, u64 b = 0, u64 c = 0) {
+        if (lane == 0) {
+            s->said[parity][0] = a;
+            s->said[parity][1] = b;
+            s->said[parity][2] = c;
+        }
     }
-    // The block's sum, in all threads.
-    __device__ __forceinline__ u64 block_sum(u64 n, u64 *by_warp) {
+    // The blocks' values (the first warp's): their sum, and that over the blocks before this one; `more`: something else for this block to hear.
+    __device__ __forceinline__ u64 exchange_sum(u64 mine, u64 *before, u64 more = 0) {
+        exchange(mine);
+        if (warp == 0) {
+            const u64 v = exchanged(0), upto = warp_prefix(v, lane), b = __shfl_sync(0xffffffffu, upto - v, block);
+            say(__shfl_sync(0xffffffffu, upto, 31), b, more);
+        }
+        __syncthreads();
+        *before = s->said[parity][1];
+        return s->said[parity][0];
+    }
+    // The warps' sums to by_warp.
+    __device__ __forceinline__ void warp_sums(u64 n, u64 *by_warp) {
         n = warp_sum(n);
-        __syncthreads();
         if (lane == 0) by_warp[warp] = n;
-        __syncthreads();
-        return warp_sum(lane < kWarps ? by_warp[lane] : 0);
     }
+    // Their sum, in the first warp.
+    __device__ __forceinline__ u64 block_sum(const u64 *by_warp) const { return warp == 0 ? warp_sum(lane < kWarps ? by_warp[lane] : 0) : 0; }
     // The sum of `make()` over this block's slice, which leaves those over the warps' stretches in s->warp, over the blocks before it, and over all.
     struct Total {
         u64 mine, before, all;
@@ -570,9 +582,13 @@ struct Row {
         u64 n = 0;
 #pragma unroll 1
         for (int k = 0; k < rounds; ++k) n += vector_sum(make, vector(k));
+        __syncthreads();
+        warp_sums(n, s->warp);
+        __syncthreads();
+        const u64 mine = block_sum(s->warp);
         Total t;
-        t.mine = block_sum(n, s->warp);
-        t.all = exchange_sum(t.mine, &t.before);
+        t.all = exchange_sum(mine, &t.before, mine);
+        t.mine = s->said[parity][2];
         return t;
     }
     template <typename M>
@@ -871,12 +887,22 @@ struct Row {
             heavies = __reduce_add_sync(0xffffffffu, heavies);
             if (lane == 0 && heavies) atomicAdd(&s->heavies, heavies);
         }
-        n = block_sum(n, s->warp);
-        h = block_sum(h, s->warp);
+        __syncthreads();
+        warp_sums(n, s->warp);
+        warp_sums(h, s->scan[1]);
+        __syncthreads();
+        n = block_sum(s->warp);
+        h = block_sum(s->scan[1]);
         exchange<3>(n, h, s->heavies);
-        *z = warp_sum(exchanged(0));
-        h = warp_sum(exchanged(1));
-        const unsigned heavies = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(exchanged(2)));  // vectors with some
+        if (warp == 0) {
+            n = warp_sum(exchanged(0));
+            h = warp_sum(exchanged(1));
+            say(n, h, __reduce_add_sync(0xffffffffu, static_cast<unsigned>(exchanged(2))));
+        }
+        __syncthreads();
+        *z = s->said[parity][0];
+        h = s->said[parity][1];
+        const unsigned heavies = static_cast<unsigned>(s->said[parity][2]);  // pieces with some
         unsigned counted = 0;
         {
             unsigned v[kMaxBlocks];
@@ -968,11 +994,18 @@ struct Row {
                     if (at < kNear) s->near_end[at] = static_cast<u64>(float_order_code(l)) << 32 | (0xffffffffu - static_cast<unsigned>(i));
                 }
             }
-            n = block_sum(n, s->warp);
+            __syncthreads();
+            warp_sums(n, s->warp);
+            __syncthreads();
+            n = block_sum(s->warp);
             exchange<2>(n, s->nears);
-            const u64 above = warp_sum(exchanged(0));
-            const unsigned nears = static_cast<unsigned>(exchanged(1));
-            if (__reduce_max_sync(0xffffffffu, nears) <= kNear && above < target && select<true>(kept, w, target, from, to, above, true)) return 0;
+            if (warp == 0) {
+                n = warp_sum(exchanged(0));
+                say(n, __reduce_max_sync(0xffffffffu, static_cast<unsigned>(exchanged(1))));
+            }
+            __syncthreads();
+            const u64 above = s->said[parity][0], nears = s->said[parity][1];  // the most that a block has
+            if (nears <= kNear && above < target && select<true>(kept, w, target, from, to, above, true)) return 0;
             if (to_bin < 0) break;
             anchor = to_bin;  // not between these: once more, from a place whose weight is known now
             known = static_cast<float>(above) * 0x1p-44f;
@@ -1001,7 +1034,11 @@ struct Row {
     }
     // The least and the largest of the cluster's codes.
     __device__ __forceinline__ void exchange_range(unsigned least, unsigned most, unsigned *c0, unsigned *c1) {
-        const u64 all = join(exchange(join(by_warp(least, most))));
+        const u64 mine = by_warp(least, most);
+        exchange(warp == 0 ? join(mine) : 0);
+        if (warp == 0) say(join(exchanged(0)));
+        __syncthreads();
+        const u64 all = s->said[parity][0];
         *c0 = 0xffffffffu - static_cast<unsigned>(all);
         *c1 = static_cast<unsigned>(all >> 32);
     }
@@ -1009,22 +1046,37 @@ struct Row {
     // many of each block's warps have a logit of.
     __device__ __forceinline__ void exchange_largest(unsigned code, bool some, unsigned *least, unsigned *most, unsigned (&nth)[3]) {
         const u64 mine = by_warp(some ? code : 0xffffffffu, code);
-        unsigned c = static_cast<unsigned>(mine >> 32);  // a warp's to a lane of 16: sorted, the largest first
+        unsigned second = 0, fourth = 0, eighth = 0;
+        u64 range = 0;
+        if (warp == 0) {
+            unsigned c = static_cast<unsigned>(mine >> 32);  // a warp's to a lane of 16: sorted, the largest first
 #pragma unroll
-        for (int k = 2; k <= kWarps; k *= 2)
+            for (int k = 2; k <= kWarps; k *= 2)
 #pragma unroll
-            for (int j = k / 2; j > 0; j /= 2) {
-                const unsigned other = __shfl_xor_sync(0xffffffffu, c, j);
-                c = ((lane & k) == 0) == ((lane & j) == 0) ? max(c, other) : min(c, other);
-            }
-        const unsigned second = __shfl_sync(0xffffffffu, c, 1), fourth = __shfl_sync(0xffffffffu, c, 3), eighth = __shfl_sync(0xffffffffu, c, 7);
-        const u64 all = join(exchange<3>(join(mine), static_cast<u64>(second) << 32 | fourth, eighth));
+                for (int j = k / 2; j > 0; j /= 2) {
+                    const unsigned other = __shfl_xor_sync(0xffffffffu, c, j);
+                    c = ((lane & k) == 0) == ((lane & j) == 0) ? max(c, other) : min(c, other);
+                }
+            second = __shfl_sync(0xffffffffu, c, 1);
+            fourth = __shfl_sync(0xffffffffu, c, 3);
+            eighth = __shfl_sync(0xffffffffu, c, 7);
+            range = join(mine);
+        }
+        exchange<3>(range, static_cast<u64>(second) << 32 | fourth, eighth);
+        if (warp == 0) {
+            const u64 none = ~0ull, b = lane < blocks ? exchanged(1) : none, d = lane < blocks ? exchanged(2) : none;
+            second = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(b >> 32));
+            fourth = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(b));
+            eighth = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(d));
+            say(join(exchanged(0)), static_cast<u64>(second) << 32 | fourth, eighth);
+        }
+        __syncthreads();
+        const u64 all = s->said[parity][0];
         *least = 0xffffffffu - static_cast<unsigned>(all);
         *most = static_cast<unsigned>(all >> 32);
-        const u64 none = ~0ull, b = lane < blocks ? exchanged(1) : none, d = lane < blocks ? exchanged(2) : none;
-        nth[0] = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(b >> 32));
-        nth[1] = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(b));
-        nth[2] = __reduce_min_sync(0xffffffffu, static_cast<unsigned>(d));
+        nth[0] = static_cast<unsigned>(s->said[parity][1] >> 32);
+        nth[1] = static_cast<unsigned>(s->said[parity][1]);
+        nth[2] = static_cast<unsigned>(s->said[parity][2]);
     }
     // A warp's largest and (turned round) least code to each of kWarps lanes.
     __device__ __forceinline__ u64 by_warp(unsigned least, unsigned most) {
