@@ -7,7 +7,14 @@
 // exponential (2^-22) of a difference rounded to 32 bits (2^-24 of |ln w|): 2^-27 of the heaviest token's weight at most.
 //
 // Work.  A row belongs to a cluster of thread blocks, each of which keeps its slice in shared memory, so the logits are read from
-// memory once whatever the settings ask for.  The blocks exchange maxima, sums and histograms through distributed shared memory.
+// memory once whatever the settings ask for.  The blocks exchange maxima, sums and histograms through distributed shared memory, at 1 to 1.5
+// microseconds an exchange (the cluster's barrier and the wait for the slowest block).  What is decided by what was exchanged is the same in
+// all blocks, so that they meet at the same barriers.
+//
+// Measured (GB300).  256 rows of 248320 bf16, nothing dropped: 67 us, 1.9 TB/s (the bytes alone 19); 8 x 15 drafts of 248320 fp32 76 us; 96
+// rows of 151936 bf16 whose nuclei hold 75,000 tokens 163 us; 28 of fp32 with nuclei of 20,000 and their distributions 55; one row with top-k
+// 50 10.3, of which 2.5 are the launch; one request's seven drafts, nuclei of a few to 20,000 tokens, 35.  Blocks wait at barriers for most of
+// the time that is not instructions (44 to 60 % of the issue slots are used).
 #include <atomic>
 #include <cmath>
 #include <cstddef>
