@@ -23,12 +23,17 @@
 // leaves partial sums (32-bit O, maximum, sum) in the workspace; the block that arrives last joins them in
 // block order, many of them in two steps, so the result does not depend on which one that is.
 //
+// Sinks.  Of a window and a row's first tokens an item has the key tiles of those tokens and then the window's, in a numbering of its own:
+// what lies between costs nothing.
+//
 // Measured (GB300). 8192 tokens after 8192, 32 / 8 heads of 128: 0.93 ms, 1.77 PFLOP/s, for ten launches after a pause;
 // 1.02 ms, 1.62 PFLOP/s, under the power cap, where the library's matrix product sustains 1.75. 1-8 tokens over 16,000-66,000
 // keys: 182 us for 1.2 GB, 98 % of a copy's rate. 16 x 7 tokens over 300-6000 keys: 42 us for 183 MB, of which about 30 are that
 // stream, the rest start and joins. Chunks of 90-1500 tokens in a window of 1000, 28 / 4 heads of 64: 69 us, where the chain
 // of one stream (scores, softmax, second product) takes 2500 cycles a pair of key tiles and the products 1024. One token
-// over 777 keys: 11 us.
+// over 777 keys: 11 us. With a row's first tokens beside a window: one token over 50,001 keys, window 1024, 4 sinks 12.0 us; 16 x 7 tokens
+// over 300-30,000 keys, window 2048, 20 sinks 31.4 us for 131 MB; 64 single tokens, 28 / 4 heads of 64, window 4000, 64 sinks 60.4 us for
+// 244 MB (the chain of one stream again); 4096 tokens after 12,288, window 4096, 128 sinks 196 us, 1.45 PFLOP/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
