@@ -29,7 +29,7 @@
 // Measured (GB300). 8192 tokens after 8192, 32 / 8 heads of 128: 0.93 ms, 1.77 PFLOP/s, for ten launches after a pause;
 // 1.02 ms, 1.62 PFLOP/s, under the power cap, where the library's matrix product sustains 1.75. 1-8 tokens over 16,000-66,000
 // keys: 182 us for 1.2 GB, 98 % of a copy's rate. 16 x 7 tokens over 300-6000 keys: 42 us for 183 MB, of which about 30 are that
-// stream, the rest start and joins. Chunks of 90-1500 tokens in a window of 1000, 28 / 4 heads of 64: 69 us, where the chain
+// stream, the rest start and joins. Chunks of 90-1500 tokens in a window of 1000, 28 / 4 heads of 64: 66 us (69 with each masked score compared with both ends), where the chain
 // of one stream (scores, softmax, second product) takes 2500 cycles a pair of key tiles and the products 1024. One token
 // over 777 keys: 11 us. With a row's first tokens beside a window: one token over 50,001 keys, window 1024, 4 sinks 12.0 us; 16 x 7 tokens
 // over 300-30,000 keys, window 2048, 20 sinks 31.4 us for 131 MB; 64 single tokens, 28 / 4 heads of 64, window 4000, 64 sinks 60.4 us for
@@ -266,6 +266,9 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t *v) {
         "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+
+// The lowest n bits: none where n < 0, all where n > 32.
+__device__ __forceinline__ uint32_t first_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
 // Lane l of four holds w[0..3] of its row; afterwards w[k] is the l-th of lane k's.
 __device__ __forceinline__ void transpose_4(uint32_t (&w)[4][4], int lane) {
@@ -809,14 +812,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // masked in place, a quarter at a time: few tiles have an edge, and their code stands here once
 #pragma unroll 1
                         for (int q = 0; q < 4; ++q) {
-                            const int lo = see_lo - key0 - q * 32, hi = see_hi - key0 - q * 32, sinks = g.sinks - key0 - q * 32;
+                            const int lo = see_lo - key0 - q * 32, hi = see_hi - key0 - q * 32;
                             if (!__any_sync(0xffffffffu, lo > 0 || hi < 32)) continue;
+                            const uint32_t hidden = (first_bits(lo) & ~first_bits(g.sinks - key0 - q * 32)) | ~first_bits(hi);
                             uint32_t w[32];
                             tmem_ld_32(t_s + q * 32, w);
                             tmem_wait_ld();
 #pragma unroll
                             for (int u = 0; u < 32; ++u)
-                                if ((u < lo && u >= sinks) || u >= hi) w[u] = 0xff800000u;
+                                if (hidden & (1u << u)) w[u] = 0xff800000u;
                             tmem_st_32(t_s + q * 32, w);
                         }
                         tmem_wait_st();
