@@ -80,9 +80,9 @@ enum { kNotDrawn, kGreedy, kDrawn };
 struct alignas(16) Shared {
     uint2 table[64];
     Given given;
-    int found, to_bin, from_bin, likely;
+    int found, to_bin, from_bin, likely, least_from;
     float share_hi, share_lo;    // what turns a light weight into a probability
-    float at_anchor[2], at_to, at_from;
+    float at_anchor[2], at_to, at_from, at_likely;
     unsigned listed, nears, heavies;
     u64 slot[2][3][kMaxBlocks];  // [parity][value][block]: what the blocks exchange
     u64 said[2][4];              // [parity][value]: what the first warp makes of it
@@ -945,8 +945,7 @@ struct Row {
             }
         }
         // The place by what was counted: the weight up to each bin's end from the nearest place whose weight is known (`anchor`), and four times
-        // how far that may be off: a token's place in its bin, and how many stand for how many. Where too many tokens lie within, the most likely
-        // place's weight is taken and the others' from there.
+        // how far that may be off: a token's place in its bin, and how many stand for how many.
         const int bin = threadIdx.x;
         const bool every = bin < kOctave * kCounted;
         const float one = exp2f(-(static_cast<float>(bin) + 0.5f) / kOctave), c = (every ? 1 : kNoted) * static_cast<float>(counted);
@@ -960,7 +959,7 @@ struct Row {
             __syncthreads();
             if (bin == 0) {
                 s->to_bin = -1;
-                s->from_bin = s->likely = kBins;
+                s->from_bin = s->likely = s->least_from = kBins;
                 s->at_to = 0.f;
                 s->nears = 0;
                 if (anchor < 0) s->at_anchor[0] = s->at_anchor[1] = 0.f;
@@ -977,16 +976,19 @@ struct Row {
             if (known + from_there - off >= goal) atomicMin(&s->from_bin, bin);
             if (known + from_there >= goal) atomicMin(&s->likely, bin);
             __syncthreads();
-            const int to_bin = s->to_bin, from_bin = s->from_bin;
+            int to_bin = s->to_bin, from_bin = s->from_bin;
+            const int likely = min(s->likely, kBins - 1);
             if (bin == to_bin) s->at_to = number;
             if (bin == min(from_bin, kBins - 1)) s->at_from = number;
+            if (bin == likely) s->at_likely = number - 0.5f * c;
             __syncthreads();
-            if (attempt < 3 && s->at_from - s->at_to > static_cast<float>(kNear / 2) * blocks) {
-                anchor = min(s->likely, kBins - 1);
-                const Kept upper{edge(anchor), 0x7fffffff};
-                if (!(upper.value > prior.value)) break;
-                known = static_cast<float>(total([&] { return MassSum<T>(w, upper); }).all) * 0x1p-44f;
-                continue;
+            const float most_near = 0.8f * kNear * blocks;
+            if (s->at_from - s->at_to > most_near) {  // more than the lists hold: those nearest to where it most likely is
+                if (number <= s->at_likely - 0.5f * most_near) atomicMax(&s->to_bin, bin);
+                if (number >= s->at_likely + 0.5f * most_near) atomicMin(&s->least_from, bin);
+                __syncthreads();
+                to_bin = s->to_bin;
+                from_bin = min(from_bin, max(s->least_from - 1, likely));
             }
             const float to = to_bin >= 0 ? edge(to_bin) : INFINITY, from = from_bin < kBins ? fmaxf(lowest, edge(from_bin)) : lowest;
             if (!(from < to && to > prior.value)) break;
