@@ -93,14 +93,14 @@ struct alignas(16) Shared {
     u64 count_before, mass_before, count_in;
     // from here on not used, and not there, where nothing is dropped
     alignas(16) unsigned count[2][kBins];  // histograms, read by the cluster's other blocks
-    unsigned mass[2][kBins][2];  // low and high half of 64 bits
+    union {                      // lists are sorted when all blocks have done with the last histogram
+        unsigned mass[2][kBins][2];  // low and high half of 64 bits
+        u64 sort[2][kList];
+    };
     u64 all_mass[kBins];         // of all blocks
     unsigned all_count[kBins];
     u64 list[kList];             // this block's tokens of a list, read by the first block: order code and what is left of 2^32 behind the index
-    union {                      // lists are sorted when what lies near a nucleus' end is no longer wanted
-        u64 near_end[kNear];     // tokens in the same form, this block's own
-        u64 sort[2][kList];
-    };
+    u64 near_end[kNear];         // tokens near a nucleus' end in the same form, this block's own
 };
 
 constexpr size_t shared_bytes(bool whole) { return whole ? offsetof(Shared, count) : sizeof(Shared); }
@@ -618,16 +618,20 @@ struct Row {
             if (lane == 0) s->scan[1][warp] = all;
             __syncthreads();
             u64 upto;
-            const int j = first_past(s->scan[1], before, target, &upto);  // the round among these
+            int j = first_past(s->scan[1], before, target, &upto);  // the round among these
             if (upto + s->scan[1][j] <= target) {
-                before = upto + s->scan[1][j];
-                continue;
+                if (k0 + kWarps < rounds) {
+                    before = upto + s->scan[1][j];
+                    continue;
+                }
+                // the stretch's sum was a rounding larger: the last token of it that weighs anything
+                const unsigned any = __ballot_sync(0xffffffffu, lane < kWarps && s->scan[1][lane % kWarps] > 0);
+                j = any ? 31 - __clz(any) : 0;
             }
             if (warp != j) return;
             const u64 prefix = upto + warp_prefix(mine, lane);
-            const unsigned past = __ballot_sync(0xffffffffu, prefix > target);
-            if (past == 0) return;  // not the case, as the sums are the same ones
-            const int owner = __ffs(past) - 1;
+            const unsigned past = __ballot_sync(0xffffffffu, prefix > target), some = __ballot_sync(0xffffffffu, mine > 0);
+            const int owner = past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
             upto = __shfl_sync(0xffffffffu, prefix - mine, owner);
             const int at = first + __shfl_sync(0xffffffffu, v, owner) * kPer;
             // a lane to each of its tokens; their sum may be a rounding less than the vector's: then the last that weighs anything
@@ -875,8 +879,10 @@ struct Row {
     // eighths of powers of two: the heavier ones, and of the lighter ones an eighth (fp32: a quarter). That gives the place within some percent
     // or less; the next pass weighs what is before it and lists what is near it, exactly. (A histogram with weights of all tokens took 100
     // instructions and 3 atomics, of a cycle each, a token: 96 rows at temperature 1.6 326 us instead of 180.)
+    //
+    // `kept_sum`, unless null: where the nucleus was narrowed down to by the lists, the total of what is kept (else left as it is).
     template <bool LIST>
-    __device__ __forceinline__ int nucleus(Kept *kept, const Weights<T> &w, float top_p, int most, u64 *z) {
+    __device__ __forceinline__ int nucleus(Kept *kept, const Weights<T> &w, float top_p, int most, u64 *z, Total *kept_sum) {
         constexpr int kNoted = Type<T>::kVector;  // one of so many
         const Kept prior = *kept;
         if (threadIdx.x == 0) s->heavies = s->nears = 0;
@@ -1027,13 +1033,40 @@ struct Row {
             }
             __syncthreads();
             const u64 above = s->said[parity][0], nears = s->said[parity][1];  // the most that a block has
-            if (nears <= kNear && above < target && select<true>(kept, w, target, from, to, above, true)) return 0;
+            const u64 before_end = threadIdx.x < kWarps ? s->warp[threadIdx.x] : 0;
+            if (nears <= kNear && above < target && select<true>(kept, w, target, from, to, above, true)) {
+                if (kept_sum) *kept_sum = tally(*kept, w, before_end);
+                return 0;
+            }
             if (to_bin < 0) break;
             anchor = to_bin;  // not between these: once more, from a place whose weight is known now
             known = static_cast<float>(above) * 0x1p-44f;
         }
         select<true>(kept, w, target, lowest);
         return 0;
+    }
+    // The total of what is kept: what weighs before the lists' tokens, by warps (the first threads' `before_end`), and the kept ones of those.
+    __device__ __forceinline__ Total tally(const Kept &kept, const Weights<T> &w, u64 before_end) {
+        unsigned(*sums)[2] = s->mass[histogram ^ 1];  // of the last histogram, which all blocks have done with
+        __syncthreads();
+        if (threadIdx.x < kWarps) sums[threadIdx.x][0] = sums[threadIdx.x][1] = 0;
+        __syncthreads();
+        over(true, [&](float l, int i) {
+            if (!kept.order(l, i)) return;
+            const int at = (i - first) / (kPer * 32 * rounds);
+            const u64 v = w.weight(l);
+            const unsigned low = static_cast<unsigned>(v), was = atomicAdd(&sums[at][0], low);
+            const unsigned high = static_cast<unsigned>(v >> 32) + (was + low < low ? 1 : 0);
+            if (high) atomicAdd(&sums[at][1], high);
+        });
+        __syncthreads();
+        if (threadIdx.x < kWarps) s->warp[threadIdx.x] = before_end + (static_cast<u64>(sums[threadIdx.x][1]) << 32 | sums[threadIdx.x][0]);
+        __syncthreads();
+        const u64 mine = block_sum(s->warp);
+        Total t;
+        t.all = exchange_sum(mine, &t.before, mine);
+        t.mine = s->said[parity][2];
+        return t;
     }
     // Narrows `kept` to tokens of at least min_p. Weights never fall with the logits, so there is a largest one that is too small: each
     // warp looks for its code, in 31 places at a time.
@@ -1338,7 +1371,7 @@ __global__ void __launch_bounds__(kThreads, WHOLE ? 3 : 2) draw_kernel(const __g
         }
         if (bounded) list_all();
     } else if (by_p) {
-        candidates = row.template nucleus<true>(&kept, weights, given.top_p, g.vocab, &z);
+        candidates = row.template nucleus<true>(&kept, weights, given.top_p, g.vocab, &z, by_floor ? nullptr : &sums);
         finish = candidates > 0;
     } else if (by_floor) {
         list_all();
@@ -1414,10 +1447,10 @@ __global__ void __launch_bounds__(kThreads, WHOLE ? 3 : 2) draw_kernel(const __g
     if (!finish) {
         if (top_k > 0) {
             row.template select<false>(&kept, weights, top_k, cut);
-            if (by_p) row.template nucleus<false>(&kept, weights, given.top_p, top_k, &z);
+            if (by_p) row.template nucleus<false>(&kept, weights, given.top_p, top_k, &z, by_floor ? nullptr : &sums);
         }
         if (by_floor) row.drop_below(&kept, weights, given);
-        sums = row.total(mass);
+        if (sums.all == 0) sums = row.total(mass);
         z = sums.all;
     }
 
