@@ -82,7 +82,7 @@ struct alignas(16) Shared {
     Given given;
     int found, to_bin, from_bin, likely, least_from;
     float share_hi, share_lo;    // what turns a light weight into a probability
-    float at_anchor[2], at_to, at_from, at_likely;
+    float at_low[2], at_high[2], at_to, at_from, at_likely;
     unsigned listed, nears, heavies;
     u64 slot[2][3][kMaxBlocks];  // [parity][value][block]: what the blocks exchange
     u64 said[2][4];              // [parity][value]: what the first warp makes of it
@@ -950,16 +950,17 @@ struct Row {
                 return 0;
             }
         }
-        // The place by what was counted: the weight up to each bin's end from the nearest place whose weight is known (`anchor`), and four times
-        // how far that may be off: a token's place in its bin, and how many stand for how many.
+        // The place by what was counted: the weight up to each bin's end, between the two nearest places whose weight is known, in proportion
+        // to the counted one, and four times how far that may be off: a token's place in its bin, and how many stand for how many. (From the
+        // lower place alone, 45% of wide nuclei of 152,064 tokens ended outside the lists and took one more pass.)
         const int bin = threadIdx.x;
         const bool every = bin < kOctave * kCounted;
         const float one = exp2f(-(static_cast<float>(bin) + 0.5f) / kOctave), c = (every ? 1 : kNoted) * static_cast<float>(counted);
         const float noted = block_prefix(c * one), number = block_prefix(c);
         const float square = block_prefix(c * one * one * (every ? 1e-3f : kNoted));
         const float goal = static_cast<float>(target) * 0x1p-44f;
-        int anchor = in_heavy ? -1 : kOctave * kHeavy - 1;
-        float known = in_heavy ? 0.f : static_cast<float>(h) * 0x1p-44f;
+        int low_bin = in_heavy ? -1 : kOctave * kHeavy - 1, high_bin = in_heavy ? kOctave * kHeavy - 1 : kBins - 1;
+        float low = in_heavy ? 0.f : static_cast<float>(h) * 0x1p-44f, high = static_cast<float>(in_heavy ? h : *z) * 0x1p-44f;
         auto edge = [&](int b) { return w.top - static_cast<float>(b + 1) / (kOctave * w.hi); };
         for (int attempt = 0; attempt < 4 && w.simple; ++attempt) {
             __syncthreads();
@@ -968,19 +969,27 @@ struct Row {
                 s->from_bin = s->likely = s->least_from = kBins;
                 s->at_to = 0.f;
                 s->nears = 0;
-                if (anchor < 0) s->at_anchor[0] = s->at_anchor[1] = 0.f;
+                if (low_bin < 0) s->at_low[0] = s->at_low[1] = 0.f;
             }
             __syncthreads();
-            if (bin == anchor) {
-                s->at_anchor[0] = noted;
-                s->at_anchor[1] = square;
+            if (bin == low_bin) {
+                s->at_low[0] = noted;
+                s->at_low[1] = square;
+            }
+            if (bin == high_bin) {
+                s->at_high[0] = noted;
+                s->at_high[1] = square;
             }
             __syncthreads();
-            const float from_there = noted - s->at_anchor[0];
-            const float off = 4.f * sqrtf(fabsf(square - s->at_anchor[1])) + 0.004f * fabsf(from_there) + 0.1f * one;
-            if (known + from_there + off < goal) atomicMax(&s->to_bin, bin);
-            if (known + from_there - off >= goal) atomicMin(&s->from_bin, bin);
-            if (known + from_there >= goal) atomicMin(&s->likely, bin);
+            const float between = s->at_high[0] - s->at_low[0], part = between > 0.f ? (noted - s->at_low[0]) / between : 0.f;
+            const float behind = s->at_high[1] - square, before = square - s->at_low[1];
+            const float upto = low + part * (high - low);
+            float off = 0.f;
+            if (bin > low_bin && bin < high_bin)
+                off = 4.f * sqrtf(fmaxf(before * (1.f - part) * (1.f - part) + behind * part * part, 0.f)) + 0.008f * fabsf(part * (1.f - part)) * between + 0.1f * one;
+            if (upto + off < goal) atomicMax(&s->to_bin, bin);
+            if (upto - off >= goal) atomicMin(&s->from_bin, bin);
+            if (upto >= goal) atomicMin(&s->likely, bin);
             __syncthreads();
             int to_bin = s->to_bin, from_bin = s->from_bin;
             const int likely = min(s->likely, kBins - 1);
@@ -990,7 +999,7 @@ struct Row {
             __syncthreads();
             const float most_near = 0.8f * kNear * blocks;
             if (s->at_from - s->at_to > most_near) {  // more than the lists hold: those nearest to where it most likely is
-                if (number <= s->at_likely - 0.5f * most_near) atomicMax(&s->to_bin, bin);
+                if (bin < likely && number - c <= s->at_likely - 0.5f * most_near) atomicMax(&s->to_bin, bin);
                 if (number >= s->at_likely + 0.5f * most_near) atomicMin(&s->least_from, bin);
                 __syncthreads();
                 to_bin = s->to_bin;
@@ -1039,8 +1048,9 @@ struct Row {
                 return 0;
             }
             if (to_bin < 0) break;
-            anchor = to_bin;  // not between these: once more, from a place whose weight is known now
-            known = static_cast<float>(above) * 0x1p-44f;
+            // not between these: once more, from a place whose weight is known now
+            (above < target ? low_bin : high_bin) = to_bin;
+            (above < target ? low : high) = static_cast<float>(above) * 0x1p-44f;
         }
         select<true>(kept, w, target, lowest);
         return 0;
