@@ -1,8 +1,9 @@
 // Drawing tokens from logits (temperature, top-k, top-p, min-p), and judging drafted tokens against the target's logits.
 //
 // Weights.  A row's token v weighs w_v = exp((l_v - m) / T), m the largest logit.  Sums over a vocabulary decide which token a
-// uniform number falls on and where a nucleus ends, so they have to come out the same whatever their order: weights are whole
-// numbers of 2^-44, sums 64-bit integers.  With y = (l - m) log2(e) / T in two 32-bit parts, 2^y of the tokens that matter (y >= -6) comes
+// uniform number falls on and where a nucleus ends, so they have to come out the same each time they are taken, in whatever order blocks and
+// warps add: weights are whole numbers of 2^-44, sums 64-bit integers; only light tokens of 32 bytes are added in 32-bit floating point
+// first, in one order (2^-21 of what they weigh at most).  With y = (l - m) log2(e) / T in two 32-bit parts, 2^y of the tokens that matter (y >= -6) comes
 // from a table of 2^(j/64) and a cubic in the rest |r| <= 2^-7, whose next term is 4e-11: 28 bits.  Lighter tokens take the fast
 // exponential (2^-22) of a difference rounded to 32 bits (2^-24 of |ln w|): 2^-27 of the heaviest token's weight at most.
 //
@@ -12,8 +13,8 @@
 // all blocks, so that they meet at the same barriers.
 //
 // Measured (GB300).  256 rows of 248320 bf16, nothing dropped: 67 us, 1.9 TB/s (the bytes alone 19); 8 x 15 drafts of 248320 fp32 76 us; 96
-// rows of 151936 bf16 whose nuclei hold 75,000 tokens 163 us; 28 of fp32 with nuclei of 20,000 and their distributions 55; one row with top-k
-// 50 10.3, of which 2.5 are the launch; one request's seven drafts, nuclei of a few to 20,000 tokens, 35.  Blocks wait at barriers for most of
+// rows of 151936 bf16 whose nuclei hold 75,000 tokens 121 us; 28 of fp32 with nuclei of 20,000 and their distributions 45; one row with top-k
+// 50 10, of which 2.5 are the launch; one request's seven drafts, nuclei of a few to 20,000 tokens, 30.  Blocks wait at barriers for most of
 // the time that is not instructions (44 to 60 % of the issue slots are used).
 #include <atomic>
 #include <cmath>
@@ -878,7 +879,7 @@ struct Row {
     // Where the nucleus ends is looked for with as few instructions a token as there are. The sum's pass counts tokens in a histogram of
     // eighths of powers of two: the heavier ones, and of the lighter ones an eighth (fp32: a quarter). That gives the place within some percent
     // or less; the next pass weighs what is before it and lists what is near it, exactly. (A histogram with weights of all tokens took 100
-    // instructions and 3 atomics, of a cycle each, a token: 96 rows at temperature 1.6 326 us instead of 180.)
+    // instructions and 3 atomics, of a cycle each, a token: 96 rows at temperature 1.6 took 326 us instead of then 180.)
     //
     // `kept_sum`, unless null: where the nucleus was narrowed down to by the lists, the total of what is kept (else left as it is).
     template <bool LIST>
@@ -1586,7 +1587,7 @@ dspark_status launch(Draw g, int sms, cudaStream_t stream) {
         if (dev < 64) configured.fetch_or(1ull << dev);
     }
     // Blocks of a row's cluster: a block takes some time whatever its slice, about that of 8 KB of it, and two of them (three, where nothing is
-    // dropped) share an SM. 96 rows of 151936 (bf16, nuclei) over 4 | 8 | 16 blocks 227 | 186 | 212 us, 28 of them (fp32) over 8 | 16 61 | 83.
+    // dropped) share an SM. 96 rows of 151936 (bf16, nuclei) over 4 | 8 | 16 blocks 198 | 121 | 207 us, 28 of them (fp32) over 8 | 16 44 | 61.
     constexpr int kShare = WHOLE ? 3 : 2;
     constexpr long long kGoodSlice = 227 * 1024 / kShare - 1024 - static_cast<long long>(shared_bytes(WHOLE)) - 64;
     const long long size = sizeof(T), bytes = g.vocab * size, slots = static_cast<long long>(kShare) * sms;

@@ -727,8 +727,11 @@ dspark_status dspark_paged_attention_debug(const dspark_cache *cache, const dspa
  * uniform number u in [0, 1) draws the lowest token whose p, added up in index order to it, exceeds u.
  * Logits of -infinity and NaN are not tokens; where one is +infinity, those of +infinity weigh the
  * same and the others nothing.  A row without tokens draws -1 and has p = 0.
- * Sums are taken in 64-bit fixed point and do not depend on their order: the same inputs give the
- * same tokens, whatever the number of rows or SMs.  Weights are off by less than 2^-27 of themselves,
+ * The same call gives the same tokens.  Sums are taken in 64-bit fixed point and do not depend on
+ * the order in which they are added; only the weights of 32 neighbouring bytes of logits, where
+ * they are below 2^-6 of the heaviest, are added in 32-bit floating point first.  So a row that is
+ * drawn at another address, or among another number of rows, can draw a neighbouring token where
+ * u or a filter's end is within 2^-21 of a border between two.  Weights are off by less than 2^-27 of themselves,
  * those below 2^-6 by less than 2^-27 of the heaviest one.
  *
  * Filters: each setting is an array, an entry for each row (dspark_sample) or sequence

@@ -46,7 +46,7 @@ def test_judging_keeps_the_targets_distribution():
 
 
 def weight(l, m, temperature):
-    """The kernel's weight of a token of y >= -8, in its steps: fp32 operations (a fused multiply-add rounds once), whole numbers of 2^-44."""
+    """The kernel's weight of a token of y >= -6, in its steps: fp32 operations (a fused multiply-add rounds once), whole numbers of 2^-44."""
     f = np.float32
     c = 1.4426950408889634 / temperature
     hi = f(c)
