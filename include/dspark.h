@@ -723,16 +723,16 @@ dspark_status dspark_paged_attention_debug(const dspark_cache *cache, const dspa
  *          weigh together; the first one always does (1: all)
  *   min_p  of those, the ones stay that weigh at least min_p (the first one weighs 1; 0: all)
  * p_v = w_v over the sum of what is left, 0 for what is not.  T = 0 leaves the first token only;
- * one above 0 and beyond 1e-30 .. 1e30 is taken as that bound.  A
- * uniform number u in [0, 1) draws the lowest token whose p, added up in index order to it, exceeds u.
+ * one above 0 and beyond 1e-30 .. 1e30 is taken as that bound.  A uniform number u in [0, 1) draws the
+ * lowest token whose p, added up in index order to it, exceeds u.
  * Logits of -infinity and NaN are not tokens; where one is +infinity, those of +infinity weigh the
  * same and the others nothing.  A row without tokens draws -1 and has p = 0.
  * The same call gives the same tokens.  Sums are taken in 64-bit fixed point and do not depend on
  * the order in which they are added; only the weights of 32 neighbouring bytes of logits, where
  * they are below 2^-6 of the heaviest, are added in 32-bit floating point first.  So a row that is
  * drawn at another address, or among another number of rows, can draw a neighbouring token where
- * u or a filter's end is within 2^-21 of a border between two.  Weights are off by less than 2^-27 of themselves,
- * those below 2^-6 by less than 2^-27 of the heaviest one.
+ * u or a filter's end is within 2^-21 of a border between two.  Weights are off by less than 2^-27
+ * of themselves, those below 2^-6 by less than 2^-27 of the heaviest one.
  *
  * Filters: each setting is an array, an entry for each row (dspark_sample) or sequence
  * (dspark_verify_drafts), or where that is NULL the number for all.  The numbers are checked
