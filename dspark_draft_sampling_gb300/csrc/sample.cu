@@ -1184,16 +1184,23 @@ __device__ __forceinline__ void give(const Draw &g, long long r, size_t row_at, 
     int setting = static_cast<int>(r), draft = -1;
     if (VERIFY) {  // the first sequence whose rows r is among
         setting = g.n_seqs;
-        for (int q0 = 0; q0 < g.n_seqs && setting == g.n_seqs; q0 += 32) {
-            const int q = q0 + lane;
-            int a = 0, b = -1;
-            if (q < g.n_seqs) a = g.cu_drafts[q], b = g.cu_drafts[q + 1];
-            const bool here = q < g.n_seqs && a >= 0 && b >= a && b <= g.n_drafts && r >= a + q && r <= b + q;
-            const unsigned found = __ballot_sync(0xffffffffu, here);
-            if (found) {
-                setting = q0 + __ffs(found) - 1;
-                draft = __shfl_sync(0xffffffffu, r < b + q ? static_cast<int>(r) - q : -1, __ffs(found) - 1);
-            }
+        // their first rows ascend: 32 places at a time, until 32 sequences are left (each 32 sequences in turn: 2048 of 3 drafts of 4000 tokens
+        // 340 us instead of 260)
+        int q0 = 0;
+        for (int q1 = g.n_seqs; q1 - q0 > 32;) {
+            const int step = (q1 - q0 + 31) / 32, at = min(q0 + lane * step, q1 - 1);
+            const unsigned upto = __ballot_sync(0xffffffffu, g.cu_drafts[at] + static_cast<long long>(at) <= r);
+            q0 = min(q0 + max(31 - __clz(upto), 0) * step, q1 - 1);
+            q1 = min(q0 + step, q1);
+        }
+        const int q = q0 + lane;
+        int a = 0, b = -1;
+        if (q < g.n_seqs) a = g.cu_drafts[q], b = g.cu_drafts[q + 1];
+        const bool here = q < g.n_seqs && a >= 0 && b >= a && b <= g.n_drafts && r >= a + q && r <= b + q;
+        const unsigned found = __ballot_sync(0xffffffffu, here);
+        if (found) {
+            setting = q0 + __ffs(found) - 1;
+            draft = __shfl_sync(0xffffffffu, r < b + q ? static_cast<int>(r) - q : -1, __ffs(found) - 1);
         }
     }
     if (lane == 0) {

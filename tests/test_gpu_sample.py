@@ -348,6 +348,25 @@ def test_drafts_that_are_none_and_sequences_without_any():
     judge(gen, [0] * 1300, 40, torch.float32, (1.0, 0, 1.0, 0.0), drawn=False, scalar=True)
 
 
+def test_judging_many_sequences():
+    """More sequences than a row's own is looked for among at a time, of none to three drafts, each with its settings; then rows behind them
+    and a last sequence whose end is out of range."""
+    gen = torch.Generator().manual_seed(29)
+    for seqs in (33, 64, 1025):
+        settings = [SETTINGS[i % len(SETTINGS)] for i in range(seqs)]
+        judge(gen, [(i * 7 + i // 5) % 4 for i in range(seqs)], 40, torch.float32, settings, drawn=seqs % 2 == 0)
+    seqs = 1100
+    cu = torch.arange(0, 2 * seqs + 1, 2, dtype=torch.int32)
+    cu[-1] = 4 * seqs
+    x = torch.randn((4 * seqs, 50), generator=gen).cuda()
+    drafts = torch.zeros(3 * seqs, dtype=torch.int64)
+    drafts[:2 * seqs] = x.cpu().view(-1, 50)[torch.arange(3 * seqs).view(seqs, 3)[:, :2].reshape(-1)].argmax(1)
+    ids, taken = torch.full((4 * seqs,), -77).cuda(), torch.full((seqs,), -77, dtype=torch.int32).cuda()
+    api.verify_drafts(x, drafts.cuda(), cu.cuda(), torch.zeros((4 * seqs, 2)).cuda(), temperature=0.0, out=ids, accepted=taken)
+    assert taken.tolist() == [2] * (seqs - 1) + [-77]
+    assert (ids[3 * (seqs - 1):] == -77).all() and torch.equal(ids[:3 * (seqs - 1)], x[:3 * (seqs - 1)].argmax(1))
+
+
 def test_special_distributions():
     """The draft's distribution is the target's (all accepted), misses it altogether (none), and rows without tokens."""
     vocab, k = 333, 6
