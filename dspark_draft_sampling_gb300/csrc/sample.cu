@@ -39,6 +39,8 @@ constexpr float kSpread = kBins - 0.1f;   // bins of equal width over a range, s
 constexpr int kList = kThreads;           // tokens that one block sorts: a thread to each
 constexpr int kNear = 1024;               // tokens of a block's slice around a nucleus' end
 constexpr int kMaxBlocks = 16;            // of a cluster
+constexpr int kMostSlice = 128 * 1024;    // bytes; 2^19 fp32 logits over kMaxBlocks blocks
+static_assert(kMostSlice / (kThreads * 32) + 1 <= kWarps, "a slice's rounds of 32 bytes a thread are one for each warp at most");
 constexpr int kHeavy = 6;                 // powers of two below the heaviest token down to which weights are exact to 28 bits
 constexpr int kCounted = 10;               // powers of two below it down to which a nucleus' end is looked for among all tokens
 constexpr float kLowest = -3.402823466e38f;
@@ -407,6 +409,20 @@ struct MassSum {
         else c += w.light_weight(p, e);
     }
     __device__ __forceinline__ u64 sum() const { return h + w.whole(c); }
+    __device__ __forceinline__ static u64 up(float x) {  // light weights in whole numbers, rounded up
+        const u64 v = to_whole(x);
+        return v + (v >> 24) + (static_cast<float>(v) < x ? 1 : 0);
+    }
+    // What token t of a vector adds to vector(), in h and c.
+    __device__ __forceinline__ void token(const uint4 *at, int first, int t) {
+        const unsigned special = light_weights(w, kept, at, [&](int u, u64 two) {
+            float a, b;
+            split_f32(two, &a, &b);
+            if (u == t >> 1) c = (t & 1 ? b : a) * 0x1p44f;
+        });
+        if (SKIP && first + t == skip) c = 0.f;
+        if (special >> t & 1) add(Type<T>::one(at, t), first + t);
+    }
     __device__ __forceinline__ u64 vector(const uint4 *at, int first) {
         constexpr int P = Type<T>::kPer;
         u64 s[2] = {0, 0};
@@ -434,17 +450,19 @@ template <typename T>
 struct TieSum {
     float value;
     const Kept &kept;
-    u64 n = 0;
+    u64 h = 0;
+    static constexpr float c = 0.f;
     __device__ __forceinline__ TieSum(float v, const Kept &b) : value(v), kept(b) {}
-    __device__ __forceinline__ void add(float l, int i) { n += l == value && kept.order(l, i) ? 1 : 0; }
-    __device__ __forceinline__ u64 sum() const { return n; }
+    __device__ __forceinline__ void add(float l, int i) { h += l == value && kept.order(l, i) ? 1 : 0; }
+    __device__ __forceinline__ static u64 up(float) { return 0; }
+    __device__ __forceinline__ void token(const uint4 *at, int first, int t) { add(Type<T>::one(at, t), first + t); }
     __device__ __forceinline__ u64 vector(const uint4 *at, int first) {
         float x[Type<T>::kPer];
         Type<T>::spread(at[0], x);
         Type<T>::spread(at[1], x + Type<T>::kVector);
 #pragma unroll
         for (int u = 0; u < Type<T>::kPer; ++u) add(x[u], first + u);
-        return n;
+        return h;
     }
 };
 
@@ -492,6 +510,21 @@ struct RestSum {
         else c += light_rest(w.light_weight(p, e) * 0x1p-44f, q[i]);
     }
     __device__ __forceinline__ u64 sum() const { return h + to_whole(c * 0x1p62f); }
+    __device__ __forceinline__ static u64 up(float x) {
+        const u64 v = to_whole(x * 0x1p62f);
+        return v + (static_cast<float>(v) < x * 0x1p62f ? 1 : 0);
+    }
+    // What token t of a vector adds to vector(), in h and c.
+    __device__ __forceinline__ void token(const uint4 *at, int first, int t) {
+        if (Type<T>::largest(Type<T>::larger(at[0], at[1])) < kept.value) return;
+        const float share = first + t >= 0 && first + t < vocab ? q[first + t] : 0.f;
+        const unsigned special = light_weights(w, kept, at, [&](int u, u64 two) {
+            float a, b;
+            split_f32(two, &a, &b);
+            if (u == t >> 1) c = light_rest(t & 1 ? b : a, share);
+        });
+        if (special >> t & 1) add(Type<T>::one(at, t), first + t);
+    }
     __device__ __forceinline__ u64 vector(const uint4 *at, int first) {
         constexpr int P = Type<T>::kPer;
         if (Type<T>::largest(Type<T>::larger(at[0], at[1])) < kept.value) return 0;
@@ -606,47 +639,39 @@ struct Row {
         auto a = make();
         return v < vectors ? a.vector(data + 2 * v, first + v * kPer) : 0;
     }
-    // The first token at which the sum over the slice, taken just before by total(), exceeds `target` (less than it): its index, in s->found.
-    // Called by the whole block. The stretch of the warp that it falls to is looked at by all warps, a round each.
+    // The first token at which the sum over the slice, taken just before by total() or tally(), exceeds `target` (less than it): its index, in
+    // s->found. Called by the whole block. The stretch of the warp that it falls to is looked at by all warps, a round each.
+    //
+    // Sums are whole numbers from vectors on, so within a vector, whose tokens may each be less than one, they are taken as they are: exact sums and
+    // 32-bit ones, of the very terms that the vector's sum has. So where that is not 0, neither is each of them, and what is found weighs something:
+    // never a token that is masked, dropped or not the slice's.
     template <typename M>
     __device__ __forceinline__ void find(M make, u64 target) {
-        u64 before;
-        const int w = first_past(s->warp, 0, target, &before);
-        for (int k0 = 0; k0 < rounds; k0 += kWarps) {
-            const int k = k0 + warp, v = k < rounds ? (w * rounds + k) * 32 + lane : vectors;
-            const u64 mine = vector_sum(make, v), all = warp_sum(mine);
-            __syncthreads();
-            if (lane == 0) s->scan[1][warp] = all;
-            __syncthreads();
-            u64 upto;
-            int j = first_past(s->scan[1], before, target, &upto);  // the round among these
-            if (upto + s->scan[1][j] <= target) {
-                if (k0 + kWarps < rounds) {
-                    before = upto + s->scan[1][j];
-                    continue;
-                }
-                // the stretch's sum was a rounding larger: the last token of it that weighs anything
-                const unsigned any = __ballot_sync(0xffffffffu, lane < kWarps && s->scan[1][lane % kWarps] > 0);
-                j = any ? 31 - __clz(any) : 0;
-            }
-            if (warp != j) return;
-            const u64 prefix = upto + warp_prefix(mine, lane);
-            const unsigned past = __ballot_sync(0xffffffffu, prefix > target), some = __ballot_sync(0xffffffffu, mine > 0);
-            const int owner = past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
-            upto = __shfl_sync(0xffffffffu, prefix - mine, owner);
-            const int at = first + __shfl_sync(0xffffffffu, v, owner) * kPer;
-            // a lane to each of its tokens; their sum may be a rounding less than the vector's: then the last that weighs anything
-            float x[kPer];
-            spread(__shfl_sync(0xffffffffu, v, owner), x);
-            auto a = make();
-#pragma unroll
-            for (int u = 0; u < kPer; ++u)
-                if (lane == u) a.add(x[u], at + u);
-            const u64 one = a.sum(), here_upto = upto + warp_prefix(one, lane);
-            const unsigned any = __ballot_sync(0xffffffffu, one > 0), here = any & __ballot_sync(0xffffffffu, here_upto > target);
-            if (lane == 0) s->found = at + (here ? __ffs(here) - 1 : any ? 31 - __clz(any) : 0);
-            return;
-        }
+        u64 before, upto;
+        const int w = first_past(s->warp, 0, target, &before), v = warp < rounds ? (w * rounds + warp) * 32 + lane : vectors;
+        const u64 mine = vector_sum(make, v), all = warp_sum(mine);
+        __syncthreads();
+        if (lane == 0) s->scan[1][warp] = all;
+        __syncthreads();
+        int j = first_past(s->scan[1], before, target, &upto);
+        // tally() adds tokens one by one, which may be a rounding more than this: then the last one of the stretch that weighs anything. There is one, as each
+        // token of a nucleus weighs two units at least: with those behind it, fewer than 2^19 and none heavier, it weighs more than 1 - top_p >= 2^-24
+        // of 2^44 units.
+        const bool short_of = upto + s->scan[1][j] <= target;
+        if (short_of) j = 31 - __clz(__ballot_sync(0xffffffffu, lane < kWarps && s->scan[1][lane % kWarps] > 0) | 1u);
+        if (warp != j) return;
+        const u64 prefix = upto + warp_prefix(mine, lane);
+        const unsigned past = __ballot_sync(0xffffffffu, prefix > target), some = __ballot_sync(0xffffffffu, mine > 0);
+        const int owner = past && !short_of ? __ffs(past) - 1 : 31 - __clz(some | 1u);
+        upto = __shfl_sync(0xffffffffu, prefix - mine, owner);
+        const int at = __shfl_sync(0xffffffffu, v, owner);
+        auto a = make();
+        if (lane < kPer) a.token(data + 2 * at, first + at * kPer, lane);
+        const u64 h = upto + warp_prefix(a.h, lane);
+        const float c = warp_prefix(static_cast<float>(a.c), lane);
+        const unsigned any = __ballot_sync(0xffffffffu, a.h > 0 || a.c > 0.f);
+        const unsigned here = any & __ballot_sync(0xffffffffu, h > target || a.up(c) > target - h);
+        if (lane == 0) s->found = first + at * kPer + (here && !short_of ? __ffs(here) - 1 : 31 - __clz(any | 1u));
     }
 
     // The first of kWarps numbers at which their sum, with `before`, exceeds `target` (the last one if none does), and the sum before it.
@@ -1577,8 +1602,6 @@ cudaError_t launch_cluster(void (*kernel)(Args...), int grid, int cluster, int t
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
-
-constexpr int kMostSlice = 128 * 1024;  // bytes; kMaxVocab fp32 logits over kMaxBlocks blocks
 
 template <typename T, bool VERIFY, bool WHOLE>
 dspark_status launch(Draw g, int sms, cudaStream_t stream) {
