@@ -1121,7 +1121,7 @@ struct Row {
             low += first * step;
         }
         const float value = value_of(static_cast<u64>(low) << 32);
-        if (value > kept->value) *kept = {value, kNoIndex};
+        if (value >= kept->value) *kept = {value, kNoIndex};  // also of the logit that another setting ended on, of which some are left
     }
     // The least and the largest of the cluster's codes.
     __device__ __forceinline__ void exchange_range(unsigned least, unsigned most, unsigned *c0, unsigned *c1) {

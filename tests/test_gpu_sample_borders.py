@@ -126,3 +126,32 @@ def test_rests_that_are_rounding_alone(dtype):
             at = np.arange(seqs)
             assert ((got >= 0) & (got < vocab)).all() and (p[at, got] > 0).all()
             assert (p[at, got] >= q.double().numpy()[at, got] * (1 - 2.0**-19)).all()
+
+
+# ---- filters that end among equal logits ----
+
+@pytest.mark.parametrize("per_row", [False, True])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("settings", [dict(top_k=600), dict(top_p=0.5), dict(top_k=900, top_p=0.7), dict(top_k=1001), dict()])
+def test_min_p_drops_the_logit_that_another_filter_ended_on(settings, dtype, per_row):
+    """One token of logit 0 and 1000 of -1, of which top_k or top_p leaves some hundred: too many to be listed.  min_p is exp(-1) rounded up, by 2.5e-8
+    of itself where a weight is off by 2^-27 = 7.5e-9 at most, so that one token is left."""
+    vocab, min_p = 2500, float(np.float32(math.exp(-1)))
+    assert min_p > math.exp(-1) * (1 + 2.0**-26)
+    x = torch.full((2, vocab), -INF)
+    x[:, 700:1700] = -1.0
+    x[:, 1234] = 0.0
+    x = x.to(TYPES[dtype]).cuda()
+    kw = dict(settings, min_p=min_p)
+    if per_row:
+        kw = {n: torch.full((2,), v, dtype=torch.int32 if n == "top_k" else torch.float32, device="cuda") for n, v in kw.items()}
+    u = torch.tensor([0.0, 0.999], device="cuda")
+    ids, p = api.sample(x, u, return_probs=True, **kw)
+    assert ids.tolist() == [1234, 1234]
+    assert (p[:, 1234] == 1).all() and (p != 0).sum() == 2
+    # no draft of the others is accepted
+    one = {n: v[:1] if per_row else v for n, v in kw.items()}
+    for draft, want in ((700, [1234, -1]), (1234, [1234, 1234])):
+        ids, n = api.verify_drafts(x, torch.tensor([draft], device="cuda"), torch.tensor([0, 1], dtype=torch.int32, device="cuda"),
+                                   torch.tensor([[0.0, 0.7], [0.5, 0.2]], device="cuda"), **one)
+        assert ids.tolist() == want and n.tolist() == [int(draft == 1234)]
