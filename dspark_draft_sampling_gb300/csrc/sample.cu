@@ -1243,7 +1243,7 @@ __device__ __forceinline__ void give(const Draw &g, long long r, size_t row_at, 
                     v.draft = draft;
                     v.token = static_cast<int>(x);
                     v.logit = Type<T>::one(g.logits, row_at + x);
-                    v.accept = g.uniforms[2 * r];
+                    v.accept = fminf(fmaxf(g.uniforms[2 * r], 0.f), 0x1.fffffep-1f);  // NaN: 0
                     v.share = g.draft_probs ? fmaxf(g.draft_probs[static_cast<size_t>(draft) * g.draft_probs_stride + x], 0.f) : 1.f;
                 }
             }

@@ -755,7 +755,8 @@ dspark_status dspark_paged_attention_debug(const dspark_cache *cache, const dspa
  *   x is accepted if u0 q_x < p_x.  At the first row that does not accept, a token is drawn with u1
  *   from max(0, p - q) (from p, where that is nothing); where all accept, from the last row's p.
  *   logits       [n_drafts + n_seqs, vocab] of dtype
- *   uniforms     float [n_drafts + n_seqs, 2]: u0 and u1 of each row (the last rows' u0 is not used)
+ *   uniforms     float [n_drafts + n_seqs, 2]: u0 and u1 of each row (the last rows' u0 is not used);
+ *                both taken as dspark_sample's where they lie outside [0, 1)
  *   cu_drafts    int32 [n_seqs + 1], from 0, ascending, at most n_drafts
  *   drafts       int64 [n_drafts]; one outside 0 .. vocab - 1 is not accepted, and the token drawn from p
  *   draft_probs  float [n_drafts, vocab], the rows draft_probs_stride apart, or NULL

@@ -155,3 +155,29 @@ def test_min_p_drops_the_logit_that_another_filter_ended_on(settings, dtype, per
         ids, n = api.verify_drafts(x, torch.tensor([draft], device="cuda"), torch.tensor([0, 1], dtype=torch.int32, device="cuda"),
                                    torch.tensor([[0.0, 0.7], [0.5, 0.2]], device="cuda"), **one)
         assert ids.tolist() == want and n.tolist() == [int(draft == 1234)]
+
+
+# ---- uniform numbers outside 0..1 ----
+
+@pytest.mark.parametrize("settings", [dict(), dict(top_k=5), dict(top_p=0.9), dict(temperature=0.0)])
+def test_judging_by_numbers_outside_their_range(settings):
+    """u0 below 0 or NaN is 0, 1 and above just below 1: a draft that the target never takes is not accepted, one that it always takes is."""
+    vocab, k = 1000, 7
+    u = torch.rand((k + 1, 2), generator=torch.Generator().manual_seed(3))
+    cu = torch.tensor([0, k], dtype=torch.int32, device="cuda")
+    x = torch.randn((k + 1, vocab), generator=torch.Generator().manual_seed(4))
+    x[:, 17] = -INF
+    best = x.argmax(1)
+    for q in (None, torch.full((k, vocab), 1.0 / vocab, device="cuda")):
+        for u0 in (-0.5, -INF, NAN, 0.0):
+            u[:, 0] = u0
+            ids, n = api.verify_drafts(x.cuda(), torch.full((k,), 17, device="cuda"), cu, u.cuda(), draft_probs=q, **settings)
+            assert n.tolist() == [0] and ids[0] != 17 and ids[0] >= 0, (u0, q is None)
+            ids, n = api.verify_drafts(x.cuda(), best[:k].cuda(), cu, u.cuda(), draft_probs=q, **settings)
+            assert n.tolist() == [k] and ids[:k].tolist() == best[:k].tolist(), (u0, q is None)
+    one = torch.full((k + 1, vocab), -INF)
+    one[:, 33] = 2.0
+    for u0 in (1.0, 1.5, INF):
+        u[:, 0] = u0
+        ids, n = api.verify_drafts(one.cuda(), torch.full((k,), 33, device="cuda"), cu, u.cuda(), **settings)
+        assert n.tolist() == [k] and (ids == 33).all(), u0
