@@ -290,7 +290,7 @@ struct Weights {
     __device__ __forceinline__ Weights(float m, const Given &g, const uint2 *t) : top(m), hi(g.hi), lo(g.lo), least(g.least), table(t) {
         clamp = Type<T>::down(top + least);
         const float y = (Type<T>::low(clamp) - top) * hi;
-        simple = y <= -100.f && y > -1.0e4f && top + least > Type<T>::kLeast && top < 1.0e37f;
+        simple = y <= -127.f && y > -1.0e4f && top + least > Type<T>::kLeast && top < 1.0e37f;  // 2^y is flushed to 0
     }
     // y of a logit that is not NaN, as two parts
     __device__ __forceinline__ void exponent(float l, float *p, float *e) const {

@@ -181,3 +181,35 @@ def test_judging_by_numbers_outside_their_range(settings):
         u[:, 0] = u0
         ids, n = api.verify_drafts(one.cuda(), torch.full((k,), 33, device="cuda"), cu, u.cuda(), **settings)
         assert n.tolist() == [k] and (ids == 33).all(), u0
+
+
+# ---- what is dropped has no probability at all ----
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_dropped_tokens_have_a_probability_of_zero(dtype):
+    """Exactly 0, whatever stands in for them on the way; and what is left sums to 1 (each value is off by 2^-21 of itself at most, and by
+    |ln w| 2^-24, which is largest where w is least: w |ln w| < 0.4)."""
+    t = TYPES[dtype]
+    gen = torch.Generator().manual_seed(41)
+    far = float(torch.finfo(t).max) / 4
+    settings = [(1.0, 0, 1.0, 0.0), (0.7, 40, 1.0, 0.0), (1.3, 700, 1.0, 0.0), (1.3, 0, 0.9, 0.0), (8.0, 0, 0.9, 0.0), (1.0, 0, 1.0, 0.01), (2.0, 900, 0.8, 0.001),
+                (0.0, 0, 1.0, 0.0), (1e-3, 0, 1.0, 0.0), (1e4, 0, 0.6, 0.0)]
+    for vocab in (300, 5003):
+        for shift, spread in ((0.0, 3.0), (-1000.0, 3.0), (1000.0, 30.0), (0.0, far), (-far, 1.0)):
+            x = (torch.randn((len(settings), vocab), generator=gen).clamp(-3, 3) * spread + shift).to(t)
+            x[:, 3::7] = -INF
+            x[:, 5::11] = NAN
+            columns = [torch.tensor(c) for c in zip(*settings)]
+            kw = dict(temperature=columns[0].float().cuda(), top_k=columns[1].int().cuda(), top_p=columns[2].float().cuda(), min_p=columns[3].float().cuda())
+            _, p = api.sample(x.cuda(), torch.full((len(settings),), 0.5, device="cuda"), return_probs=True, **kw)
+            p = p.cpu().double().numpy()
+            for r, (temperature, k, top_p, m) in enumerate(settings):
+                host = x[r].double().numpy()
+                f = lambda v: float(np.float32(v))  # noqa: E731
+                want = ref.distribution(host, f(temperature), k, 1.0, f(m))  # top_p's end may lie between two tokens: what the others leave
+                assert (p[r][~(host > -INF)] == 0).all() and (p[r][want == 0] == 0).all(), (vocab, shift, spread, settings[r])
+                kept = np.flatnonzero(p[r])
+                if top_p < 1:  # the first ones of the order
+                    order = np.lexsort((np.arange(vocab), -np.where(host > -INF, host, -INF)))
+                    assert set(kept) == set(order[:len(kept)])
+                assert abs(p[r].sum() - 1) < 2.0**-20, (vocab, shift, spread, settings[r])
