@@ -1118,7 +1118,8 @@ def paged_attention(q, cache: PagedCache, layer: int, cu_new, *, rows=None, max_
     if sinks == 0:
         status = _launch(lib.dspark_paged_attention, d, stream, cache._ref, args)
     else:
-        status = _launch(lib.dspark_paged_attention_sinks, d, stream, cache._ref, args, sinks)
+        # the call takes 32 bits, as which larger numbers (all tokens) would pass for others
+        status = _launch(lib.dspark_paged_attention_sinks, d, stream, cache._ref, args, max(-1, min(sinks, 2**31 - 1)))
     if status:
         _check(lib, status)
     return (out, lse) if return_lse else out
