@@ -31,9 +31,8 @@ namespace dspark {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = kThreads;           // of a histogram: a thread looks after one
-constexpr int kBinBits = kBins == 512 ? 9 : 8;
-static_assert(1 << kBinBits == kBins, "");
+constexpr int kBinBits = 9, kBins = 1 << kBinBits;  // of a histogram
+static_assert(kBins == kThreads, "a thread looks after a bin");
 constexpr int kOctave = kBins / 64;       // of them to a power of two, where they divide weights
 constexpr float kSpread = kBins - 0.1f;   // bins of equal width over a range, short of the end
 constexpr int kList = kThreads;           // tokens that one block sorts: a thread to each
@@ -1617,7 +1616,8 @@ dspark_status launch(Draw g, int sms, cudaStream_t stream) {
         if (dev < 64) configured.fetch_or(1ull << dev);
     }
     // Blocks of a row's cluster: a block takes some time whatever its slice, about that of 8 KB of it, and two of them (three, where nothing is
-    // dropped) share an SM. 96 rows of 151936 (bf16, nuclei) over 4 | 8 | 16 blocks 198 | 121 | 207 us, 28 of them (fp32) over 8 | 16 44 | 61.
+    // dropped) share an SM. 96 rows of 151936 (bf16, nuclei) over 4 | 8 | 16 blocks 198 | 121 | 207 us, 28 of them (fp32) over 8 | 16 44 | 61. An
+    // estimate: it counts SMs, where a cluster has to fit into one of the GPU's groups of them, and tries powers of two alone.
     constexpr int kShare = WHOLE ? 3 : 2;
     constexpr long long kGoodSlice = 227 * 1024 / kShare - 1024 - static_cast<long long>(shared_bytes(WHOLE)) - 64;
     const long long size = sizeof(T), bytes = g.vocab * size, slots = static_cast<long long>(kShare) * sms;
