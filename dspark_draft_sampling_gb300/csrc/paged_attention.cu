@@ -32,8 +32,8 @@
 // stream, the rest start and joins. Chunks of 90-1500 tokens in a window of 1000, 28 / 4 heads of 64: 66 us (69 with each masked score compared with both ends), where the chain
 // of one stream (scores, softmax, second product) takes 2500 cycles a pair of key tiles and the products 1024. One token
 // over 777 keys: 11 us. With a row's first tokens beside a window: one token over 50,001 keys, window 1024, 4 sinks 12.0 us; 16 x 7 tokens
-// over 300-30,000 keys, window 2048, 20 sinks 31.4 us for 131 MB; 64 single tokens, 28 / 4 heads of 64, window 4000, 64 sinks 60.4 us for
-// 244 MB (the chain of one stream again); 4096 tokens after 12,288, window 4096, 128 sinks 196 us, 1.45 PFLOP/s.
+// over 300-30,000 keys, window 2048, 20 sinks 30.3 us for 131 MB; 64 single tokens, 28 / 4 heads of 64, window 4000, 64 sinks 59 us for
+// 244 MB (the chain of one stream again); 4096 tokens after 12,288, window 4096, 128 sinks 196-207 us, 1.37-1.45 PFLOP/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -3,7 +3,8 @@
 // Weights.  A row's token v weighs w_v = exp((l_v - m) / T), m the largest logit.  Sums over a vocabulary decide which token a
 // uniform number falls on and where a nucleus ends, so they have to come out the same each time they are taken, in whatever order blocks and
 // warps add: weights are whole numbers of 2^-44, sums 64-bit integers; only light tokens of 32 bytes are added in 32-bit floating point
-// first, in one order (2^-21 of what they weigh at most).  With y = (l - m) log2(e) / T in two 32-bit parts, 2^y of the tokens that matter (y >= -6) comes
+// first, in one order (2^-21 of what they weigh at most), and cut to whole units together; a draw that falls on them looks at their terms
+// uncut.  With y = (l - m) log2(e) / T in two 32-bit parts, 2^y of the tokens that matter (y >= -6) comes
 // from a table of 2^(j/64) and a cubic in the rest |r| <= 2^-7, whose next term is 4e-11: 28 bits.  Lighter tokens take the fast
 // exponential (2^-22) of a difference rounded to 32 bits (2^-24 of |ln w|): 2^-27 of the heaviest token's weight at most.
 //
@@ -12,9 +13,9 @@
 // microseconds an exchange (the cluster's barrier and the wait for the slowest block).  What is decided by what was exchanged is the same in
 // all blocks, so that they meet at the same barriers.
 //
-// Measured (GB300).  256 rows of 248320 bf16, nothing dropped: 67 us, 1.9 TB/s (the bytes alone 19); 8 x 15 drafts of 248320 fp32 76 us; 96
-// rows of 151936 bf16 whose nuclei hold 75,000 tokens 121 us; 28 of fp32 with nuclei of 20,000 and their distributions 45; one row with top-k
-// 50 10, of which 2.5 are the launch; one request's seven drafts, nuclei of a few to 20,000 tokens, 30.  Blocks wait at barriers for most of
+// Measured (GB300).  256 rows of 248320 bf16, nothing dropped: 65 us, 2.0 TB/s (the bytes alone 19); 8 x 15 drafts of 248320 fp32 79 us; 96
+// rows of 151936 bf16 whose nuclei hold 75,000 tokens 120 us; 28 of fp32 with nuclei of 20,000 and their distributions 45; one row with top-k
+// 50 10, of which 2.5 are the launch; one request's seven drafts, nuclei of a few to 20,000 tokens, 24 to 29.  Blocks wait at barriers for most of
 // the time that is not instructions (44 to 60 % of the issue slots are used).
 #include <atomic>
 #include <cmath>
@@ -1208,8 +1209,8 @@ __device__ __forceinline__ void give(const Draw &g, long long r, size_t row_at, 
     int setting = static_cast<int>(r), draft = -1;
     if (VERIFY) {  // the first sequence whose rows r is among
         setting = g.n_seqs;
-        // their first rows ascend: 32 places at a time, until 32 sequences are left (each 32 sequences in turn: 2048 of 3 drafts of 4000 tokens
-        // 340 us instead of 260)
+        // their first rows ascend: 32 places at a time, until 32 sequences are left (each 32 sequences in turn: 80 us more for 2048 of 3 drafts
+        // of 4000 tokens, which take 224)
         int q0 = 0;
         for (int q1 = g.n_seqs; q1 - q0 > 32;) {
             const int step = (q1 - q0 + 31) / 32, at = min(q0 + lane * step, q1 - 1);
