@@ -664,7 +664,7 @@ struct Row {
         const unsigned past = __ballot_sync(0xffffffffu, prefix > target), some = __ballot_sync(0xffffffffu, mine > 0);
         const int owner = past && !short_of ? __ffs(past) - 1 : 31 - __clz(some | 1u);
         upto = __shfl_sync(0xffffffffu, prefix - mine, owner);
-        const int at = __shfl_sync(0xffffffffu, v, owner);
+        const int at = min(__shfl_sync(0xffffffffu, v, owner), vectors - 1);  // a vector of the slice, whatever the sums are
         auto a = make();
         if (lane < kPer) a.token(data + 2 * at, first + at * kPer, lane);
         const u64 h = upto + warp_prefix(a.h, lane);
